@@ -4,7 +4,9 @@ The product is the C-ABI library ``libgemmpipe.so`` (header
 ``include/gemm_pipelined.h``); this package holds its sources (``csrc/``), the
 in-tree build (``build.py``), a thin ctypes binding (``_binding``) with the same
 entry-point names, and a torch convenience wrapper ``gemm`` that only
-allocates the output and passes pointers.  ``synth`` generates the seeded
+allocates the output and passes pointers.  ``fp8`` does the same for the 8-bit
+operators (``include/gemm_fp8.h``): quantisation, the scaled product, and the
+RMS norm with its gradient.  ``synth`` generates the seeded
 synthetic operands.
 """
 from ._binding import (  # noqa: F401
@@ -12,6 +14,19 @@ from ._binding import (  # noqa: F401
     GP_ERR_SIZE, GP_ERR_SCRATCH, GemmError, abi_version, gemm_pipelined, gemm_pipelined_noalloc, gemm_plan,
     gemm_plan_rc, gemm_stats, probe_hbm, probe_peak, release, strerror, lib,
 )
+
+
+# the operators of fp8.py, which needs torch: loaded when first used
+_FP8 = ("dequantize_fp8", "gemm_fp8", "gemm_fp8_plan", "quantize_fp8", "rmsnorm_backward", "rmsnorm_fp8")
+
+
+def __getattr__(name):
+    if name not in _FP8:
+        raise AttributeError("module %r has no attribute %r" % (__name__, name))
+    from . import fp8
+    globals().update({f: getattr(fp8, f) for f in _FP8})
+    return globals()[name]
+
 
 _OUT_DTYPE = {"i8": "int32", "f16": "float16", "bf16": "bfloat16", "f32": "float32"}
 

@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in include/gemm_pipelined.h.
+"""ctypes binding of the C ABI in include/gemm_pipelined.h, gemm_probe.h and gemm_fp8.h.
 
 Argument marshalling only: every step of the GEMM runs in the CUDA kernels of
 libgemmpipe.so.  If the library is missing the first call raises -- there is
@@ -36,13 +36,18 @@ SITES = {1: "device", 2: "event", 3: "capacity", 4: "workspace", 5: "tensor_map"
          8: "sync"}
 
 DTYPES = {"i8": GP_I8_I32, "f16": GP_F16_F32ACC_F16OUT, "bf16": GP_BF16_F32ACC_BF16OUT, "f32": GP_F32}
+# gp_fp8_format, gp_real
+FP8_FORMATS = {"e4m3": 0, "e5m2": 1}
+REALS = {"f16": 0, "bf16": 1, "f32": 2}
+GP_PLAN_FP8 = 16      # gp_plan.dtype of a gemm_fp8 call
+
 LAYOUTS = {"row_col": GP_A_ROW_B_COL, "row_row": GP_A_ROW_B_ROW}
 VARIANTS = {"pingpong": GP_PINGPONG, "pipelined": GP_PIPELINED, "nopipe": GP_NOPIPE}
 
 # exported symbols, in header order
 SYMBOLS = ["gemm_pipelined", "gemm_pipelined_ex", "gemm_plan", "gemm_plan_ex", "gemm_stats", "gemm_strerror",
            "gemm_abi_version", "gemm_release", "gemm_pipelined_noalloc", "gemm_probe_peak",
-           "gemm_probe_hbm"]
+           "gemm_probe_hbm", "gemm_fp8", "gemm_fp8_plan", "fp8_quantize", "fp8_rmsnorm", "fp8_rmsnorm_backward"]
 
 
 class GpPlan(ctypes.Structure):
@@ -88,6 +93,21 @@ class GpOptions(ctypes.Structure):
     ]
 
 
+class GpFp8Matrix(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("ld", ctypes.c_int64),
+        ("stride_row", ctypes.c_int64), ("stride_col", ctypes.c_int64), ("format", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+    ]
+
+
+class GpFp8Options(ctypes.Structure):
+    _fields_ = [
+        ("timeout_ns", ctypes.c_uint64), ("bn", ctypes.c_int32), ("no_split", ctypes.c_int32),
+        ("inject_lost_load", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -128,6 +148,17 @@ def lib():
     L.gemm_probe_peak.restype = ci
     L.gemm_probe_hbm.argtypes = [ci, vp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_double), vp]
     L.gemm_probe_hbm.restype = ci
+    mat, fopt = ctypes.POINTER(GpFp8Matrix), ctypes.POINTER(GpFp8Options)
+    L.gemm_fp8.argtypes = [mat, mat, vp, i64, vp, i64, i64, i64, i64, ci, vp, fopt]
+    L.gemm_fp8.restype = ci
+    L.gemm_fp8_plan.argtypes = [i64, i64, i64, ci, ci, ci, fopt, ctypes.POINTER(GpPlan)]
+    L.gemm_fp8_plan.restype = ci
+    L.fp8_quantize.argtypes = [vp, i64, i64, i64, ci, mat, mat, vp]
+    L.fp8_quantize.restype = ci
+    L.fp8_rmsnorm.argtypes = [vp, i64, vp, i64, vp, ci, ctypes.c_float, i64, i64, ci, vp, i64, vp, vp, i64, mat, vp]
+    L.fp8_rmsnorm.restype = ci
+    L.fp8_rmsnorm_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, ci, vp, i64, i64, ci, vp, i64, vp, vp]
+    L.fp8_rmsnorm_backward.restype = ci
     _lib = L
     return L
 

@@ -10,6 +10,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "fp8_internal.h"
 #include "gp_internal.h"
 
 namespace gp {
@@ -106,6 +107,9 @@ struct Workspace {
   uint32_t* ov_ctrs = nullptr;   // INT8 conversion / GEMM hand-off counters: two sets of ov_kcap + 1 words
   int32_t ov_kcap = 0;
   uint32_t ov_launches = 0;
+  float* fp8 = nullptr;       // FP8 operators: partial tiles and partial sums
+  size_t fp8_bytes = 0;
+  uint32_t* fp8_ctrs = nullptr;   // kFp8Counters counters, zero between launches
 };
 constexpr int kMaxWorkspaces = 64;
 Workspace g_ws[kMaxWorkspaces];
@@ -117,6 +121,8 @@ void free_workspace(Workspace& w) {
   if (w.flags) cudaFree(w.flags);
   if (w.conv) cudaFree(w.conv);
   if (w.ov_ctrs) cudaFree(w.ov_ctrs);
+  if (w.fp8) cudaFree(w.fp8);
+  if (w.fp8_ctrs) cudaFree(w.fp8_ctrs);
   w = Workspace();
 }
 
@@ -707,6 +713,78 @@ void record(int status, int cuda_err, int site = 0) {
 }
 
 }  // namespace
+
+// ---------------------------------------------------------------------------
+// per-call state of the FP8 entry points (fp8_api.cu)
+// ---------------------------------------------------------------------------
+void call_reset(cudaStream_t stream) {
+  std::memset(&t_last.stats, 0, sizeof(t_last.stats));
+  t_last.status_slot = nullptr;
+  t_last.call_id = 0;
+  t_last.device = -1;
+  t_fail_site = 0;
+  t_last.stats.last_ms = -1.f;
+  t_last.kernel = nullptr;
+  t_last.timed = false;
+  t_last.stream = stream;
+}
+
+cudaError_t call_begin(uint64_t timeout_ns, CallInfo* info) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  unsigned long long* status = nullptr;
+  uint32_t call_id = 0;
+  int sms = 0;
+  if (e == cudaSuccess) e = device_info(dev, &sms, &call_id, &status);
+  if (e != cudaSuccess) return e;
+  t_last.device = dev;
+  t_last.status_slot = status;
+  t_last.call_id = call_id;
+  t_last.stats.sm_count = sms;
+  info->device = dev;
+  info->sm_count = sms;
+  info->ctl = KernelCtl{status, call_id, timeout_ns ? timeout_ns : kDefaultTimeoutNs, 0, 0};
+  return cudaSuccess;
+}
+
+void call_launched(const gp_plan& plan, const void* kernel) {
+  t_last.stats.plan = plan;
+  t_last.kernel = kernel;
+}
+
+int call_finish(int status, cudaError_t error, int site) {
+  record(status, error, site ? site : (t_fail_site ? t_fail_site : GP_SITE_LAUNCH));
+  return status;
+}
+
+cudaError_t call_workspace(int device, cudaStream_t stream, size_t bytes, float** partials, uint32_t** counters) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  Workspace* w = nullptr;
+  cudaError_t e = find_workspace(device, stream, &w);
+  if (e != cudaSuccess) return e;
+  if (!w->fp8_ctrs) {
+    uint32_t* p = nullptr;
+    if ((e = cudaMalloc(&p, kFp8Counters * sizeof(uint32_t))) != cudaSuccess) return e;
+    if ((e = cudaMemsetAsync(p, 0, kFp8Counters * sizeof(uint32_t), stream)) != cudaSuccess) {
+      cudaFree(p);
+      return e;
+    }
+    w->fp8_ctrs = p;
+  }
+  if (w->fp8_bytes < bytes) {
+    if (w->fp8) {
+      if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return e;   // nothing uses the old buffer now
+      cudaFree(w->fp8);
+      w->fp8 = nullptr;
+      w->fp8_bytes = 0;
+    }
+    if ((e = cudaMalloc(&w->fp8, bytes)) != cudaSuccess) return e;
+    w->fp8_bytes = bytes;
+  }
+  *partials = w->fp8;
+  *counters = w->fp8_ctrs;
+  return cudaSuccess;
+}
 
 // ---------------------------------------------------------------------------
 // helpers used by the kernel translation units

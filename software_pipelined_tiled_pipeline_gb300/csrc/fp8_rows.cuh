@@ -1,0 +1,147 @@
+// fp8_rows.cuh -- what the FP8 row kernels share: eight values at a time from
+// and to memory, the scale of a group, and the 8-bit conversions.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fp8_internal.h"
+#include "gp_device.cuh"
+
+namespace gp {
+
+// ---------------------------------------------------------------------------
+// eight values of a row
+// ---------------------------------------------------------------------------
+template <typename T>
+struct Raw8 {
+  static constexpr int WORDS = static_cast<int>(sizeof(T)) * 8 / 16;
+  uint4 w[WORDS];
+};
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
+__device__ __forceinline__ void from_f32(float v, __half& o) { o = __float2half_rn(v); }
+__device__ __forceinline__ void from_f32(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
+
+// Eight values at p, `valid` of them inside the row (the others read as 0).
+// vec: every chunk of the matrix starts on a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ void load8(Raw8<T>& r, const T* p, int valid, bool vec) {
+  if (vec && valid >= 8) {
+#pragma unroll
+    for (int i = 0; i < Raw8<T>::WORDS; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+    return;
+  }
+  T t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (i < valid)
+      t[i] = p[i];
+    else
+      from_f32(0.f, t[i]);
+  }
+  memcpy(&r, t, sizeof(t));
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&v)[8]) {
+  T t[8];
+  memcpy(t, &r, sizeof(t));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
+}
+
+// Round eight FP32 values to T (nearest even).
+template <typename T>
+__device__ __forceinline__ void pack8(const float (&v)[8], Raw8<T>& r) {
+  T t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) from_f32(v[i], t[i]);
+  memcpy(&r, t, sizeof(t));
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const Raw8<T>& r, int valid, bool vec) {
+  if (vec && valid >= 8) {
+#pragma unroll
+    for (int i = 0; i < Raw8<T>::WORDS; ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
+    return;
+  }
+  T t[8];
+  memcpy(t, &r, sizeof(t));
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < valid) p[i] = t[i];
+}
+
+// Eight values of a vector of one of the gp_real types, as FP32.
+__device__ __forceinline__ void load8_any(float (&v)[8], const void* base, int type, int64_t at, int valid, bool vec) {
+  if (type == GP_REAL_F32) {
+    Raw8<float> r;
+    load8(r, static_cast<const float*>(base) + at, valid, vec);
+    unpack8(r, v);
+  } else if (type == GP_REAL_BF16) {
+    Raw8<__nv_bfloat16> r;
+    load8(r, static_cast<const __nv_bfloat16*>(base) + at, valid, vec);
+    unpack8(r, v);
+  } else {
+    Raw8<__half> r;
+    load8(r, static_cast<const __half*>(base) + at, valid, vec);
+    unpack8(r, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// scales and 8-bit codes
+// ---------------------------------------------------------------------------
+// |x| as an ordered integer.  The bit patterns of non-negative floats order as
+// the floats do and a NaN's lies above all of them, so an integer maximum of
+// these also carries a NaN or an infinity of the group to its scale.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+constexpr float kScaleFloor = 5.42101086e-20f;   // 2^-64
+
+// Scale of a group from its largest magnitude's bits, and the factor applied
+// to its values.  Both divisions are correctly rounded.
+struct GroupScale {
+  float scale, inv;
+};
+__device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, float fmax) {
+  GroupScale g;
+  g.scale = __fdiv_rn(__uint_as_float(amax_bits), fmax);
+  if (g.scale < kScaleFloor) g.scale = kScaleFloor;   // false for NaN, which stays
+  g.inv = __fdiv_rn(1.0f, g.scale);
+  return g;
+}
+
+// Two values to two 8-bit codes (nearest even, saturated; NaN stays NaN), lo in the low byte.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t fp8x2(float lo, float hi) {
+  uint16_t r;
+  if (E5M2)
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <bool E5M2>
+__device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
+  return fp8x2<E5M2>(a, b) | (fp8x2<E5M2>(c, d) << 16);
+}
+
+// Eight codes at p (8-byte aligned), `valid` of them inside the row.
+__device__ __forceinline__ void store_codes8(uint8_t* p, uint2 codes, int valid) {
+  if (valid >= 8) {
+    *reinterpret_cast<uint2*>(p) = codes;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < valid) p[i] = static_cast<uint8_t>((i < 4 ? codes.x : codes.y) >> (8 * (i & 3)));
+}
+
+}  // namespace gp

@@ -1,0 +1,493 @@
+// k_fp8_norm.cu -- RMS norm with the residual's addition and an 8-bit output,
+// and its gradient.
+//
+//   h = round(x + residual),  rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight
+//   g = dy * weight,  dx = rstd * (g - h * rstd * mean(g * h * rstd)) + dres,  dw = sum_rows dy * h * rstd
+//
+// Both are bound by memory: each input is read once and each output written
+// once.  A row stays in the registers of its threads (NCH chunks of 8 values
+// each) from the load to the store, so the sum over the row costs one exchange
+// between warps and no second read.  Chunk i of thread t holds columns
+// 8 (i * threads + t) .., so a group of 128 columns is 16 neighbouring lanes
+// and its maximum four shuffles.  Rows too long for the registers
+// (kRowsMaxCols) are read twice.
+#include <cstring>
+#include "fp8_rows.cuh"
+
+namespace gp {
+namespace {
+
+constexpr int kLongThreads = 1024;
+constexpr int kMaxChunks = 4;
+// Threads of a block that holds NCH chunks per thread: with 512, a thread may
+// use 128 registers.
+template <int NCH>
+constexpr int kRowThreads = NCH == 1 ? 256 : 512;
+constexpr int64_t kRowsMaxCols = int64_t(kRowThreads<kMaxChunks>) * kMaxChunks * 8;   // 16384
+
+// Sum over the threads of one row: blockDim.x threads, blockDim.y rows side by
+// side.  `slots` holds two sets of 32 floats, used in turn, so one barrier per
+// sum is enough.
+__device__ __forceinline__ float row_sum(float v, float* slots) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return v;
+  const int warp = threadIdx.x >> 5;
+  float* mine = slots + threadIdx.y * warps;
+  if ((threadIdx.x & 31) == 0) mine[warp] = v;
+  __syncthreads();
+  float s = (threadIdx.x & 31) < warps ? mine[threadIdx.x & 31] : 0.f;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+  return s;
+}
+
+// y of one chunk to its 8-bit codes; the 16 lanes of a group agree on its scale.
+__device__ __forceinline__ void quantize_chunk(const NormArgs& a, const float (&y)[8], int64_t row, int64_t col,
+                                               int valid, int lane) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = max(m, abs_bits(y[k]));
+#pragma unroll
+  for (int d = 1; d < 16; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if (valid <= 0) return;
+  const GroupScale g = group_scale(m, a.fmax);
+  if ((lane & 15) == 0) a.q.scales[row * a.q.stride_row + (col >> 7) * a.q.stride_col] = g.scale;
+  uint2 w;
+  if (a.e5m2) {
+    w.x = fp8x4<true>(y[0] * g.inv, y[1] * g.inv, y[2] * g.inv, y[3] * g.inv);
+    w.y = fp8x4<true>(y[4] * g.inv, y[5] * g.inv, y[6] * g.inv, y[7] * g.inv);
+  } else {
+    w.x = fp8x4<false>(y[0] * g.inv, y[1] * g.inv, y[2] * g.inv, y[3] * g.inv);
+    w.y = fp8x4<false>(y[4] * g.inv, y[5] * g.inv, y[6] * g.inv, y[7] * g.inv);
+  }
+  store_codes8(static_cast<uint8_t*>(a.q.data) + row * a.q.ld + col, w, valid);
+}
+
+__device__ __forceinline__ int chunk_valid(int64_t cols, int64_t col) {
+  const int64_t left = cols - col;
+  return left <= 0 ? 0 : (left >= 8 ? 8 : static_cast<int>(left));
+}
+
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+template <typename T, int NCH>
+__global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float slots[32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool live = row < a.rows;       // (a block's spare rows take part in its barriers)
+  const bool vec = a.vec != 0;
+  const int lane = threadIdx.x & 31;
+
+  Raw8<T> rx[NCH], rr[NCH];
+  int valid[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
+    valid[i] = live ? chunk_valid(a.cols, col) : 0;
+    load8(rx[i], static_cast<const T*>(a.x) + row * a.ldx + col, valid[i], vec);
+  }
+  if (a.residual) {
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
+      load8(rr[i], static_cast<const T*>(a.residual) + row * a.ld_res + col, valid[i], vec);
+    }
+  }
+  float h[NCH][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    unpack8(rx[i], h[i]);
+    if (a.residual) {
+      float r[8];
+      unpack8(rr[i], r);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[i][k] += r[k];
+      pack8(h[i], rx[i]);
+      unpack8(rx[i], h[i]);             // the norm is of the rounded sum
+    }
+    if (a.h) {
+      const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
+      store8(static_cast<T*>(a.h) + row * a.ld_h + col, rx[i], valid[i], vec);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = fmaf(h[i][k], h[i][k], ss);
+  }
+  ss = row_sum(ss, slots);
+  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.cols)) + a.eps));
+  if (a.rstd && live && threadIdx.x == 0) a.rstd[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
+    float w[8];
+    load8_any(w, a.weight, a.weight_type, col, valid[i], a.vec_w != 0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = h[i][k] * rstd * w[k];
+    if (a.y) {
+      Raw8<T> ry;
+      pack8(w, ry);
+      store8(static_cast<T*>(a.y) + row * a.ld_y + col, ry, valid[i], vec);
+    }
+    if (a.q.data) quantize_chunk(a, w, row, col, valid[i], lane);
+  }
+}
+
+// Rows longer than kRowsMaxCols: one block per row, two passes over it.  The
+// second pass takes h from where the first stored it (x or the residual may be
+// that place), else forms it again.
+template <typename T>
+__global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float slots[32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t row = blockIdx.x;
+  const bool vec = a.vec != 0;
+  const int lane = threadIdx.x & 31;
+  const int64_t step = static_cast<int64_t>(blockDim.x) * 8;
+  auto form = [&](int64_t col, int valid, Raw8<T>& raw, float (&h)[8]) {
+    load8(raw, static_cast<const T*>(a.x) + row * a.ldx + col, valid, vec);
+    unpack8(raw, h);
+    if (!a.residual) return;
+    float r[8];
+    load8(raw, static_cast<const T*>(a.residual) + row * a.ld_res + col, valid, vec);
+    unpack8(raw, r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[k] += r[k];
+    pack8(h, raw);
+    unpack8(raw, h);
+  };
+  float ss = 0.f;
+  for (int64_t c = static_cast<int64_t>(threadIdx.x) * 8; c < a.cols; c += step) {
+    const int valid = chunk_valid(a.cols, c);
+    Raw8<T> raw;
+    float h[8];
+    form(c, valid, raw, h);
+    if (a.h) store8(static_cast<T*>(a.h) + row * a.ld_h + c, raw, valid, vec);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = fmaf(h[k], h[k], ss);
+  }
+  ss = row_sum(ss, slots);
+  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.cols)) + a.eps));
+  if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+  for (int64_t base = 0; base < a.cols; base += step) {   // (whole blocks: the shuffles need every lane)
+    const int64_t c = base + static_cast<int64_t>(threadIdx.x) * 8;
+    const int valid = chunk_valid(a.cols, c);
+    Raw8<T> raw;
+    float h[8], w[8];
+    if (a.h) {
+      load8(raw, static_cast<const T*>(a.h) + row * a.ld_h + c, valid, vec);
+      unpack8(raw, h);
+    } else {
+      form(c, valid, raw, h);
+    }
+    load8_any(w, a.weight, a.weight_type, c, valid, a.vec_w != 0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = h[k] * rstd * w[k];
+    if (a.y) {
+      pack8(w, raw);
+      store8(static_cast<T*>(a.y) + row * a.ld_y + c, raw, valid, vec);
+    }
+    if (a.q.data) quantize_chunk(a, w, row, c, valid, lane);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+// Each block takes every gridDim.x-th row (or group of blockDim.y rows) and
+// keeps its columns' share of the weight's gradient in registers; the blocks'
+// shares are added in order by sum_parts_kernel.
+template <typename T, int NCH>
+__global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_grad_kernel(const __grid_constant__ NormGradArgs a) {
+  __shared__ float slots[2][32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const bool vec = a.vec != 0;
+  const float inv_cols = 1.0f / static_cast<float>(a.cols);
+  // The weight stays in registers where they suffice (the loads of four chunks
+  // would spill), else each row reads it again from the L1 cache.
+  constexpr bool KEEP_W = NCH <= 2;
+  float w[KEEP_W ? NCH : 1][8], dw[NCH][8];
+  int valid[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
+    valid[i] = chunk_valid(a.cols, col);
+    if (KEEP_W) load8_any(w[KEEP_W ? i : 0], a.weight, a.weight_type, col, valid[i], a.vec_w != 0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dw[i][k] = 0.f;
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+  int set = 0;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * blockDim.y; base < a.rows; base += step, set ^= 1) {
+    const int64_t row = base + threadIdx.y;
+    const bool live = row < a.rows;
+    Raw8<T> rdy[NCH], rh[NCH], rr[NCH];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
+      const int n = live ? valid[i] : 0;
+      load8(rdy[i], static_cast<const T*>(a.dy) + row * a.ld_dy + col, n, vec);
+      load8(rh[i], static_cast<const T*>(a.h) + row * a.ld_h + col, n, vec);
+      if (a.dres) load8(rr[i], static_cast<const T*>(a.dres) + row * a.ld_dres + col, n, vec);
+    }
+    const float rstd = live ? a.rstd[row] : 0.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int wi = KEEP_W ? i : 0;
+      if (!KEEP_W)
+        load8_any(w[0], a.weight, a.weight_type, (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8, valid[i],
+                  a.vec_w != 0);
+      float dy[8], h[8];
+      unpack8(rdy[i], dy);
+      unpack8(rh[i], h);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float unit = h[k] * rstd;
+        const float p = dy[k] * unit;
+        dw[i][k] += p;
+        sum = fmaf(p, w[wi][k], sum);
+      }
+    }
+    const float mean = row_sum(sum, slots[set]) * inv_cols;
+    if (!live) continue;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
+      const int wi = KEEP_W ? i : 0;
+      if (!KEEP_W) load8_any(w[0], a.weight, a.weight_type, col, valid[i], a.vec_w != 0);
+      float dy[8], h[8], o[8];
+      unpack8(rdy[i], dy);
+      unpack8(rh[i], h);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = rstd * (dy[k] * w[wi][k] - h[k] * rstd * mean);
+      if (a.dres) {
+        float r[8];
+        unpack8(rr[i], r);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] += r[k];
+      }
+      Raw8<T> out;
+      pack8(o, out);
+      store8(static_cast<T*>(a.dx) + row * a.ld_dx + col, out, valid[i], vec);
+    }
+  }
+  if (!a.partials) return;
+  float* part = a.partials + (static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y) * a.cols;
+  const bool vec_p = a.cols % 4 == 0;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
+    Raw8<float> out;
+    pack8(dw[i], out);
+    store8(part + col, out, valid[i], vec_p);
+  }
+}
+
+// Rows longer than kRowsMaxCols: dx in two passes over the row, dw by columns.
+template <typename T>
+__global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_long_kernel(const __grid_constant__ NormGradArgs a) {
+  __shared__ float slots[32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t row = blockIdx.x;
+  const bool vec = a.vec != 0;
+  const float rstd = a.rstd[row];
+  const int64_t step = static_cast<int64_t>(blockDim.x) * 8;
+  float sum = 0.f;
+  for (int pass = 0; pass < 2; ++pass) {
+    const float mean = pass ? row_sum(sum, slots) / static_cast<float>(a.cols) : 0.f;
+    for (int64_t c = static_cast<int64_t>(threadIdx.x) * 8; c < a.cols; c += step) {
+      const int valid = chunk_valid(a.cols, c);
+      Raw8<T> raw;
+      float dy[8], h[8], w[8];
+      load8(raw, static_cast<const T*>(a.dy) + row * a.ld_dy + c, valid, vec);
+      unpack8(raw, dy);
+      load8(raw, static_cast<const T*>(a.h) + row * a.ld_h + c, valid, vec);
+      unpack8(raw, h);
+      load8_any(w, a.weight, a.weight_type, c, valid, a.vec_w != 0);
+      if (pass == 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum = fmaf(dy[k] * (h[k] * rstd), w[k], sum);
+        continue;
+      }
+      float o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = rstd * (dy[k] * w[k] - h[k] * rstd * mean);
+      if (a.dres) {
+        float r[8];
+        load8(raw, static_cast<const T*>(a.dres) + row * a.ld_dres + c, valid, vec);
+        unpack8(raw, r);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] += r[k];
+      }
+      pack8(o, raw);
+      store8(static_cast<T*>(a.dx) + row * a.ld_dx + c, raw, valid, vec);
+    }
+  }
+}
+
+constexpr int kLongParts = 32;   // shares of the rows in the column sums of long rows
+
+template <typename T>
+__global__ void __launch_bounds__(256) rmsnorm_dw_long_kernel(const __grid_constant__ NormGradArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 8;
+  const int valid = chunk_valid(a.cols, c);
+  const int parts = gridDim.y;
+  float dw[8] = {};
+  for (int64_t row = blockIdx.y; row < a.rows; row += parts) {
+    Raw8<T> raw;
+    float dy[8], h[8];
+    load8(raw, static_cast<const T*>(a.dy) + row * a.ld_dy + c, valid, a.vec != 0);
+    unpack8(raw, dy);
+    load8(raw, static_cast<const T*>(a.h) + row * a.ld_h + c, valid, a.vec != 0);
+    unpack8(raw, h);
+    const float rstd = a.rstd[row];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dw[k] += dy[k] * (h[k] * rstd);
+  }
+  Raw8<float> out;
+  pack8(dw, out);
+  store8(a.partials + static_cast<int64_t>(blockIdx.y) * a.cols + c, out, valid, a.cols % 4 == 0);
+}
+
+// dw[c] = sum over parts of partials[part][c], in a fixed order: 8 threads per
+// column take every eighth part each, then meet in shared memory.
+constexpr int kSumCols = 32, kSumWays = 8;
+__global__ void __launch_bounds__(kSumCols * kSumWays) sum_parts_kernel(const float* partials, float* dw, int64_t parts,
+                                                                       int64_t cols) {
+  __shared__ float s[kSumWays][kSumCols];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kSumCols + threadIdx.x;
+  float v = 0.f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int64_t p = threadIdx.y; p < parts; p += kSumWays) v += partials[p * cols + c];
+  }
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y != 0 || c >= cols) return;
+#pragma unroll
+  for (int k = 1; k < kSumWays; ++k) v += s[k][threadIdx.x];
+  dw[c] = v;
+}
+
+__global__ void __launch_bounds__(256) zero_kernel(float* p, int64_t n) {
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    p[i] = 0.f;
+}
+
+// Threads per row, chunks per thread and rows per block for a row of `cols`.
+struct RowShape {
+  int threads, chunks, rows;
+};
+RowShape row_shape(int64_t cols) {
+  RowShape s;
+  const int64_t chunks = (cols + 7) / 8;
+  s.chunks = chunks <= kRowThreads<1> ? 1 : (chunks <= 2 * kRowThreads<2> ? 2 : 4);
+  const int64_t per = (chunks + s.chunks - 1) / s.chunks;
+  s.threads = static_cast<int>((per + 31) / 32 * 32);
+  s.rows = s.threads >= 128 ? 1 : 128 / s.threads;
+  return s;
+}
+
+template <typename T>
+cudaError_t forward_type(const NormArgs& a, cudaStream_t stream, const void** kernel, gp_plan* plan) {
+  if (a.cols > kRowsMaxCols) {
+    auto k = rmsnorm_long_kernel<T>;
+    *kernel = reinterpret_cast<const void*>(k);
+    plan->threads = kLongThreads;
+    plan->grid = static_cast<int32_t>(a.rows);
+    return launch_dependent(k, dim3(static_cast<unsigned>(a.rows)), dim3(kLongThreads), 0, stream, a);
+  }
+  const RowShape s = row_shape(a.cols);
+  auto k = s.chunks == 1 ? rmsnorm_kernel<T, 1> : (s.chunks == 2 ? rmsnorm_kernel<T, 2> : rmsnorm_kernel<T, 4>);
+  *kernel = reinterpret_cast<const void*>(k);
+  plan->threads = s.threads * s.rows;
+  plan->grid = static_cast<int32_t>((a.rows + s.rows - 1) / s.rows);
+  return launch_dependent(k, dim3(static_cast<unsigned>(plan->grid)), dim3(s.threads, s.rows), 0, stream, a);
+}
+
+// Blocks of the backward kernel: two per SM are enough to keep its loads in flight.
+int64_t grad_blocks(int64_t rows, const RowShape& s, int sm_count) {
+  const int64_t want = (rows + s.rows - 1) / s.rows;
+  const int64_t most = static_cast<int64_t>(sm_count) * (s.threads * s.rows > 512 ? 1 : 2);
+  return want < most ? want : most;
+}
+
+template <typename T>
+cudaError_t backward_type(const NormGradArgs& a, int sm_count, cudaStream_t stream, const void** kernel,
+                          gp_plan* plan) {
+  if (a.cols > kRowsMaxCols) {
+    cudaError_t e;
+    if (a.partials) {
+      const int64_t chunks = (a.cols + 7) / 8;
+      const dim3 grid(static_cast<unsigned>((chunks + 255) / 256),
+                      static_cast<unsigned>(a.rows < kLongParts ? a.rows : kLongParts));
+      if ((e = launch_dependent(rmsnorm_dw_long_kernel<T>, grid, dim3(256), 0, stream, a)) != cudaSuccess) return e;
+    }
+    auto k = rmsnorm_grad_long_kernel<T>;
+    *kernel = reinterpret_cast<const void*>(k);
+    plan->threads = kLongThreads;
+    plan->grid = static_cast<int32_t>(a.rows);
+    return launch_dependent(k, dim3(static_cast<unsigned>(a.rows)), dim3(kLongThreads), 0, stream, a);
+  }
+  const RowShape s = row_shape(a.cols);
+  auto k = s.chunks == 1 ? rmsnorm_grad_kernel<T, 1>
+                         : (s.chunks == 2 ? rmsnorm_grad_kernel<T, 2> : rmsnorm_grad_kernel<T, 4>);
+  *kernel = reinterpret_cast<const void*>(k);
+  plan->threads = s.threads * s.rows;
+  plan->grid = static_cast<int32_t>(grad_blocks(a.rows, s, sm_count));
+  return launch_dependent(k, dim3(static_cast<unsigned>(plan->grid)), dim3(s.threads, s.rows), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_rmsnorm(const NormArgs& a, cudaStream_t stream, const void** kernel, gp_plan* plan) {
+  plan->kernel = "fp8_rmsnorm";
+  switch (a.type) {
+    case GP_REAL_F16: return forward_type<__half>(a, stream, kernel, plan);
+    case GP_REAL_BF16: return forward_type<__nv_bfloat16>(a, stream, kernel, plan);
+    default: return forward_type<float>(a, stream, kernel, plan);
+  }
+}
+
+int64_t fp8_rmsnorm_backward_parts(int64_t rows, int64_t cols, int sm_count) {
+  if (cols > kRowsMaxCols) return rows < kLongParts ? rows : kLongParts;
+  const RowShape s = row_shape(cols);
+  return grad_blocks(rows, s, sm_count) * s.rows;
+}
+
+cudaError_t launch_fp8_rmsnorm_backward(const NormGradArgs& a, float* dw, int sm_count, cudaStream_t stream,
+                                        const void** kernel, gp_plan* plan) {
+  plan->kernel = "fp8_rmsnorm_backward";
+  if (a.rows == 0) {
+    const int64_t blocks = (a.cols + 255) / 256;
+    return launch_dependent(zero_kernel, dim3(static_cast<unsigned>(blocks < 1024 ? blocks : 1024)), dim3(256), 0,
+                            stream, dw, a.cols);
+  }
+  cudaError_t e;
+  switch (a.type) {
+    case GP_REAL_F16: e = backward_type<__half>(a, sm_count, stream, kernel, plan); break;
+    case GP_REAL_BF16: e = backward_type<__nv_bfloat16>(a, sm_count, stream, kernel, plan); break;
+    default: e = backward_type<float>(a, sm_count, stream, kernel, plan); break;
+  }
+  if (e != cudaSuccess || !a.partials) return e;
+  return launch_dependent(sum_parts_kernel, dim3(static_cast<unsigned>((a.cols + kSumCols - 1) / kSumCols)),
+                          dim3(kSumCols, kSumWays), 0, stream, static_cast<const float*>(a.partials), dw,
+                          fp8_rmsnorm_backward_parts(a.rows, a.cols, sm_count), a.cols);
+}
+
+}  // namespace gp

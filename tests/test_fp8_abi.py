@@ -1,0 +1,180 @@
+"""Host-side checks of the 8-bit operators' C ABI (no GPU): argument errors are
+reported before anything is launched, struct layouts match the header, the
+plan follows its rules, and the tests' own plain formats agree with torch's."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_ref as ref
+from software_pipelined_tiled_pipeline_gb300 import build as gbuild
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PTR = 0x10000
+
+
+@pytest.fixture(scope="module")
+def gp():
+    gbuild.build()
+    import software_pipelined_tiled_pipeline_gb300 as mod
+    mod.lib()
+    return mod
+
+
+def matrix(data=PTR, scales=PTR, ld=256, row=1, col=64, fmt=0, group=1):
+    from software_pipelined_tiled_pipeline_gb300 import _binding as b
+    return b.GpFp8Matrix(data, scales, ld, row, col, fmt, group)
+
+
+def gemm(gp, A=None, B=None, C=PTR, ldc=64, add=None, ld_add=64, M=64, N=64, K=256, out=1, opts=None):
+    return gp.lib().gemm_fp8(A or matrix(), B or matrix(), C, ldc, add, ld_add, M, N, K, out, None, opts)
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(M=-1), "ARG"), (dict(K=-1), "ARG"), (dict(N=1 << 31), "SIZE"), (dict(K=1 << 31), "SIZE"),
+    (dict(out=3), "ARG"), (dict(C=None), "ARG"), (dict(ldc=63), "ARG"), (dict(add=PTR, ld_add=63), "ARG"),
+    (dict(A=matrix(data=None)), "ARG"), (dict(B=matrix(scales=None)), "ARG"), (dict(A=matrix(fmt=2)), "ARG"),
+    (dict(B=matrix(group=64)), "ARG"), (dict(A=matrix(ld=240)), "ARG"), (dict(A=matrix(ld=260)), "UNSUPPORTED"),
+    (dict(B=matrix(data=PTR + 8)), "UNSUPPORTED"), (dict(B=matrix(scales=PTR + 2)), "UNSUPPORTED"),
+    (dict(C=PTR + 1), "UNSUPPORTED"), (dict(C=PTR + 2, out=2), "UNSUPPORTED"),
+    (dict(add=PTR + 1), "UNSUPPORTED"),
+])
+def test_gemm_argument_errors_need_no_device(gp, args, code):
+    assert gemm(gp, **args) == getattr(gp, "GP_ERR_" + code)
+    assert gp.gemm_stats(sync=False)["status"] == getattr(gp, "GP_ERR_" + code)
+
+
+def test_gemm_null_matrix_and_forced_width(gp):
+    from software_pipelined_tiled_pipeline_gb300 import _binding as b
+    f = gp.lib().gemm_fp8
+    assert f(None, matrix(), PTR, 64, None, 0, 64, 64, 256, 1, None, None) == gp.GP_ERR_ARG
+    assert gemm(gp, opts=b.GpFp8Options(0, 48, 0, 0)) == gp.GP_ERR_UNSUPPORTED
+
+
+def test_empty_output_needs_no_device(gp):
+    f = gp.lib().gemm_fp8
+    assert f(None, None, None, 0, None, 0, 0, 64, 256, 1, None, None) == gp.GP_OK
+    assert f(None, None, None, 0, None, 0, 64, 0, 256, 1, None, None) == gp.GP_OK
+    assert gp.lib().fp8_quantize(None, 0, 0, 128, 0, matrix(), None, None) == gp.GP_OK
+    assert gp.lib().fp8_rmsnorm(None, 0, None, 0, None, 0, 0.0, 0, 64, 0, None, 0, None, None, 0, None, None) == gp.GP_OK
+    assert gp.lib().fp8_rmsnorm_backward(None, 0, None, 0, None, 0, None, 0, None, 0, 64, 0, None, 0, None, None) == gp.GP_OK
+
+
+def quantize(gp, x=PTR, ldx=256, rows=64, cols=256, type=1, q=None, qt=None):
+    return gp.lib().fp8_quantize(x, ldx, rows, cols, type, q, qt, None)
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(), "ARG"),                                             # neither q nor qt
+    (dict(q=matrix(), rows=-1), "ARG"), (dict(q=matrix(), cols=1 << 31), "SIZE"), (dict(q=matrix(), type=3), "ARG"),
+    (dict(q=matrix(), x=None), "ARG"), (dict(q=matrix(), ldx=255), "ARG"), (dict(q=matrix(), x=PTR + 1), "UNSUPPORTED"),
+    (dict(q=matrix(ld=240)), "ARG"), (dict(qt=matrix(ld=48)), "ARG"), (dict(qt=matrix(ld=72)), "UNSUPPORTED"),
+    (dict(q=matrix(data=None)), "ARG"), (dict(q=matrix(), qt=matrix(fmt=1)), "ARG"),
+    (dict(q=matrix(), qt=matrix(group=128)), "ARG"), (dict(q=matrix(group=2)), "ARG"),
+])
+def test_quantize_argument_errors_need_no_device(gp, args, code):
+    assert quantize(gp, **args) == getattr(gp, "GP_ERR_" + code)
+
+
+def norm(gp, x=PTR, ldx=256, res=None, ld_res=256, w=PTR, wtype=1, eps=1e-6, rows=4, cols=256, type=1, h=None, ld_h=256,
+         rstd=PTR, y=None, ld_y=256, q=None):
+    return gp.lib().fp8_rmsnorm(x, ldx, res, ld_res, w, wtype, eps, rows, cols, type, h, ld_h, rstd, y, ld_y, q, None)
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(x=None), "ARG"), (dict(w=None), "ARG"), (dict(type=5), "ARG"), (dict(wtype=-1), "ARG"), (dict(eps=-1.0), "ARG"),
+    (dict(eps=float("nan")), "ARG"), (dict(rows=-1), "ARG"), (dict(cols=1 << 31), "SIZE"), (dict(ldx=255), "ARG"),
+    (dict(res=PTR, ld_res=255), "ARG"), (dict(h=PTR, ld_h=4), "ARG"), (dict(y=PTR, ld_y=4), "ARG"),
+    (dict(h=PTR + 1), "UNSUPPORTED"), (dict(rstd=PTR + 2), "UNSUPPORTED"), (dict(q=matrix(group=128)), "ARG"),
+    (dict(q=matrix(ld=248)), "ARG"), (dict(q=matrix(data=PTR + 4)), "UNSUPPORTED"),
+])
+def test_norm_argument_errors_need_no_device(gp, args, code):
+    assert norm(gp, **args) == getattr(gp, "GP_ERR_" + code)
+
+
+def backward(gp, dy=PTR, ld_dy=256, h=PTR, ld_h=256, dres=None, ld_dres=256, w=PTR, wtype=1, rstd=PTR, rows=4, cols=256,
+             type=1, dx=PTR, ld_dx=256, dw=PTR):
+    return gp.lib().fp8_rmsnorm_backward(dy, ld_dy, h, ld_h, dres, ld_dres, w, wtype, rstd, rows, cols, type, dx, ld_dx, dw,
+                                         None)
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(dy=None), "ARG"), (dict(h=None), "ARG"), (dict(w=None), "ARG"), (dict(rstd=None), "ARG"), (dict(dx=None), "ARG"),
+    (dict(ld_dy=8), "ARG"), (dict(ld_h=8), "ARG"), (dict(dres=PTR, ld_dres=8), "ARG"), (dict(ld_dx=8), "ARG"),
+    (dict(type=4), "ARG"), (dict(wtype=4), "ARG"), (dict(rows=1 << 31), "SIZE"), (dict(dw=PTR + 1), "UNSUPPORTED"),
+    (dict(dx=PTR + 1), "UNSUPPORTED"),
+])
+def test_backward_argument_errors_need_no_device(gp, args, code):
+    assert backward(gp, **args) == getattr(gp, "GP_ERR_" + code)
+
+
+def test_struct_layout_matches_the_header(tmp_path):
+    from software_pipelined_tiled_pipeline_gb300 import _binding as b
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    checks = [("gp_fp8_matrix", b.GpFp8Matrix), ("gp_fp8_options", b.GpFp8Options)]
+    lines = ['#include <stddef.h>', '#include <stdio.h>', '#include "gemm_fp8.h"', "int main(void) {"]
+    for cname, cls in checks:
+        lines.append('  printf("%zu\\n", sizeof(' + cname + '));')
+        lines += ['  printf("%%zu\\n", offsetof(%s, %s));' % (cname, f) for f, _ in cls._fields_]
+    (tmp_path / "s.c").write_text("\n".join(lines + ["  return 0;\n}"]))
+    subprocess.run([cc, "-I", os.path.join(ROOT, "include"), str(tmp_path / "s.c"), "-o", str(tmp_path / "s")], check=True)
+    got = [int(v) for v in subprocess.run([str(tmp_path / "s")], check=True, capture_output=True, text=True).stdout.split()]
+    want = []
+    for _, cls in checks:
+        want += [ctypes.sizeof(cls)] + [getattr(cls, f).offset for f, _ in cls._fields_]
+    assert got == want
+
+
+def test_plan_errors(gp):
+    from software_pipelined_tiled_pipeline_gb300 import _binding as b
+    f, p = gp.lib().gemm_fp8_plan, b.GpPlan()
+    assert f(64, 64, 64, 1, 128, 152, None, None) == gp.GP_ERR_ARG
+    assert f(64, 64, 64, 2, 128, 152, None, p) == gp.GP_ERR_ARG
+    assert f(64, 64, 64, 1, 128, -1, None, p) == gp.GP_ERR_ARG
+    assert f(-1, 64, 64, 1, 128, 152, None, p) == gp.GP_ERR_ARG
+    assert f(64, 1 << 31, 64, 1, 128, 152, None, p) == gp.GP_ERR_SIZE
+    assert f((1 << 31) - 1, (1 << 31) - 1, 64, 1, 128, 152, None, p) == gp.GP_ERR_SIZE
+
+
+@pytest.mark.parametrize("M,N,swapped", [(1, 4096, 1), (17, 4096, 1), (4096, 1, 0), (128, 512, 1), (512, 128, 0), (64, 64, 0)])
+def test_the_narrow_operand_takes_the_n_side(gp, M, N, swapped):
+    p = gp.gemm_fp8_plan(M, N, 4096, sms=152)
+    assert p["layout"] == swapped
+    assert p["bn"] >= min(M, N) and p["dtype"] == 16
+
+
+def test_plan_invariants_over_many_shapes(gp):
+    rng = np.random.default_rng(5)
+    for _ in range(400):
+        M, N, K = (int(np.exp(rng.uniform(0, np.log(9000)))) for _ in range(3))
+        a, b = rng.choice(["rows", "blocks"], 2)
+        p = gp.gemm_fp8_plan(M, N, K, a, b, sms=152)
+        P, Q = (N, M) if p["layout"] else (M, N)
+        assert p["tiles"] == -(-P // p["bm"]) * -(-Q // p["bn"])
+        assert p["k_tiles"] == -(-K // 128)
+        assert 1 <= p["grid"] <= 152 and p["smem_bytes"] <= 232448 and p["tmem_cols"] <= 512
+        assert p["stages"] >= 2
+        assert p["dp_tiles"] + p["sk_tiles"] == p["tiles"]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_plain_formats_agree_with_torch(fmt):
+    # every code's value, and the nearest code of values all over the range (finite ones: torch does not saturate)
+    every = torch.arange(256, dtype=torch.int32).to(torch.uint8).view(ref.TORCH[fmt])
+    np.testing.assert_array_equal(every.float().numpy().astype(np.float64), ref.TABLE[fmt])
+    rng = np.random.default_rng(1)
+    x = (rng.standard_normal(20000) * np.exp2(rng.uniform(-20, 8 if fmt == "e4m3" else 15, 20000))).astype(np.float32)
+    x = x[np.abs(x) <= ref.FMAX[fmt]]
+    pos = ref.TABLE[fmt][:128]
+    pos = pos[np.isfinite(pos)]
+    mid = ((pos[1:] + pos[:-1]) / 2).astype(np.float32)
+    x = np.concatenate([x, mid, -mid, np.nextafter(mid, np.float32(0)), np.nextafter(mid, np.float32(1e9))])
+    x = x[np.abs(x) <= ref.FMAX[fmt]]
+    want = torch.from_numpy(x).to(ref.TORCH[fmt]).view(torch.uint8).numpy()
+    assert np.array_equal(ref.encode(x, fmt), want)
