@@ -101,6 +101,8 @@ int gemm_fp8(const gp_fp8_matrix* A, const gp_fp8_matrix* B, void* C, int64_t ld
   Fp8GemmArgs a = {};
   rc = fp8_plan_impl(M, N, K, A->group, B->group, info.sm_count, opts, &a.plan);
   if (rc != GP_OK) return call_finish(rc);
+  e = fp8_fit_pairs(&a.plan, opts && opts->no_split);
+  if (e != cudaSuccess) return call_finish(GP_ERR_CUDA, e, GP_SITE_CAPACITY);
   a.A = *A;
   a.B = *B;
   a.C = C;

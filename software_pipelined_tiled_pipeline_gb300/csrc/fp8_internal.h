@@ -83,6 +83,8 @@ struct Fp8GemmArgs {
 };
 int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int sms, const gp_fp8_options* opts,
                   gp_plan* p);
+// Pairs must sit on one TPC each: where fewer fit at once than the plan counted on, plan for those.
+cudaError_t fp8_fit_pairs(gp_plan* plan, bool no_split);
 cudaError_t launch_fp8_gemm(Fp8GemmArgs& a, const void** kernel);
 // C = addend, or zeros (K == 0).
 cudaError_t launch_fp8_fill(void* C, int64_t ldc, const void* addend, int64_t ld_add, int64_t M, int64_t N,

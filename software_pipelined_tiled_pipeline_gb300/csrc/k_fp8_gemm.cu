@@ -8,14 +8,16 @@
 // output and K block: acc = fma(d, sP * sQ, acc).  Persistent and
 // warp-specialised, 12 warps per CTA:
 //   warp 0      TMA producer: one ring slot = one K block = 128 bytes of each row
-//   warp 1      allocates TMEM, issues the MMAs of a K block into the next TMEM
-//               buffer, releases the slot and signals the buffer
-//   warp 2      brings the K block's scales into a small ring (cp.async)
-//   warps 4-11  add each TMEM buffer, scaled, to the sums in their registers;
-//               at a tile's end they write C
+//   warp 1      allocates TMEM and issues the MMAs of a K block into the next
+//               TMEM buffer; their one commit both frees the ring slot and
+//               hands the buffer to the adding warps
+//   warps 4-11  bring the scales of kScaleBatch K blocks at a time into shared
+//               memory (cp.async), add each TMEM buffer, scaled, to the sums in
+//               their registers, and write C at a tile's end
 // Warp w may read TMEM lanes 32 (w mod 4) .. +31; the two warps of a quarter
 // take half the columns each.  "P" is the operand on the MMA's M side (128
 // rows per CTA), "Q" the one on its N side (BN rows); either may be A.
+#include <atomic>
 #include <cstring>
 #include "fp8_internal.h"
 #include "gp_device.cuh"
@@ -27,42 +29,53 @@ constexpr int kBK = 128;                  // K block: bytes of a row per ring sl
 constexpr int kMmaK = 32;                 // K of one kind::f8f6f4 instruction
 constexpr int kThreads = 384;
 constexpr int kAddWarps = 8;
-constexpr int kScaleSlots = 8;
+constexpr int kAddThreads = 32 * kAddWarps;
+constexpr int kScaleBatch = 8;            // K blocks whose scales are staged together (two batches in turn)
 constexpr int kStageWarpBytes = 32 * 128;   // output staging of one warp: 32 rows of 32 FP32
+constexpr int kLaunchRegs = 168;          // registers per thread at launch, where warps trade them
 constexpr int kMaxRing = 12;
 constexpr int64_t kMaxTiles = int64_t(1) << 30;   // tile numbers plus a grid stay below 2^31
 
 struct Fp8Barriers {
   uint64_t full[kMaxRing];
-  uint64_t empty[kMaxRing];
-  uint64_t acc_full[8];
-  uint64_t acc_empty[8];
-  uint64_t sc_full[kScaleSlots];
-  uint64_t sc_empty[kScaleSlots];
+  uint64_t done[kMaxRing];   // the MMAs of the slot's K block have completed
+  uint64_t acc_empty[4];
   uint64_t drain;
   uint32_t tmem_base;
-  int32_t consumed_hi;       // K blocks that the MMA thread has taken (low 31 bits)
   CtaCtl ctl;
   int32_t last;              // this CTA completed the last segment of a split tile
 };
-constexpr int kFp8BarrierBytes = 576;
+constexpr int kFp8BarrierBytes = 256;
 static_assert(sizeof(Fp8Barriers) <= kFp8BarrierBytes, "barrier region too small");
 
-template <int BN>
+// PAIR: a cluster of two CTAs shares a 256 x BN tile, each holding 128 rows of
+// P and BN / 2 of Q; one thread of the even CTA issues the MMAs (M = 256),
+// which read both CTAs' halves and leave each its own 128 rows.
+template <int BN, bool PAIR>
 struct Fp8Shape {
+  static constexpr int CTAS = PAIR ? 2 : 1;
   static constexpr int P_ROWS = 128;
-  static constexpr int Q_ROWS = BN;
-  static constexpr int TILE_P = 128;
+  static constexpr int Q_ROWS = BN / CTAS;
+  static constexpr int TILE_P = P_ROWS * CTAS;
   static constexpr int P_BYTES = P_ROWS * kBK;
   static constexpr int STAGE = (P_ROWS + Q_ROWS) * kBK;
-  static constexpr int BUFS = BN == 256 ? 2 : (BN == 128 ? 4 : 8);   // TMEM accumulators
+  static constexpr int BUFS = BN == 256 ? 2 : 4;       // TMEM accumulators
   static constexpr uint32_t TMEM_COLS = BUFS * BN;
   static constexpr int HALF = BN / 2;                  // columns per adding warp
-  static constexpr int SCALES = P_ROWS + BN;           // floats per scale slot
-  static constexpr int FIXED = kAddWarps * kStageWarpBytes + kScaleSlots * SCALES * 4 + kFp8BarrierBytes + 1024;
+  static constexpr int SCALES = P_ROWS + BN;           // floats per K block: P's, then Q's
+  static constexpr int FIXED = kAddWarps * kStageWarpBytes + 2 * kScaleBatch * SCALES * 4 + kFp8BarrierBytes + 1024;
   static constexpr int FIT = (kSmemPerCtaMax - FIXED) / STAGE;
   static constexpr int STAGES = FIT < kMaxRing ? FIT : kMaxRing;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
+  // A slot's barrier tells the adding warps one phase from the next only while
+  // the MMAs cannot be a whole ring ahead of them.
+  static_assert(BUFS < STAGES, "more accumulators than ring slots");
+  // The adding warps of a wide tile hold its sums in registers, and take them
+  // from the other four warps: ADD_REGS and OTHER_REGS per thread.
+  static constexpr bool SPLIT_REGS = BN >= 128;
+  static constexpr int ADD_REGS = BN == 256 ? 216 : 208, OTHER_REGS = BN == 256 ? 72 : 88;
+  static_assert(kThreads * kLaunchRegs == 32 * (kAddWarps * ADD_REGS + (kThreads / 32 - kAddWarps) * OTHER_REGS),
+                "register split");
 };
 
 // One operand's scales: element (row, block) at base[(row / group) * stride_row + block * stride_col].
@@ -84,6 +97,10 @@ struct Fp8Params {
   int32_t vec;               // groups of 4 outputs are aligned to their size
   uint32_t idesc;
   int32_t raster_gp;         // P blocks per raster group
+  int32_t dp_tiles;          // tiles computed whole (raster order first)
+  int32_t sk_tiles;          // tiles after those whose K-loops are dealt out evenly to all workers
+  float* partials;           // split tiles: two 128 x BN FP32 slots per CTA
+  uint32_t* counters;        // ... one counter per tile and CTA rank, zero between launches
   KernelCtl ctl;
 };
 
@@ -105,6 +122,16 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64
       : "memory");
 }
 
+__device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -115,20 +142,65 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[8]) { tmem_ld_
 __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(t, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(t, r); }
 
+// Arrive on an mbarrier of another CTA of the cluster without ordering memory:
+// the TMEM buffer it hands back has been read into registers, and nothing else
+// is handed over.  (The releasing form waits for this warp's earlier stores
+// with every K block.)
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
 // 4 bytes from global to shared memory without a register; zeros where !valid (nothing is read then).
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
 }
-// Arrive on bar when this thread's copies so far have landed (counts against the barrier's count).
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Wait of a whole warp; false in every lane if it gave up in one.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const KernelCtl& ctl, CtaCtl* cta,
-                                          uint32_t site) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl, cta, site));
+// Waits that come with every K block.  The try itself waits in hardware, up to
+// kTryNs; the clock is read only where that is not enough.  One that gives up
+// leaves its site in the CTA's abort flag, which makes every further wait
+// return at once and is reported when the kernel ends; code and registers here
+// are counted, as the K loop of the adding warps fills both.
+constexpr uint32_t kTryNs = 100000;
+constexpr uint64_t kMostWaitNs = 4000000000ull;   // the 32-bit clock wraps after 4.29 s
+__device__ __forceinline__ bool try_wait(uint32_t bar_addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar_addr), "r"(parity), "n"(kTryNs)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint32_t clock_ns() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ void ring_wait(uint32_t bar_addr, uint32_t parity, uint32_t limit_ns, CtaCtl* cta,
+                                          int site) {
+  if (try_wait(bar_addr, parity)) return;
+  const uint32_t t0 = clock_ns();
+  while (!try_wait(bar_addr, parity)) {
+    if (cta->abort) return;
+    if (clock_ns() - t0 > limit_ns) {
+      cta->abort = site;
+      return;
+    }
+  }
 }
 
 // Output tile -> its P and Q blocks: groups of `gp` P blocks, each swept over all Q blocks.
@@ -141,6 +213,74 @@ __device__ __forceinline__ void tile_blocks(int tile, int p_blocks, int q_blocks
   pb = first + in % n;
   qb = in / n;
 }
+
+// The work of one worker (a CTA or a pair), walked alike by all its warps: a
+// whole tile, then its contiguous share of the split tiles' K blocks (cut at
+// tile boundaries), then its other whole tiles.
+struct Items {
+  int dp_tiles, next_dp, step, kt;
+  int64_t u, u_end;
+  bool first;
+
+  __device__ __forceinline__ static int64_t start(int w, int64_t units, int workers) { return w * units / workers; }
+  // the worker whose share holds unit u
+  __device__ __forceinline__ static int owner(int64_t u, int64_t units, int workers) {
+    return static_cast<int>(((u + 1) * workers - 1) / units);
+  }
+  __device__ __forceinline__ Items(const Fp8Params& g, int kt_, int worker, int workers)
+      : dp_tiles(g.dp_tiles), next_dp(worker), step(workers), kt(kt_), first(true) {
+    const int64_t units = static_cast<int64_t>(g.sk_tiles) * kt;
+    u = start(worker, units, workers);
+    u_end = start(worker + 1, units, workers);
+  }
+  __device__ __forceinline__ bool whole(int& tile, int& k0, int& k1) {
+    if (next_dp >= dp_tiles) return false;
+    tile = next_dp;
+    k0 = 0;
+    k1 = kt;
+    next_dp += step;
+    return true;
+  }
+  __device__ __forceinline__ bool next(int& tile, int& k0, int& k1) {
+    if (first) {
+      first = false;
+      if (whole(tile, k0, k1)) return true;
+    }
+    if (u < u_end) {
+      const int t = static_cast<int>(u / kt);
+      k0 = static_cast<int>(u - static_cast<int64_t>(t) * kt);
+      const int64_t left = u_end - u;
+      k1 = left < kt - k0 ? k0 + static_cast<int>(left) : kt;
+      tile = dp_tiles + t;
+      u += k1 - k0;
+      return true;
+    }
+    return whole(tile, k0, k1);
+  }
+};
+
+// Where the partial sums of a split tile lie.  A worker's share touches at most
+// two tiles in part: slot 0 holds the one that its share starts in, slot 1 the
+// one that it ends in.  A CTA's slot is 128 x BN FP32, 16-byte column groups
+// outermost, so that a warp's 32 rows are 512 contiguous bytes.
+struct Partial {
+  int64_t units, begin;      // K blocks of all split tiles; the tile's first
+  int workers, ctas, rank, w_first, w_last;
+
+  __device__ __forceinline__ Partial(const Fp8Params& g, int tile, int kt, int workers_, int ctas_, int rank_)
+      : workers(workers_), ctas(ctas_), rank(rank_) {
+    units = static_cast<int64_t>(g.sk_tiles) * kt;
+    begin = static_cast<int64_t>(tile - g.dp_tiles) * kt;
+    w_first = Items::owner(begin, units, workers);
+    w_last = Items::owner(begin + kt - 1, units, workers);
+  }
+  __device__ __forceinline__ int64_t slot(int w) const {
+    return (2 * w + (Items::start(w, units, workers) >= begin ? 0 : 1)) * static_cast<int64_t>(ctas) + rank;
+  }
+  __device__ __forceinline__ int segments() const { return w_last - w_first + 1; }
+};
+
+__device__ __forceinline__ void add_warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kAddThreads) : "memory"); }
 
 // Four neighbouring outputs of a row: FP32 sums (+ addend) rounded to the output type.
 template <typename T>
@@ -224,40 +364,35 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
 }
 
 // QROWS: Q has a scale for each row (a column of the tile); else one for each 128 rows.
-template <int BN, bool QROWS>
+template <int BN, bool QROWS, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_ring_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ Fp8Params g) {
-  using Sh = Fp8Shape<BN>;
+  using Sh = Fp8Shape<BN, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = ring + Sh::STAGES * Sh::STAGE;
   float* scales = reinterpret_cast<float*>(staging + kAddWarps * kStageWarpBytes);
-  Fp8Barriers* bar = reinterpret_cast<Fp8Barriers*>(scales + kScaleSlots * Sh::SCALES);
+  Fp8Barriers* bar = reinterpret_cast<Fp8Barriers*>(scales + 2 * kScaleBatch * Sh::SCALES);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // (uniform for the compiler too)
   const int lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const int worker = static_cast<int>(blockIdx.x) / Sh::CTAS;
+  const int workers = static_cast<int>(gridDim.x) / Sh::CTAS;
   const int p_blocks = (g.p.rows + Sh::TILE_P - 1) / Sh::TILE_P;
   const int q_blocks = (g.q.rows + BN - 1) / BN;
-  const int tiles = p_blocks * q_blocks;
+  const int last_tile = p_blocks * q_blocks - 1;
   const int kt = (g.K + kBK - 1) / kBK;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Sh::STAGES; ++s) {
       mbar_init(&bar->full[s], 1);
-      mbar_init(&bar->empty[s], 1);
+      mbar_init(&bar->done[s], 1);
     }
-    for (int a = 0; a < Sh::BUFS; ++a) {
-      mbar_init(&bar->acc_full[a], 1);
-      mbar_init(&bar->acc_empty[a], kAddWarps);
-    }
-    for (int s = 0; s < kScaleSlots; ++s) {
-      mbar_init(&bar->sc_full[s], 32);
-      mbar_init(&bar->sc_empty[s], kAddWarps);
-    }
+    for (int a = 0; a < Sh::BUFS; ++a) mbar_init(&bar->acc_empty[a], Sh::CTAS * kAddWarps);
     mbar_init(&bar->drain, 1);
     bar->ctl.abort = 0;
-    bar->consumed_hi = 0;
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -265,179 +400,257 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmQ);
   }
   if (warp == 1) {
-    tmem_alloc(&bar->tmem_base, Sh::TMEM_COLS);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(&bar->tmem_base, Sh::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&bar->tmem_base, Sh::TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if (PAIR)
+    cluster_sync();   // both CTAs' barriers and TMEM exist before any signal between them
+  else
+    __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();
+  Items items(g, kt, worker, workers);
+  int tile, k0, k1;
+  // While the work before this kernel finishes, its first boxes come into L2:
+  // a prefetch writes nothing, and L2 stays coherent with what is still written.
+  if (warp == 0 && lane == 0) {
+    Items ahead = items;
+    int left = Sh::STAGES;
+    while (left > 0 && ahead.next(tile, k0, k1)) {
+      int pb, qb;
+      tile_blocks(tile, p_blocks, q_blocks, g.raster_gp, pb, qb);
+      for (int kb = k0; kb < k1 && left > 0; ++kb, --left) {
+        tma_prefetch_l2_2d(&tmP, kb * kBK, pb * Sh::TILE_P + rank * Sh::P_ROWS);
+        tma_prefetch_l2_2d(&tmQ, kb * kBK, qb * BN + rank * Sh::Q_ROWS);
+      }
+    }
+  }
   pdl_wait();
   const uint32_t tmem = bar->tmem_base;
   CtaCtl* cta = &bar->ctl;
+  const uint32_t limit_ns = static_cast<uint32_t>(g.ctl.timeout_ns < kMostWaitNs ? g.ctl.timeout_ns : kMostWaitNs);
+  const uint32_t full0 = smem_u32(&bar->full[0]), done0 = smem_u32(&bar->done[0]), free0 = smem_u32(&bar->acc_empty[0]);
   int issued = 0;   // producer only
 
-  if (warp == 0) {
-    // ---------------- producer ----------------
-    if (lane == 0) {
+  if (warp < 4) {
+    if (Sh::SPLIT_REGS) regs_decrease<Sh::OTHER_REGS>();
+    if (warp == 0 && lane == 0) {
+      // ---------------- producer (every CTA) ----------------
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      while (ok && items.next(tile, k0, k1)) {
         int pb, qb;
         tile_blocks(tile, p_blocks, q_blocks, g.raster_gp, pb, qb);
-        for (int kb = 0; kb < kt; ++kb) {
-          if (!mbar_wait(&bar->empty[s], ph ^ 1u, g.ctl, cta, kSiteProducerEmpty)) { ok = false; break; }
+        const int p_row = pb * Sh::TILE_P + rank * Sh::P_ROWS;
+        const int q_row = qb * BN + rank * Sh::Q_ROWS;
+        for (int kb = k0; kb < k1; ++kb) {
+          ring_wait(done0 + s * 8, ph ^ 1u, limit_ns, cta, kSiteProducerEmpty);
+          if (cta->abort) { ok = false; break; }
           uint8_t* slot = ring + s * Sh::STAGE;
-          if (!(g.ctl.inject_lost_load && tile == tiles - 1 && kb == kt - 1)) {
+          if (PAIR) {
+            // the even CTA's barrier counts the bytes of both CTAs' loads
+            if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], 2 * Sh::STAGE);
+            const uint32_t full = mapa_shared(smem_u32(&bar->full[s]), 0);
+            tma_load_2d_pair(smem_u32(slot), &tmP, full, kb * kBK, p_row);
+            tma_load_2d_pair(smem_u32(slot + Sh::P_BYTES), &tmQ, full, kb * kBK, q_row);
+            ++issued;
+          } else if (!(g.ctl.inject_lost_load && tile == last_tile && kb == kt - 1)) {
             mbar_arrive_expect_tx(&bar->full[s], Sh::STAGE);
-            tma_load_2d(smem_u32(slot), &tmP, &bar->full[s], kb * kBK, pb * Sh::TILE_P);
-            tma_load_2d(smem_u32(slot + Sh::P_BYTES), &tmQ, &bar->full[s], kb * kBK, qb * BN);
+            tma_load_2d(smem_u32(slot), &tmP, &bar->full[s], kb * kBK, p_row);
+            tma_load_2d(smem_u32(slot + Sh::P_BYTES), &tmQ, &bar->full[s], kb * kBK, q_row);
             ++issued;
           }
           if (++s == Sh::STAGES) { s = 0; ph ^= 1u; }
         }
       }
-    }
-  } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
+    } else if (warp == 1 && rank == 0) {
+      // ---------------- MMA issuer (the even CTA of a pair) ----------------
+      // The whole warp walks the loop, so that addresses and descriptors stay
+      // in uniform registers; one lane issues.
       int s = 0, a = 0;
       uint32_t ph = 0, aph = 0;
-      int consumed = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-        for (int kb = 0; kb < kt; ++kb) {
-          if (!mbar_wait(&bar->acc_empty[a], aph ^ 1u, g.ctl, cta, kSiteMmaAccEmpty) ||
-              !mbar_wait(&bar->full[s], ph, g.ctl, cta, kSiteConsumerFull)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t addr = smem_u32(ring + s * Sh::STAGE);
-          const uint64_t dp = umma_desc_sw128(addr);
-          const uint64_t dq = umma_desc_sw128(addr + Sh::P_BYTES);
+      const bool leader = elect_one();
+      const uint64_t desc0 = umma_desc_sw128(smem_u32(ring));
+      while (ok && items.next(tile, k0, k1)) {
+        for (int kb = k0; kb < k1; ++kb) {
+          ring_wait(full0 + s * 8, ph, limit_ns, cta, kSiteConsumerFull);
+          ring_wait(free0 + a * 8, aph ^ 1u, limit_ns, cta, kSiteMmaAccEmpty);
+          tc_fence_after();   // (after a wait that gave up: MMAs of whatever the slot holds)
+          const uint64_t dp = desc0 + static_cast<uint32_t>(s * Sh::STAGE) / 16;
+          const uint64_t dq = dp + Sh::P_BYTES / 16;
           const uint32_t d = tmem + a * BN;
+          if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < kBK / kMmaK; ++kk)   // 32 bytes along K: the start address field moves by 2
-            umma_f8(d, dp + 2 * kk, dq + 2 * kk, g.idesc, kk == 0 ? 0u : 1u);
-          umma_commit(&bar->empty[s]);
-          umma_commit(&bar->acc_full[a]);
-          ++consumed;
+            for (int kk = 0; kk < kBK / kMmaK; ++kk) {   // 32 bytes along K: the start address field moves by 2
+              if (PAIR)
+                umma_f8_pair(d, dp + 2 * kk, dq + 2 * kk, g.idesc, kk == 0 ? 0u : 1u);
+              else
+                umma_f8(d, dp + 2 * kk, dq + 2 * kk, g.idesc, kk == 0 ? 0u : 1u);
+            }
+            if (PAIR) umma_commit_pair(&bar->done[s], 0x3); else umma_commit(&bar->done[s]);
+          }
+          __syncwarp();
           if (++s == Sh::STAGES) { s = 0; ph ^= 1u; }
           if (++a == Sh::BUFS) { a = 0; aph ^= 1u; }
         }
+        if (__any_sync(0xffffffffu, cta->abort)) ok = false;
       }
-      bar->consumed_hi = consumed;
-      umma_commit(&bar->drain);   // fires when every MMA issued above has completed
-      CtaCtl never_abort{0};
-      mbar_wait(&bar->drain, 0, g.ctl, &never_abort, kSiteDrain);
-    }
-  } else if (warp == 2) {
-    // ---------------- scales ----------------
-    int s = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-      int pb, qb;
-      tile_blocks(tile, p_blocks, q_blocks, g.raster_gp, pb, qb);
-      for (int kb = 0; kb < kt; ++kb) {
-        if (!warp_wait(&bar->sc_empty[s], ph ^ 1u, g.ctl, cta, kSiteProducerEmpty)) { ok = false; break; }
-        const uint32_t dst = smem_u32(scales + s * Sh::SCALES);
-        const float* pk = g.p.base + kb * g.p.stride_col;
-        const float* qk = g.q.base + kb * g.q.stride_col;
-#pragma unroll
-        for (int i = 0; i < Sh::P_ROWS / 32; ++i) {
-          const int r = i * 32 + lane;
-          const int64_t row = static_cast<int64_t>(pb) * Sh::TILE_P + r;
-          const bool in = row < g.p.rows;
-          cp_async4(dst + r * 4, in ? pk + (row >> g.p.shift) * g.p.stride_row : pk, in);
-        }
-        if (QROWS) {
-#pragma unroll
-          for (int i = 0; i < (BN + 31) / 32; ++i) {
-            const int r = i * 32 + lane;
-            const int64_t row = static_cast<int64_t>(qb) * BN + r;
-            const bool in = r < BN && row < g.q.rows;
-            if (r < BN) cp_async4(dst + (Sh::P_ROWS + r) * 4, in ? qk + (row >> g.q.shift) * g.q.stride_row : qk, in);
-          }
-        } else if (lane < (BN + 127) / 128) {
-          const int64_t row = static_cast<int64_t>(qb) * BN + lane * 128;
-          const bool in = row < g.q.rows;
-          cp_async4(dst + (Sh::P_ROWS + lane) * 4, in ? qk + (row >> g.q.shift) * g.q.stride_row : qk, in);
-        }
-        cp_async_arrive(&bar->sc_full[s]);
-        if (++s == kScaleSlots) { s = 0; ph ^= 1u; }
+      if (leader) {
+        // fires when every MMA issued above has completed
+        if (PAIR) umma_commit_pair(&bar->drain, 0x1); else umma_commit(&bar->drain);
+        CtaCtl never_abort{0};
+        mbar_wait(&bar->drain, 0, g.ctl, &never_abort, kSiteDrain);
       }
     }
-    cp_async_wait_all();
-  } else if (warp >= 4) {
+  } else {
     // ---------------- scaled sums and output ----------------
+    if (Sh::SPLIT_REGS) regs_increase<Sh::ADD_REGS>();
     const int e = warp - 4;
     const int quarter = warp & 3;          // TMEM lanes this warp may access
     const int half = e >> 2;               // which half of the columns
-    const int row = quarter * 32 + lane;   // row of the tile that this thread holds
+    const int row = quarter * 32 + lane;   // row of the CTA's tile that this thread holds
     uint8_t* my_stage = staging + e * kStageWarpBytes;
     constexpr int CW = Sh::HALF < 32 ? Sh::HALF : 32;
     constexpr int CHUNKS = Sh::HALF / CW;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    int a = 0, sc = 0;
-    uint32_t aph = 0, sph = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+    int s = 0, a = 0, batch = 0;
+    uint32_t ph = 0;
+    const int t = threadIdx.x - 128;
+    const uint32_t lead_free0 = PAIR ? mapa_shared(free0, 0) : free0;
+    bool ok = true;   // after a wait that gave up: no more data, but the barriers and the split tiles' counts go on
+
+    // Scales of K blocks kb .. of the tile (pb, qb) into staging batch `to`:
+    // one per row, or one per 128 rows where that is all there is.
+    const int p_log = g.p.shift ? 0 : 7;                                   // log2 of P's values per K block
+    constexpr int Q_LOG = QROWS ? (BN == 256 ? 8 : BN == 128 ? 7 : BN == 64 ? 6 : BN == 32 ? 5 : 4) : (BN == 256 ? 1 : 0);
+    auto stage_scales = [&](int to, int pb, int qb, int kb, int n) {
+      const uint32_t dst = smem_u32(scales + to * kScaleBatch * Sh::SCALES);
+      auto one = [&](const ScaleView& v, int64_t first, int log, int step, int at) {
+        for (int i = t; i < n << log; i += kAddThreads) {
+          const int b = i >> log, r = i & ((1 << log) - 1);
+          const int64_t row = first + r * step;
+          const bool in = row < v.rows;
+          cp_async4(dst + (b * Sh::SCALES + at + r) * 4,
+                    v.base + (in ? (row >> v.shift) * v.stride_row + (kb + b) * v.stride_col : 0), in);
+        }
+      };
+      one(g.p, static_cast<int64_t>(pb) * Sh::TILE_P + rank * Sh::P_ROWS, p_log, 1, 0);
+      one(g.q, static_cast<int64_t>(qb) * BN, Q_LOG, QROWS ? 1 : 128, Sh::P_ROWS);
+    };
+    while (items.next(tile, k0, k1)) {
+      const bool split = k1 - k0 < kt;
       float acc[Sh::HALF];
 #pragma unroll
       for (int i = 0; i < Sh::HALF; ++i) acc[i] = 0.f;
-      for (int kb = 0; kb < kt; ++kb) {
-        ok = warp_wait(&bar->sc_full[sc], sph, g.ctl, cta, kSiteConsumerFull) &&
-             warp_wait(&bar->acc_full[a], aph, g.ctl, cta, kSiteEpilogueAccFull);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t src = tmem + lanes + a * BN + half * Sh::HALF;
-        uint32_t v[2][CW];
-        tmem_ld(src, v[0]);
-        const float* slot = scales + sc * Sh::SCALES;
-        const float sp = slot[row];
-        const float* sq = slot + Sh::P_ROWS;
-        const float both = QROWS ? 0.f : sp * sq[BN == 256 ? half : 0];
-#pragma unroll
-        for (int j = 0; j < CHUNKS; ++j) {
-          tmem_wait_ld();
-          regs_after_wait(v[j & 1]);
-          if (j + 1 < CHUNKS) {
-            tmem_ld(src + (j + 1) * CW, v[(j + 1) & 1]);
-          } else {
-            // the buffer is in registers: hand it back
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->acc_empty[a]);
-          }
-          if (QROWS) {
-            const float4* q4 = reinterpret_cast<const float4*>(sq + half * Sh::HALF + j * CW);
-#pragma unroll
-            for (int i = 0; i < CW / 4; ++i) {
-              const float4 q = q4[i];
-              float* o = acc + j * CW + 4 * i;
-              const uint32_t* d = v[j & 1] + 4 * i;
-              o[0] = fmaf(__uint_as_float(d[0]), sp * q.x, o[0]);
-              o[1] = fmaf(__uint_as_float(d[1]), sp * q.y, o[1]);
-              o[2] = fmaf(__uint_as_float(d[2]), sp * q.z, o[2]);
-              o[3] = fmaf(__uint_as_float(d[3]), sp * q.w, o[3]);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < CW; ++i) acc[j * CW + i] = fmaf(__uint_as_float(v[j & 1][i]), both, acc[j * CW + i]);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->sc_empty[sc]);
-        if (++a == Sh::BUFS) { a = 0; aph ^= 1u; }
-        if (++sc == kScaleSlots) { sc = 0; sph ^= 1u; }
-      }
-      if (!ok) break;
       int pb, qb;
       tile_blocks(tile, p_blocks, q_blocks, g.raster_gp, pb, qb);
-      const int64_t p0 = static_cast<int64_t>(pb) * Sh::TILE_P + quarter * 32;
+      if (ok) stage_scales(batch, pb, qb, k0, min(kScaleBatch, k1 - k0));
+      for (int kc = k0; kc < k1; kc += kScaleBatch, batch ^= 1) {
+        const int end = min(kc + kScaleBatch, k1);
+        cp_async_wait_all();
+        add_warps_sync();      // this batch is there for all, and all have read the one before
+        if (!ok) continue;
+        if (end < k1) stage_scales(batch ^ 1, pb, qb, end, min(kScaleBatch, k1 - end));
+        const float* slot = scales + batch * kScaleBatch * Sh::SCALES;
+        // A wait that gave up in here leaves wrong sums behind, which are never
+        // written: the abort flag is looked at after each batch.
+        for (int kb = kc; kb < end; ++kb, slot += Sh::SCALES) {
+          const float sp = slot[g.p.shift ? 0 : row];
+          const float* sq = slot + Sh::P_ROWS;
+          const float both = QROWS ? 0.f : sp * sq[BN == 256 ? half : 0];
+          ring_wait(done0 + s * 8, ph, limit_ns, cta, kSiteEpilogueAccFull);
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t src = tmem + lanes + a * BN + half * Sh::HALF;
+          uint32_t v[2][CW];
+          tmem_ld(src, v[0]);
+#pragma unroll
+          for (int j = 0; j < CHUNKS; ++j) {
+            tmem_wait_ld();
+            regs_after_wait(v[j & 1]);
+            if (j + 1 < CHUNKS) {
+              tmem_ld(src + (j + 1) * CW, v[(j + 1) & 1]);
+            } else {
+              // the buffer is in registers: hand it back to the MMA issuer
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if (PAIR)
+                  mbar_arrive_cluster_relaxed(lead_free0 + a * 8);
+                else
+                  mbar_arrive(&bar->acc_empty[a]);
+              }
+            }
+            if (QROWS) {
+              const float4* q4 = reinterpret_cast<const float4*>(sq + half * Sh::HALF + j * CW);
+#pragma unroll
+              for (int i = 0; i < CW / 4; ++i) {
+                const float4 q = q4[i];
+                float* o = acc + j * CW + 4 * i;
+                const uint32_t* d = v[j & 1] + 4 * i;
+                o[0] = fmaf(__uint_as_float(d[0]), sp * q.x, o[0]);
+                o[1] = fmaf(__uint_as_float(d[1]), sp * q.y, o[1]);
+                o[2] = fmaf(__uint_as_float(d[2]), sp * q.z, o[2]);
+                o[3] = fmaf(__uint_as_float(d[3]), sp * q.w, o[3]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < CW; ++i) acc[j * CW + i] = fmaf(__uint_as_float(v[j & 1][i]), both, acc[j * CW + i]);
+            }
+          }
+          if (++s == Sh::STAGES) { s = 0; ph ^= 1u; }
+          if (++a == Sh::BUFS) a = 0;
+        }
+        if (__any_sync(0xffffffffu, cta->abort)) ok = false;
+      }
+      if (split) {
+        // Every segment stores its FP32 sums; the one that completes the tile
+        // adds them all in K order, so the result does not depend on timing.
+        const Partial part(g, tile, kt, workers, Sh::CTAS, static_cast<int>(rank));
+        float4* base = reinterpret_cast<float4*>(g.partials) + (half * (Sh::HALF / 4)) * 128 + row;
+        constexpr int64_t SLOT = 128 * BN / 4;
+        if (ok) {
+          float4* dst = base + part.slot(worker) * SLOT;
+#pragma unroll
+          for (int i = 0; i < Sh::HALF / 4; ++i)
+            __stcg(dst + i * 128, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
+        }
+        __threadfence();
+        add_warps_sync();
+        if (threadIdx.x == 128) {
+          // wraps to zero with the last segment, ready for the next launch
+          const uint32_t seen = atomicInc(g.counters + static_cast<int64_t>(tile - g.dp_tiles) * Sh::CTAS + rank,
+                                          static_cast<uint32_t>(part.segments() - 1));
+          bar->last = seen == static_cast<uint32_t>(part.segments() - 1);
+          __threadfence();
+        }
+        add_warps_sync();
+        const bool finish = bar->last != 0;
+        if (!finish || !ok) continue;
+#pragma unroll
+        for (int i = 0; i < Sh::HALF; ++i) acc[i] = 0.f;
+        for (int w = part.w_first; w <= part.w_last; ++w) {
+          const float4* from = base + part.slot(w) * SLOT;
+#pragma unroll
+          for (int i = 0; i < Sh::HALF / 4; ++i) {
+            const float4 p = __ldcg(from + i * 128);
+            acc[4 * i] += p.x;
+            acc[4 * i + 1] += p.y;
+            acc[4 * i + 2] += p.z;
+            acc[4 * i + 3] += p.w;
+          }
+        }
+      }
+      if (!ok) continue;
+      const int64_t p0 = static_cast<int64_t>(pb) * Sh::TILE_P + rank * Sh::P_ROWS + quarter * 32;
       const int64_t q0 = static_cast<int64_t>(qb) * BN + half * Sh::HALF;
       if (g.out_type == GP_REAL_BF16)
         write_out<Sh::HALF, __nv_bfloat16>(g, acc, my_stage, lane, p0, q0);
@@ -450,16 +663,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   __syncthreads();
   if (cta->abort && warp == 0 && lane == 0) {
-    // loads still in flight land in shared memory: wait for them before exit
-    CtaCtl never_abort{0};
-    for (int i = bar->consumed_hi; i < issued; ++i)
-      mbar_wait(&bar->full[i % Sh::STAGES], static_cast<uint32_t>((i / Sh::STAGES) & 1), g.ctl, &never_abort,
-                kSiteDrain);
+    report_error(g.ctl, kDevErrTimeout, static_cast<uint32_t>(cta->abort));
+    if (PAIR) {
+      // this CTA's loads count on the even CTA's barrier: give any still in
+      // flight time to land before the pair tears down
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 200000ull) __nanosleep(1000);
+    } else {
+      // loads still in flight land in shared memory: wait for them before exit
+      CtaCtl never_abort{0};
+      for (int i = issued > Sh::STAGES ? issued - Sh::STAGES : 0; i < issued; ++i)
+        mbar_wait(&bar->full[i % Sh::STAGES], static_cast<uint32_t>((i / Sh::STAGES) & 1), g.ctl, &never_abort,
+                  kSiteDrain);
+    }
   }
-  __syncthreads();
+  if (PAIR) {
+    tc_fence_before();
+    cluster_sync();   // the even CTA's MMAs, which touch both CTAs, have completed
+  } else {
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, Sh::TMEM_COLS);
+    if (PAIR) tmem_dealloc_pair(tmem, Sh::TMEM_COLS); else tmem_dealloc(tmem, Sh::TMEM_COLS);
   }
 }
 
@@ -477,9 +703,32 @@ __global__ void __launch_bounds__(256) fill_kernel(T* c, int64_t ldc, const T* a
   }
 }
 
-template <int BN, bool QROWS>
+// Launch configuration of a kernel of CTAS CTAs per cluster.
+struct Config {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  Config(int grid, int ctas, int smem, cudaStream_t stream) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    if (ctas > 1) {
+      attr[1].id = cudaLaunchAttributeClusterDimension;
+      attr[1].val.clusterDim.x = ctas;
+      attr[1].val.clusterDim.y = 1;
+      attr[1].val.clusterDim.z = 1;
+      cfg.numAttrs = 2;
+    }
+    cfg.attrs = attr;
+  }
+};
+
+template <int BN, bool QROWS, bool PAIR>
 cudaError_t launch_ring(Fp8GemmArgs& a, const void** kernel) {
-  using Sh = Fp8Shape<BN>;
+  using Sh = Fp8Shape<BN, PAIR>;
   const bool swapped = a.plan.layout != 0;
   const gp_fp8_matrix& P = swapped ? a.B : a.A;
   const gp_fp8_matrix& Q = swapped ? a.A : a.B;
@@ -510,16 +759,33 @@ cudaError_t launch_ring(Fp8GemmArgs& a, const void** kernel) {
   g.vec = aligned(a.C, a.ldc) && (!a.addend || aligned(a.addend, a.ld_add));
   g.idesc = idesc_f8(P.format, Q.format, Sh::TILE_P, BN);
   g.raster_gp = a.plan.raster_gm;
+  g.dp_tiles = a.plan.dp_tiles;
+  g.sk_tiles = a.plan.sk_tiles;
+  g.partials = a.partials;
+  g.counters = a.counters;
   g.ctl = a.ctl;
-  auto k = fp8_ring_kernel<BN, QROWS>;
+  auto k = fp8_ring_kernel<BN, QROWS, PAIR>;
   *kernel = reinterpret_cast<const void*>(k);
+  if (Sh::SPLIT_REGS) {
+    // The register split counts on exactly kLaunchRegs per thread at launch:
+    // with fewer, the increase would wait for ever.  Refuse such a build.
+    static std::atomic<int> regs{-1};
+    if (regs.load() < 0) {
+      cudaFuncAttributes fa;
+      if ((e = cudaFuncGetAttributes(&fa, k)) != cudaSuccess) return e;
+      regs.store(fa.numRegs);
+    }
+    if (regs.load() != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  }
   if ((e = ensure_smem_attr(*kernel, Sh::SMEM)) != cudaSuccess) return e;
-  return launch_dependent(k, dim3(a.plan.grid), dim3(kThreads), Sh::SMEM, a.stream, tmP, tmQ, g);
+  Config c(a.plan.grid, Sh::CTAS, Sh::SMEM, a.stream);
+  return cudaLaunchKernelEx(&c.cfg, k, tmP, tmQ, g);
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 void shape_of(gp_plan* p) {
-  using Sh = Fp8Shape<BN>;
+  using Sh = Fp8Shape<BN, PAIR>;
+  p->cta_pair = PAIR;
   p->bm = Sh::TILE_P;
   p->bn = BN;
   p->bk = kBK;
@@ -530,13 +796,54 @@ void shape_of(gp_plan* p) {
   p->tmem_cols = Sh::TMEM_COLS;
 }
 
+// Deal out the K-loops of the tiles that would leave a part-empty last wave.
+// A split costs the partial sums' way through L2 and a wait for the last
+// segment; it pays where workers would idle for kMinIdle K blocks on average.
+void split_tiles(gp_plan* p, int64_t workers, bool allowed) {
+  constexpr int64_t kMinIdle = 4;      // K blocks
+  constexpr int64_t kMinShare = 2;     // K blocks per worker
+  const int64_t T = p->tiles, ctas = p->cta_pair ? 2 : 1;
+  p->dp_tiles = static_cast<int32_t>(T);
+  p->sk_tiles = 0;
+  p->workspace_bytes = 0;
+  p->grid = static_cast<int32_t>(ctas * (T < workers ? T : workers));
+  if (!allowed || workers <= 0 || T % workers == 0) return;
+  const int64_t idle = (T + workers - 1) / workers * workers - T;
+  if (idle * p->k_tiles < kMinIdle * workers) return;
+  const int64_t dp = T / workers * workers, sk = T - dp;
+  int64_t use = workers;
+  if (dp == 0 && sk * p->k_tiles / kMinShare < use) use = sk * p->k_tiles / kMinShare;
+  if (use <= sk || sk * p->k_tiles < kMinShare * use || sk * ctas > kFp8Counters) return;
+  p->dp_tiles = static_cast<int32_t>(dp);
+  p->sk_tiles = static_cast<int32_t>(sk);
+  p->grid = static_cast<int32_t>(ctas * use);
+  p->workspace_bytes = 2 * static_cast<int64_t>(p->grid) * 128 * p->bn * 4;
+}
+
+// Pairs that fit on the device at once (cached per device).
+cudaError_t pair_capacity(int* pairs) {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && (*pairs = cached[dev].load()) > 0) return cudaSuccess;
+  using Sh = Fp8Shape<256, true>;
+  const void* k = reinterpret_cast<const void*>(fp8_ring_kernel<256, false, true>);
+  if ((e = ensure_smem_attr(k, Sh::SMEM)) != cudaSuccess) return e;
+  Config c(2, 2, Sh::SMEM, nullptr);
+  if ((e = cudaOccupancyMaxActiveClusters(pairs, k, &c.cfg)) != cudaSuccess) return e;
+  if (*pairs < 1) return cudaErrorLaunchOutOfResources;
+  if (dev >= 0 && dev < 64) cached[dev].store(*pairs);
+  return cudaSuccess;
+}
+
 }  // namespace
 
 int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int sms, const gp_fp8_options* opts,
                   gp_plan* p) {
   std::memset(p, 0, sizeof(*p));
   const int want = opts ? opts->bn : 0;
-  if (want != 0 && want != 16 && want != 32 && want != 64 && want != 128) return GP_ERR_UNSUPPORTED;
+  if (want != 0 && want != 16 && want != 32 && want != 64 && want != 128 && want != 256) return GP_ERR_UNSUPPORTED;
   // Q, the operand on the MMA's N side, is the narrower one where that is at
   // most one tile wide; else the one with block scales (one product of scales
   // per row instead of one per output), B if both or neither.
@@ -548,38 +855,50 @@ int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int
     swapped = a_group == kFp8Group && b_group == 1;
   const int64_t p_rows = swapped ? N : M, q_rows = swapped ? M : N;
   int bn = want;
-  if (bn == 0) bn = narrow <= 16 ? 16 : (narrow <= 32 ? 32 : (narrow <= 64 ? 64 : 128));
+  if (bn == 0) bn = narrow <= 16 ? 16 : (narrow <= 32 ? 32 : (narrow <= 64 ? 64 : (narrow <= 128 ? 128 : 256)));
+  // (a lost load is injected into the one-CTA kernel)
+  if (opts && opts->inject_lost_load && bn == 256) bn = 128;
   p->dtype = GP_PLAN_FP8;
   p->layout = swapped;
   p->variant = GP_PIPELINED;
   p->threads = kThreads;
   p->persistent = 1;
-  p->kernel = "fp8_ring";
+  p->kernel = bn == 256 ? "fp8_pair_ring" : "fp8_ring";
   switch (bn) {
-    case 16: shape_of<16>(p); break;
-    case 32: shape_of<32>(p); break;
-    case 64: shape_of<64>(p); break;
-    default: shape_of<128>(p); break;
+    case 16: shape_of<16, false>(p); break;
+    case 32: shape_of<32, false>(p); break;
+    case 64: shape_of<64, false>(p); break;
+    case 128: shape_of<128, false>(p); break;
+    default: shape_of<256, true>(p); break;
   }
   p->tiles = (p_rows + p->bm - 1) / p->bm * ((q_rows + p->bn - 1) / p->bn);
   p->k_tiles = (K + kBK - 1) / kBK;
   if (p->tiles > kMaxTiles) return GP_ERR_SIZE;
-  p->grid = sms > 0 ? static_cast<int32_t>(p->tiles < sms ? p->tiles : sms) : 0;
   p->dp_tiles = static_cast<int32_t>(p->tiles);
   p->k_splits = 1;
   p->raster_gm = 8;
   p->compute_load_ratio = 2.0 * p->bm * p->bn / (p->bm + p->bn);
+  if (sms > (p->cta_pair ? 1 : 0)) split_tiles(p, p->cta_pair ? sms / 2 : sms, !(opts && opts->no_split));
   return GP_OK;
 }
 
 cudaError_t launch_fp8_gemm(Fp8GemmArgs& a, const void** kernel) {
   const gp_fp8_matrix& Q = a.plan.layout ? a.A : a.B;
   switch (a.plan.bn) {
-    case 16: return launch_ring<16, true>(a, kernel);
-    case 32: return launch_ring<32, true>(a, kernel);
-    case 64: return launch_ring<64, true>(a, kernel);
-    default: return Q.group == 1 ? launch_ring<128, true>(a, kernel) : launch_ring<128, false>(a, kernel);
+    case 16: return launch_ring<16, true, false>(a, kernel);
+    case 32: return launch_ring<32, true, false>(a, kernel);
+    case 64: return launch_ring<64, true, false>(a, kernel);
+    case 128: return Q.group == 1 ? launch_ring<128, true, false>(a, kernel) : launch_ring<128, false, false>(a, kernel);
+    default: return Q.group == 1 ? launch_ring<256, true, true>(a, kernel) : launch_ring<256, false, true>(a, kernel);
   }
+}
+
+cudaError_t fp8_fit_pairs(gp_plan* plan, bool no_split) {
+  if (!plan->cta_pair) return cudaSuccess;
+  int pairs = 0;
+  const cudaError_t e = pair_capacity(&pairs);
+  if (e == cudaSuccess && 2 * pairs < plan->grid) split_tiles(plan, pairs, !no_split);
+  return e;
 }
 
 cudaError_t launch_fp8_fill(void* C, int64_t ldc, const void* addend, int64_t ld_add, int64_t M, int64_t N,

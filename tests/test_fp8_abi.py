@@ -178,3 +178,20 @@ def test_plain_formats_agree_with_torch(fmt):
     x = x[np.abs(x) <= ref.FMAX[fmt]]
     want = torch.from_numpy(x).to(ref.TORCH[fmt]).view(torch.uint8).numpy()
     assert np.array_equal(ref.encode(x, fmt), want)
+
+
+def test_split_tiles_fill_the_device(gp):
+    # few tiles with long K-loops: dealt out to all SMs (152), or to fewer with at least two K blocks each
+    p = gp.gemm_fp8_plan(1, 4096, 4096, sms=152)
+    assert (p["tiles"], p["sk_tiles"], p["grid"]) == (32, 32, 152)
+    assert p["workspace_bytes"] == 2 * 152 * 128 * 16 * 4
+    p = gp.gemm_fp8_plan(1, 128, 1024, sms=152)
+    assert (p["sk_tiles"], p["grid"]) == (1, 4)
+    # whole waves, short K-loops, or a caller's wish: none
+    for M, N, K, kw in ((1, 152 * 128, 4096, {}), (1, 4096, 128, {}), (1, 4096, 4096, {"no_split": True})):
+        p = gp.gemm_fp8_plan(M, N, K, sms=152, **kw)
+        assert p["sk_tiles"] == 0 and p["workspace_bytes"] == 0
+    # 80 pair tiles on 76 pairs: a full wave and four tiles split
+    p = gp.gemm_fp8_plan(8 * 256, 10 * 256, 16384, sms=152)
+    assert (p["cta_pair"], p["bm"], p["bn"]) == (1, 256, 256)
+    assert (p["dp_tiles"], p["sk_tiles"], p["grid"]) == (76, 4, 152)
