@@ -95,6 +95,7 @@ struct Fp8Params {
   int32_t out_type;
   int32_t swapped;           // P is B: C's rows run along Q
   int32_t vec;               // groups of 4 outputs are aligned to their size
+  int32_t vec16;             // groups of 8 16-bit outputs are aligned to 16 bytes
   uint32_t idesc;
   int32_t raster_gp;         // P blocks per raster group
   int32_t dp_tiles;          // tiles computed whole (raster order first)
@@ -203,6 +204,22 @@ __device__ __forceinline__ void ring_wait(uint32_t bar_addr, uint32_t parity, ui
   }
 }
 
+// Pairs of FP32 values in one 64-bit register: a packed product is one
+// instruction, and rounds each half as a single one does.  (Packed FMAs on what
+// the TMEM loads return cost as many moves as they save.)
+__device__ __forceinline__ uint64_t pack2f(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Output tile -> its P and Q blocks: groups of `gp` P blocks, each swept over all Q blocks.
 __device__ __forceinline__ void tile_blocks(int tile, int p_blocks, int q_blocks, int gp, int& pb, int& qb) {
   const int per = gp * q_blocks;
@@ -282,63 +299,105 @@ struct Partial {
 
 __device__ __forceinline__ void add_warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kAddThreads) : "memory"); }
 
-// Four neighbouring outputs of a row: FP32 sums (+ addend) rounded to the output type.
 template <typename T>
-__device__ __forceinline__ void store4(const Fp8Params& g, float4 v, int64_t row, int64_t col, int64_t cols) {
-  T* c = static_cast<T*>(g.c) + row * g.ldc + col;
-  const T* add = g.addend ? static_cast<const T*>(g.addend) + row * g.ld_add + col : nullptr;
+__device__ __forceinline__ float widen(T t) { return static_cast<float>(t); }
+template <typename T>
+__device__ __forceinline__ T narrow(float f) { return static_cast<T>(f); }   // nearest even
+template <typename T>
+struct alignas(4 * sizeof(T)) Four {
+  T e[4];
+};
+
+// Four neighbouring outputs of a row: FP32 sums (+ addend) rounded to the output type.  FULL: all are inside C and
+// aligned to their size.
+template <typename T, bool FULL>
+__device__ __forceinline__ void store4(T* c, const T* add, float4 v, bool vec, int64_t left) {
   float x[4] = {v.x, v.y, v.z, v.w};
-  struct alignas(4 * sizeof(T)) Four { T e[4]; };
-  auto widen = [](T t) {
-    if constexpr (sizeof(T) == 4) return t; else return static_cast<float>(t);
-  };
-  auto narrow = [](float f) {
-    if constexpr (sizeof(T) == 4) return f; else return static_cast<T>(f);   // nearest even
-  };
-  if (g.vec && col + 4 <= cols) {
+  if (FULL || (vec && left >= 4)) {
     if (add) {
-      const Four a = *reinterpret_cast<const Four*>(add);
+      const Four<T> a = *reinterpret_cast<const Four<T>*>(add);
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] += widen(a.e[i]);
     }
-    Four o;
+    Four<T> o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o.e[i] = narrow(x[i]);
-    *reinterpret_cast<Four*>(c) = o;
+    for (int i = 0; i < 4; ++i) o.e[i] = narrow<T>(x[i]);
+    *reinterpret_cast<Four<T>*>(c) = o;
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (col + i >= cols) break;
-    c[i] = narrow(add ? x[i] + widen(add[i]) : x[i]);
-  }
+  for (int i = 0; i < 4; ++i)
+    if (i < left) c[i] = narrow<T>(add ? x[i] + widen(add[i]) : x[i]);
 }
 
 template <typename T>
-__device__ __forceinline__ void store1(const Fp8Params& g, float v, int64_t row, int64_t col) {
-  if (g.addend) v += static_cast<float>(static_cast<const T*>(g.addend)[row * g.ld_add + col]);
-  static_cast<T*>(g.c)[row * g.ldc + col] = static_cast<T>(v);
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  const T v[2] = {narrow<T>(lo), narrow<T>(hi)};
+  uint32_t r;
+  memcpy(&r, v, 4);
+  return r;
 }
 
-// Write a warp's 32 rows x HALF columns of sums (thread: one row) to C.
+// Write a warp's 32 rows x HALF columns of sums (thread: one row) to C: through
+// shared memory, so that a row's outputs leave side by side.  16-byte chunk c
+// of row r of the staged 32 x 128 bytes lies at c ^ (r mod 8).
 template <int HALF, typename T>
 __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)[HALF], uint8_t* stage, int lane,
                                           int64_t p0, int64_t q0) {
+  T* const c = static_cast<T*>(g.c);
+  const T* const add = static_cast<const T*>(g.addend);
   if (g.swapped) {
     // the lanes' rows are C's columns: each of C's rows gets 32 neighbouring outputs
     const int64_t col = p0 + lane;
-    if (col < g.p.rows) {
+    if (col >= g.p.rows) return;
+    const int rows = static_cast<int>(g.q.rows - q0 < HALF ? g.q.rows - q0 : HALF);
 #pragma unroll
-      for (int i = 0; i < HALF; ++i)
-        if (q0 + i < g.q.rows) store1<T>(g, acc[i], q0 + i, col);
+    for (int i = 0; i < HALF; ++i) {
+      if (i < rows) {
+        float v = acc[i];
+        if (add) v += widen(add[(q0 + i) * g.ld_add + col]);
+        c[(q0 + i) * g.ldc + col] = narrow<T>(v);
+      }
     }
     return;
   }
-  // Through shared memory, so that a row's outputs leave side by side.  16-byte
-  // chunk c of row r lies at c ^ (r mod 8).
-  constexpr int CW = HALF < 32 ? HALF : 32;      // columns staged at a time
-  constexpr int PER = CW / 4;                    // lanes per row when they leave
   const uint32_t base = smem_u32(stage);
+  const bool full = g.vec && p0 + 32 <= g.p.rows && q0 + HALF <= g.q.rows;
+  if constexpr (sizeof(T) == 2 && HALF >= 64) {
+    if (full && !add && g.vec16) {
+      // 64 columns at a time, rounded before they are staged: 16 bytes per lane, 8 lanes per row
+      T* out = c + (p0 + lane / 8) * g.ldc + q0 + lane % 8 * 8;
+#pragma unroll
+      for (int j = 0; j < HALF / 64; ++j, out += 64) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float* x = acc + j * 64 + 8 * i;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + sw128_offset(lane, i)),
+                       "r"(pack16<T>(x[0], x[1])), "r"(pack16<T>(x[2], x[3])), "r"(pack16<T>(x[4], x[5])),
+                       "r"(pack16<T>(x[6], x[7]))
+                       : "memory");
+        }
+        __syncwarp();
+        uint4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                       : "r"(base + sw128_offset(i * 4 + lane / 8, lane % 8))
+                       : "memory");
+        T* o = out;
+#pragma unroll
+        for (int i = 0; i < 8; ++i, o += 4 * g.ldc) *reinterpret_cast<uint4*>(o) = w[i];
+      }
+      return;
+    }
+  }
+  constexpr int CW = HALF < 32 ? HALF : 32;      // columns staged at a time, in FP32
+  constexpr int PER = CW / 4;                    // lanes per row when they leave
+  const int64_t row = p0 + lane / PER, col = q0 + lane % PER * 4;
+  T* out = c + row * g.ldc + col;
+  const T* from = add ? add + row * g.ld_add + col : nullptr;
 #pragma unroll
   for (int j = 0; j < HALF / CW; ++j) {
     __syncwarp();
@@ -349,16 +408,20 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
                    "f"(acc[j * CW + 4 * i + 3])
                    : "memory");
     __syncwarp();
+    const int64_t left = g.q.rows - col - j * CW;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int r = i * (32 / PER) + lane / PER, ch = lane % PER;
       float4 v;
       asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                    : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                   : "r"(base + sw128_offset(r, ch))
+                   : "r"(base + sw128_offset(i * (32 / PER) + lane / PER, lane % PER))
                    : "memory");
-      const int64_t col = q0 + j * CW + 4 * ch;
-      if (p0 + r < g.p.rows && col < g.q.rows) store4<T>(g, v, p0 + r, col, g.q.rows);
+      T* o = out + i * (32 / PER) * g.ldc + j * CW;
+      const T* f = from ? from + i * (32 / PER) * g.ld_add + j * CW : nullptr;
+      if (full)
+        store4<T, true>(o, f, v, true, 4);
+      else if (row + i * (32 / PER) < g.p.rows && left > 0)
+        store4<T, false>(o, f, v, g.vec != 0, left);
     }
   }
 }
@@ -565,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = kc; kb < end; ++kb, slot += Sh::SCALES) {
           const float sp = slot[g.p.shift ? 0 : row];
           const float* sq = slot + Sh::P_ROWS;
-          const float both = QROWS ? 0.f : sp * sq[BN == 256 ? half : 0];
+          const float one = QROWS ? sp : sp * sq[BN == 256 ? half : 0];
           ring_wait(done0 + s * 8, ph, limit_ns, cta, kSiteEpilogueAccFull);
           __syncwarp();
           tc_fence_after();
@@ -589,21 +652,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mbar_arrive(&bar->acc_empty[a]);
               }
             }
+            float* o = acc + j * CW;
+            const uint32_t* d = v[j & 1];
             if (QROWS) {
-              const float4* q4 = reinterpret_cast<const float4*>(sq + half * Sh::HALF + j * CW);
+              const ulonglong2* q4 = reinterpret_cast<const ulonglong2*>(sq + half * Sh::HALF + j * CW);
+              const uint64_t sp2 = pack2f(one, one);
 #pragma unroll
               for (int i = 0; i < CW / 4; ++i) {
-                const float4 q = q4[i];
-                float* o = acc + j * CW + 4 * i;
-                const uint32_t* d = v[j & 1] + 4 * i;
-                o[0] = fmaf(__uint_as_float(d[0]), sp * q.x, o[0]);
-                o[1] = fmaf(__uint_as_float(d[1]), sp * q.y, o[1]);
-                o[2] = fmaf(__uint_as_float(d[2]), sp * q.z, o[2]);
-                o[3] = fmaf(__uint_as_float(d[3]), sp * q.w, o[3]);
+                const ulonglong2 q = q4[i];      // four columns' scales
+                const uint64_t m = mul2(sp2, q.x), n = mul2(sp2, q.y);
+                o[4 * i] = fmaf(__uint_as_float(d[4 * i]), lo2(m), o[4 * i]);
+                o[4 * i + 1] = fmaf(__uint_as_float(d[4 * i + 1]), hi2(m), o[4 * i + 1]);
+                o[4 * i + 2] = fmaf(__uint_as_float(d[4 * i + 2]), lo2(n), o[4 * i + 2]);
+                o[4 * i + 3] = fmaf(__uint_as_float(d[4 * i + 3]), hi2(n), o[4 * i + 3]);
               }
             } else {
 #pragma unroll
-              for (int i = 0; i < CW; ++i) acc[j * CW + i] = fmaf(__uint_as_float(v[j & 1][i]), both, acc[j * CW + i]);
+              for (int i = 0; i < CW; ++i) o[i] = fmaf(__uint_as_float(d[i]), one, o[i]);
             }
           }
           if (++s == Sh::STAGES) { s = 0; ph ^= 1u; }
@@ -752,11 +817,12 @@ cudaError_t launch_ring(Fp8GemmArgs& a, const void** kernel) {
   g.K = a.K;
   g.out_type = a.out_type;
   g.swapped = swapped;
-  const uint64_t four = 4 * real_bytes(a.out_type);
-  auto aligned = [&](const void* p, int64_t ld) {
-    return reinterpret_cast<uintptr_t>(p) % four == 0 && static_cast<uint64_t>(ld) * real_bytes(a.out_type) % four == 0;
+  const int size = real_bytes(a.out_type);
+  auto aligned = [&](const void* p, int64_t ld, int64_t to) {
+    return reinterpret_cast<uintptr_t>(p) % to == 0 && ld * size % to == 0;
   };
-  g.vec = aligned(a.C, a.ldc) && (!a.addend || aligned(a.addend, a.ld_add));
+  g.vec = aligned(a.C, a.ldc, 4 * size) && (!a.addend || aligned(a.addend, a.ld_add, 4 * size));
+  g.vec16 = size == 2 && aligned(a.C, a.ldc, 16);
   g.idesc = idesc_f8(P.format, Q.format, Sh::TILE_P, BN);
   g.raster_gp = a.plan.raster_gm;
   g.dp_tiles = a.plan.dp_tiles;
