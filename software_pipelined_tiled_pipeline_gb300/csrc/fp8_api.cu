@@ -192,7 +192,7 @@ int fp8_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ld_res
   a.vec_w = aligned(weight, 16);
   gp_plan plan = {};
   const void* kernel = nullptr;
-  e = launch_fp8_rmsnorm(a, st, &kernel, &plan);
+  e = launch_fp8_rmsnorm(a, info.sm_count, st, &kernel, &plan);
   call_launched(plan, kernel);
   return e == cudaSuccess ? call_finish(GP_OK) : call_finish(GP_ERR_CUDA, e);
 }

@@ -51,7 +51,7 @@ struct NormArgs {
   int32_t type, weight_type, e5m2;
   int32_t vec, vec_w;    // the matrices' and the weight's chunks of 8 values are 16-byte aligned
 };
-cudaError_t launch_fp8_rmsnorm(const NormArgs& a, cudaStream_t stream, const void** kernel, gp_plan* plan);
+cudaError_t launch_fp8_rmsnorm(const NormArgs& a, int sm_count, cudaStream_t stream, const void** kernel, gp_plan* plan);
 
 struct NormGradArgs {
   const void *dy, *h, *dres, *weight;

@@ -94,6 +94,20 @@ __device__ __forceinline__ void load8_any(float (&v)[8], const void* base, int t
   }
 }
 
+// Value k of eight as FP32, straight from the raw words.
+template <typename T>
+__device__ __forceinline__ float value_of(const Raw8<T>& r, int k) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(w[k]);
+  } else {
+    const uint16_t h = static_cast<uint16_t>(k & 1 ? w[k / 2] >> 16 : w[k / 2]);
+    T t;
+    memcpy(&t, &h, 2);
+    return to_f32(t);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // scales and 8-bit codes
 // ---------------------------------------------------------------------------
@@ -101,6 +115,32 @@ __device__ __forceinline__ void load8_any(float (&v)[8], const void* base, int t
 // the floats do and a NaN's lies above all of them, so an integer maximum of
 // these also carries a NaN or an infinity of the group to its scale.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// Magnitudes of raw values in their own bits: 16-bit types two to a word, with
+// the same order and the same way of carrying a NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t raw_abs(uint32_t word) {
+  return word & (sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t raw_max(uint32_t a, uint32_t b) {
+  if constexpr (sizeof(T) == 4) return max(a, b);
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The magnitude in a word's only (32-bit types), lower or upper value, as FP32 bits.
+template <typename T>
+__device__ __forceinline__ uint32_t raw_to_bits(uint32_t word, int upper) {
+  if constexpr (sizeof(T) == 4) {
+    return word;
+  } else {
+    const uint16_t h = static_cast<uint16_t>(upper ? word >> 16 : word);
+    T t;
+    memcpy(&t, &h, 2);
+    return __float_as_uint(to_f32(t));
+  }
+}
 
 constexpr float kScaleFloor = 5.42101086e-20f;   // 2^-64
 

@@ -73,67 +73,80 @@ __device__ __forceinline__ int chunk_valid(int64_t cols, int64_t col) {
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
+// Each block takes every gridDim.x-th row (or group of blockDim.y rows); the
+// next row's loads are under way while this one is reduced and written.
 template <typename T, int NCH>
 __global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float slots[32];
+  __shared__ float slots[2][32];
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const bool live = row < a.rows;       // (a block's spare rows take part in its barriers)
   const bool vec = a.vec != 0;
   const int lane = threadIdx.x & 31;
-
-  Raw8<T> rx[NCH], rr[NCH];
+  constexpr bool KEEP_W = NCH <= 2;     // (four chunks' weights would spill: read again for each row)
+  float w[KEEP_W ? NCH : 1][8];
   int valid[NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
-    valid[i] = live ? chunk_valid(a.cols, col) : 0;
-    load8(rx[i], static_cast<const T*>(a.x) + row * a.ldx + col, valid[i], vec);
+    valid[i] = chunk_valid(a.cols, col);
+    if (KEEP_W) load8_any(w[KEEP_W ? i : 0], a.weight, a.weight_type, col, valid[i], a.vec_w != 0);
   }
-  if (a.residual) {
+  Raw8<T> rx[NCH], rr[NCH];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
-      load8(rr[i], static_cast<const T*>(a.residual) + row * a.ld_res + col, valid[i], vec);
+      const int n = row < a.rows ? valid[i] : 0;
+      load8(rx[i], static_cast<const T*>(a.x) + row * a.ldx + col, n, vec);
+      if (a.residual) load8(rr[i], static_cast<const T*>(a.residual) + row * a.ld_res + col, n, vec);
     }
-  }
-  float h[NCH][8];
-  float ss = 0.f;
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  fetch(row);
+  int set = 0;
+  // (a block's spare rows take part in its barriers)
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * blockDim.y; base < a.rows; base += step, row += step, set ^= 1) {
+    const bool live = row < a.rows;
+    float h[NCH][8];
+    float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    unpack8(rx[i], h[i]);
-    if (a.residual) {
-      float r[8];
-      unpack8(rr[i], r);
+    for (int i = 0; i < NCH; ++i) {
+      unpack8(rx[i], h[i]);
+      if (a.residual) {
+        float r[8];
+        unpack8(rr[i], r);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) h[i][k] += r[k];
-      pack8(h[i], rx[i]);
-      unpack8(rx[i], h[i]);             // the norm is of the rounded sum
+        for (int k = 0; k < 8; ++k) h[i][k] += r[k];
+        pack8(h[i], rx[i]);
+        unpack8(rx[i], h[i]);             // the norm is of the rounded sum
+      }
+      if (a.h && live) {
+        const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
+        store8(static_cast<T*>(a.h) + row * a.ld_h + col, rx[i], valid[i], vec);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ss = fmaf(h[i][k], h[i][k], ss);
     }
-    if (a.h) {
+    fetch(row + step);
+    ss = row_sum(ss, slots[set]);
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.cols)) + a.eps));
+    if (a.rstd && live && threadIdx.x == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
       const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
-      store8(static_cast<T*>(a.h) + row * a.ld_h + col, rx[i], valid[i], vec);
+      if (!KEEP_W) load8_any(w[0], a.weight, a.weight_type, col, valid[i], a.vec_w != 0);
+      const int n = live ? valid[i] : 0;
+      float y[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = h[i][k] * rstd * w[KEEP_W ? i : 0][k];
+      if (a.y) {
+        Raw8<T> ry;
+        pack8(y, ry);
+        store8(static_cast<T*>(a.y) + row * a.ld_y + col, ry, n, vec);
+      }
+      if (a.q.data) quantize_chunk(a, y, row, col, n, lane);
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fmaf(h[i][k], h[i][k], ss);
-  }
-  ss = row_sum(ss, slots);
-  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.cols)) + a.eps));
-  if (a.rstd && live && threadIdx.x == 0) a.rstd[row] = rstd;
-#pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
-    float w[8];
-    load8_any(w, a.weight, a.weight_type, col, valid[i], a.vec_w != 0);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = h[i][k] * rstd * w[k];
-    if (a.y) {
-      Raw8<T> ry;
-      pack8(w, ry);
-      store8(static_cast<T*>(a.y) + row * a.ld_y + col, ry, valid[i], vec);
-    }
-    if (a.q.data) quantize_chunk(a, w, row, col, valid[i], lane);
   }
 }
 
@@ -222,21 +235,37 @@ __global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_grad_kernel(const __
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[i][k] = 0.f;
   }
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
-  int set = 0;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * blockDim.y; base < a.rows; base += step, set ^= 1) {
-    const int64_t row = base + threadIdx.y;
-    const bool live = row < a.rows;
-    Raw8<T> rdy[NCH], rh[NCH], rr[NCH];
+  // The next row's values come while this one is reduced and written.
+  constexpr bool AHEAD = NCH <= 2;
+  Raw8<T> ndy[NCH], nh[NCH], nr[NCH];
+  float nrstd = 0.f;
+  auto fetch = [&](int64_t row) {
+    const bool in = row < a.rows;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
-      const int n = live ? valid[i] : 0;
-      load8(rdy[i], static_cast<const T*>(a.dy) + row * a.ld_dy + col, n, vec);
-      load8(rh[i], static_cast<const T*>(a.h) + row * a.ld_h + col, n, vec);
-      if (a.dres) load8(rr[i], static_cast<const T*>(a.dres) + row * a.ld_dres + col, n, vec);
+      const int n = in ? valid[i] : 0;
+      load8(ndy[i], static_cast<const T*>(a.dy) + row * a.ld_dy + col, n, vec);
+      load8(nh[i], static_cast<const T*>(a.h) + row * a.ld_h + col, n, vec);
+      if (a.dres) load8(nr[i], static_cast<const T*>(a.dres) + row * a.ld_dres + col, n, vec);
     }
-    const float rstd = live ? a.rstd[row] : 0.f;
+    nrstd = in ? a.rstd[row] : 0.f;
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+  int set = 0;
+  if (AHEAD) fetch(static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y);
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * blockDim.y; base < a.rows; base += step, set ^= 1) {
+    const int64_t row = base + threadIdx.y;
+    const bool live = row < a.rows;
+    if (!AHEAD) fetch(row);
+    Raw8<T> rdy[NCH], rh[NCH], rr[NCH];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      rdy[i] = ndy[i];
+      rh[i] = nh[i];
+      rr[i] = nr[i];
+    }
+    const float rstd = nrstd;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
@@ -255,6 +284,7 @@ __global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_grad_kernel(const __
         sum = fmaf(p, w[wi][k], sum);
       }
     }
+    if (AHEAD) fetch(row + step);
     const float mean = row_sum(sum, slots[set]) * inv_cols;
     if (!live) continue;
 #pragma unroll
@@ -403,8 +433,17 @@ RowShape row_shape(int64_t cols) {
   return s;
 }
 
+// Blocks for `rows` rows, each looping over its own: what fits on the device at `per_sm` threads per SM.
+constexpr int kForwardThreads = 1024, kBackwardThreads = 512;
+int64_t row_blocks(int64_t rows, const RowShape& s, int sm_count, int per_sm) {
+  const int64_t want = (rows + s.rows - 1) / s.rows;
+  const int at_once = per_sm / (s.threads * s.rows);
+  const int64_t most = static_cast<int64_t>(sm_count) * (at_once > 1 ? at_once : 1);
+  return want < most ? want : most;
+}
+
 template <typename T>
-cudaError_t forward_type(const NormArgs& a, cudaStream_t stream, const void** kernel, gp_plan* plan) {
+cudaError_t forward_type(const NormArgs& a, int sm_count, cudaStream_t stream, const void** kernel, gp_plan* plan) {
   if (a.cols > kRowsMaxCols) {
     auto k = rmsnorm_long_kernel<T>;
     *kernel = reinterpret_cast<const void*>(k);
@@ -416,15 +455,8 @@ cudaError_t forward_type(const NormArgs& a, cudaStream_t stream, const void** ke
   auto k = s.chunks == 1 ? rmsnorm_kernel<T, 1> : (s.chunks == 2 ? rmsnorm_kernel<T, 2> : rmsnorm_kernel<T, 4>);
   *kernel = reinterpret_cast<const void*>(k);
   plan->threads = s.threads * s.rows;
-  plan->grid = static_cast<int32_t>((a.rows + s.rows - 1) / s.rows);
+  plan->grid = static_cast<int32_t>(row_blocks(a.rows, s, sm_count, kForwardThreads));
   return launch_dependent(k, dim3(static_cast<unsigned>(plan->grid)), dim3(s.threads, s.rows), 0, stream, a);
-}
-
-// Blocks of the backward kernel: two per SM are enough to keep its loads in flight.
-int64_t grad_blocks(int64_t rows, const RowShape& s, int sm_count) {
-  const int64_t want = (rows + s.rows - 1) / s.rows;
-  const int64_t most = static_cast<int64_t>(sm_count) * (s.threads * s.rows > 512 ? 1 : 2);
-  return want < most ? want : most;
 }
 
 template <typename T>
@@ -449,25 +481,25 @@ cudaError_t backward_type(const NormGradArgs& a, int sm_count, cudaStream_t stre
                          : (s.chunks == 2 ? rmsnorm_grad_kernel<T, 2> : rmsnorm_grad_kernel<T, 4>);
   *kernel = reinterpret_cast<const void*>(k);
   plan->threads = s.threads * s.rows;
-  plan->grid = static_cast<int32_t>(grad_blocks(a.rows, s, sm_count));
+  plan->grid = static_cast<int32_t>(row_blocks(a.rows, s, sm_count, kBackwardThreads));
   return launch_dependent(k, dim3(static_cast<unsigned>(plan->grid)), dim3(s.threads, s.rows), 0, stream, a);
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_rmsnorm(const NormArgs& a, cudaStream_t stream, const void** kernel, gp_plan* plan) {
+cudaError_t launch_fp8_rmsnorm(const NormArgs& a, int sm_count, cudaStream_t stream, const void** kernel, gp_plan* plan) {
   plan->kernel = "fp8_rmsnorm";
   switch (a.type) {
-    case GP_REAL_F16: return forward_type<__half>(a, stream, kernel, plan);
-    case GP_REAL_BF16: return forward_type<__nv_bfloat16>(a, stream, kernel, plan);
-    default: return forward_type<float>(a, stream, kernel, plan);
+    case GP_REAL_F16: return forward_type<__half>(a, sm_count, stream, kernel, plan);
+    case GP_REAL_BF16: return forward_type<__nv_bfloat16>(a, sm_count, stream, kernel, plan);
+    default: return forward_type<float>(a, sm_count, stream, kernel, plan);
   }
 }
 
 int64_t fp8_rmsnorm_backward_parts(int64_t rows, int64_t cols, int sm_count) {
   if (cols > kRowsMaxCols) return rows < kLongParts ? rows : kLongParts;
   const RowShape s = row_shape(cols);
-  return grad_blocks(rows, s, sm_count) * s.rows;
+  return row_blocks(rows, s, sm_count, kBackwardThreads) * s.rows;
 }
 
 cudaError_t launch_fp8_rmsnorm_backward(const NormGradArgs& a, float* dw, int sm_count, cudaStream_t stream,

@@ -32,32 +32,39 @@ struct QuantArgs {
 };
 
 // Codes of the thread's eight rows, 8 at a time along each row.
-template <bool E5M2>
-__device__ __forceinline__ void write_rows(const float (&v)[8][8], const float (&inv)[8], const QuantArgs& a,
+template <bool E5M2, typename T>
+__device__ __forceinline__ void write_rows(const Raw8<T> (&v)[8], const float (&inv)[8], const QuantArgs& a,
                                            int64_t r, int64_t c, int rows_in, int cols_in) {
+  if (cols_in <= 0) return;
   uint8_t* out = static_cast<uint8_t*>(a.q.data) + r * a.q.ld + c;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i >= rows_in || cols_in <= 0) break;
+  for (int i = 0; i < 8; ++i, out += a.q.ld) {
+    if (i >= rows_in) break;
     const float f = inv[i];
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = value_of(v[i], k) * f;
     uint2 w;
-    w.x = fp8x4<E5M2>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f);
-    w.y = fp8x4<E5M2>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f);
-    store_codes8(out + i * a.q.ld, w, cols_in);
+    w.x = fp8x4<E5M2>(x[0], x[1], x[2], x[3]);
+    w.y = fp8x4<E5M2>(x[4], x[5], x[6], x[7]);
+    store_codes8(out, w, cols_in);
   }
 }
 
 // The transposed tile in shared memory: 128 rows (x's columns) of 16 words of
 // 8 bytes; word w of row 8 k + j lies at w ^ k, so that the 16 threads of half
 // a warp (k = 0..15, one w) and the 8 readers of a row touch all banks once.
-template <bool E5M2>
-__device__ __forceinline__ void stage_columns(const float (&v)[8][8], const float* inv_col, uint2* tile, int rb, int cc) {
+template <bool E5M2, typename T>
+__device__ __forceinline__ void stage_columns(const Raw8<T> (&v)[8], const float* inv_col, uint2* tile, int rb, int cc) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float f = inv_col[cc * 8 + j];
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = value_of(v[i], j) * f;
     uint2 w;
-    w.x = fp8x4<E5M2>(v[0][j] * f, v[1][j] * f, v[2][j] * f, v[3][j] * f);
-    w.y = fp8x4<E5M2>(v[4][j] * f, v[5][j] * f, v[6][j] * f, v[7][j] * f);
+    w.x = fp8x4<E5M2>(x[0], x[1], x[2], x[3]);
+    w.y = fp8x4<E5M2>(x[4], x[5], x[6], x[7]);
     tile[(cc * 8 + j) * 16 + (rb ^ cc)] = w;
   }
 }
@@ -78,21 +85,26 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
   const int rows_in = static_cast<int>(a.rows - r < 0 ? 0 : (a.rows - r > 8 ? 8 : a.rows - r));
   const int cols_in = static_cast<int>(a.cols - c < 0 ? 0 : (a.cols - c > 8 ? 8 : a.cols - c));
 
-  Raw8<T> raw[8];
+  // The values stay as they came (16-bit ones two to a register), so that four
+  // blocks of 16-bit tiles fit on an SM and its loads overlap their work.
+  Raw8<T> v[8];
   const T* x = static_cast<const T*>(a.x) + r * a.ldx + c;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load8(raw[i], x + i * a.ldx, i < rows_in ? cols_in : 0, a.vec != 0);
-  float v[8][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) unpack8(raw[i], v[i]);
+  for (int i = 0; i < 8; ++i) load8(v[i], x + i * a.ldx, i < rows_in ? cols_in : 0, a.vec != 0);
+  constexpr int WORDS = static_cast<int>(sizeof(T)) * 2;       // 32-bit words of eight values
+  constexpr int PER = 8 / WORDS;                                // values per word
+  auto word = [&](int i, int k) { return raw_abs<T>(reinterpret_cast<const uint32_t*>(&v[i])[k]); };
+  auto widest = [&](uint32_t m) {                               // the larger of a word's magnitudes, as FP32 bits
+    return PER == 1 ? m : max(raw_to_bits<T>(m, 0), raw_to_bits<T>(m, 1));
+  };
 
   if (BLOCKS) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
-    m = __reduce_max_sync(0xffffffffu, m);
+      for (int k = 0; k < WORDS; ++k) m = raw_max<T>(m, word(i, k));
+    m = __reduce_max_sync(0xffffffffu, widest(m));
     if (lane == 0) part[warp] = m;
     __syncthreads();
     m = part[0];
@@ -113,33 +125,41 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
     if (!a.qt.data) return;
     if (t < kTile) inv_col[t] = g.inv;
   } else {
+    if (a.qt.data) {
+      // a warp's rows of each column: two half warps of eight rows each
+#pragma unroll
+      for (int k = 0; k < WORDS; ++k) {
+        uint32_t m = word(0, k);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = raw_max<T>(m, word(i, k));
+        m = raw_max<T>(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (lane < 16) {
+#pragma unroll
+          for (int u = 0; u < PER; ++u) part[warp * kTile + cc * 8 + k * PER + u] = raw_to_bits<T>(m, u);
+        }
+      }
+    }
     if (a.q.data) {
       float inv[8];
-      float mine = 0.f;
+      // Thread cc of a row's 16 works out the scale of row cc mod 8 and the others take it from there.
+      uint32_t most = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        uint32_t m = 0;
+        uint32_t m = word(i, 0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
+        for (int k = 1; k < WORDS; ++k) m = raw_max<T>(m, word(i, k));
 #pragma unroll
-        for (int d = 1; d < 16; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const GroupScale g = group_scale(m, a.fmax);
-        inv[i] = g.inv;
-        if (cc == i) mine = g.scale;
+        for (int d = 1; d < 16; d *= 2) m = raw_max<T>(m, __shfl_xor_sync(0xffffffffu, m, d));
+        if ((cc & 7) == i) most = m;
       }
-      if (cc < rows_in) a.q.scales[(r + cc) * a.q.stride_row + tc * a.q.stride_col] = mine;   // rows_in <= 8
+      const GroupScale g = group_scale(widest(most), a.fmax);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) inv[i] = __shfl_sync(0xffffffffu, g.inv, (lane & 16) + i);
+      if (cc < rows_in) a.q.scales[(r + cc) * a.q.stride_row + tc * a.q.stride_col] = g.scale;   // (rows_in <= 8)
       if (a.e5m2) write_rows<true>(v, inv, a, r, c, rows_in, cols_in);
       else write_rows<false>(v, inv, a, r, c, rows_in, cols_in);
     }
     if (!a.qt.data) return;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i][j]));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
-      if (lane < 16) part[warp * kTile + cc * 8 + j] = m;
-    }
     __syncthreads();
     if (t < kTile) {
       uint32_t m = part[t];
