@@ -163,6 +163,29 @@ def lib():
     return L
 
 
+class _Fp8Calls:
+    """The 8-bit entry points taking their gp_fp8_matrix arguments as packed bytes."""
+
+    def __init__(self):
+        L, vp = lib(), ctypes.c_void_p
+        for name, symbol, mats in (("gemm", "gemm_fp8", (0, 1)), ("quantize", "fp8_quantize", (5, 6)),
+                                   ("rmsnorm", "fp8_rmsnorm", (15,)), ("backward", "fp8_rmsnorm_backward", ())):
+            f = L[symbol]              # a function object of its own
+            f.restype = ctypes.c_int
+            f.argtypes = [vp if i in mats else t for i, t in enumerate(getattr(L, symbol).argtypes)]
+            setattr(self, name, f)
+
+
+_fp8_calls = None
+
+
+def fp8_calls():
+    global _fp8_calls
+    if _fp8_calls is None:
+        _fp8_calls = _Fp8Calls()
+    return _fp8_calls
+
+
 def _ptr(x):
     if x is None:
         return None

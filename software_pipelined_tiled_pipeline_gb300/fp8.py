@@ -11,18 +11,27 @@ Everything runs on the current stream of the tensors' device (or ``stream``);
 this module allocates outputs and passes pointers, and a failing call raises
 ``GemmError``.
 """
-import ctypes
+import struct
 
 import torch
 
 from . import _binding
-from ._binding import GP_OK, FP8_FORMATS, GemmError, GpFp8Matrix, GpFp8Options, GpPlan, lib
+from ._binding import GP_OK, FP8_FORMATS, GemmError, GpFp8Options, GpPlan, fp8_calls, lib
 
 GROUP = 128
 
 _FORMAT_OF = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 _FP8_DTYPE = (torch.float8_e4m3fn, torch.float8_e5m2)
 _REAL_OF = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_F32 = torch.float32
+
+# The calls below are short (a few microseconds on the GPU at the smallest
+# sizes), so this module counts its own steps: one allocation per output,
+# descriptors packed as bytes, no views.
+_pack = struct.Struct("PPqqqii").pack       # gp_fp8_matrix
+_empty = torch.empty_strided
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _check(rc, where):
@@ -35,21 +44,19 @@ class _On:
     __slots__ = ("device", "stream", "before", "other")
 
     def __init__(self, device, stream):
-        self.device, self.stream, self.before, self.other = device.index, stream, None, None
+        self.device, self.stream, self.before, self.other = device, stream, None, None
 
     def __enter__(self):
         now = torch.cuda.current_device()
         if now != self.device:
             self.before = now
             torch.cuda.set_device(self.device)
-        if self.stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.device)
         s = self.stream
-        if not isinstance(s, torch.cuda.Stream):
-            s = torch.cuda.ExternalStream(s, self.device) if s else torch.cuda.default_stream(self.device)
-        self.other = torch.cuda.stream(s)
-        self.other.__enter__()
-        return s.cuda_stream
+        if s is not None:
+            if not isinstance(s, torch.cuda.Stream):
+                s = torch.cuda.ExternalStream(s, self.device) if s else torch.cuda.default_stream(self.device)
+            self.other = torch.cuda.stream(s)
+            self.other.__enter__()
 
     def __exit__(self, *exc):
         if self.other is not None:
@@ -59,17 +66,26 @@ class _On:
         return False
 
 
+def _elsewhere(x, name, stream):
+    """Whether the call has to change the current device or stream first."""
+    device = x.get_device()
+    if device < 0:
+        raise ValueError("%s must be on a CUDA device" % name)
+    return stream is not None or device != _device()
+
+
 def _matrix(x, name):
     """Shape of a 2-D CUDA tensor whose rows are contiguous, and its row stride."""
-    if x.dim() != 2:
-        raise ValueError("%s must have two dimensions, got %d" % (name, x.dim()))
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("%s must have two dimensions, got %d" % (name, len(shape)))
     if not x.is_cuda:
         raise ValueError("%s must be on a CUDA device" % name)
-    rows, cols = x.shape
+    rows, cols = shape
     ld, inner = x.stride()
     if inner != 1 and cols > 1:
         raise ValueError("%s must have contiguous rows (stride 1 along the last dimension)" % name)
-    return rows, cols, (ld if rows > 1 else max(ld, cols))
+    return rows, cols, (ld if rows > 1 or ld > cols else cols)
 
 
 def _real(x, name):
@@ -80,7 +96,7 @@ def _real(x, name):
 
 
 def _same(x, like, name):
-    if x.shape != like.shape or x.dtype != like.dtype or x.device != like.device:
+    if x.shape != like.shape or x.dtype != like.dtype or x.get_device() != like.get_device():
         raise ValueError("%s must have the shape, type and device of the other operand: got %s %s %s, want %s %s %s" % (
             name, tuple(x.shape), x.dtype, x.device, tuple(like.shape), like.dtype, like.device))
 
@@ -92,27 +108,24 @@ def _fp8(data, scales, name):
         raise ValueError("%s must be float8_e4m3fn or float8_e5m2, got %s" % (name, data.dtype))
     rows, cols, ld = _matrix(data, name)
     if rows <= 1:
-        ld = -(-ld // 16) * 16         # the stride of a single row is never used
-    if scales.dtype != torch.float32 or scales.dim() != 2 or scales.device != data.device:
+        ld = (ld + 15) // 16 * 16      # the stride of a single row is never used
+    if scales.dtype is not _F32 or len(scales.shape) != 2 or scales.get_device() != data.get_device():
         raise ValueError("the scales of %s must be a float32 matrix on its device" % name)
     groups, blocks = scales.shape
-    if blocks != -(-cols // GROUP) or groups not in (rows, -(-rows // GROUP)):
+    if blocks != (cols + 127) // 128 or (groups != rows and groups != (rows + 127) // 128):
         raise ValueError("the scales of %s have shape %s: want (%d or %d, %d)" % (
-            name, (groups, blocks), rows, -(-rows // GROUP), -(-cols // GROUP)))
+            name, (groups, blocks), rows, (rows + 127) // 128, (cols + 127) // 128))
     sr, sc = scales.stride()
-    return rows, cols, GpFp8Matrix(data.data_ptr(), scales.data_ptr(), ld, sr, sc, fmt, 1 if groups == rows else GROUP)
+    return rows, cols, _pack(data.data_ptr(), scales.data_ptr(), ld, sr, sc, fmt, 1 if groups == rows else GROUP)
 
 
 def _new_fp8(rows, cols, fmt, group, device):
     """An 8-bit matrix to be written: rows 16 bytes aligned, the scales of one group of columns side by side."""
-    ld = -(-cols // 16) * 16
-    data = torch.empty((rows, ld), dtype=_FP8_DTYPE[fmt], device=device)
-    if ld != cols:
-        data = data[:, :cols]
-    groups = rows if group == 1 else -(-rows // GROUP)
-    blocks = -(-cols // GROUP)
-    scales = torch.empty((blocks, groups), dtype=torch.float32, device=device).t()
-    return data, scales, GpFp8Matrix(data.data_ptr(), scales.data_ptr(), ld, 1, groups, fmt, group)
+    ld = (cols + 15) // 16 * 16
+    data = _empty((rows, cols), (ld, 1), dtype=_FP8_DTYPE[fmt], device=device)
+    groups = rows if group == 1 else (rows + 127) // 128
+    scales = _empty((groups, (cols + 127) // 128), (1, groups or 1), dtype=_F32, device=device)
+    return data, scales, _pack(data.data_ptr(), scales.data_ptr(), ld, 1, groups, fmt, group)
 
 
 def quantize_fp8(x, scales="rows", *, format="e4m3", transpose=False, stream=None):
@@ -126,23 +139,29 @@ def quantize_fp8(x, scales="rows", *, format="e4m3", transpose=False, stream=Non
 
     Returns (data, scales), or (data, scales, data_t, scales_t).
     """
+    if _elsewhere(x, "x", stream):
+        with _On(x.get_device(), stream):
+            return quantize_fp8(x, scales, format=format, transpose=transpose)
     rows, cols, ld = _matrix(x, "x")
     real = _real(x, "x")
-    if scales not in ("rows", "blocks"):
+    if scales == "rows":
+        group = 1
+    elif scales == "blocks":
+        group = GROUP
+    else:
         raise ValueError("unknown scales %r" % (scales,))
     if transpose not in (False, True, "only"):
         raise ValueError("unknown transpose %r" % (transpose,))
     fmt = _binding._enum(format, FP8_FORMATS, "format")
-    group = 1 if scales == "rows" else GROUP
+    device = x.device
     out, q, qt = (), None, None
-    with _On(x.device, stream) as st:
-        if transpose != "only":
-            data, s, q = _new_fp8(rows, cols, fmt, group, x.device)
-            out = (data, s)
-        if transpose:
-            data, s, qt = _new_fp8(cols, rows, fmt, group, x.device)
-            out += (data, s)
-        _check(lib().fp8_quantize(x.data_ptr(), ld, rows, cols, real, q, qt, st), "fp8_quantize")
+    if transpose != "only":
+        data, s, q = _new_fp8(rows, cols, fmt, group, device)
+        out = (data, s)
+    if transpose:
+        data, s, qt = _new_fp8(cols, rows, fmt, group, device)
+        out += (data, s)
+    _check(fp8_calls().quantize(x.data_ptr(), ld, rows, cols, real, q, qt, _raw_stream(x.get_device())), "fp8_quantize")
     return out
 
 
@@ -165,30 +184,34 @@ def gemm_fp8(A, A_scales, B, B_scales, *, out_dtype=torch.bfloat16, addend=None,
     to write (M x N, rows contiguous).  ``bn``, ``no_split``, ``timeout_ns``,
     ``inject_lost_load``: see gp_fp8_options.
     """
+    if _elsewhere(A, "A", stream):
+        with _On(A.get_device(), stream):
+            return gemm_fp8(A, A_scales, B, B_scales, out_dtype=out_dtype, addend=addend, out=out, bn=bn,
+                            no_split=no_split, timeout_ns=timeout_ns, inject_lost_load=inject_lost_load)
     M, K, a = _fp8(A, A_scales, "A")
     N, kb, b = _fp8(B, B_scales, "B")
     if kb != K:
         raise ValueError("A has %d columns and B %d" % (K, kb))
-    if B.device != A.device:
+    if B.get_device() != A.get_device():
         raise ValueError("A is on %s and B on %s" % (A.device, B.device))
+    if out is None:
+        out = _empty((M, N), (N, 1), dtype=out_dtype, device=A.device)
+        ldc = N
+    else:
+        rows, cols, ldc = _matrix(out, "out")
+        if (rows, cols) != (M, N) or out.get_device() != A.get_device():
+            raise ValueError("out has shape %s on %s: want %s on %s" % ((rows, cols), out.device, (M, N), A.device))
+    real = _real(out, "out")
+    add_ptr, ld_add = None, 0
+    if addend is not None:
+        _same(addend, out, "addend")
+        ld_add = _matrix(addend, "addend")[2]
+        add_ptr = addend.data_ptr()
     opts = None
     if bn or no_split or timeout_ns or inject_lost_load:
         opts = GpFp8Options(int(timeout_ns), int(bn), int(no_split), int(inject_lost_load))
-    with _On(A.device, stream) as st:
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=A.device)
-            ldc = N
-        else:
-            rows, cols, ldc = _matrix(out, "out")
-            if (rows, cols) != (M, N) or out.device != A.device:
-                raise ValueError("out has shape %s on %s: want %s on %s" % ((rows, cols), out.device, (M, N), A.device))
-        real = _real(out, "out")
-        add_ptr, ld_add = None, 0
-        if addend is not None:
-            _same(addend, out, "addend")
-            ld_add = _matrix(addend, "addend")[2]
-            add_ptr = addend.data_ptr()
-        _check(lib().gemm_fp8(a, b, out.data_ptr(), ldc, add_ptr, ld_add, M, N, K, real, st, opts), "gemm_fp8")
+    _check(fp8_calls().gemm(a, b, out.data_ptr(), ldc, add_ptr, ld_add, M, N, K, real, _raw_stream(A.get_device()), opts),
+           "gemm_fp8")
     return out
 
 
@@ -209,28 +232,30 @@ def rmsnorm_fp8(x, weight, residual=None, *, eps=1e-6, format="e4m3", normed=Fal
     Returns (data, scales, h, rstd), and y rounded to x's type as a fifth with
     ``normed``.  Without a residual h is x itself.
     """
+    if _elsewhere(x, "x", stream):
+        with _On(x.get_device(), stream):
+            return rmsnorm_fp8(x, weight, residual, eps=eps, format=format, normed=normed)
     rows, cols, ld = _matrix(x, "x")
     real = _real(x, "x")
-    wtype = _weight(weight, cols, x.device)
+    wtype = _weight(weight, cols, x)
     fmt = _binding._enum(format, FP8_FORMATS, "format")
+    device = x.device
     h, res_ptr, ld_res, h_ptr, y_ptr = x, None, 0, None, None
     if residual is not None:
         _same(residual, x, "residual")
         ld_res = _matrix(residual, "residual")[2]
         res_ptr = residual.data_ptr()
-    with _On(x.device, stream) as st:
-        if residual is not None:
-            h = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-            h_ptr = h.data_ptr()
-        data, scales, q = _new_fp8(rows, cols, fmt, 1, x.device)
-        rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
-        out = (data, scales, h, rstd)
-        if normed:
-            y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-            y_ptr = y.data_ptr()
-            out += (y,)
-        _check(lib().fp8_rmsnorm(x.data_ptr(), ld, res_ptr, ld_res, weight.data_ptr(), wtype, eps, rows, cols, real,
-                                 h_ptr, cols, rstd.data_ptr(), y_ptr, cols, q, st), "fp8_rmsnorm")
+        h = _empty((rows, cols), (cols, 1), dtype=x.dtype, device=device)
+        h_ptr = h.data_ptr()
+    data, scales, q = _new_fp8(rows, cols, fmt, 1, device)
+    rstd = _empty((rows,), (1,), dtype=_F32, device=device)
+    out = (data, scales, h, rstd)
+    if normed:
+        y = _empty((rows, cols), (cols, 1), dtype=x.dtype, device=device)
+        y_ptr = y.data_ptr()
+        out += (y,)
+    _check(fp8_calls().rmsnorm(x.data_ptr(), ld, res_ptr, ld_res, weight.data_ptr(), wtype, eps, rows, cols, real, h_ptr,
+                               cols, rstd.data_ptr(), y_ptr, cols, q, _raw_stream(x.get_device())), "fp8_rmsnorm")
     return out
 
 
@@ -241,28 +266,33 @@ def rmsnorm_backward(dy, h, weight, rstd, dresidual=None, *, weight_grad=True, s
     (the gradient that reaches h past the norm) is added to it.  dweight is
     float32, or None with ``weight_grad=False``.
     """
+    if _elsewhere(dy, "dy", stream):
+        with _On(dy.get_device(), stream):
+            return rmsnorm_backward(dy, h, weight, rstd, dresidual, weight_grad=weight_grad)
     rows, cols, ld_dy = _matrix(dy, "dy")
     real = _real(dy, "dy")
     _same(h, dy, "h")
     ld_h = _matrix(h, "h")[2]
-    wtype = _weight(weight, cols, dy.device)
-    if rstd.dtype != torch.float32 or rstd.shape != (rows,) or rstd.device != dy.device or not rstd.is_contiguous():
+    wtype = _weight(weight, cols, dy)
+    if rstd.dtype is not _F32 or rstd.shape != (rows,) or rstd.get_device() != dy.get_device() or (
+            rows > 1 and rstd.stride(0) != 1):
         raise ValueError("rstd must be %d contiguous float32 values on %s" % (rows, dy.device))
     res_ptr, ld_res = None, 0
     if dresidual is not None:
         _same(dresidual, dy, "dresidual")
         ld_res = _matrix(dresidual, "dresidual")[2]
         res_ptr = dresidual.data_ptr()
-    with _On(dy.device, stream) as st:
-        dx = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device)
-        dw = torch.empty((cols,), dtype=torch.float32, device=dy.device) if weight_grad else None
-        _check(lib().fp8_rmsnorm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, res_ptr, ld_res,
-                                          weight.data_ptr(), wtype, rstd.data_ptr(), rows, cols, real, dx.data_ptr(),
-                                          cols, dw.data_ptr() if weight_grad else None, st), "fp8_rmsnorm_backward")
+    device = dy.device
+    dx = _empty((rows, cols), (cols, 1), dtype=dy.dtype, device=device)
+    dw = _empty((cols,), (1,), dtype=_F32, device=device) if weight_grad else None
+    _check(fp8_calls().backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, res_ptr, ld_res, weight.data_ptr(), wtype,
+                                rstd.data_ptr(), rows, cols, real, dx.data_ptr(), cols,
+                                dw.data_ptr() if weight_grad else None, _raw_stream(dy.get_device())),
+           "fp8_rmsnorm_backward")
     return dx, dw
 
 
-def _weight(weight, cols, device):
-    if weight.shape != (cols,) or weight.device != device or (cols > 1 and weight.stride(0) != 1):
-        raise ValueError("weight must be %d contiguous values on %s" % (cols, device))
+def _weight(weight, cols, like):
+    if weight.shape != (cols,) or weight.get_device() != like.get_device() or (cols > 1 and weight.stride(0) != 1):
+        raise ValueError("weight must be %d contiguous values on %s" % (cols, like.device))
     return _real(weight, "weight")
