@@ -107,9 +107,8 @@ struct Workspace {
   uint32_t* ov_ctrs = nullptr;   // INT8 conversion / GEMM hand-off counters: two sets of ov_kcap + 1 words
   int32_t ov_kcap = 0;
   uint32_t ov_launches = 0;
-  float* fp8 = nullptr;       // FP8 operators: partial tiles and partial sums
+  float* fp8 = nullptr;       // FP8 operators: partial sums of the norm's weight gradient
   size_t fp8_bytes = 0;
-  uint32_t* fp8_ctrs = nullptr;   // kFp8Counters counters, zero between launches
 };
 constexpr int kMaxWorkspaces = 64;
 Workspace g_ws[kMaxWorkspaces];
@@ -122,7 +121,6 @@ void free_workspace(Workspace& w) {
   if (w.conv) cudaFree(w.conv);
   if (w.ov_ctrs) cudaFree(w.ov_ctrs);
   if (w.fp8) cudaFree(w.fp8);
-  if (w.fp8_ctrs) cudaFree(w.fp8_ctrs);
   w = Workspace();
 }
 
@@ -757,20 +755,11 @@ int call_finish(int status, cudaError_t error, int site) {
   return status;
 }
 
-cudaError_t call_workspace(int device, cudaStream_t stream, size_t bytes, float** partials, uint32_t** counters) {
+cudaError_t call_workspace(int device, cudaStream_t stream, size_t bytes, float** partials) {
   std::lock_guard<std::mutex> lk(g_mu);
   Workspace* w = nullptr;
   cudaError_t e = find_workspace(device, stream, &w);
   if (e != cudaSuccess) return e;
-  if (!w->fp8_ctrs) {
-    uint32_t* p = nullptr;
-    if ((e = cudaMalloc(&p, kFp8Counters * sizeof(uint32_t))) != cudaSuccess) return e;
-    if ((e = cudaMemsetAsync(p, 0, kFp8Counters * sizeof(uint32_t), stream)) != cudaSuccess) {
-      cudaFree(p);
-      return e;
-    }
-    w->fp8_ctrs = p;
-  }
   if (w->fp8_bytes < bytes) {
     if (w->fp8) {
       if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return e;   // nothing uses the old buffer now
@@ -782,7 +771,6 @@ cudaError_t call_workspace(int device, cudaStream_t stream, size_t bytes, float*
     w->fp8_bytes = bytes;
   }
   *partials = w->fp8;
-  *counters = w->fp8_ctrs;
   return cudaSuccess;
 }
 

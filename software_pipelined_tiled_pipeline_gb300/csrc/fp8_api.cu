@@ -101,7 +101,7 @@ int gemm_fp8(const gp_fp8_matrix* A, const gp_fp8_matrix* B, void* C, int64_t ld
   Fp8GemmArgs a = {};
   rc = fp8_plan_impl(M, N, K, A->group, B->group, info.sm_count, opts, &a.plan);
   if (rc != GP_OK) return call_finish(rc);
-  e = fp8_fit_pairs(&a.plan, opts && opts->no_split);
+  e = fp8_fit_pairs(&a.plan);
   if (e != cudaSuccess) return call_finish(GP_ERR_CUDA, e, GP_SITE_CAPACITY);
   a.A = *A;
   a.B = *B;
@@ -116,10 +116,6 @@ int gemm_fp8(const gp_fp8_matrix* A, const gp_fp8_matrix* B, void* C, int64_t ld
   a.stream = st;
   a.ctl = info.ctl;
   a.ctl.inject_lost_load = opts ? opts->inject_lost_load : 0;
-  if (a.plan.workspace_bytes > 0) {
-    e = call_workspace(info.device, st, static_cast<size_t>(a.plan.workspace_bytes), &a.partials, &a.counters);
-    if (e != cudaSuccess) return call_finish(GP_ERR_CUDA, e, GP_SITE_WORKSPACE);
-  }
   const void* kernel = nullptr;
   e = launch_fp8_gemm(a, &kernel);
   call_launched(a.plan, kernel);
@@ -235,9 +231,8 @@ int fp8_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t l
   a.vec_w = aligned(weight, 16);
   gp_plan plan = {};
   if (dw && rows > 0) {
-    uint32_t* counters;
     plan.workspace_bytes = fp8_rmsnorm_backward_parts(rows, cols, info.sm_count) * cols * 4;
-    e = call_workspace(info.device, st, static_cast<size_t>(plan.workspace_bytes), &a.partials, &counters);
+    e = call_workspace(info.device, st, static_cast<size_t>(plan.workspace_bytes), &a.partials);
     if (e != cudaSuccess) return call_finish(GP_ERR_CUDA, e, GP_SITE_WORKSPACE);
   }
   const void* kernel = nullptr;

@@ -78,14 +78,16 @@ struct Fp8GemmArgs {
   gp_plan plan;
   cudaStream_t stream;
   KernelCtl ctl;
-  float* partials;
-  uint32_t* counters;
 };
 int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int sms, const gp_fp8_options* opts,
                   gp_plan* p);
-// Pairs must sit on one TPC each: where fewer fit at once than the plan counted on, plan for those.
-cudaError_t fp8_fit_pairs(gp_plan* plan, bool no_split);
+// Pairs must sit on one TPC each: where fewer fit at once than the plan counted on, launch those.
+cudaError_t fp8_fit_pairs(gp_plan* plan);
 cudaError_t launch_fp8_gemm(Fp8GemmArgs& a, const void** kernel);
+// The product with at most kFp8GemvRows rows on one side, without tiles.
+constexpr int kFp8GemvRows = 4;
+void fp8_gemv_plan(int64_t n, gp_plan* p);
+cudaError_t launch_fp8_gemv(Fp8GemmArgs& a, const void** kernel);
 // C = addend, or zeros (K == 0).
 cudaError_t launch_fp8_fill(void* C, int64_t ldc, const void* addend, int64_t ld_add, int64_t M, int64_t N,
                             int out_type, cudaStream_t stream);
@@ -106,9 +108,7 @@ cudaError_t call_begin(uint64_t timeout_ns, CallInfo* info);
 void call_launched(const gp_plan& plan, const void* kernel);
 // Close the record; returns `status`.  A CUDA error's site defaults to the launch, or what a helper noted.
 int call_finish(int status, cudaError_t error = cudaSuccess, int site = 0);
-// FP32 workspace of (device, stream) of at least `bytes`, and kFp8Counters counters that are zero
-// between launches (a kernel that counts on one leaves it at zero).
-constexpr int kFp8Counters = 4096;
-cudaError_t call_workspace(int device, cudaStream_t stream, size_t bytes, float** partials, uint32_t** counters);
+// FP32 workspace of (device, stream) of at least `bytes`.
+cudaError_t call_workspace(int device, cudaStream_t stream, size_t bytes, float** partials);
 
 }  // namespace gp

@@ -43,7 +43,6 @@ struct Fp8Barriers {
   uint64_t drain;
   uint32_t tmem_base;
   CtaCtl ctl;
-  int32_t last;              // this CTA completed the last segment of a split tile
 };
 constexpr int kFp8BarrierBytes = 256;
 static_assert(sizeof(Fp8Barriers) <= kFp8BarrierBytes, "barrier region too small");
@@ -98,10 +97,7 @@ struct Fp8Params {
   int32_t vec16;             // groups of 8 16-bit outputs are aligned to 16 bytes
   uint32_t idesc;
   int32_t raster_gp;         // P blocks per raster group
-  int32_t dp_tiles;          // tiles computed whole (raster order first)
-  int32_t sk_tiles;          // tiles after those whose K-loops are dealt out evenly to all workers
-  float* partials;           // split tiles: two 128 x BN FP32 slots per CTA
-  uint32_t* counters;        // ... one counter per tile and CTA rank, zero between launches
+  int32_t k_log;             // log2 of the CTAs (one cluster) that share a tile's K blocks; one tile per cluster then
   KernelCtl ctl;
 };
 
@@ -149,6 +145,11 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[32]) { tmem_ld
 // with every K block.)
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Store 4 bytes into another CTA's shared memory (cluster-window address).
+__device__ __forceinline__ void st_cluster_f1(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
 // True in one lane of a converged warp, always the same one.
@@ -231,70 +232,14 @@ __device__ __forceinline__ void tile_blocks(int tile, int p_blocks, int q_blocks
   qb = in / n;
 }
 
-// The work of one worker (a CTA or a pair), walked alike by all its warps: a
-// whole tile, then its contiguous share of the split tiles' K blocks (cut at
-// tile boundaries), then its other whole tiles.
+// The work of one worker (a CTA, a pair, or a cluster that splits the K loop),
+// walked alike by all its warps: every `step`-th tile, K blocks k0 .. k1 - 1.
 struct Items {
-  int dp_tiles, next_dp, step, kt;
-  int64_t u, u_end;
-  bool first;
-
-  __device__ __forceinline__ static int64_t start(int w, int64_t units, int workers) { return w * units / workers; }
-  // the worker whose share holds unit u
-  __device__ __forceinline__ static int owner(int64_t u, int64_t units, int workers) {
-    return static_cast<int>(((u + 1) * workers - 1) / units);
+  int tile, tiles, step, k0, k1;
+  __device__ __forceinline__ bool next() {
+    tile += step;
+    return tile < tiles;
   }
-  __device__ __forceinline__ Items(const Fp8Params& g, int kt_, int worker, int workers)
-      : dp_tiles(g.dp_tiles), next_dp(worker), step(workers), kt(kt_), first(true) {
-    const int64_t units = static_cast<int64_t>(g.sk_tiles) * kt;
-    u = start(worker, units, workers);
-    u_end = start(worker + 1, units, workers);
-  }
-  __device__ __forceinline__ bool whole(int& tile, int& k0, int& k1) {
-    if (next_dp >= dp_tiles) return false;
-    tile = next_dp;
-    k0 = 0;
-    k1 = kt;
-    next_dp += step;
-    return true;
-  }
-  __device__ __forceinline__ bool next(int& tile, int& k0, int& k1) {
-    if (first) {
-      first = false;
-      if (whole(tile, k0, k1)) return true;
-    }
-    if (u < u_end) {
-      const int t = static_cast<int>(u / kt);
-      k0 = static_cast<int>(u - static_cast<int64_t>(t) * kt);
-      const int64_t left = u_end - u;
-      k1 = left < kt - k0 ? k0 + static_cast<int>(left) : kt;
-      tile = dp_tiles + t;
-      u += k1 - k0;
-      return true;
-    }
-    return whole(tile, k0, k1);
-  }
-};
-
-// Where the partial sums of a split tile lie.  A worker's share touches at most
-// two tiles in part: slot 0 holds the one that its share starts in, slot 1 the
-// one that it ends in.  A CTA's slot is 128 x BN FP32, 16-byte column groups
-// outermost, so that a warp's 32 rows are 512 contiguous bytes.
-struct Partial {
-  int64_t units, begin;      // K blocks of all split tiles; the tile's first
-  int workers, ctas, rank, w_first, w_last;
-
-  __device__ __forceinline__ Partial(const Fp8Params& g, int tile, int kt, int workers_, int ctas_, int rank_)
-      : workers(workers_), ctas(ctas_), rank(rank_) {
-    units = static_cast<int64_t>(g.sk_tiles) * kt;
-    begin = static_cast<int64_t>(tile - g.dp_tiles) * kt;
-    w_first = Items::owner(begin, units, workers);
-    w_last = Items::owner(begin + kt - 1, units, workers);
-  }
-  __device__ __forceinline__ int64_t slot(int w) const {
-    return (2 * w + (Items::start(w, units, workers) >= begin ? 0 : 1)) * static_cast<int64_t>(ctas) + rank;
-  }
-  __device__ __forceinline__ int segments() const { return w_last - w_first + 1; }
 };
 
 __device__ __forceinline__ void add_warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kAddThreads) : "memory"); }
@@ -347,16 +292,29 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
   T* const c = static_cast<T*>(g.c);
   const T* const add = static_cast<const T*>(g.addend);
   if (g.swapped) {
-    // the lanes' rows are C's columns: each of C's rows gets 32 neighbouring outputs
+    // The lanes' rows are C's columns: each of C's rows gets 32 neighbouring
+    // outputs.  Sums go through shared memory (each lane reads back its own) so
+    // that the loop over them is short code: a cold instruction costs more than
+    // the round trip.
+    constexpr int CW = HALF < 32 ? HALF : 32;
     const int64_t col = p0 + lane;
-    if (col >= g.p.rows) return;
-    const int rows = static_cast<int>(g.q.rows - q0 < HALF ? g.q.rows - q0 : HALF);
+    float* mine = reinterpret_cast<float*>(stage) + lane;
 #pragma unroll
-    for (int i = 0; i < HALF; ++i) {
-      if (i < rows) {
-        float v = acc[i];
-        if (add) v += widen(add[(q0 + i) * g.ld_add + col]);
-        c[(q0 + i) * g.ldc + col] = narrow<T>(v);
+    for (int j = 0; j < HALF / CW; ++j) {
+#pragma unroll
+      for (int i = 0; i < CW; ++i) mine[i * 32] = acc[j * CW + i];
+      const int64_t first = q0 + j * CW, left = g.q.rows - first;
+      const int rows = col < g.p.rows ? static_cast<int>(left < CW ? left : CW) : 0;
+      T* o = c + first * g.ldc + col;
+      const T* f = add ? add + first * g.ld_add + col : nullptr;
+#pragma unroll 1
+      for (int i = 0; i < rows; ++i, o += g.ldc) {
+        float v = mine[i * 32];
+        if (f) {
+          v += widen(*f);
+          f += g.ld_add;
+        }
+        *o = narrow<T>(v);
       }
     }
     return;
@@ -408,7 +366,21 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
                    "f"(acc[j * CW + 4 * i + 3])
                    : "memory");
     __syncwarp();
-    const int64_t left = g.q.rows - col - j * CW;
+    if (!full) {
+      const int64_t left = g.q.rows - col - j * CW;
+#pragma unroll 1
+      for (int i = 0; i < PER; ++i) {
+        float4 v;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(base + sw128_offset(i * (32 / PER) + lane / PER, lane % PER))
+                     : "memory");
+        T* o = out + i * (32 / PER) * g.ldc + j * CW;
+        const T* f = from ? from + i * (32 / PER) * g.ld_add + j * CW : nullptr;
+        if (row + i * (32 / PER) < g.p.rows && left > 0) store4<T, false>(o, f, v, g.vec != 0, left);
+      }
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       float4 v;
@@ -418,11 +390,28 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
                    : "memory");
       T* o = out + i * (32 / PER) * g.ldc + j * CW;
       const T* f = from ? from + i * (32 / PER) * g.ld_add + j * CW : nullptr;
-      if (full)
-        store4<T, true>(o, f, v, true, 4);
-      else if (row + i * (32 / PER) < g.p.rows && left > 0)
-        store4<T, false>(o, f, v, g.vec != 0, left);
+      store4<T, true>(o, f, v, true, 4);
     }
+  }
+}
+
+// The K loop split over a cluster: every CTA hands each of the others the
+// columns that are theirs, and writes its own.  Buffer of a CTA: for each
+// source, its BN / CTAs columns of 128 rows.
+template <typename T>
+__device__ __forceinline__ void write_shared(const Fp8Params& g, const float* buf, int t, int ctas, int per, int64_t p0,
+                                             int64_t q0) {
+  T* const c = static_cast<T*>(g.c);
+  const T* const add = static_cast<const T*>(g.addend);
+#pragma unroll 1
+  for (int i = t; i < per * 128; i += kAddThreads) {
+    float v = 0.f;
+    for (int s = 0; s < ctas; ++s) v += buf[s * per * 128 + i];      // in K order
+    const int64_t p = p0 + (i & 127), q = q0 + (i >> 7);
+    if (p >= g.p.rows || q >= g.q.rows) continue;
+    const int64_t m = g.swapped ? q : p, n = g.swapped ? p : q;
+    if (add) v += widen(add[m * g.ld_add + n]);
+    c[m * g.ldc + n] = narrow<T>(v);
   }
 }
 
@@ -440,13 +429,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // (uniform for the compiler too)
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
-  const int worker = static_cast<int>(blockIdx.x) / Sh::CTAS;
-  const int workers = static_cast<int>(gridDim.x) / Sh::CTAS;
+  const int k_ctas = PAIR ? 1 : 1 << g.k_log;                 // CTAs that share a tile's K blocks
+  const uint32_t in_cluster = PAIR || k_ctas > 1 ? cluster_ctarank() : 0u;
+  const uint32_t rank = PAIR ? in_cluster : 0u;               // in the pair
+  const int per_worker = Sh::CTAS * k_ctas;
+  const int worker = static_cast<int>(blockIdx.x) / per_worker;
+  const int workers = static_cast<int>(gridDim.x) / per_worker;
   const int p_blocks = (g.p.rows + Sh::TILE_P - 1) / Sh::TILE_P;
   const int q_blocks = (g.q.rows + BN - 1) / BN;
-  const int last_tile = p_blocks * q_blocks - 1;
   const int kt = (g.K + kBK - 1) / kBK;
+  Items items{worker - workers, p_blocks * q_blocks, workers, 0, kt};
+  if (!PAIR && k_ctas > 1) {
+    items.k0 = static_cast<int>((static_cast<int64_t>(kt) * in_cluster) >> g.k_log);
+    items.k1 = static_cast<int>((static_cast<int64_t>(kt) * (in_cluster + 1)) >> g.k_log);
+  }
+  const int k0 = items.k0, k1 = items.k1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Sh::STAGES; ++s) {
@@ -478,20 +475,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();
-  Items items(g, kt, worker, workers);
-  int tile, k0, k1;
   // While the work before this kernel finishes, its first boxes come into L2:
   // a prefetch writes nothing, and L2 stays coherent with what is still written.
-  if (warp == 0 && lane == 0) {
-    Items ahead = items;
-    int left = Sh::STAGES;
-    while (left > 0 && ahead.next(tile, k0, k1)) {
-      int pb, qb;
-      tile_blocks(tile, p_blocks, q_blocks, g.raster_gp, pb, qb);
-      for (int kb = k0; kb < k1 && left > 0; ++kb, --left) {
-        tma_prefetch_l2_2d(&tmP, kb * kBK, pb * Sh::TILE_P + rank * Sh::P_ROWS);
-        tma_prefetch_l2_2d(&tmQ, kb * kBK, qb * BN + rank * Sh::Q_ROWS);
-      }
+  if (warp == 0 && lane == 0 && worker < items.tiles) {
+    int pb, qb;
+    tile_blocks(worker, p_blocks, q_blocks, g.raster_gp, pb, qb);
+    for (int kb = k0; kb < k1 && kb < k0 + Sh::STAGES; ++kb) {
+      tma_prefetch_l2_2d(&tmP, kb * kBK, pb * Sh::TILE_P + rank * Sh::P_ROWS);
+      tma_prefetch_l2_2d(&tmQ, kb * kBK, qb * BN + rank * Sh::Q_ROWS);
     }
   }
   pdl_wait();
@@ -508,9 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      while (ok && items.next(tile, k0, k1)) {
+      while (ok && items.next()) {
         int pb, qb;
-        tile_blocks(tile, p_blocks, q_blocks, g.raster_gp, pb, qb);
+        tile_blocks(items.tile, p_blocks, q_blocks, g.raster_gp, pb, qb);
         const int p_row = pb * Sh::TILE_P + rank * Sh::P_ROWS;
         const int q_row = qb * BN + rank * Sh::Q_ROWS;
         for (int kb = k0; kb < k1; ++kb) {
@@ -524,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d_pair(smem_u32(slot), &tmP, full, kb * kBK, p_row);
             tma_load_2d_pair(smem_u32(slot + Sh::P_BYTES), &tmQ, full, kb * kBK, q_row);
             ++issued;
-          } else if (!(g.ctl.inject_lost_load && tile == last_tile && kb == kt - 1)) {
+          } else if (!(g.ctl.inject_lost_load && items.tile == items.tiles - 1 && kb == kt - 1)) {
             mbar_arrive_expect_tx(&bar->full[s], Sh::STAGE);
             tma_load_2d(smem_u32(slot), &tmP, &bar->full[s], kb * kBK, p_row);
             tma_load_2d(smem_u32(slot + Sh::P_BYTES), &tmQ, &bar->full[s], kb * kBK, q_row);
@@ -542,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const bool leader = elect_one();
       const uint64_t desc0 = umma_desc_sw128(smem_u32(ring));
-      while (ok && items.next(tile, k0, k1)) {
+      while (ok && items.next()) {
         for (int kb = k0; kb < k1; ++kb) {
           ring_wait(full0 + s * 8, ph, limit_ns, cta, kSiteConsumerFull);
           ring_wait(free0 + a * 8, aph ^ 1u, limit_ns, cta, kSiteMmaAccEmpty);
@@ -573,6 +564,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&bar->drain, 0, g.ctl, &never_abort, kSiteDrain);
       }
     }
+    if (!PAIR && k_ctas > 1 && worker < items.tiles) {
+      // the adding warps' two barriers around their exchange (below)
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     // ---------------- scaled sums and output ----------------
     if (Sh::SPLIT_REGS) regs_increase<Sh::ADD_REGS>();
@@ -583,17 +580,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* my_stage = staging + e * kStageWarpBytes;
     constexpr int CW = Sh::HALF < 32 ? Sh::HALF : 32;
     constexpr int CHUNKS = Sh::HALF / CW;
+    constexpr int LOG_BN = BN == 256 ? 8 : BN == 128 ? 7 : BN == 64 ? 6 : BN == 32 ? 5 : 4;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     int s = 0, a = 0, batch = 0;
     uint32_t ph = 0;
     const int t = threadIdx.x - 128;
     const uint32_t lead_free0 = PAIR ? mapa_shared(free0, 0) : free0;
-    bool ok = true;   // after a wait that gave up: no more data, but the barriers and the split tiles' counts go on
+    bool ok = true;   // after a wait that gave up: no more data, but the barriers go on
 
     // Scales of K blocks kb .. of the tile (pb, qb) into staging batch `to`:
     // one per row, or one per 128 rows where that is all there is.
     const int p_log = g.p.shift ? 0 : 7;                                   // log2 of P's values per K block
-    constexpr int Q_LOG = QROWS ? (BN == 256 ? 8 : BN == 128 ? 7 : BN == 64 ? 6 : BN == 32 ? 5 : 4) : (BN == 256 ? 1 : 0);
+    constexpr int Q_LOG = QROWS ? LOG_BN : (BN == 256 ? 1 : 0);
     auto stage_scales = [&](int to, int pb, int qb, int kb, int n) {
       const uint32_t dst = smem_u32(scales + to * kScaleBatch * Sh::SCALES);
       auto one = [&](const ScaleView& v, int64_t first, int log, int step, int at) {
@@ -608,13 +606,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       one(g.p, static_cast<int64_t>(pb) * Sh::TILE_P + rank * Sh::P_ROWS, p_log, 1, 0);
       one(g.q, static_cast<int64_t>(qb) * BN, Q_LOG, QROWS ? 1 : 128, Sh::P_ROWS);
     };
-    while (items.next(tile, k0, k1)) {
-      const bool split = k1 - k0 < kt;
+    while (items.next()) {
       float acc[Sh::HALF];
 #pragma unroll
       for (int i = 0; i < Sh::HALF; ++i) acc[i] = 0.f;
       int pb, qb;
-      tile_blocks(tile, p_blocks, q_blocks, g.raster_gp, pb, qb);
+      tile_blocks(items.tile, p_blocks, q_blocks, g.raster_gp, pb, qb);
       if (ok) stage_scales(batch, pb, qb, k0, min(kScaleBatch, k1 - k0));
       for (int kc = k0; kc < k1; kc += kScaleBatch, batch ^= 1) {
         const int end = min(kc + kScaleBatch, k1);
@@ -676,43 +673,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (__any_sync(0xffffffffu, cta->abort)) ok = false;
       }
-      if (split) {
-        // Every segment stores its FP32 sums; the one that completes the tile
-        // adds them all in K order, so the result does not depend on timing.
-        const Partial part(g, tile, kt, workers, Sh::CTAS, static_cast<int>(rank));
-        float4* base = reinterpret_cast<float4*>(g.partials) + (half * (Sh::HALF / 4)) * 128 + row;
-        constexpr int64_t SLOT = 128 * BN / 4;
+      if (!PAIR && k_ctas > 1) {
+        // The ring has served its last K block, in every CTA of the cluster
+        // after this: its memory takes the others' sums.
+        cluster_sync();
+        const int per_log = LOG_BN - g.k_log, per = 1 << per_log;    // columns per CTA
+        const uint32_t at = smem_u32(ring) + ((in_cluster << per_log) * 128 + row) * 4;
+#pragma unroll
+        for (int i = 0; i < Sh::HALF; ++i) {
+          const int col = half * Sh::HALF + i;
+          st_cluster_f1(mapa_shared(at + (col & (per - 1)) * 512, static_cast<uint32_t>(col >> per_log)), acc[i]);
+        }
+        cluster_sync();
         if (ok) {
-          float4* dst = base + part.slot(worker) * SLOT;
-#pragma unroll
-          for (int i = 0; i < Sh::HALF / 4; ++i)
-            __stcg(dst + i * 128, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
+          const float* buf = reinterpret_cast<const float*>(ring);
+          const int64_t p0 = static_cast<int64_t>(pb) * Sh::TILE_P, q0 = static_cast<int64_t>(qb) * BN + in_cluster * per;
+          if (g.out_type == GP_REAL_BF16)
+            write_shared<__nv_bfloat16>(g, buf, t, k_ctas, per, p0, q0);
+          else if (g.out_type == GP_REAL_F16)
+            write_shared<__half>(g, buf, t, k_ctas, per, p0, q0);
+          else
+            write_shared<float>(g, buf, t, k_ctas, per, p0, q0);
         }
-        __threadfence();
-        add_warps_sync();
-        if (threadIdx.x == 128) {
-          // wraps to zero with the last segment, ready for the next launch
-          const uint32_t seen = atomicInc(g.counters + static_cast<int64_t>(tile - g.dp_tiles) * Sh::CTAS + rank,
-                                          static_cast<uint32_t>(part.segments() - 1));
-          bar->last = seen == static_cast<uint32_t>(part.segments() - 1);
-          __threadfence();
-        }
-        add_warps_sync();
-        const bool finish = bar->last != 0;
-        if (!finish || !ok) continue;
-#pragma unroll
-        for (int i = 0; i < Sh::HALF; ++i) acc[i] = 0.f;
-        for (int w = part.w_first; w <= part.w_last; ++w) {
-          const float4* from = base + part.slot(w) * SLOT;
-#pragma unroll
-          for (int i = 0; i < Sh::HALF / 4; ++i) {
-            const float4 p = __ldcg(from + i * 128);
-            acc[4 * i] += p.x;
-            acc[4 * i + 1] += p.y;
-            acc[4 * i + 2] += p.z;
-            acc[4 * i + 3] += p.w;
-          }
-        }
+        continue;
       }
       if (!ok) continue;
       const int64_t p0 = static_cast<int64_t>(pb) * Sh::TILE_P + rank * Sh::P_ROWS + quarter * 32;
@@ -825,10 +808,7 @@ cudaError_t launch_ring(Fp8GemmArgs& a, const void** kernel) {
   g.vec16 = size == 2 && aligned(a.C, a.ldc, 16);
   g.idesc = idesc_f8(P.format, Q.format, Sh::TILE_P, BN);
   g.raster_gp = a.plan.raster_gm;
-  g.dp_tiles = a.plan.dp_tiles;
-  g.sk_tiles = a.plan.sk_tiles;
-  g.partials = a.partials;
-  g.counters = a.counters;
+  g.k_log = a.plan.k_splits == 8 ? 3 : (a.plan.k_splits == 4 ? 2 : (a.plan.k_splits == 2 ? 1 : 0));
   g.ctl = a.ctl;
   auto k = fp8_ring_kernel<BN, QROWS, PAIR>;
   *kernel = reinterpret_cast<const void*>(k);
@@ -844,7 +824,7 @@ cudaError_t launch_ring(Fp8GemmArgs& a, const void** kernel) {
     if (regs.load() != kLaunchRegs) return cudaErrorInvalidConfiguration;
   }
   if ((e = ensure_smem_attr(*kernel, Sh::SMEM)) != cudaSuccess) return e;
-  Config c(a.plan.grid, Sh::CTAS, Sh::SMEM, a.stream);
+  Config c(a.plan.grid, Sh::CTAS * a.plan.k_splits, Sh::SMEM, a.stream);
   return cudaLaunchKernelEx(&c.cfg, k, tmP, tmQ, g);
 }
 
@@ -862,28 +842,17 @@ void shape_of(gp_plan* p) {
   p->tmem_cols = Sh::TMEM_COLS;
 }
 
-// Deal out the K-loops of the tiles that would leave a part-empty last wave.
-// A split costs the partial sums' way through L2 and a wait for the last
-// segment; it pays where workers would idle for kMinIdle K blocks on average.
-void split_tiles(gp_plan* p, int64_t workers, bool allowed) {
-  constexpr int64_t kMinIdle = 4;      // K blocks
-  constexpr int64_t kMinShare = 2;     // K blocks per worker
-  const int64_t T = p->tiles, ctas = p->cta_pair ? 2 : 1;
-  p->dp_tiles = static_cast<int32_t>(T);
-  p->sk_tiles = 0;
-  p->workspace_bytes = 0;
-  p->grid = static_cast<int32_t>(ctas * (T < workers ? T : workers));
-  if (!allowed || workers <= 0 || T % workers == 0) return;
-  const int64_t idle = (T + workers - 1) / workers * workers - T;
-  if (idle * p->k_tiles < kMinIdle * workers) return;
-  const int64_t dp = T / workers * workers, sk = T - dp;
-  int64_t use = workers;
-  if (dp == 0 && sk * p->k_tiles / kMinShare < use) use = sk * p->k_tiles / kMinShare;
-  if (use <= sk || sk * p->k_tiles < kMinShare * use || sk * ctas > kFp8Counters) return;
-  p->dp_tiles = static_cast<int32_t>(dp);
-  p->sk_tiles = static_cast<int32_t>(sk);
-  p->grid = static_cast<int32_t>(ctas * use);
-  p->workspace_bytes = 2 * static_cast<int64_t>(p->grid) * 128 * p->bn * 4;
+// Clusters of up to 8 CTAs share the K blocks of a tile where the tiles leave
+// SMs idle: all of them at once (clusters of 4 and 8 cannot use every SM), and
+// at least kMinShare K blocks for each CTA.
+void split_k(gp_plan* p, int sms, bool allowed) {
+  constexpr int64_t kMinShare = 4;
+  p->k_splits = 1;
+  if (!allowed || p->cta_pair) return;
+  for (int c = 2; c <= 8; c *= 2) {
+    const int64_t fit = c > 2 ? sms * 7 / 8 : sms;
+    if (p->tiles * c <= fit && p->k_tiles >= kMinShare * c) p->k_splits = c;
+  }
 }
 
 // Pairs that fit on the device at once (cached per device).
@@ -920,6 +889,17 @@ int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int
   else
     swapped = a_group == kFp8Group && b_group == 1;
   const int64_t p_rows = swapped ? N : M, q_rows = swapped ? M : N;
+  if (want == 0 && narrow <= kFp8GemvRows && !(opts && opts->inject_lost_load)) {
+    p->dtype = GP_PLAN_FP8;
+    p->layout = swapped;
+    p->variant = GP_PIPELINED;
+    p->stages = 1;
+    p->k_tiles = (K + kBK - 1) / kBK;
+    fp8_gemv_plan(p_rows, p);
+    p->dp_tiles = static_cast<int32_t>(p->tiles);
+    p->k_splits = 1;
+    return GP_OK;
+  }
   int bn = want;
   if (bn == 0) bn = narrow <= 16 ? 16 : (narrow <= 32 ? 32 : (narrow <= 64 ? 64 : (narrow <= 128 ? 128 : 256)));
   // (a lost load is injected into the one-CTA kernel)
@@ -944,12 +924,15 @@ int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int
   p->k_splits = 1;
   p->raster_gm = 8;
   p->compute_load_ratio = 2.0 * p->bm * p->bn / (p->bm + p->bn);
-  if (sms > (p->cta_pair ? 1 : 0)) split_tiles(p, p->cta_pair ? sms / 2 : sms, !(opts && opts->no_split));
+  split_k(p, sms, !(opts && (opts->no_split || opts->inject_lost_load)));
+  const int64_t ctas = p->cta_pair ? 2 : p->k_splits, workers = sms / ctas;
+  p->grid = static_cast<int32_t>(ctas * (p->tiles < workers ? p->tiles : workers));
   return GP_OK;
 }
 
 cudaError_t launch_fp8_gemm(Fp8GemmArgs& a, const void** kernel) {
   const gp_fp8_matrix& Q = a.plan.layout ? a.A : a.B;
+  if (a.plan.bn == kFp8GemvRows) return launch_fp8_gemv(a, kernel);
   switch (a.plan.bn) {
     case 16: return launch_ring<16, true, false>(a, kernel);
     case 32: return launch_ring<32, true, false>(a, kernel);
@@ -959,11 +942,11 @@ cudaError_t launch_fp8_gemm(Fp8GemmArgs& a, const void** kernel) {
   }
 }
 
-cudaError_t fp8_fit_pairs(gp_plan* plan, bool no_split) {
+cudaError_t fp8_fit_pairs(gp_plan* plan) {
   if (!plan->cta_pair) return cudaSuccess;
   int pairs = 0;
   const cudaError_t e = pair_capacity(&pairs);
-  if (e == cudaSuccess && 2 * pairs < plan->grid) split_tiles(plan, pairs, !no_split);
+  if (e == cudaSuccess && 2 * pairs < plan->grid) plan->grid = 2 * pairs;
   return e;
 }
 

@@ -52,7 +52,8 @@ def check(a, b, out="bf16", addend=None, ld=None, **kw):
 SHAPES = [(1, 1, 1), (1, 16, 16), (1, 300, 4096), (2, 129, 128), (16, 128, 130), (17, 127, 257), (31, 1000, 520),
           (33, 257, 129), (64, 640, 1024), (65, 200, 384), (128, 128, 128), (129, 130, 1000), (300, 70, 257),
           (70, 300, 2057), (511, 385, 640), (260, 1030, 300), (1000, 776, 2056), (5, 4096, 8192), (4100, 3, 700),
-          (500, 600, 8200), (2100, 2300, 256)]
+          (500, 600, 8200), (2100, 2300, 256), (3, 700, 513), (4, 129, 4100), (300, 2, 777),
+          (1, 41, 20001), (4, 40, 9000), (2, 64, 17000), (8, 700, 2050)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
