@@ -19,8 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgemmpipe.so")
 
-SOURCES = ["api.cu", "fp8_api.cu", "k_ffma.cu", "k_fp8_gemm.cu", "k_fp8_gemv.cu", "k_fp8_norm.cu", "k_fp8_quant.cu",
-           "k_imma.cu", "k_umma.cu", "probe.cu"]
+SOURCES = ["api.cu", "fp8_api.cu", "k_ffma.cu", "k_fp8_gemm.cu", "k_fp8_norm.cu", "k_fp8_quant.cu", "k_imma.cu",
+           "k_umma.cu", "probe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

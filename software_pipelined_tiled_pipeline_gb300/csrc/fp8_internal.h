@@ -84,10 +84,6 @@ int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int
 // Pairs must sit on one TPC each: where fewer fit at once than the plan counted on, launch those.
 cudaError_t fp8_fit_pairs(gp_plan* plan);
 cudaError_t launch_fp8_gemm(Fp8GemmArgs& a, const void** kernel);
-// The product with at most kFp8GemvRows rows on one side, without tiles.
-constexpr int kFp8GemvRows = 4;
-void fp8_gemv_plan(int64_t n, gp_plan* p);
-cudaError_t launch_fp8_gemv(Fp8GemmArgs& a, const void** kernel);
 // C = addend, or zeros (K == 0).
 cudaError_t launch_fp8_fill(void* C, int64_t ldc, const void* addend, int64_t ld_add, int64_t M, int64_t N,
                             int out_type, cudaStream_t stream);

@@ -397,17 +397,22 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
 
 // The K loop split over a cluster: every CTA hands each of the others the
 // columns that are theirs, and writes its own.  Buffer of a CTA: for each
-// source, its BN / CTAs columns of 128 rows.
+// source, its columns of kXRow floats, one per row and one to keep the lanes of either walk off each
+// other's banks.
+constexpr int kXRow = 129;
 template <typename T>
-__device__ __forceinline__ void write_shared(const Fp8Params& g, const float* buf, int t, int ctas, int per, int64_t p0,
-                                             int64_t q0) {
+__device__ __forceinline__ void write_shared(const Fp8Params& g, const float* buf, int t, int ctas, int per_log,
+                                             int64_t p0, int64_t q0) {
   T* const c = static_cast<T*>(g.c);
   const T* const add = static_cast<const T*>(g.addend);
-#pragma unroll 1
-  for (int i = t; i < per * 128; i += kAddThreads) {
-    float v = 0.f;
-    for (int s = 0; s < ctas; ++s) v += buf[s * per * 128 + i];      // in K order
-    const int64_t p = p0 + (i & 127), q = q0 + (i >> 7);
+#pragma unroll 4
+  for (int i = t; i < 128 << per_log; i += kAddThreads) {
+    // neighbouring lanes along a row of C
+    const int col = g.swapped ? i >> 7 : i & ((1 << per_log) - 1);
+    const int row = g.swapped ? i & 127 : i >> per_log;
+    float v = 0.f;       // in K order
+    for (int s = 0; s < ctas; ++s) v += buf[((s << per_log) + col) * kXRow + row];
+    const int64_t p = p0 + row, q = q0 + col;
     if (p >= g.p.rows || q >= g.q.rows) continue;
     const int64_t m = g.swapped ? q : p, n = g.swapped ? p : q;
     if (add) v += widen(add[m * g.ld_add + n]);
@@ -678,22 +683,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // after this: its memory takes the others' sums.
         cluster_sync();
         const int per_log = LOG_BN - g.k_log, per = 1 << per_log;    // columns per CTA
-        const uint32_t at = smem_u32(ring) + ((in_cluster << per_log) * 128 + row) * 4;
+        const uint32_t at = smem_u32(ring) + ((in_cluster << per_log) * kXRow + row) * 4;
 #pragma unroll
         for (int i = 0; i < Sh::HALF; ++i) {
           const int col = half * Sh::HALF + i;
-          st_cluster_f1(mapa_shared(at + (col & (per - 1)) * 512, static_cast<uint32_t>(col >> per_log)), acc[i]);
+          st_cluster_f1(mapa_shared(at + (col & (per - 1)) * (kXRow * 4), static_cast<uint32_t>(col >> per_log)), acc[i]);
         }
         cluster_sync();
         if (ok) {
           const float* buf = reinterpret_cast<const float*>(ring);
           const int64_t p0 = static_cast<int64_t>(pb) * Sh::TILE_P, q0 = static_cast<int64_t>(qb) * BN + in_cluster * per;
           if (g.out_type == GP_REAL_BF16)
-            write_shared<__nv_bfloat16>(g, buf, t, k_ctas, per, p0, q0);
+            write_shared<__nv_bfloat16>(g, buf, t, k_ctas, per_log, p0, q0);
           else if (g.out_type == GP_REAL_F16)
-            write_shared<__half>(g, buf, t, k_ctas, per, p0, q0);
+            write_shared<__half>(g, buf, t, k_ctas, per_log, p0, q0);
           else
-            write_shared<float>(g, buf, t, k_ctas, per, p0, q0);
+            write_shared<float>(g, buf, t, k_ctas, per_log, p0, q0);
         }
         continue;
       }
@@ -842,19 +847,6 @@ void shape_of(gp_plan* p) {
   p->tmem_cols = Sh::TMEM_COLS;
 }
 
-// Clusters of up to 8 CTAs share the K blocks of a tile where the tiles leave
-// SMs idle: all of them at once (clusters of 4 and 8 cannot use every SM), and
-// at least kMinShare K blocks for each CTA.
-void split_k(gp_plan* p, int sms, bool allowed) {
-  constexpr int64_t kMinShare = 4;
-  p->k_splits = 1;
-  if (!allowed || p->cta_pair) return;
-  for (int c = 2; c <= 8; c *= 2) {
-    const int64_t fit = c > 2 ? sms * 7 / 8 : sms;
-    if (p->tiles * c <= fit && p->k_tiles >= kMinShare * c) p->k_splits = c;
-  }
-}
-
 // Pairs that fit on the device at once (cached per device).
 cudaError_t pair_capacity(int* pairs) {
   static std::atomic<int> cached[64];
@@ -874,43 +866,85 @@ cudaError_t pair_capacity(int* pairs) {
 
 }  // namespace
 
+namespace {
+
+// What the planner knows of a tile width, in ns, measured on a 152-SM GB300
+// (device time of whole calls in a graph, operands from HBM): a K block with Q
+// block-scaled and row-scaled, the call around one tile per CTA, each further
+// tile, and the exchange where a cluster splits the K loop.  For example, unsplit
+// against two CTAs per tile: 48 x 8192 x 8192 25.6 -> 19.2 us (BN 64), 256 x
+// 4096 x 4096 14.0 -> 20.0 us (BN 128); BN 64 against 128 at 1000 x 776 x 2056
+// 9.5 and 9.8 us, BN 128 against 256 at 1024 x 4096 x 4096 25.8 and 20.1 us and
+// at 512 x 4096 x 4096 14.6 and 18.9 us.
+struct TileCost {
+  int bn, k_block, k_rows, call, more, exchange;
+};
+constexpr TileCost kTileCosts[] = {{16, 210, 210, 3200, 300, 800},
+                                   {32, 270, 270, 3500, 400, 1200},
+                                   {64, 350, 350, 4200, 600, 2000},
+                                   {128, 330, 480, 5000, 1000, 5000},
+                                   {256, 500, 850, 6500, 1800, 0}};
+constexpr double kReadGbs = 6500;        // operands from HBM
+constexpr double kStageGbs = 72;         // one CTA's ring
+constexpr int kSwappedNs = 13;           // a column of a swapped tile's epilogue
+constexpr int kMinShare = 4;             // K blocks of each CTA of a cluster, at least
+
+}  // namespace
+
 int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int sms, const gp_fp8_options* opts,
                   gp_plan* p) {
   std::memset(p, 0, sizeof(*p));
   const int want = opts ? opts->bn : 0;
-  if (want != 0 && want != 16 && want != 32 && want != 64 && want != 128 && want != 256) return GP_ERR_UNSUPPORTED;
-  // Q, the operand on the MMA's N side, is the narrower one where that is at
-  // most one tile wide; else the one with block scales (one product of scales
-  // per row instead of one per output), B if both or neither.
-  const int64_t narrow = M < N ? M : N;
-  bool swapped;
-  if (narrow <= 128)
-    swapped = M < N;
-  else
-    swapped = a_group == kFp8Group && b_group == 1;
-  const int64_t p_rows = swapped ? N : M, q_rows = swapped ? M : N;
-  if (want == 0 && narrow <= kFp8GemvRows && !(opts && opts->inject_lost_load)) {
-    p->dtype = GP_PLAN_FP8;
-    p->layout = swapped;
-    p->variant = GP_PIPELINED;
-    p->stages = 1;
-    p->k_tiles = (K + kBK - 1) / kBK;
-    fp8_gemv_plan(p_rows, p);
-    p->dp_tiles = static_cast<int32_t>(p->tiles);
-    p->k_splits = 1;
-    return GP_OK;
+  bool known = want == 0;
+  for (const TileCost& t : kTileCosts) known |= t.bn == want;
+  if (!known) return GP_ERR_UNSUPPORTED;
+  const bool one_cta = opts && opts->inject_lost_load;   // (a lost load is injected into whole tiles of one CTA)
+  const int64_t kt = (K + kBK - 1) / kBK;
+  const int have = sms > 0 ? sms : 152;
+  // Try every width with either operand on the MMA's N side (Q), and every
+  // cluster that keeps all of its tiles resident (clusters of 4 and 8 cannot
+  // use every SM); take the least estimate.
+  double best = 0;
+  const TileCost* tile = nullptr;
+  int best_c = 1;
+  bool swapped = false;
+  for (int sw = 0; sw < 2; ++sw) {
+    const int64_t P = sw ? N : M, Q = sw ? M : N;
+    const bool q_rows = (sw ? a_group : b_group) == 1;
+    for (const TileCost& t : kTileCosts) {
+      if (want ? t.bn != want : (one_cta && t.bn == 256)) continue;
+      const int ctas = t.bn == 256 ? 2 : 1;
+      const int64_t tiles = (P + 128 * ctas - 1) / (128 * ctas) * ((Q + t.bn - 1) / t.bn);
+      const int stage = 128 * (128 + t.bn / ctas);
+      for (int c = 1; c <= 8; c *= 2) {
+        if (c > 1 && (ctas == 2 || one_cta || (opts && opts->no_split) || tiles * c > (c > 2 ? have * 7 / 8 : have) ||
+                      kt < kMinShare * c))
+          break;
+        const int64_t workers = have / (ctas * c);
+        if (workers < 1) break;
+        const int64_t waves = (tiles + workers - 1) / workers, blocks = waves * ((kt + c - 1) / c);
+        const double k_block = q_rows ? t.k_rows : t.k_block, ring = stage / kStageGbs;
+        double ns = blocks * (k_block > ring ? k_block : ring);
+        const double read = (M + N) * static_cast<double>(K) / kReadGbs;
+        if (ns < read) ns = read;
+        ns += t.call + (waves - 1) * t.more + (c > 1 ? t.exchange : 0) + (sw ? waves * t.bn * kSwappedNs : 0);
+        if (!tile || ns < best) {
+          best = ns;
+          tile = &t;
+          best_c = c;
+          swapped = sw != 0;
+        }
+      }
+    }
   }
-  int bn = want;
-  if (bn == 0) bn = narrow <= 16 ? 16 : (narrow <= 32 ? 32 : (narrow <= 64 ? 64 : (narrow <= 128 ? 128 : 256)));
-  // (a lost load is injected into the one-CTA kernel)
-  if (opts && opts->inject_lost_load && bn == 256) bn = 128;
+  const int64_t p_rows = swapped ? N : M, q_rows = swapped ? M : N;
   p->dtype = GP_PLAN_FP8;
   p->layout = swapped;
   p->variant = GP_PIPELINED;
   p->threads = kThreads;
   p->persistent = 1;
-  p->kernel = bn == 256 ? "fp8_pair_ring" : "fp8_ring";
-  switch (bn) {
+  p->kernel = tile->bn == 256 ? "fp8_pair_ring" : "fp8_ring";
+  switch (tile->bn) {
     case 16: shape_of<16, false>(p); break;
     case 32: shape_of<32, false>(p); break;
     case 64: shape_of<64, false>(p); break;
@@ -918,21 +952,19 @@ int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int
     default: shape_of<256, true>(p); break;
   }
   p->tiles = (p_rows + p->bm - 1) / p->bm * ((q_rows + p->bn - 1) / p->bn);
-  p->k_tiles = (K + kBK - 1) / kBK;
+  p->k_tiles = kt;
   if (p->tiles > kMaxTiles) return GP_ERR_SIZE;
   p->dp_tiles = static_cast<int32_t>(p->tiles);
-  p->k_splits = 1;
+  p->k_splits = best_c;
   p->raster_gm = 8;
   p->compute_load_ratio = 2.0 * p->bm * p->bn / (p->bm + p->bn);
-  split_k(p, sms, !(opts && (opts->no_split || opts->inject_lost_load)));
-  const int64_t ctas = p->cta_pair ? 2 : p->k_splits, workers = sms / ctas;
+  const int64_t ctas = p->cta_pair ? 2 : best_c, workers = sms / ctas;
   p->grid = static_cast<int32_t>(ctas * (p->tiles < workers ? p->tiles : workers));
   return GP_OK;
 }
 
 cudaError_t launch_fp8_gemm(Fp8GemmArgs& a, const void** kernel) {
   const gp_fp8_matrix& Q = a.plan.layout ? a.A : a.B;
-  if (a.plan.bn == kFp8GemvRows) return launch_fp8_gemv(a, kernel);
   switch (a.plan.bn) {
     case 16: return launch_ring<16, true, false>(a, kernel);
     case 32: return launch_ring<32, true, false>(a, kernel);

