@@ -253,12 +253,11 @@ struct alignas(4 * sizeof(T)) Four {
   T e[4];
 };
 
-// Four neighbouring outputs of a row: FP32 sums (+ addend) rounded to the output type.  FULL: all are inside C and
-// aligned to their size.
-template <typename T, bool FULL>
+// Four neighbouring outputs of a row, `left` of them inside C: FP32 sums (+ addend) rounded to the output type.
+template <typename T>
 __device__ __forceinline__ void store4(T* c, const T* add, float4 v, bool vec, int64_t left) {
   float x[4] = {v.x, v.y, v.z, v.w};
-  if (FULL || (vec && left >= 4)) {
+  if (vec && left >= 4) {
     if (add) {
       const Four<T> a = *reinterpret_cast<const Four<T>*>(add);
 #pragma unroll
@@ -286,11 +285,11 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // Write a warp's 32 rows x HALF columns of sums (thread: one row) to C: through
 // shared memory, so that a row's outputs leave side by side.  16-byte chunk c
 // of row r of the staged 32 x 128 bytes lies at c ^ (r mod 8).
-template <int HALF, typename T>
+template <int HALF, bool ADD, typename T>
 __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)[HALF], uint8_t* stage, int lane,
                                           int64_t p0, int64_t q0) {
   T* const c = static_cast<T*>(g.c);
-  const T* const add = static_cast<const T*>(g.addend);
+  const T* const add = ADD ? static_cast<const T*>(g.addend) : nullptr;
   if (g.swapped) {
     // The lanes' rows are C's columns: each of C's rows gets 32 neighbouring
     // outputs.  Sums go through shared memory (each lane reads back its own) so
@@ -306,11 +305,11 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
       const int64_t first = q0 + j * CW, left = g.q.rows - first;
       const int rows = col < g.p.rows ? static_cast<int>(left < CW ? left : CW) : 0;
       T* o = c + first * g.ldc + col;
-      const T* f = add ? add + first * g.ld_add + col : nullptr;
+      const T* f = ADD ? add + first * g.ld_add + col : nullptr;
 #pragma unroll 1
       for (int i = 0; i < rows; ++i, o += g.ldc) {
         float v = mine[i * 32];
-        if (f) {
+        if (ADD) {
           v += widen(*f);
           f += g.ld_add;
         }
@@ -322,7 +321,7 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
   const uint32_t base = smem_u32(stage);
   const bool full = g.vec && p0 + 32 <= g.p.rows && q0 + HALF <= g.q.rows;
   if constexpr (sizeof(T) == 2 && HALF >= 64) {
-    if (full && !add && g.vec16) {
+    if (!ADD && full && g.vec16) {
       // 64 columns at a time, rounded before they are staged: 16 bytes per lane, 8 lanes per row
       T* out = c + (p0 + lane / 8) * g.ldc + q0 + lane % 8 * 8;
 #pragma unroll
@@ -355,7 +354,7 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
   constexpr int PER = CW / 4;                    // lanes per row when they leave
   const int64_t row = p0 + lane / PER, col = q0 + lane % PER * 4;
   T* out = c + row * g.ldc + col;
-  const T* from = add ? add + row * g.ld_add + col : nullptr;
+  const T* from = ADD ? add + row * g.ld_add + col : nullptr;
 #pragma unroll
   for (int j = 0; j < HALF / CW; ++j) {
     __syncwarp();
@@ -377,20 +376,35 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
                      : "memory");
         T* o = out + i * (32 / PER) * g.ldc + j * CW;
         const T* f = from ? from + i * (32 / PER) * g.ld_add + j * CW : nullptr;
-        if (row + i * (32 / PER) < g.p.rows && left > 0) store4<T, false>(o, f, v, g.vec != 0, left);
+        if (row + i * (32 / PER) < g.p.rows && left > 0) store4<T>(o, f, v, g.vec != 0, left);
       }
       continue;
     }
+    // Addends are asked for four rows' worth at a time before the first of
+    // these outputs is written: they may be the same memory.
+    constexpr int GROUP = ADD && PER > 4 ? 4 : PER;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      float4 v;
-      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                   : "r"(base + sw128_offset(i * (32 / PER) + lane / PER, lane % PER))
-                   : "memory");
-      T* o = out + i * (32 / PER) * g.ldc + j * CW;
-      const T* f = from ? from + i * (32 / PER) * g.ld_add + j * CW : nullptr;
-      store4<T, true>(o, f, v, true, 4);
+    for (int i0 = 0; i0 < PER; i0 += GROUP) {
+      Four<T> was[GROUP];
+      if (ADD) {
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i)
+          was[i] = *reinterpret_cast<const Four<T>*>(from + (i0 + i) * (32 / PER) * g.ld_add + j * CW);
+      }
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) {
+        float4 v;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(base + sw128_offset((i0 + i) * (32 / PER) + lane / PER, lane % PER))
+                     : "memory");
+        Four<T> o;
+        o.e[0] = narrow<T>(ADD ? v.x + widen(was[i].e[0]) : v.x);
+        o.e[1] = narrow<T>(ADD ? v.y + widen(was[i].e[1]) : v.y);
+        o.e[2] = narrow<T>(ADD ? v.z + widen(was[i].e[2]) : v.z);
+        o.e[3] = narrow<T>(ADD ? v.w + widen(was[i].e[3]) : v.w);
+        *reinterpret_cast<Four<T>*>(out + (i0 + i) * (32 / PER) * g.ldc + j * CW) = o;
+      }
     }
   }
 }
@@ -400,11 +414,11 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
 // source, its columns of kXRow floats, one per row and one to keep the lanes of either walk off each
 // other's banks.
 constexpr int kXRow = 129;
-template <typename T>
+template <bool ADD, typename T>
 __device__ __forceinline__ void write_shared(const Fp8Params& g, const float* buf, int t, int ctas, int per_log,
                                              int64_t p0, int64_t q0) {
   T* const c = static_cast<T*>(g.c);
-  const T* const add = static_cast<const T*>(g.addend);
+  const T* const add = ADD ? static_cast<const T*>(g.addend) : nullptr;
 #pragma unroll 4
   for (int i = t; i < 128 << per_log; i += kAddThreads) {
     // neighbouring lanes along a row of C
@@ -415,13 +429,13 @@ __device__ __forceinline__ void write_shared(const Fp8Params& g, const float* bu
     const int64_t p = p0 + row, q = q0 + col;
     if (p >= g.p.rows || q >= g.q.rows) continue;
     const int64_t m = g.swapped ? q : p, n = g.swapped ? p : q;
-    if (add) v += widen(add[m * g.ld_add + n]);
+    if (ADD) v += widen(add[m * g.ld_add + n]);
     c[m * g.ldc + n] = narrow<T>(v);
   }
 }
 
-// QROWS: Q has a scale for each row (a column of the tile); else one for each 128 rows.
-template <int BN, bool QROWS, bool PAIR>
+// QROWS: Q has a scale for each row (a column of the tile); else one for each 128 rows.  ADD: there is an addend.
+template <int BN, bool QROWS, bool PAIR, bool ADD>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_ring_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ Fp8Params g) {
@@ -618,6 +632,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       int pb, qb;
       tile_blocks(items.tile, p_blocks, q_blocks, g.raster_gp, pb, qb);
       if (ok) stage_scales(batch, pb, qb, k0, min(kScaleBatch, k1 - k0));
+      if (ADD && !g.swapped) {
+        // this thread's row of the addend comes into L2 while the K loop runs
+        const int size = g.out_type == GP_REAL_F32 ? 4 : 2;
+        const int64_t p = static_cast<int64_t>(pb) * Sh::TILE_P + rank * Sh::P_ROWS + row;
+        const int64_t q = static_cast<int64_t>(qb) * BN + half * Sh::HALF;
+        if (p < g.p.rows) {
+          const uint8_t* at = static_cast<const uint8_t*>(g.addend) + (p * g.ld_add + q) * size;
+#pragma unroll 1
+          for (int i = 0; i < Sh::HALF && q + i < g.q.rows; i += 128 / size)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * size));
+        }
+      }
       for (int kc = k0; kc < k1; kc += kScaleBatch, batch ^= 1) {
         const int end = min(kc + kScaleBatch, k1);
         cp_async_wait_all();
@@ -694,11 +720,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float* buf = reinterpret_cast<const float*>(ring);
           const int64_t p0 = static_cast<int64_t>(pb) * Sh::TILE_P, q0 = static_cast<int64_t>(qb) * BN + in_cluster * per;
           if (g.out_type == GP_REAL_BF16)
-            write_shared<__nv_bfloat16>(g, buf, t, k_ctas, per_log, p0, q0);
+            write_shared<ADD, __nv_bfloat16>(g, buf, t, k_ctas, per_log, p0, q0);
           else if (g.out_type == GP_REAL_F16)
-            write_shared<__half>(g, buf, t, k_ctas, per_log, p0, q0);
+            write_shared<ADD, __half>(g, buf, t, k_ctas, per_log, p0, q0);
           else
-            write_shared<float>(g, buf, t, k_ctas, per_log, p0, q0);
+            write_shared<ADD, float>(g, buf, t, k_ctas, per_log, p0, q0);
         }
         continue;
       }
@@ -706,11 +732,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t p0 = static_cast<int64_t>(pb) * Sh::TILE_P + rank * Sh::P_ROWS + quarter * 32;
       const int64_t q0 = static_cast<int64_t>(qb) * BN + half * Sh::HALF;
       if (g.out_type == GP_REAL_BF16)
-        write_out<Sh::HALF, __nv_bfloat16>(g, acc, my_stage, lane, p0, q0);
+        write_out<Sh::HALF, ADD, __nv_bfloat16>(g, acc, my_stage, lane, p0, q0);
       else if (g.out_type == GP_REAL_F16)
-        write_out<Sh::HALF, __half>(g, acc, my_stage, lane, p0, q0);
+        write_out<Sh::HALF, ADD, __half>(g, acc, my_stage, lane, p0, q0);
       else
-        write_out<Sh::HALF, float>(g, acc, my_stage, lane, p0, q0);
+        write_out<Sh::HALF, ADD, float>(g, acc, my_stage, lane, p0, q0);
     }
   }
 
@@ -779,8 +805,8 @@ struct Config {
   }
 };
 
-template <int BN, bool QROWS, bool PAIR>
-cudaError_t launch_ring(Fp8GemmArgs& a, const void** kernel) {
+template <int BN, bool QROWS, bool PAIR, bool ADD>
+cudaError_t launch_as(Fp8GemmArgs& a, const void** kernel) {
   using Sh = Fp8Shape<BN, PAIR>;
   const bool swapped = a.plan.layout != 0;
   const gp_fp8_matrix& P = swapped ? a.B : a.A;
@@ -815,7 +841,7 @@ cudaError_t launch_ring(Fp8GemmArgs& a, const void** kernel) {
   g.raster_gp = a.plan.raster_gm;
   g.k_log = a.plan.k_splits == 8 ? 3 : (a.plan.k_splits == 4 ? 2 : (a.plan.k_splits == 2 ? 1 : 0));
   g.ctl = a.ctl;
-  auto k = fp8_ring_kernel<BN, QROWS, PAIR>;
+  auto k = fp8_ring_kernel<BN, QROWS, PAIR, ADD>;
   *kernel = reinterpret_cast<const void*>(k);
   if (Sh::SPLIT_REGS) {
     // The register split counts on exactly kLaunchRegs per thread at launch:
@@ -831,6 +857,11 @@ cudaError_t launch_ring(Fp8GemmArgs& a, const void** kernel) {
   if ((e = ensure_smem_attr(*kernel, Sh::SMEM)) != cudaSuccess) return e;
   Config c(a.plan.grid, Sh::CTAS * a.plan.k_splits, Sh::SMEM, a.stream);
   return cudaLaunchKernelEx(&c.cfg, k, tmP, tmQ, g);
+}
+
+template <int BN, bool QROWS, bool PAIR>
+cudaError_t launch_ring(Fp8GemmArgs& a, const void** kernel) {
+  return a.addend ? launch_as<BN, QROWS, PAIR, true>(a, kernel) : launch_as<BN, QROWS, PAIR, false>(a, kernel);
 }
 
 template <int BN, bool PAIR>
@@ -855,7 +886,7 @@ cudaError_t pair_capacity(int* pairs) {
   if (e != cudaSuccess) return e;
   if (dev >= 0 && dev < 64 && (*pairs = cached[dev].load()) > 0) return cudaSuccess;
   using Sh = Fp8Shape<256, true>;
-  const void* k = reinterpret_cast<const void*>(fp8_ring_kernel<256, false, true>);
+  const void* k = reinterpret_cast<const void*>(fp8_ring_kernel<256, false, true, false>);
   if ((e = ensure_smem_attr(k, Sh::SMEM)) != cudaSuccess) return e;
   Config c(2, 2, Sh::SMEM, nullptr);
   if ((e = cudaOccupancyMaxActiveClusters(pairs, k, &c.cfg)) != cudaSuccess) return e;
