@@ -2,6 +2,8 @@
 // and to memory, the scale of a group, and the 8-bit conversions.
 #pragma once
 #include <cstdint>
+#include <cstring>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -46,21 +48,54 @@ __device__ __forceinline__ void load8(Raw8<T>& r, const T* p, int valid, bool ve
   memcpy(&r, t, sizeof(t));
 }
 
+// The values of one raw word: one FP32, or two 16-bit ones (the lower first).
+template <typename T>
+__device__ __forceinline__ float word_lo(uint32_t w) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(w << 16);
+  __half2 h;
+  memcpy(&h, &w, 4);
+  return __low2float(h);
+}
+template <typename T>
+__device__ __forceinline__ float word_hi(uint32_t w) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(w & 0xFFFF0000u);
+  __half2 h;
+  memcpy(&h, &w, 4);
+  return __high2float(h);
+}
+template <typename T>
+__device__ __forceinline__ const uint32_t* words(const Raw8<T>& r) {
+  return reinterpret_cast<const uint32_t*>(&r);
+}
+
 template <typename T>
 __device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&v)[8]) {
-  T t[8];
-  memcpy(t, &r, sizeof(t));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 4)
+      v[i] = word_lo<T>(words(r)[i]);
+    else
+      v[i] = i & 1 ? word_hi<T>(words(r)[i / 2]) : word_lo<T>(words(r)[i / 2]);
+  }
 }
 
 // Round eight FP32 values to T (nearest even).
 template <typename T>
 __device__ __forceinline__ void pack8(const float (&v)[8], Raw8<T>& r) {
-  T t[8];
+  uint32_t* w = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) from_f32(v[i], t[i]);
-  memcpy(&r, t, sizeof(t));
+  for (int i = 0; i < Raw8<T>::WORDS * 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(v[i]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      memcpy(&w[i], &p, 4);
+    } else {
+      const __half2 p = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      memcpy(&w[i], &p, 4);
+    }
+  }
 }
 
 template <typename T>
@@ -94,18 +129,11 @@ __device__ __forceinline__ void load8_any(float (&v)[8], const void* base, int t
   }
 }
 
-// Value k of eight as FP32, straight from the raw words.
+// Value k of eight as FP32.
 template <typename T>
 __device__ __forceinline__ float value_of(const Raw8<T>& r, int k) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
-  if constexpr (sizeof(T) == 4) {
-    return __uint_as_float(w[k]);
-  } else {
-    const uint16_t h = static_cast<uint16_t>(k & 1 ? w[k / 2] >> 16 : w[k / 2]);
-    T t;
-    memcpy(&t, &h, 2);
-    return to_f32(t);
-  }
+  if constexpr (sizeof(T) == 4) return word_lo<T>(words(r)[k]);
+  return k & 1 ? word_hi<T>(words(r)[k / 2]) : word_lo<T>(words(r)[k / 2]);
 }
 
 // ---------------------------------------------------------------------------
@@ -132,20 +160,14 @@ __device__ __forceinline__ uint32_t raw_max(uint32_t a, uint32_t b) {
 // The magnitude in a word's only (32-bit types), lower or upper value, as FP32 bits.
 template <typename T>
 __device__ __forceinline__ uint32_t raw_to_bits(uint32_t word, int upper) {
-  if constexpr (sizeof(T) == 4) {
-    return word;
-  } else {
-    const uint16_t h = static_cast<uint16_t>(upper ? word >> 16 : word);
-    T t;
-    memcpy(&t, &h, 2);
-    return __float_as_uint(to_f32(t));
-  }
+  if constexpr (sizeof(T) == 4) return word;
+  return __float_as_uint(upper ? word_hi<T>(word) : word_lo<T>(word));
 }
 
 constexpr float kScaleFloor = 5.42101086e-20f;   // 2^-64
 
 // Scale of a group from its largest magnitude's bits, and the factor applied
-// to its values.  Both divisions are correctly rounded.
+// to its values.  Both are correctly rounded quotients.
 struct GroupScale {
   float scale, inv;
 };
@@ -153,7 +175,7 @@ __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, float fmax
   GroupScale g;
   g.scale = __fdiv_rn(__uint_as_float(amax_bits), fmax);
   if (g.scale < kScaleFloor) g.scale = kScaleFloor;   // false for NaN, which stays
-  g.inv = __fdiv_rn(1.0f, g.scale);
+  g.inv = __frcp_rn(g.scale);
   return g;
 }
 

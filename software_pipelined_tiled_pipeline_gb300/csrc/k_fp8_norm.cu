@@ -43,26 +43,33 @@ __device__ __forceinline__ float row_sum(float v, float* slots) {
   return s;
 }
 
-// y of one chunk to its 8-bit codes; the 16 lanes of a group agree on its scale.
-__device__ __forceinline__ void quantize_chunk(const NormArgs& a, const float (&y)[8], int64_t row, int64_t col,
-                                               int valid, int lane) {
+// Largest magnitude of eight values of each of the 16 lanes of a group.
+__device__ __forceinline__ uint32_t group_max(const float (&y)[8]) {
   uint32_t m = 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) m = max(m, abs_bits(y[k]));
 #pragma unroll
   for (int d = 1; d < 16; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-  if (valid <= 0) return;
-  const GroupScale g = group_scale(m, a.fmax);
-  if ((lane & 15) == 0) a.q.scales[row * a.q.stride_row + (col >> 7) * a.q.stride_col] = g.scale;
+  return m;
+}
+__device__ __forceinline__ void write_codes(uint8_t* p, const float (&y)[8], float inv, bool e5m2, int valid) {
   uint2 w;
-  if (a.e5m2) {
-    w.x = fp8x4<true>(y[0] * g.inv, y[1] * g.inv, y[2] * g.inv, y[3] * g.inv);
-    w.y = fp8x4<true>(y[4] * g.inv, y[5] * g.inv, y[6] * g.inv, y[7] * g.inv);
+  if (e5m2) {
+    w.x = fp8x4<true>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    w.y = fp8x4<true>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
   } else {
-    w.x = fp8x4<false>(y[0] * g.inv, y[1] * g.inv, y[2] * g.inv, y[3] * g.inv);
-    w.y = fp8x4<false>(y[4] * g.inv, y[5] * g.inv, y[6] * g.inv, y[7] * g.inv);
+    w.x = fp8x4<false>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    w.y = fp8x4<false>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
   }
-  store_codes8(static_cast<uint8_t*>(a.q.data) + row * a.q.ld + col, w, valid);
+  store_codes8(p, w, valid);
+}
+// y of one chunk to its 8-bit codes; the 16 lanes of a group agree on its scale.
+__device__ __forceinline__ void quantize_chunk(const NormArgs& a, const float (&y)[8], int64_t row, int64_t col,
+                                               int valid, int lane) {
+  const GroupScale g = group_scale(group_max(y), a.fmax);
+  if (valid <= 0) return;
+  if ((lane & 15) == 0) a.q.scales[row * a.q.stride_row + (col >> 7) * a.q.stride_col] = g.scale;
+  write_codes(static_cast<uint8_t*>(a.q.data) + row * a.q.ld + col, y, g.inv, a.e5m2 != 0, valid);
 }
 
 __device__ __forceinline__ int chunk_valid(int64_t cols, int64_t col) {
@@ -74,31 +81,36 @@ __device__ __forceinline__ int chunk_valid(int64_t cols, int64_t col) {
 // forward
 // ---------------------------------------------------------------------------
 // Each block takes every gridDim.x-th row (or group of blockDim.y rows); the
-// next row's loads are under way while this one is reduced and written.
+// next row's loads are under way while this one is reduced and written.  h is
+// kept as it is stored, and the weight is read again for each row (from the L1
+// cache) where keeping it would cost the second block on an SM.
 template <typename T, int NCH>
-__global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
+constexpr int kForwardBlocks = NCH == 1 ? 4 : (sizeof(T) == 2 && NCH == 2 ? 2 : 1);   // per SM
+template <typename T, int NCH>
+__global__ void __launch_bounds__(kRowThreads<NCH>, kForwardBlocks<T, NCH>)
+    rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float slots[2][32];
   pdl_launch_dependents();
   pdl_wait();
   const bool vec = a.vec != 0;
   const int lane = threadIdx.x & 31;
-  constexpr bool KEEP_W = NCH <= 2;     // (four chunks' weights would spill: read again for each row)
-  float w[KEEP_W ? NCH : 1][8];
+  const int col0 = threadIdx.x * 8, chunk = blockDim.x * 8;    // column of chunk i: col0 + i * chunk
+  const float inv_cols = 1.0f / static_cast<float>(a.cols);
+  constexpr bool KEEP_W = NCH == 1;
+  float w[8];
   int valid[NCH];
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
-    valid[i] = chunk_valid(a.cols, col);
-    if (KEEP_W) load8_any(w[KEEP_W ? i : 0], a.weight, a.weight_type, col, valid[i], a.vec_w != 0);
-  }
+  for (int i = 0; i < NCH; ++i) valid[i] = chunk_valid(a.cols, col0 + i * chunk);
+  if (KEEP_W) load8_any(w, a.weight, a.weight_type, col0, valid[0], a.vec_w != 0);
   Raw8<T> rx[NCH], rr[NCH];
   auto fetch = [&](int64_t row) {
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx + col0;
+    const T* r = static_cast<const T*>(a.residual) + row * a.ld_res + col0;
+    const bool in = row < a.rows;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
-      const int n = row < a.rows ? valid[i] : 0;
-      load8(rx[i], static_cast<const T*>(a.x) + row * a.ldx + col, n, vec);
-      if (a.residual) load8(rr[i], static_cast<const T*>(a.residual) + row * a.ld_res + col, n, vec);
+      load8(rx[i], x + i * chunk, in ? valid[i] : 0, vec);
+      if (a.residual) load8(rr[i], r + i * chunk, in ? valid[i] : 0, vec);
     }
   };
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
@@ -108,44 +120,68 @@ __global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_kernel(const __grid_
   // (a block's spare rows take part in its barriers)
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * blockDim.y; base < a.rows; base += step, row += step, set ^= 1) {
     const bool live = row < a.rows;
-    float h[NCH][8];
+    Raw8<T> h[NCH];
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      unpack8(rx[i], h[i]);
+      float v[8];
+      unpack8(rx[i], v);
+      h[i] = rx[i];
       if (a.residual) {
         float r[8];
         unpack8(rr[i], r);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[i][k] += r[k];
-        pack8(h[i], rx[i]);
-        unpack8(rx[i], h[i]);             // the norm is of the rounded sum
-      }
-      if (a.h && live) {
-        const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
-        store8(static_cast<T*>(a.h) + row * a.ld_h + col, rx[i], valid[i], vec);
+        for (int k = 0; k < 8; ++k) v[k] += r[k];
+        pack8(v, h[i]);
+        unpack8(h[i], v);               // the norm is of the rounded sum
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(h[i][k], h[i][k], ss);
+      for (int k = 0; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
     }
     fetch(row + step);
+    if (a.h && live) {
+      T* to = static_cast<T*>(a.h) + row * a.ld_h + col0;
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) store8(to + i * chunk, h[i], valid[i], vec);
+    }
     ss = row_sum(ss, slots[set]);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.cols)) + a.eps));
+    const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
     if (a.rstd && live && threadIdx.x == 0) a.rstd[row] = rstd;
+    // y, the group maxima of all chunks, then their scales: the two divisions of
+    // a scale are made once for two chunks, by half of a group's lanes each.
+    float y[NCH][8];
+    uint32_t most[NCH];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
-      if (!KEEP_W) load8_any(w[0], a.weight, a.weight_type, col, valid[i], a.vec_w != 0);
-      const int n = live ? valid[i] : 0;
-      float y[8];
+      const int col = col0 + i * chunk;
+      if (!KEEP_W) load8_any(w, a.weight, a.weight_type, col, valid[i], a.vec_w != 0);
+      unpack8(h[i], y[i]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = h[i][k] * rstd * w[KEEP_W ? i : 0][k];
-      if (a.y) {
+      for (int k = 0; k < 8; ++k) y[i][k] = y[i][k] * rstd * w[k];
+      if (a.y && live) {
         Raw8<T> ry;
-        pack8(y, ry);
-        store8(static_cast<T*>(a.y) + row * a.ld_y + col, ry, n, vec);
+        pack8(y[i], ry);
+        store8(static_cast<T*>(a.y) + row * a.ld_y + col, ry, valid[i], vec);
       }
-      if (a.q.data) quantize_chunk(a, y, row, col, n, lane);
+      if (a.q.data) most[i] = group_max(y[i]);
+    }
+    if (!a.q.data) continue;
+    uint8_t* to = static_cast<uint8_t*>(a.q.data) + row * a.q.ld + col0;
+    float* scales = a.q.scales + row * a.q.stride_row;
+    constexpr int PAIRS = NCH > 1 ? 2 : 1;
+#pragma unroll
+    for (int i = 0; i < NCH; i += PAIRS) {
+      const bool second = PAIRS == 2 && (lane & 8);
+      const GroupScale g = group_scale(second ? most[i + PAIRS - 1] : most[i], a.fmax);
+      const int col = col0 + (i + (second ? 1 : 0)) * chunk;
+      // (the group's first column is inside the row exactly if the group has a scale)
+      if ((lane & (PAIRS == 2 ? 7 : 15)) == 0 && live && (col & ~127) < a.cols)
+        scales[(col >> 7) * a.q.stride_col] = g.scale;
+#pragma unroll
+      for (int u = 0; u < PAIRS; ++u) {
+        const float inv = PAIRS == 2 ? __shfl_sync(0xffffffffu, g.inv, (lane & 16) + 8 * u) : g.inv;
+        if (live) write_codes(to + (i + u) * chunk, y[i + u], inv, a.e5m2 != 0, valid[i + u]);
+      }
     }
   }
 }
@@ -160,6 +196,7 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(const __grid
   pdl_wait();
   const int64_t row = blockIdx.x;
   const bool vec = a.vec != 0;
+  const float inv_cols = 1.0f / static_cast<float>(a.cols);
   const int lane = threadIdx.x & 31;
   const int64_t step = static_cast<int64_t>(blockDim.x) * 8;
   auto form = [&](int64_t col, int valid, Raw8<T>& raw, float (&h)[8]) {
@@ -185,7 +222,7 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(const __grid
     for (int k = 0; k < 8; ++k) ss = fmaf(h[k], h[k], ss);
   }
   ss = row_sum(ss, slots);
-  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.cols)) + a.eps));
+  const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
   for (int64_t base = 0; base < a.cols; base += step) {   // (whole blocks: the shuffles need every lane)
     const int64_t c = base + static_cast<int64_t>(threadIdx.x) * 8;
@@ -434,7 +471,7 @@ RowShape row_shape(int64_t cols) {
 }
 
 // Blocks for `rows` rows, each looping over its own: what fits on the device at `per_sm` threads per SM.
-constexpr int kForwardThreads = 1024, kBackwardThreads = 512;
+constexpr int kBackwardThreads = 512;
 int64_t row_blocks(int64_t rows, const RowShape& s, int sm_count, int per_sm) {
   const int64_t want = (rows + s.rows - 1) / s.rows;
   const int at_once = per_sm / (s.threads * s.rows);
@@ -453,9 +490,11 @@ cudaError_t forward_type(const NormArgs& a, int sm_count, cudaStream_t stream, c
   }
   const RowShape s = row_shape(a.cols);
   auto k = s.chunks == 1 ? rmsnorm_kernel<T, 1> : (s.chunks == 2 ? rmsnorm_kernel<T, 2> : rmsnorm_kernel<T, 4>);
+  const int per_sm = s.chunks == 1 ? kForwardBlocks<T, 1> * kRowThreads<1>
+                                   : (s.chunks == 2 ? kForwardBlocks<T, 2> * kRowThreads<2> : kRowThreads<4>);
   *kernel = reinterpret_cast<const void*>(k);
   plan->threads = s.threads * s.rows;
-  plan->grid = static_cast<int32_t>(row_blocks(a.rows, s, sm_count, kForwardThreads));
+  plan->grid = static_cast<int32_t>(row_blocks(a.rows, s, sm_count, per_sm));
   return launch_dependent(k, dim3(static_cast<unsigned>(plan->grid)), dim3(s.threads, s.rows), 0, stream, a);
 }
 
