@@ -253,27 +253,6 @@ struct alignas(4 * sizeof(T)) Four {
   T e[4];
 };
 
-// Four neighbouring outputs of a row, `left` of them inside C: FP32 sums (+ addend) rounded to the output type.
-template <typename T>
-__device__ __forceinline__ void store4(T* c, const T* add, float4 v, bool vec, int64_t left) {
-  float x[4] = {v.x, v.y, v.z, v.w};
-  if (vec && left >= 4) {
-    if (add) {
-      const Four<T> a = *reinterpret_cast<const Four<T>*>(add);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] += widen(a.e[i]);
-    }
-    Four<T> o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o.e[i] = narrow<T>(x[i]);
-    *reinterpret_cast<Four<T>*>(c) = o;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < left) c[i] = narrow<T>(add ? x[i] + widen(add[i]) : x[i]);
-}
-
 template <typename T>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   const T v[2] = {narrow<T>(lo), narrow<T>(hi)};
@@ -366,17 +345,32 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
                    : "memory");
     __syncwarp();
     if (!full) {
-      const int64_t left = g.q.rows - col - j * CW;
+      // A tile that C ends in, or whose rows are off their alignment: one
+      // output per lane, CW lanes to a row, eight steps' addends at a time.
+      constexpr int AT_ONCE = 32 / CW;             // rows per step
+      const int cl = lane % CW, rl = lane / CW;
+      const int64_t q = q0 + j * CW + cl;
+      const int rows = q < g.q.rows ? static_cast<int>(g.p.rows - p0 < 32 ? g.p.rows - p0 : 32) : 0;   // (may be < 0)
+      const uint32_t from_col = static_cast<uint32_t>(cl / 4);
 #pragma unroll 1
-      for (int i = 0; i < PER; ++i) {
-        float4 v;
-        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                     : "r"(base + sw128_offset(i * (32 / PER) + lane / PER, lane % PER))
-                     : "memory");
-        T* o = out + i * (32 / PER) * g.ldc + j * CW;
-        const T* f = from ? from + i * (32 / PER) * g.ld_add + j * CW : nullptr;
-        if (row + i * (32 / PER) < g.p.rows && left > 0) store4<T>(o, f, v, g.vec != 0, left);
+      for (int r0 = rl; r0 < rows; r0 += 8 * AT_ONCE) {
+        T* o = c + (p0 + r0) * g.ldc + q;
+        T was[8];
+        if (ADD) {
+          const T* f = add + (p0 + r0) * g.ld_add + q;
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (r0 + u * AT_ONCE < rows) was[u] = f[u * AT_ONCE * g.ld_add];
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int r = r0 + u * AT_ONCE;
+          if (r < rows) {
+            float v;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(base + sw128_offset(r, from_col) + cl % 4 * 4) : "memory");
+            o[u * AT_ONCE * g.ldc] = narrow<T>(ADD ? v + widen(was[u]) : v);
+          }
+        }
       }
       continue;
     }
