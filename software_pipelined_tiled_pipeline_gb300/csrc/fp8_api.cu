@@ -35,6 +35,8 @@ int check_real(const void* p, int64_t ld, int64_t cols, int type, bool optional)
   return aligned(p, real_bytes(type)) ? GP_OK : GP_ERR_UNSUPPORTED;
 }
 
+constexpr int64_t kMaxNormCols = int64_t(1) << 30;   // column numbers plus a step stay below 2^31
+
 int first_error(std::initializer_list<int> codes) {
   for (int c : codes)
     if (c != GP_OK) return c;
@@ -151,6 +153,7 @@ int fp8_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ld_res
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   call_reset(st);
   int rc = check_sizes(rows, cols);
+  if (rc == GP_OK && cols > kMaxNormCols) rc = GP_ERR_SIZE;
   if (rc == GP_OK && (!real_ok(type) || !real_ok(weight_type) || !(eps >= 0.f))) rc = GP_ERR_ARG;
   if (rc != GP_OK) return call_finish(rc);
   if (rows == 0 || cols == 0) return call_finish(GP_OK);
@@ -199,6 +202,7 @@ int fp8_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t l
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   call_reset(st);
   int rc = check_sizes(rows, cols);
+  if (rc == GP_OK && cols > kMaxNormCols) rc = GP_ERR_SIZE;
   if (rc == GP_OK && (!real_ok(type) || !real_ok(weight_type))) rc = GP_ERR_ARG;
   if (rc != GP_OK) return call_finish(rc);
   if (cols == 0 || (rows == 0 && !dw)) return call_finish(GP_OK);

@@ -28,22 +28,32 @@ __device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
 __device__ __forceinline__ void from_f32(float v, __half& o) { o = __float2half_rn(v); }
 __device__ __forceinline__ void from_f32(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
 
-// Eight values at p, `valid` of them inside the row (the others read as 0).
-// vec: every chunk of the matrix starts on a 16-byte boundary.
+// A thread's eight columns of a group of 128: with rows on 16-byte boundaries
+// (vec) columns c .. c + 7, c a multiple of 8, else every 16th from (c / 8) mod
+// 16 on, so that the 16 lanes of a group still read neighbouring values.  A
+// group is the same 16 lanes either way.
+struct Eight {
+  int first, stride;
+};
+__device__ __forceinline__ Eight eight_columns(int c, bool vec) {
+  return vec ? Eight{c, 1} : Eight{(c & ~127) + ((c >> 3) & 15), 16};
+}
+
+// The eight values of a row of `cols` (those past its end read as 0; cols 0: nothing is read).
 template <typename T>
-__device__ __forceinline__ void load8(Raw8<T>& r, const T* p, int valid, bool vec) {
-  if (vec && valid >= 8) {
+__device__ __forceinline__ void load8(Raw8<T>& r, const T* row, int c, int cols, bool vec) {
+  if (vec && c + 8 <= cols) {
 #pragma unroll
-    for (int i = 0; i < Raw8<T>::WORDS; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+    for (int i = 0; i < Raw8<T>::WORDS; ++i) r.w[i] = reinterpret_cast<const uint4*>(row + c)[i];
     return;
   }
+  const Eight e = eight_columns(c, vec);
+  const T* p = row + e.first;
   T t[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (i < valid)
-      t[i] = p[i];
-    else
-      from_f32(0.f, t[i]);
+    from_f32(0.f, t[i]);
+    if (e.first + i * e.stride < cols) t[i] = p[i * e.stride];
   }
   memcpy(&r, t, sizeof(t));
 }
@@ -99,34 +109,42 @@ __device__ __forceinline__ void pack8(const float (&v)[8], Raw8<T>& r) {
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const Raw8<T>& r, int valid, bool vec) {
-  if (vec && valid >= 8) {
+__device__ __forceinline__ void store8(T* row, const Raw8<T>& r, int c, int cols, bool vec) {
+  if (vec && c + 8 <= cols) {
 #pragma unroll
-    for (int i = 0; i < Raw8<T>::WORDS; ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
+    for (int i = 0; i < Raw8<T>::WORDS; ++i) reinterpret_cast<uint4*>(row + c)[i] = r.w[i];
     return;
   }
+  const Eight e = eight_columns(c, vec);
+  T* p = row + e.first;
   T t[8];
   memcpy(t, &r, sizeof(t));
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (i < valid) p[i] = t[i];
+    if (e.first + i * e.stride < cols) p[i * e.stride] = t[i];
 }
 
-// Eight values of a vector of one of the gp_real types, as FP32.
-__device__ __forceinline__ void load8_any(float (&v)[8], const void* base, int type, int64_t at, int valid, bool vec) {
-  if (type == GP_REAL_F32) {
-    Raw8<float> r;
-    load8(r, static_cast<const float*>(base) + at, valid, vec);
-    unpack8(r, v);
-  } else if (type == GP_REAL_BF16) {
-    Raw8<__nv_bfloat16> r;
-    load8(r, static_cast<const __nv_bfloat16*>(base) + at, valid, vec);
-    unpack8(r, v);
-  } else {
-    Raw8<__half> r;
-    load8(r, static_cast<const __half*>(base) + at, valid, vec);
-    unpack8(r, v);
+// The eight values of a vector of one of the gp_real types, as FP32.  aligned: the vector is on a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ void load8_as(float (&v)[8], const void* base, int c, int cols, bool vec, bool aligned) {
+  Raw8<T> r;
+  if (vec && !aligned) {     // columns c .. c + 7 one by one
+    const T* p = static_cast<const T*>(base) + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_f32(p[i]) : 0.f;
+    return;
   }
+  load8(r, static_cast<const T*>(base), c, cols, vec);
+  unpack8(r, v);
+}
+__device__ __forceinline__ void load8_any(float (&v)[8], const void* base, int type, int c, int cols, bool vec,
+                                          bool aligned) {
+  if (type == GP_REAL_F32)
+    load8_as<float>(v, base, c, cols, vec, aligned);
+  else if (type == GP_REAL_BF16)
+    load8_as<__nv_bfloat16>(v, base, c, cols, vec, aligned);
+  else
+    load8_as<__half>(v, base, c, cols, vec, aligned);
 }
 
 // Value k of eight as FP32.
@@ -195,15 +213,17 @@ __device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
   return fp8x2<E5M2>(a, b) | (fp8x2<E5M2>(c, d) << 16);
 }
 
-// Eight codes at p (8-byte aligned), `valid` of them inside the row.
-__device__ __forceinline__ void store_codes8(uint8_t* p, uint2 codes, int valid) {
-  if (valid >= 8) {
-    *reinterpret_cast<uint2*>(p) = codes;
+// The eight codes of a row (which begins on a 16-byte boundary).
+__device__ __forceinline__ void store_codes8(uint8_t* row, uint2 codes, int c, int cols, bool vec) {
+  if (vec && c + 8 <= cols) {
+    *reinterpret_cast<uint2*>(row + c) = codes;
     return;
   }
+  const Eight e = eight_columns(c, vec);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (i < valid) p[i] = static_cast<uint8_t>((i < 4 ? codes.x : codes.y) >> (8 * (i & 3)));
+    if (e.first + i * e.stride < cols)
+      row[e.first + i * e.stride] = static_cast<uint8_t>((i < 4 ? codes.x : codes.y) >> (8 * (i & 3)));
 }
 
 }  // namespace gp

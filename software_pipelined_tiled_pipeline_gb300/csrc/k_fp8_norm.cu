@@ -52,31 +52,17 @@ __device__ __forceinline__ uint32_t group_max(const float (&y)[8]) {
   for (int d = 1; d < 16; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
   return m;
 }
-__device__ __forceinline__ void write_codes(uint8_t* p, const float (&y)[8], float inv, bool e5m2, int valid) {
+__device__ __forceinline__ void write_codes(uint8_t* row, const float (&y)[8], float inv, const NormArgs& a, int c) {
   uint2 w;
-  if (e5m2) {
+  if (a.e5m2) {
     w.x = fp8x4<true>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
     w.y = fp8x4<true>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
   } else {
     w.x = fp8x4<false>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
     w.y = fp8x4<false>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
   }
-  store_codes8(p, w, valid);
+  store_codes8(row, w, c, static_cast<int>(a.cols), a.vec != 0);
 }
-// y of one chunk to its 8-bit codes; the 16 lanes of a group agree on its scale.
-__device__ __forceinline__ void quantize_chunk(const NormArgs& a, const float (&y)[8], int64_t row, int64_t col,
-                                               int valid, int lane) {
-  const GroupScale g = group_scale(group_max(y), a.fmax);
-  if (valid <= 0) return;
-  if ((lane & 15) == 0) a.q.scales[row * a.q.stride_row + (col >> 7) * a.q.stride_col] = g.scale;
-  write_codes(static_cast<uint8_t*>(a.q.data) + row * a.q.ld + col, y, g.inv, a.e5m2 != 0, valid);
-}
-
-__device__ __forceinline__ int chunk_valid(int64_t cols, int64_t col) {
-  const int64_t left = cols - col;
-  return left <= 0 ? 0 : (left >= 8 ? 8 : static_cast<int>(left));
-}
-
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
@@ -94,23 +80,21 @@ __global__ void __launch_bounds__(kRowThreads<NCH>, kForwardBlocks<T, NCH>)
   pdl_wait();
   const bool vec = a.vec != 0;
   const int lane = threadIdx.x & 31;
+  const int cols = static_cast<int>(a.cols);
   const int col0 = threadIdx.x * 8, chunk = blockDim.x * 8;    // column of chunk i: col0 + i * chunk
   const float inv_cols = 1.0f / static_cast<float>(a.cols);
   constexpr bool KEEP_W = NCH == 1;
   float w[8];
-  int valid[NCH];
-#pragma unroll
-  for (int i = 0; i < NCH; ++i) valid[i] = chunk_valid(a.cols, col0 + i * chunk);
-  if (KEEP_W) load8_any(w, a.weight, a.weight_type, col0, valid[0], a.vec_w != 0);
+  if (KEEP_W) load8_any(w, a.weight, a.weight_type, col0, cols, vec, a.vec_w != 0);
   Raw8<T> rx[NCH], rr[NCH];
   auto fetch = [&](int64_t row) {
-    const T* x = static_cast<const T*>(a.x) + row * a.ldx + col0;
-    const T* r = static_cast<const T*>(a.residual) + row * a.ld_res + col0;
-    const bool in = row < a.rows;
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const T* r = static_cast<const T*>(a.residual) + row * a.ld_res;
+    const int n = row < a.rows ? cols : 0;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      load8(rx[i], x + i * chunk, in ? valid[i] : 0, vec);
-      if (a.residual) load8(rr[i], r + i * chunk, in ? valid[i] : 0, vec);
+      load8(rx[i], x, col0 + i * chunk, n, vec);
+      if (a.residual) load8(rr[i], r, col0 + i * chunk, n, vec);
     }
   };
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
@@ -140,9 +124,9 @@ __global__ void __launch_bounds__(kRowThreads<NCH>, kForwardBlocks<T, NCH>)
     }
     fetch(row + step);
     if (a.h && live) {
-      T* to = static_cast<T*>(a.h) + row * a.ld_h + col0;
+      T* to = static_cast<T*>(a.h) + row * a.ld_h;
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) store8(to + i * chunk, h[i], valid[i], vec);
+      for (int i = 0; i < NCH; ++i) store8(to, h[i], col0 + i * chunk, cols, vec);
     }
     ss = row_sum(ss, slots[set]);
     const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
@@ -154,19 +138,19 @@ __global__ void __launch_bounds__(kRowThreads<NCH>, kForwardBlocks<T, NCH>)
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int col = col0 + i * chunk;
-      if (!KEEP_W) load8_any(w, a.weight, a.weight_type, col, valid[i], a.vec_w != 0);
+      if (!KEEP_W) load8_any(w, a.weight, a.weight_type, col, cols, vec, a.vec_w != 0);
       unpack8(h[i], y[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) y[i][k] = y[i][k] * rstd * w[k];
       if (a.y && live) {
         Raw8<T> ry;
         pack8(y[i], ry);
-        store8(static_cast<T*>(a.y) + row * a.ld_y + col, ry, valid[i], vec);
+        store8(static_cast<T*>(a.y) + row * a.ld_y, ry, col, cols, vec);
       }
       if (a.q.data) most[i] = group_max(y[i]);
     }
     if (!a.q.data) continue;
-    uint8_t* to = static_cast<uint8_t*>(a.q.data) + row * a.q.ld + col0;
+    uint8_t* to = static_cast<uint8_t*>(a.q.data) + row * a.q.ld;
     float* scales = a.q.scales + row * a.q.stride_row;
     constexpr int PAIRS = NCH > 1 ? 2 : 1;
 #pragma unroll
@@ -180,7 +164,7 @@ __global__ void __launch_bounds__(kRowThreads<NCH>, kForwardBlocks<T, NCH>)
 #pragma unroll
       for (int u = 0; u < PAIRS; ++u) {
         const float inv = PAIRS == 2 ? __shfl_sync(0xffffffffu, g.inv, (lane & 16) + 8 * u) : g.inv;
-        if (live) write_codes(to + (i + u) * chunk, y[i + u], inv, a.e5m2 != 0, valid[i + u]);
+        if (live) write_codes(to, y[i + u], inv, a, col0 + (i + u) * chunk);
       }
     }
   }
@@ -198,57 +182,80 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(const __grid
   const bool vec = a.vec != 0;
   const float inv_cols = 1.0f / static_cast<float>(a.cols);
   const int lane = threadIdx.x & 31;
-  const int64_t step = static_cast<int64_t>(blockDim.x) * 8;
-  auto form = [&](int64_t col, int valid, Raw8<T>& raw, float (&h)[8]) {
-    load8(raw, static_cast<const T*>(a.x) + row * a.ldx + col, valid, vec);
+  const int cols = static_cast<int>(a.cols), step = blockDim.x * 8;
+  const T* const x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* const res = static_cast<const T*>(a.residual) + row * a.ld_res;
+  T* const to = static_cast<T*>(a.h) + row * a.ld_h;
+  auto form = [&](int c, Raw8<T>& raw, float (&h)[8]) {
+    load8(raw, x, c, cols, vec);
     unpack8(raw, h);
     if (!a.residual) return;
     float r[8];
-    load8(raw, static_cast<const T*>(a.residual) + row * a.ld_res + col, valid, vec);
+    load8(raw, res, c, cols, vec);
     unpack8(raw, r);
 #pragma unroll
     for (int k = 0; k < 8; ++k) h[k] += r[k];
     pack8(h, raw);
     unpack8(raw, h);
   };
+  // (whole groups of 128 columns: with rows off their alignment the last one's lanes each hold some of it)
+  const int64_t end = (a.cols + 127) / 128 * 128;
   float ss = 0.f;
-  for (int64_t c = static_cast<int64_t>(threadIdx.x) * 8; c < a.cols; c += step) {
-    const int valid = chunk_valid(a.cols, c);
+  for (int64_t at = threadIdx.x * 8; at < end; at += step) {
+    const int c = static_cast<int>(at);
     Raw8<T> raw;
     float h[8];
-    form(c, valid, raw, h);
-    if (a.h) store8(static_cast<T*>(a.h) + row * a.ld_h + c, raw, valid, vec);
+    form(c, raw, h);
+    if (a.h) store8(to, raw, c, cols, vec);
 #pragma unroll
     for (int k = 0; k < 8; ++k) ss = fmaf(h[k], h[k], ss);
   }
   ss = row_sum(ss, slots);
   const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-  for (int64_t base = 0; base < a.cols; base += step) {   // (whole blocks: the shuffles need every lane)
-    const int64_t c = base + static_cast<int64_t>(threadIdx.x) * 8;
-    const int valid = chunk_valid(a.cols, c);
+  for (int64_t base = 0; base < end; base += step) {   // (whole blocks: the shuffles need every lane)
+    const int64_t at = base + threadIdx.x * 8;
+    const int n = at < end ? cols : 0;
+    const int c = at < end ? static_cast<int>(at) : 0;
     Raw8<T> raw;
     float h[8], w[8];
     if (a.h) {
-      load8(raw, static_cast<const T*>(a.h) + row * a.ld_h + c, valid, vec);
+      load8(raw, to, c, n, vec);
       unpack8(raw, h);
     } else {
-      form(c, valid, raw, h);
+      form(c, raw, h);
     }
-    load8_any(w, a.weight, a.weight_type, c, valid, a.vec_w != 0);
+    load8_any(w, a.weight, a.weight_type, c, n, vec, a.vec_w != 0);
 #pragma unroll
     for (int k = 0; k < 8; ++k) w[k] = h[k] * rstd * w[k];
     if (a.y) {
       pack8(w, raw);
-      store8(static_cast<T*>(a.y) + row * a.ld_y + c, raw, valid, vec);
+      store8(static_cast<T*>(a.y) + row * a.ld_y, raw, c, n, vec);
     }
-    if (a.q.data) quantize_chunk(a, w, row, c, valid, lane);
+    if (!a.q.data) continue;
+    const GroupScale g = group_scale(group_max(w), a.fmax);
+    if (n == 0) continue;                              // (a whole group's lanes alike)
+    if ((lane & 15) == 0) a.q.scales[row * a.q.stride_row + (c >> 7) * a.q.stride_col] = g.scale;
+    write_codes(static_cast<uint8_t*>(a.q.data) + row * a.q.ld, w, g.inv, a, c);
   }
 }
 
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
+// A thread's eight column sums to its row of the partial sums.
+__device__ __forceinline__ void store_sums(float* row, const float (&v)[8], int c, int cols, bool vec) {
+  if (vec && cols % 4 == 0 && c + 8 <= cols) {
+    reinterpret_cast<float4*>(row + c)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(row + c)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+  const Eight e = eight_columns(c, vec);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (e.first + k * e.stride < cols) row[e.first + k * e.stride] = v[k];
+}
+
 // Each block takes every gridDim.x-th row (or group of blockDim.y rows) and
 // keeps its columns' share of the weight's gradient in registers; the blocks'
 // shares are added in order by sum_parts_kernel.
@@ -262,13 +269,12 @@ __global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_grad_kernel(const __
   // The weight stays in registers where they suffice (the loads of four chunks
   // would spill), else each row reads it again from the L1 cache.
   constexpr bool KEEP_W = NCH <= 2;
+  const int cols = static_cast<int>(a.cols);
+  const int col0 = threadIdx.x * 8, chunk = blockDim.x * 8;    // column of chunk i: col0 + i * chunk
   float w[KEEP_W ? NCH : 1][8], dw[NCH][8];
-  int valid[NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
-    valid[i] = chunk_valid(a.cols, col);
-    if (KEEP_W) load8_any(w[KEEP_W ? i : 0], a.weight, a.weight_type, col, valid[i], a.vec_w != 0);
+    if (KEEP_W) load8_any(w[KEEP_W ? i : 0], a.weight, a.weight_type, col0 + i * chunk, cols, vec, a.vec_w != 0);
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[i][k] = 0.f;
   }
@@ -278,13 +284,15 @@ __global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_grad_kernel(const __
   float nrstd = 0.f;
   auto fetch = [&](int64_t row) {
     const bool in = row < a.rows;
+    const int n = in ? cols : 0;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.ld_dy;
+    const T* h = static_cast<const T*>(a.h) + row * a.ld_h;
+    const T* r = static_cast<const T*>(a.dres) + row * a.ld_dres;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
-      const int n = in ? valid[i] : 0;
-      load8(ndy[i], static_cast<const T*>(a.dy) + row * a.ld_dy + col, n, vec);
-      load8(nh[i], static_cast<const T*>(a.h) + row * a.ld_h + col, n, vec);
-      if (a.dres) load8(nr[i], static_cast<const T*>(a.dres) + row * a.ld_dres + col, n, vec);
+      load8(ndy[i], dy, col0 + i * chunk, n, vec);
+      load8(nh[i], h, col0 + i * chunk, n, vec);
+      if (a.dres) load8(nr[i], r, col0 + i * chunk, n, vec);
     }
     nrstd = in ? a.rstd[row] : 0.f;
   };
@@ -308,8 +316,7 @@ __global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_grad_kernel(const __
     for (int i = 0; i < NCH; ++i) {
       const int wi = KEEP_W ? i : 0;
       if (!KEEP_W)
-        load8_any(w[0], a.weight, a.weight_type, (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8, valid[i],
-                  a.vec_w != 0);
+        load8_any(w[0], a.weight, a.weight_type, col0 + i * chunk, cols, vec, a.vec_w != 0);
       float dy[8], h[8];
       unpack8(rdy[i], dy);
       unpack8(rh[i], h);
@@ -326,9 +333,9 @@ __global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_grad_kernel(const __
     if (!live) continue;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
+      const int col = col0 + i * chunk;
       const int wi = KEEP_W ? i : 0;
-      if (!KEEP_W) load8_any(w[0], a.weight, a.weight_type, col, valid[i], a.vec_w != 0);
+      if (!KEEP_W) load8_any(w[0], a.weight, a.weight_type, col, cols, vec, a.vec_w != 0);
       float dy[8], h[8], o[8];
       unpack8(rdy[i], dy);
       unpack8(rh[i], h);
@@ -342,19 +349,13 @@ __global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_grad_kernel(const __
       }
       Raw8<T> out;
       pack8(o, out);
-      store8(static_cast<T*>(a.dx) + row * a.ld_dx + col, out, valid[i], vec);
+      store8(static_cast<T*>(a.dx) + row * a.ld_dx, out, col, cols, vec);
     }
   }
   if (!a.partials) return;
   float* part = a.partials + (static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y) * a.cols;
-  const bool vec_p = a.cols % 4 == 0;
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int64_t col = (static_cast<int64_t>(i) * blockDim.x + threadIdx.x) * 8;
-    Raw8<float> out;
-    pack8(dw[i], out);
-    store8(part + col, out, valid[i], vec_p);
-  }
+  for (int i = 0; i < NCH; ++i) store_sums(part, dw[i], col0 + i * chunk, cols, vec);
 }
 
 // Rows longer than kRowsMaxCols: dx in two passes over the row, dw by columns.
@@ -366,19 +367,20 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_long_kernel(const _
   const int64_t row = blockIdx.x;
   const bool vec = a.vec != 0;
   const float rstd = a.rstd[row];
-  const int64_t step = static_cast<int64_t>(blockDim.x) * 8;
+  const int cols = static_cast<int>(a.cols), step = blockDim.x * 8;
+  const int64_t end = (a.cols + 127) / 128 * 128;
   float sum = 0.f;
   for (int pass = 0; pass < 2; ++pass) {
     const float mean = pass ? row_sum(sum, slots) / static_cast<float>(a.cols) : 0.f;
-    for (int64_t c = static_cast<int64_t>(threadIdx.x) * 8; c < a.cols; c += step) {
-      const int valid = chunk_valid(a.cols, c);
+    for (int64_t at = threadIdx.x * 8; at < end; at += step) {
+      const int c = static_cast<int>(at);
       Raw8<T> raw;
       float dy[8], h[8], w[8];
-      load8(raw, static_cast<const T*>(a.dy) + row * a.ld_dy + c, valid, vec);
+      load8(raw, static_cast<const T*>(a.dy) + row * a.ld_dy, c, cols, vec);
       unpack8(raw, dy);
-      load8(raw, static_cast<const T*>(a.h) + row * a.ld_h + c, valid, vec);
+      load8(raw, static_cast<const T*>(a.h) + row * a.ld_h, c, cols, vec);
       unpack8(raw, h);
-      load8_any(w, a.weight, a.weight_type, c, valid, a.vec_w != 0);
+      load8_any(w, a.weight, a.weight_type, c, cols, vec, a.vec_w != 0);
       if (pass == 0) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) sum = fmaf(dy[k] * (h[k] * rstd), w[k], sum);
@@ -389,13 +391,13 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_long_kernel(const _
       for (int k = 0; k < 8; ++k) o[k] = rstd * (dy[k] * w[k] - h[k] * rstd * mean);
       if (a.dres) {
         float r[8];
-        load8(raw, static_cast<const T*>(a.dres) + row * a.ld_dres + c, valid, vec);
+        load8(raw, static_cast<const T*>(a.dres) + row * a.ld_dres, c, cols, vec);
         unpack8(raw, r);
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] += r[k];
       }
       pack8(o, raw);
-      store8(static_cast<T*>(a.dx) + row * a.ld_dx + c, raw, valid, vec);
+      store8(static_cast<T*>(a.dx) + row * a.ld_dx, raw, c, cols, vec);
     }
   }
 }
@@ -406,24 +408,24 @@ template <typename T>
 __global__ void __launch_bounds__(256) rmsnorm_dw_long_kernel(const __grid_constant__ NormGradArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t c = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 8;
-  const int valid = chunk_valid(a.cols, c);
+  const int cols = static_cast<int>(a.cols);
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 8;
+  if (at >= (a.cols + 127) / 128 * 128) return;
+  const int c = static_cast<int>(at);
   const int parts = gridDim.y;
   float dw[8] = {};
   for (int64_t row = blockIdx.y; row < a.rows; row += parts) {
     Raw8<T> raw;
     float dy[8], h[8];
-    load8(raw, static_cast<const T*>(a.dy) + row * a.ld_dy + c, valid, a.vec != 0);
+    load8(raw, static_cast<const T*>(a.dy) + row * a.ld_dy, c, cols, a.vec != 0);
     unpack8(raw, dy);
-    load8(raw, static_cast<const T*>(a.h) + row * a.ld_h + c, valid, a.vec != 0);
+    load8(raw, static_cast<const T*>(a.h) + row * a.ld_h, c, cols, a.vec != 0);
     unpack8(raw, h);
     const float rstd = a.rstd[row];
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[k] += dy[k] * (h[k] * rstd);
   }
-  Raw8<float> out;
-  pack8(dw, out);
-  store8(a.partials + static_cast<int64_t>(blockIdx.y) * a.cols + c, out, valid, a.cols % 4 == 0);
+  store_sums(a.partials + static_cast<int64_t>(blockIdx.y) * a.cols, dw, c, cols, a.vec != 0);
 }
 
 // dw[c] = sum over parts of partials[part][c], in a fixed order: 8 threads per
@@ -462,7 +464,7 @@ struct RowShape {
 };
 RowShape row_shape(int64_t cols) {
   RowShape s;
-  const int64_t chunks = (cols + 7) / 8;
+  const int64_t chunks = (cols + 127) / 128 * 16;   // (whole groups: see Eight)
   s.chunks = chunks <= kRowThreads<1> ? 1 : (chunks <= 2 * kRowThreads<2> ? 2 : 4);
   const int64_t per = (chunks + s.chunks - 1) / s.chunks;
   s.threads = static_cast<int>((per + 31) / 32 * 32);
@@ -504,7 +506,7 @@ cudaError_t backward_type(const NormGradArgs& a, int sm_count, cudaStream_t stre
   if (a.cols > kRowsMaxCols) {
     cudaError_t e;
     if (a.partials) {
-      const int64_t chunks = (a.cols + 7) / 8;
+      const int64_t chunks = (a.cols + 127) / 128 * 16;
       const dim3 grid(static_cast<unsigned>((chunks + 255) / 256),
                       static_cast<unsigned>(a.rows < kLongParts ? a.rows : kLongParts));
       if ((e = launch_dependent(rmsnorm_dw_long_kernel<T>, grid, dim3(256), 0, stream, a)) != cudaSuccess) return e;

@@ -28,18 +28,16 @@ struct QuantArgs {
   int64_t tiles_c;       // tiles along the columns
   float fmax;
   int32_t e5m2;
-  int32_t vec;           // x's chunks of 8 values are 16-byte aligned
 };
 
-// Codes of the thread's eight rows, 8 at a time along each row.
-template <bool E5M2, typename T>
+// Codes of the thread's eight rows, 8 at a time along each row (c: the thread's columns in the tile's row r).
+template <bool E5M2, bool VEC, typename T>
 __device__ __forceinline__ void write_rows(const Raw8<T> (&v)[8], const float (&inv)[8], const QuantArgs& a,
-                                           int64_t r, int64_t c, int rows_in, int cols_in) {
-  if (cols_in <= 0) return;
-  uint8_t* out = static_cast<uint8_t*>(a.q.data) + r * a.q.ld + c;
+                                           int64_t r, int64_t c0, int c, int rows_in, int cols_in, bool whole) {
+  uint8_t* out = static_cast<uint8_t*>(a.q.data) + r * a.q.ld + c0;
 #pragma unroll
   for (int i = 0; i < 8; ++i, out += a.q.ld) {
-    if (i >= rows_in) break;
+    if (!whole && i >= rows_in) break;
     const float f = inv[i];
     float x[8];
 #pragma unroll
@@ -47,30 +45,36 @@ __device__ __forceinline__ void write_rows(const Raw8<T> (&v)[8], const float (&
     uint2 w;
     w.x = fp8x4<E5M2>(x[0], x[1], x[2], x[3]);
     w.y = fp8x4<E5M2>(x[4], x[5], x[6], x[7]);
-    store_codes8(out, w, cols_in);
+    if (whole)
+      *reinterpret_cast<uint2*>(out + c) = w;
+    else
+      store_codes8(out, w, c, cols_in, VEC);
   }
 }
 
 // The transposed tile in shared memory: 128 rows (x's columns) of 16 words of
-// 8 bytes; word w of row 8 k + j lies at w ^ k, so that the 16 threads of half
-// a warp (k = 0..15, one w) and the 8 readers of a row touch all banks once.
+// 8 bytes; word w of a row that belongs to thread k of its 16 lies at w ^ k, so
+// that the 16 threads of half a warp (k = 0..15, one w) and the 8 readers of a
+// row touch all banks once.
 template <bool E5M2, typename T>
-__device__ __forceinline__ void stage_columns(const Raw8<T> (&v)[8], const float* inv_col, uint2* tile, int rb, int cc) {
+__device__ __forceinline__ void stage_columns(const Raw8<T> (&v)[8], const float* inv_col, uint2* tile, int rb, int cc, Eight e) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float f = inv_col[cc * 8 + j];
+    const int col = e.first + j * e.stride;
+    const float f = inv_col[col];
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = value_of(v[i], j) * f;
     uint2 w;
     w.x = fp8x4<E5M2>(x[0], x[1], x[2], x[3]);
     w.y = fp8x4<E5M2>(x[4], x[5], x[6], x[7]);
-    tile[(cc * 8 + j) * 16 + (rb ^ cc)] = w;
+    tile[col * 16 + (rb ^ cc)] = w;
   }
 }
 
-template <typename T, bool BLOCKS>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constant__ QuantArgs a) {
+// VEC: x's rows are on 16-byte boundaries.
+template <typename T, bool BLOCKS, bool VEC>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quantize_kernel(const __grid_constant__ QuantArgs a) {
   __shared__ __align__(16) uint2 tile[kTile * 16];      // 16 KB
   __shared__ uint32_t part[8 * kTile];                  // per warp: column maxima (or one block maximum)
   __shared__ float inv_col[kTile];
@@ -81,16 +85,25 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
   const int rb = t >> 4, cc = t & 15;
   const int64_t tr = blockIdx.x / a.tiles_c, tc = blockIdx.x - tr * a.tiles_c;
   const int64_t r0 = tr * kTile, c0 = tc * kTile;
-  const int64_t r = r0 + rb * 8, c = c0 + cc * 8;
+  const int64_t r = r0 + rb * 8;
+  const int c = cc * 8;                                       // the thread's columns (see Eight) in the tile
+  const Eight e = eight_columns(c, VEC);
   const int rows_in = static_cast<int>(a.rows - r < 0 ? 0 : (a.rows - r > 8 ? 8 : a.rows - r));
-  const int cols_in = static_cast<int>(a.cols - c < 0 ? 0 : (a.cols - c > 8 ? 8 : a.cols - c));
+  const int cols_in = static_cast<int>(a.cols - c0 > kTile ? kTile : a.cols - c0);
 
   // The values stay as they came (16-bit ones two to a register), so that four
   // blocks of 16-bit tiles fit on an SM and its loads overlap their work.
   Raw8<T> v[8];
-  const T* x = static_cast<const T*>(a.x) + r * a.ldx + c;
+  const T* x = static_cast<const T*>(a.x) + r * a.ldx + c0;
+  // (a whole tile's loads and stores carry no checks: every thread of the block takes the same way)
+  const bool whole = VEC && a.rows - r0 >= kTile && cols_in == kTile;
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load8(v[i], x + i * a.ldx, i < rows_in ? cols_in : 0, a.vec != 0);
+    for (int i = 0; i < 8; ++i) load8(v[i], x + i * a.ldx, c, kTile, true);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load8(v[i], x + i * a.ldx, c, i < rows_in ? cols_in : 0, VEC);
+  }
   constexpr int WORDS = static_cast<int>(sizeof(T)) * 2;       // 32-bit words of eight values
   constexpr int PER = 8 / WORDS;                                // values per word
   auto word = [&](int i, int k) { return raw_abs<T>(reinterpret_cast<const uint32_t*>(&v[i])[k]); };
@@ -119,8 +132,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
       float inv[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) inv[i] = g.inv;
-      if (a.e5m2) write_rows<true>(v, inv, a, r, c, rows_in, cols_in);
-      else write_rows<false>(v, inv, a, r, c, rows_in, cols_in);
+      if (a.e5m2) write_rows<true, VEC>(v, inv, a, r, c0, c, rows_in, cols_in, whole);
+      else write_rows<false, VEC>(v, inv, a, r, c0, c, rows_in, cols_in, whole);
     }
     if (!a.qt.data) return;
     if (t < kTile) inv_col[t] = g.inv;
@@ -135,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
         m = raw_max<T>(m, __shfl_xor_sync(0xffffffffu, m, 16));
         if (lane < 16) {
 #pragma unroll
-          for (int u = 0; u < PER; ++u) part[warp * kTile + cc * 8 + k * PER + u] = raw_to_bits<T>(m, u);
+          for (int u = 0; u < PER; ++u) part[warp * kTile + e.first + (k * PER + u) * e.stride] = raw_to_bits<T>(m, u);
         }
       }
     }
@@ -156,8 +169,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
 #pragma unroll
       for (int i = 0; i < 8; ++i) inv[i] = __shfl_sync(0xffffffffu, g.inv, (lane & 16) + i);
       if (cc < rows_in) a.q.scales[(r + cc) * a.q.stride_row + tc * a.q.stride_col] = g.scale;   // (rows_in <= 8)
-      if (a.e5m2) write_rows<true>(v, inv, a, r, c, rows_in, cols_in);
-      else write_rows<false>(v, inv, a, r, c, rows_in, cols_in);
+      if (a.e5m2) write_rows<true, VEC>(v, inv, a, r, c0, c, rows_in, cols_in, whole);
+      else write_rows<false, VEC>(v, inv, a, r, c0, c, rows_in, cols_in, whole);
     }
     if (!a.qt.data) return;
     __syncthreads();
@@ -171,15 +184,15 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
     }
   }
   __syncthreads();
-  if (a.e5m2) stage_columns<true>(v, inv_col, tile, rb, cc);
-  else stage_columns<false>(v, inv_col, tile, rb, cc);
+  if (a.e5m2) stage_columns<true>(v, inv_col, tile, rb, cc, e);
+  else stage_columns<false>(v, inv_col, tile, rb, cc, e);
   __syncthreads();
   uint8_t* out = static_cast<uint8_t*>(a.qt.data);
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
     const int idx = it * kThreads + t;
     const int col = idx >> 3, pair = idx & 7;          // 16 rows of x: words 2 pair and 2 pair + 1
-    const int k = col >> 3;
+    const int k = VEC ? col >> 3 : col & 15;        // the thread that holds it
     uint4 w = *reinterpret_cast<const uint4*>(&tile[col * 16 + ((2 * pair) ^ (k & 14))]);
     if (k & 1) w = make_uint4(w.z, w.w, w.x, w.y);
     const int64_t row = r0 + pair * 16;
@@ -188,15 +201,18 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
     if (row + 16 <= a.rows) {
       *reinterpret_cast<uint4*>(p) = w;
     } else {
-      store_codes8(p, make_uint2(w.x, w.y), static_cast<int>(a.rows - row));
-      if (a.rows - row > 8) store_codes8(p + 8, make_uint2(w.z, w.w), static_cast<int>(a.rows - row - 8));
+      const int left = static_cast<int>(a.rows - row);
+      store_codes8(p, make_uint2(w.x, w.y), 0, left, true);
+      store_codes8(p, make_uint2(w.z, w.w), 8, left, true);
     }
   }
 }
 
 template <typename T>
 cudaError_t launch_type(const QuantArgs& a, bool blocks, int64_t tiles, cudaStream_t stream, const void** kernel) {
-  auto k = blocks ? quantize_kernel<T, true> : quantize_kernel<T, false>;
+  const bool vec = vec16(a.x, a.ldx, sizeof(T));
+  auto k = blocks ? (vec ? quantize_kernel<T, true, true> : quantize_kernel<T, true, false>)
+                  : (vec ? quantize_kernel<T, false, true> : quantize_kernel<T, false, false>);
   *kernel = reinterpret_cast<const void*>(k);
   return launch_dependent(k, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), 0, stream, a);
 }
@@ -217,7 +233,6 @@ cudaError_t launch_fp8_quantize(const void* x, int64_t ldx, int64_t rows, int64_
   a.e5m2 = any.format == GP_E5M2;
   a.fmax = a.e5m2 ? 57344.f : 448.f;
   a.tiles_c = (cols + kTile - 1) / kTile;
-  a.vec = vec16(x, ldx, real_bytes(type));
   const int64_t tiles = a.tiles_c * ((rows + kTile - 1) / kTile);
   plan->kernel = "fp8_quantize";
   plan->threads = kThreads;

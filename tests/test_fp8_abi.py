@@ -87,7 +87,7 @@ def norm(gp, x=PTR, ldx=256, res=None, ld_res=256, w=PTR, wtype=1, eps=1e-6, row
 
 @pytest.mark.parametrize("args,code", [
     (dict(x=None), "ARG"), (dict(w=None), "ARG"), (dict(type=5), "ARG"), (dict(wtype=-1), "ARG"), (dict(eps=-1.0), "ARG"),
-    (dict(eps=float("nan")), "ARG"), (dict(rows=-1), "ARG"), (dict(cols=1 << 31), "SIZE"), (dict(ldx=255), "ARG"),
+    (dict(eps=float("nan")), "ARG"), (dict(rows=-1), "ARG"), (dict(cols=1 << 31), "SIZE"), (dict(cols=(1 << 30) + 1), "SIZE"), (dict(ldx=255), "ARG"),
     (dict(res=PTR, ld_res=255), "ARG"), (dict(h=PTR, ld_h=4), "ARG"), (dict(y=PTR, ld_y=4), "ARG"),
     (dict(h=PTR + 1), "UNSUPPORTED"), (dict(rstd=PTR + 2), "UNSUPPORTED"), (dict(q=matrix(group=128)), "ARG"),
     (dict(q=matrix(ld=248)), "ARG"), (dict(q=matrix(data=PTR + 4)), "UNSUPPORTED"),

@@ -165,6 +165,9 @@ def test_norm_in_place_strides_and_no_quantisation():
         q, s, h, rstd, y = gp.rmsnorm_fp8(x, w, r, normed=True)
         check_norm(q, s, rstd, y, h, w, 1e-6, type, "e4m3")
         real = {"f16": 0, "bf16": 1, "f32": 2}[type]
+        # (the order of a row's FP32 sum follows its alignment: the same bits for the same strides)
+        q, s, h, rstd = gp.rmsnorm_fp8(x.contiguous(), w, r.contiguous())
+        check_norm(q, s, rstd, y, h, w, 1e-6, type, "e4m3")
         for place in (x, r):                            # h over x, then over the residual
             xx, rr = x.clone(), r.clone()
             at = xx if place is x else rr
