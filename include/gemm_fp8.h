@@ -10,8 +10,8 @@
  * return codes GP_OK and GP_ERR_*, and the per-thread record of the last call
  * read by gemm_stats().  The kernels are launched as programmatic dependents
  * of the work before them, and touch memory only once it has completed.
- * Split K-loops and the partial sums of the weight's gradient use the
- * library's workspace of the (device, stream); gemm_release frees it.  Results
+ * The norm's gradient keeps partial sums in the library's workspace of the
+ * (device, stream), which gemm_release frees; no other call needs one.  Results
  * do not depend on timing: partial sums meet in a fixed order.
  *
  * 8-bit matrices
@@ -75,9 +75,9 @@ typedef struct gp_fp8_matrix {
 /* Options of gemm_fp8.  Zero-initialise and set what you need. */
 typedef struct gp_fp8_options {
     uint64_t timeout_ns;         /* limit of every bounded wait inside the kernel (0 = 1 s) */
-    int32_t bn;                  /* force the tile width along the narrow operand: 16, 32, 64, 128 or 256 (0 = the
+    int32_t bn;                  /* force the tile width on the tensor cores' N side: 16, 32, 64, 128 or 256 (0 = the
                                     planner's choice; other values: GP_ERR_UNSUPPORTED) */
-    int32_t no_split;            /* 1: never split K-loops across CTAs */
+    int32_t no_split;            /* 1: never share a tile's K loop among CTAs */
     int32_t inject_lost_load;    /* test hook: the TMA producer skips the last tile load of the problem, so a
                                     consumer wait runs out and the call reports GP_ERR_TIMEOUT (no GPU fault) */
 } gp_fp8_options;
@@ -94,8 +94,8 @@ typedef struct gp_fp8_options {
  * GP_ERR_ARG: NULL A, B or scales with K > 0, NULL C, bad enums, group not 1
  * or 128, an ld below the columns (K, or N for C and addend), a negative size.
  * GP_ERR_UNSUPPORTED: an 8-bit matrix not 16-byte aligned or with ld % 16 != 0;
- * C, addend or scales not aligned to their element.  GP_ERR_SIZE: a size of
- * 2^31 or more, or more than 2^30 output tiles.
+ * C, addend or scales not aligned to their element.  GP_ERR_SIZE: a size above
+ * 2^31 - 256, or more than 2^30 output tiles.
  */
 int gemm_fp8(const gp_fp8_matrix* A, const gp_fp8_matrix* B, void* C, int64_t ldc, const void* addend,
              int64_t ld_add, int64_t M, int64_t N, int64_t K, int out_type, void* stream,
@@ -104,9 +104,10 @@ int gemm_fp8(const gp_fp8_matrix* A, const gp_fp8_matrix* B, void* C, int64_t ld
 /*
  * gemm_fp8_plan -- the tile, ring and split that gemm_fp8 would choose for
  * a_group x b_group scales on a device with `sms` SMs (0: the current device;
- * without one gp_plan.grid is 0 and nothing is split).  gp_plan.bm counts the
+ * without one, as on 152 SMs with gp_plan.grid left 0).  gp_plan.bm counts the
  * rows of the operand that fills the tensor cores' M side, bn those of the
- * other; gp_plan.layout is 1 where that operand is B (the roles are swapped).
+ * other; gp_plan.layout is 1 where that operand is B (the roles are swapped);
+ * gp_plan.k_splits CTAs, one cluster, share each tile's K loop.
  */
 int gemm_fp8_plan(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int sms, const gp_fp8_options* opts,
                   gp_plan* out);

@@ -35,6 +35,7 @@ int check_real(const void* p, int64_t ld, int64_t cols, int type, bool optional)
   return aligned(p, real_bytes(type)) ? GP_OK : GP_ERR_UNSUPPORTED;
 }
 
+constexpr int64_t kMaxGemm = INT32_MAX - 255;        // a size rounded up to whole tiles stays below 2^31
 constexpr int64_t kMaxNormCols = int64_t(1) << 30;   // column numbers plus a step stay below 2^31
 
 int first_error(std::initializer_list<int> codes) {
@@ -73,7 +74,8 @@ int gemm_fp8_plan(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int
                   gp_plan* out) {
   if (!out || sms < 0) return GP_ERR_ARG;
   if ((a_group != 1 && a_group != kFp8Group) || (b_group != 1 && b_group != kFp8Group)) return GP_ERR_ARG;
-  const int rc = check_sizes(M, N, K);
+  int rc = check_sizes(M, N, K);
+  if (rc == GP_OK && (M > kMaxGemm || N > kMaxGemm || K > kMaxGemm)) rc = GP_ERR_SIZE;
   if (rc != GP_OK) return rc;
   return fp8_plan_impl(M, N, K, a_group, b_group, sms > 0 ? sms : current_sms(), opts, out);
 }
@@ -83,6 +85,7 @@ int gemm_fp8(const gp_fp8_matrix* A, const gp_fp8_matrix* B, void* C, int64_t ld
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   call_reset(st);
   int rc = check_sizes(M, N, K);
+  if (rc == GP_OK && (M > kMaxGemm || N > kMaxGemm || K > kMaxGemm)) rc = GP_ERR_SIZE;
   if (rc == GP_OK && !real_ok(out_type)) rc = GP_ERR_ARG;
   if (rc != GP_OK) return call_finish(rc);
   if (M == 0 || N == 0) return call_finish(GP_OK);

@@ -17,6 +17,14 @@
 // Warp w may read TMEM lanes 32 (w mod 4) .. +31; the two warps of a quarter
 // take half the columns each.  "P" is the operand on the MMA's M side (128
 // rows per CTA), "Q" the one on its N side (BN rows); either may be A.
+//
+// What bounds it: with every K block, 128 x BN sums change hands between the
+// tensor cores and the adding warps (wait, TMEM read, FMA, release), about as
+// long as the block's MMAs; no unit is near its limit alone.  Measured: 8192 x
+// 8192 x 4096 (E4M3, row and block scales, BF16 out) 233 us in a graph, 2360
+// TFLOP/s, against 186 us when the hand-over is left out; 4096 x 4096 x 8192
+// with row scales on both sides 219 us.  For few rows the weights' bytes bound
+// it: 1 x 8192 x 8192 14.9 us, 4.5 TB/s with its start and end.
 #include <atomic>
 #include <cstring>
 #include "fp8_internal.h"
@@ -221,7 +229,8 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Output tile -> its P and Q blocks: groups of `gp` P blocks, each swept over all Q blocks.
+// Output tile -> its P and Q blocks: groups of `gp` P blocks, each swept over all Q blocks, so that the
+// CTAs at work at one time share operands in L2.
 __device__ __forceinline__ void tile_blocks(int tile, int p_blocks, int q_blocks, int gp, int& pb, int& qb) {
   const int per = gp * q_blocks;
   const int group = tile / per;

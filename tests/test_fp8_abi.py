@@ -35,7 +35,7 @@ def gemm(gp, A=None, B=None, C=PTR, ldc=64, add=None, ld_add=64, M=64, N=64, K=2
 
 
 @pytest.mark.parametrize("args,code", [
-    (dict(M=-1), "ARG"), (dict(K=-1), "ARG"), (dict(N=1 << 31), "SIZE"), (dict(K=1 << 31), "SIZE"),
+    (dict(M=-1), "ARG"), (dict(K=-1), "ARG"), (dict(N=1 << 31), "SIZE"), (dict(K=1 << 31), "SIZE"), (dict(M=(1 << 31) - 200), "SIZE"),
     (dict(out=3), "ARG"), (dict(C=None), "ARG"), (dict(ldc=63), "ARG"), (dict(add=PTR, ld_add=63), "ARG"),
     (dict(A=matrix(data=None)), "ARG"), (dict(B=matrix(scales=None)), "ARG"), (dict(A=matrix(fmt=2)), "ARG"),
     (dict(B=matrix(group=64)), "ARG"), (dict(A=matrix(ld=240)), "ARG"), (dict(A=matrix(ld=260)), "UNSUPPORTED"),
