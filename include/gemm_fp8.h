@@ -10,9 +10,9 @@
  * return codes GP_OK and GP_ERR_*, and the per-thread record of the last call
  * read by gemm_stats().  The kernels are launched as programmatic dependents
  * of the work before them, and touch memory only once it has completed.
- * The norm's gradient keeps partial sums in the library's workspace of the
- * (device, stream), which gemm_release frees; no other call needs one.  Results
- * do not depend on timing: partial sums meet in a fixed order.
+ * The norm's gradient keeps partial sums in a workspace that the caller
+ * passes, and no other call needs one: none allocates, and calls may be captured
+ * in a graph (once one call on the device has let the library load its code).  Results do not depend on timing: partial sums meet in a fixed order.
  *
  * 8-bit matrices
  * --------------
@@ -154,10 +154,15 @@ int fp8_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ld_res
  *   dx is the gradient of h, so of x and of residual; it may be dy, h or dres itself.
  *   rstd    rows FP32 values, as fp8_rmsnorm stored them.
  *   dw      cols FP32 values, written (not added to); NULL: not computed.  With rows == 0 it is filled with zeros.
+ *   workspace  16-byte aligned, workspace_bytes at least what fp8_rmsnorm_backward_workspace says for this device
+ *           (else GP_ERR_ARG): the call's own until it has run.  Where that is 0 (few rows), and without dw, NULL does.
  */
 int fp8_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* dres, int64_t ld_dres,
                          const void* weight, int weight_type, const float* rstd, int64_t rows, int64_t cols, int type,
-                         void* dx, int64_t ld_dx, float* dw, void* stream);
+                         void* dx, int64_t ld_dx, float* dw, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of a call with dw on a device with `sms` SMs (0: the current device; without one, as on 152 SMs). */
+int fp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int sms, int64_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -47,7 +47,8 @@ VARIANTS = {"pingpong": GP_PINGPONG, "pipelined": GP_PIPELINED, "nopipe": GP_NOP
 # exported symbols, in header order
 SYMBOLS = ["gemm_pipelined", "gemm_pipelined_ex", "gemm_plan", "gemm_plan_ex", "gemm_stats", "gemm_strerror",
            "gemm_abi_version", "gemm_release", "gemm_pipelined_noalloc", "gemm_probe_peak",
-           "gemm_probe_hbm", "gemm_fp8", "gemm_fp8_plan", "fp8_quantize", "fp8_rmsnorm", "fp8_rmsnorm_backward"]
+           "gemm_probe_hbm", "gemm_fp8", "gemm_fp8_plan", "fp8_quantize", "fp8_rmsnorm", "fp8_rmsnorm_backward",
+           "fp8_rmsnorm_backward_workspace"]
 
 
 class GpPlan(ctypes.Structure):
@@ -157,8 +158,10 @@ def lib():
     L.fp8_quantize.restype = ci
     L.fp8_rmsnorm.argtypes = [vp, i64, vp, i64, vp, ci, ctypes.c_float, i64, i64, ci, vp, i64, vp, vp, i64, mat, vp]
     L.fp8_rmsnorm.restype = ci
-    L.fp8_rmsnorm_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, ci, vp, i64, i64, ci, vp, i64, vp, vp]
+    L.fp8_rmsnorm_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, ci, vp, i64, i64, ci, vp, i64, vp, vp, i64, vp]
     L.fp8_rmsnorm_backward.restype = ci
+    L.fp8_rmsnorm_backward_workspace.argtypes = [i64, i64, ci, ctypes.POINTER(i64)]
+    L.fp8_rmsnorm_backward_workspace.restype = ci
     _lib = L
     return L
 

@@ -107,8 +107,6 @@ struct Workspace {
   uint32_t* ov_ctrs = nullptr;   // INT8 conversion / GEMM hand-off counters: two sets of ov_kcap + 1 words
   int32_t ov_kcap = 0;
   uint32_t ov_launches = 0;
-  float* fp8 = nullptr;       // FP8 operators: partial sums of the norm's weight gradient
-  size_t fp8_bytes = 0;
 };
 constexpr int kMaxWorkspaces = 64;
 Workspace g_ws[kMaxWorkspaces];
@@ -120,7 +118,6 @@ void free_workspace(Workspace& w) {
   if (w.flags) cudaFree(w.flags);
   if (w.conv) cudaFree(w.conv);
   if (w.ov_ctrs) cudaFree(w.ov_ctrs);
-  if (w.fp8) cudaFree(w.fp8);
   w = Workspace();
 }
 
@@ -753,25 +750,6 @@ void call_launched(const gp_plan& plan, const void* kernel) {
 int call_finish(int status, cudaError_t error, int site) {
   record(status, error, site ? site : (t_fail_site ? t_fail_site : GP_SITE_LAUNCH));
   return status;
-}
-
-cudaError_t call_workspace(int device, cudaStream_t stream, size_t bytes, float** partials) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  Workspace* w = nullptr;
-  cudaError_t e = find_workspace(device, stream, &w);
-  if (e != cudaSuccess) return e;
-  if (w->fp8_bytes < bytes) {
-    if (w->fp8) {
-      if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return e;   // nothing uses the old buffer now
-      cudaFree(w->fp8);
-      w->fp8 = nullptr;
-      w->fp8_bytes = 0;
-    }
-    if ((e = cudaMalloc(&w->fp8, bytes)) != cudaSuccess) return e;
-    w->fp8_bytes = bytes;
-  }
-  *partials = w->fp8;
-  return cudaSuccess;
 }
 
 // ---------------------------------------------------------------------------

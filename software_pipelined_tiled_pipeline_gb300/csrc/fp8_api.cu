@@ -1,5 +1,5 @@
 // fp8_api.cu -- the C ABI of the FP8 operators (include/gemm_fp8.h): argument
-// checks, workspaces and the per-thread last-call record.
+// checks and the per-thread last-call record.
 #include <cstring>
 #include <initializer_list>
 
@@ -199,9 +199,19 @@ int fp8_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ld_res
   return e == cudaSuccess ? call_finish(GP_OK) : call_finish(GP_ERR_CUDA, e);
 }
 
+int fp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int sms, int64_t* bytes) {
+  if (!bytes || sms < 0) return GP_ERR_ARG;
+  const int rc = check_sizes(rows, cols);
+  if (rc != GP_OK) return rc;
+  if (cols > kMaxNormCols) return GP_ERR_SIZE;
+  if (sms == 0) sms = current_sms();
+  *bytes = rows == 0 || cols == 0 ? 0 : fp8_rmsnorm_backward_parts(rows, cols, sms > 0 ? sms : 152) * cols * 4;
+  return GP_OK;
+}
+
 int fp8_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* dres, int64_t ld_dres,
                          const void* weight, int weight_type, const float* rstd, int64_t rows, int64_t cols, int type,
-                         void* dx, int64_t ld_dx, float* dw, void* stream) {
+                         void* dx, int64_t ld_dx, float* dw, void* workspace, int64_t workspace_bytes, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   call_reset(st);
   int rc = check_sizes(rows, cols);
@@ -213,7 +223,9 @@ int fp8_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t l
     rc = first_error({check_real(dy, ld_dy, cols, type, false), check_real(h, ld_h, cols, type, false),
                       check_real(dres, ld_dres, cols, type, true), check_real(weight, cols, cols, weight_type, false),
                       check_real(rstd, 1, 1, GP_REAL_F32, false), check_real(dx, ld_dx, cols, type, false)});
-  if (rc == GP_OK && !aligned(dw, 4)) rc = GP_ERR_UNSUPPORTED;
+  const bool parts = dw && rows > 0 && fp8_rmsnorm_backward_parts(rows, cols, 1) > 0;   // (whether, not how many)
+  if (rc == GP_OK && parts && !workspace) rc = GP_ERR_ARG;
+  if (rc == GP_OK && !(aligned(dw, 4) && aligned(workspace, 16))) rc = GP_ERR_UNSUPPORTED;
   if (rc != GP_OK) return call_finish(rc);
   CallInfo info;
   cudaError_t e = call_begin(0, &info);
@@ -225,6 +237,7 @@ int fp8_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t l
   a.weight = weight;
   a.rstd = rstd;
   a.dx = dx;
+  a.dw = dw;
   a.ld_dy = ld_dy;
   a.ld_h = ld_h;
   a.ld_dres = ld_dres;
@@ -237,13 +250,13 @@ int fp8_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t l
   a.vec = vec16(dy, ld_dy, w) && vec16(h, ld_h, w) && (!dres || vec16(dres, ld_dres, w)) && vec16(dx, ld_dx, w);
   a.vec_w = aligned(weight, 16);
   gp_plan plan = {};
-  if (dw && rows > 0) {
+  if (parts) {
     plan.workspace_bytes = fp8_rmsnorm_backward_parts(rows, cols, info.sm_count) * cols * 4;
-    e = call_workspace(info.device, st, static_cast<size_t>(plan.workspace_bytes), &a.partials);
-    if (e != cudaSuccess) return call_finish(GP_ERR_CUDA, e, GP_SITE_WORKSPACE);
+    if (workspace_bytes < plan.workspace_bytes) return call_finish(GP_ERR_ARG);
+    a.partials = static_cast<float*>(workspace);
   }
   const void* kernel = nullptr;
-  e = launch_fp8_rmsnorm_backward(a, dw, info.sm_count, st, &kernel, &plan);
+  e = launch_fp8_rmsnorm_backward(a, info.sm_count, st, &kernel, &plan);
   call_launched(plan, kernel);
   return e == cudaSuccess ? call_finish(GP_OK) : call_finish(GP_ERR_CUDA, e);
 }

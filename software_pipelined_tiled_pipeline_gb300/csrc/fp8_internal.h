@@ -57,16 +57,18 @@ struct NormGradArgs {
   const void *dy, *h, *dres, *weight;
   const float* rstd;
   void* dx;
-  float* partials;       // parts x cols sums of the weight's gradient; NULL: not computed
+  float* dw;             // the weight's gradient; NULL: not computed
+  float* partials;       // parts x cols sums of it (NULL where parts is 0)
   int64_t ld_dy, ld_h, ld_dres, ld_dx;
   int64_t rows, cols;
   int32_t type, weight_type;
   int32_t vec, vec_w;
+  int32_t col_blocks;    // blocks that work out dw by columns (the launcher's)
 };
 // Rows of partial sums that a call of this size leaves (workspace: that many x cols floats).
 int64_t fp8_rmsnorm_backward_parts(int64_t rows, int64_t cols, int sm_count);
-cudaError_t launch_fp8_rmsnorm_backward(const NormGradArgs& a, float* dw, int sm_count, cudaStream_t stream,
-                                        const void** kernel, gp_plan* plan);
+cudaError_t launch_fp8_rmsnorm_backward(const NormGradArgs& a, int sm_count, cudaStream_t stream, const void** kernel,
+                                        gp_plan* plan);
 
 struct Fp8GemmArgs {
   gp_fp8_matrix A, B;
@@ -104,7 +106,5 @@ cudaError_t call_begin(uint64_t timeout_ns, CallInfo* info);
 void call_launched(const gp_plan& plan, const void* kernel);
 // Close the record; returns `status`.  A CUDA error's site defaults to the launch, or what a helper noted.
 int call_finish(int status, cudaError_t error = cudaSuccess, int site = 0);
-// FP32 workspace of (device, stream) of at least `bytes`.
-cudaError_t call_workspace(int device, cudaStream_t stream, size_t bytes, float** partials);
 
 }  // namespace gp

@@ -11,6 +11,8 @@ Everything runs on the current stream of the tensors' device (or ``stream``);
 this module allocates outputs and passes pointers, and a failing call raises
 ``GemmError``.
 """
+import ctypes
+import functools
 import struct
 
 import torch
@@ -284,12 +286,27 @@ def rmsnorm_backward(dy, h, weight, rstd, dresidual=None, *, weight_grad=True, s
         res_ptr = dresidual.data_ptr()
     device = dy.device
     dx = _empty((rows, cols), (cols, 1), dtype=dy.dtype, device=device)
-    dw = _empty((cols,), (1,), dtype=_F32, device=device) if weight_grad else None
+    dw, dw_ptr, work_ptr, work_bytes = None, None, None, 0
+    if weight_grad:
+        dw = _empty((cols,), (1,), dtype=_F32, device=device)
+        dw_ptr = dw.data_ptr()
+        work_bytes = _backward_workspace(rows, cols, dy.get_device())
+        if work_bytes:
+            work = _empty((work_bytes // 4,), (1,), dtype=_F32, device=device)   # (freed in the call's stream order)
+            work_ptr = work.data_ptr()
     _check(fp8_calls().backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, res_ptr, ld_res, weight.data_ptr(), wtype,
                                 rstd.data_ptr(), rows, cols, real, dx.data_ptr(), cols,
-                                dw.data_ptr() if weight_grad else None, _raw_stream(dy.get_device())),
+                                dw_ptr, work_ptr, work_bytes, _raw_stream(dy.get_device())),
            "fp8_rmsnorm_backward")
     return dx, dw
+
+
+@functools.lru_cache(maxsize=256)
+def _backward_workspace(rows, cols, device):
+    """Bytes that rmsnorm_backward needs for the weight's gradient on `device`, the current one."""
+    size = ctypes.c_int64()
+    _check(lib().fp8_rmsnorm_backward_workspace(rows, cols, 0, size), "fp8_rmsnorm_backward_workspace")
+    return size.value
 
 
 def _weight(weight, cols, like):

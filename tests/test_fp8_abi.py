@@ -61,7 +61,7 @@ def test_empty_output_needs_no_device(gp):
     assert f(None, None, None, 0, None, 0, 64, 0, 256, 1, None, None) == gp.GP_OK
     assert gp.lib().fp8_quantize(None, 0, 0, 128, 0, matrix(), None, None) == gp.GP_OK
     assert gp.lib().fp8_rmsnorm(None, 0, None, 0, None, 0, 0.0, 0, 64, 0, None, 0, None, None, 0, None, None) == gp.GP_OK
-    assert gp.lib().fp8_rmsnorm_backward(None, 0, None, 0, None, 0, None, 0, None, 0, 64, 0, None, 0, None, None) == gp.GP_OK
+    assert gp.lib().fp8_rmsnorm_backward(None, 0, None, 0, None, 0, None, 0, None, 0, 64, 0, None, 0, None, None, 0, None) == gp.GP_OK
 
 
 def quantize(gp, x=PTR, ldx=256, rows=64, cols=256, type=1, q=None, qt=None):
@@ -97,19 +97,32 @@ def test_norm_argument_errors_need_no_device(gp, args, code):
 
 
 def backward(gp, dy=PTR, ld_dy=256, h=PTR, ld_h=256, dres=None, ld_dres=256, w=PTR, wtype=1, rstd=PTR, rows=4, cols=256,
-             type=1, dx=PTR, ld_dx=256, dw=PTR):
+             type=1, dx=PTR, ld_dx=256, dw=PTR, work=PTR, work_bytes=1 << 30):
     return gp.lib().fp8_rmsnorm_backward(dy, ld_dy, h, ld_h, dres, ld_dres, w, wtype, rstd, rows, cols, type, dx, ld_dx, dw,
-                                         None)
+                                         work, work_bytes, None)
 
 
 @pytest.mark.parametrize("args,code", [
     (dict(dy=None), "ARG"), (dict(h=None), "ARG"), (dict(w=None), "ARG"), (dict(rstd=None), "ARG"), (dict(dx=None), "ARG"),
     (dict(ld_dy=8), "ARG"), (dict(ld_h=8), "ARG"), (dict(dres=PTR, ld_dres=8), "ARG"), (dict(ld_dx=8), "ARG"),
     (dict(type=4), "ARG"), (dict(wtype=4), "ARG"), (dict(rows=1 << 31), "SIZE"), (dict(dw=PTR + 1), "UNSUPPORTED"),
-    (dict(dx=PTR + 1), "UNSUPPORTED"),
+    (dict(dx=PTR + 1), "UNSUPPORTED"), (dict(work=None, rows=4000), "ARG"), (dict(work=PTR + 4), "UNSUPPORTED"),
 ])
 def test_backward_argument_errors_need_no_device(gp, args, code):
     assert backward(gp, **args) == getattr(gp, "GP_ERR_" + code)
+
+
+def test_backward_workspace(gp):
+    size = ctypes.c_int64(-1)
+    f = gp.lib().fp8_rmsnorm_backward_workspace
+    for rows, cols in [(0, 64), (64, 0), (1, 1), (200, 2056)]:      # (few rows need none)
+        assert f(rows, cols, 152, size) == gp.GP_OK and size.value == 0
+    for rows, cols in [(5000, 1), (2000, 2056), (8192, 8192), (5, 20000), (4000, 20000)]:
+        assert f(rows, cols, 152, size) == gp.GP_OK
+        # whole rows of FP32 sums: never more than a block for each row, each with at most four rows side by side
+        assert size.value % (4 * cols) == 0 and 1 <= size.value // (4 * cols) <= 4 * rows
+    assert f(-1, 4, 152, size) == gp.GP_ERR_ARG and f(4, 4, -1, size) == gp.GP_ERR_ARG
+    assert f(4, 4, 152, None) == gp.GP_ERR_ARG and f(4, (1 << 30) + 1, 152, size) == gp.GP_ERR_SIZE
 
 
 def test_struct_layout_matches_the_header(tmp_path):

@@ -208,7 +208,7 @@ def test_replays_in_a_graph():
     want = gp.gemm_fp8(a.data, a.scales, b.data, b.scales)
     C = torch.zeros_like(want)
     s = torch.cuda.Stream()
-    gp.gemm_fp8(a.data, a.scales, b.data, b.scales, out=C, stream=s)   # the stream's workspace, before the capture
+    gp.gemm_fp8(a.data, a.scales, b.data, b.scales, out=C, stream=s)   # a first call, outside the capture
     s.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g, stream=s):

@@ -264,11 +264,50 @@ def test_norm_gradient_in_place(over, cols):
     rstd = torch.rsqrt(h.float().square().mean(1) + 1e-6)
     want, want_w = gp.rmsnorm_backward(dy, h, w, rstd, dres)
     place = {"dy": dy, "h": h, "dres": dres}[over]
-    dw = torch.empty(cols, device="cuda")
+    dw, work = torch.empty(cols, device="cuda"), torch.empty(4 << 20, device="cuda")
     assert gp.lib().fp8_rmsnorm_backward(dy.data_ptr(), cols, h.data_ptr(), cols, dres.data_ptr(), cols, w.data_ptr(), 1,
-                                         rstd.data_ptr(), 40, cols, 1, place.data_ptr(), cols, dw.data_ptr(), None) == 0
+                                         rstd.data_ptr(), 40, cols, 1, place.data_ptr(), cols, dw.data_ptr(), work.data_ptr(),
+                                         work.numel() * 4, None) == 0
     torch.cuda.synchronize()
     assert torch.equal(place, want) and torch.equal(dw, want_w)
+
+
+def test_norm_gradient_replays_in_graphs():
+    # Two graphs captured on one stream, a larger call between, then both replayed side by side on two streams: each
+    # has sums of its own, so their results are those of the calls.
+    rng = np.random.default_rng(8)
+    sets = [[matrix(rows, 1000, "bf16", rng) for _ in range(2)] for rows in (1700, 1900)]
+    w = torch.ones(1000, device="cuda")
+    side, graphs, outs, wants = torch.cuda.Stream(), [], [], []
+    for dy, h in sets:
+        rstd = torch.rsqrt(h.float().square().mean(1))
+        wants.append(gp.rmsnorm_backward(dy, h, w, rstd))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(gp.rmsnorm_backward(dy, h, w, rstd))
+        graphs.append((g, rstd))
+    big = torch.ones((3000, 8000), device="cuda")
+    gp.rmsnorm_backward(big, big, big[0], big[:, 0].contiguous(), stream=side)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(10):
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for got, want in zip(outs, wants):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_norm_gradient_with_too_small_a_workspace():
+    x = torch.ones((4000, 600), device="cuda")
+    dw, dx = torch.full((600,), 7.0, device="cuda"), torch.full((4000, 600), 7.0, device="cuda")
+    p = x.data_ptr()
+    assert gp.lib().fp8_rmsnorm_backward(p, 600, p, 600, None, 0, p, 2, p, 4000, 600, 2, dx.data_ptr(), 600, dw.data_ptr(),
+                                         p, 600 * 4, None) == gp.GP_ERR_ARG
+    torch.cuda.synchronize()
+    assert bool((dx == 7).all()) and bool((dw == 7).all())
 
 
 def test_norm_gradient_of_no_rows_and_same_bits():
