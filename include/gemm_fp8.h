@@ -12,7 +12,8 @@
  * of the work before them, and touch memory only once it has completed.
  * The norm's gradient keeps partial sums in a workspace that the caller
  * passes, and no other call needs one: none allocates, and calls may be captured
- * in a graph (once one call on the device has let the library load its code).  Results do not depend on timing: partial sums meet in a fixed order.
+ * in a graph (once one call on the device has let the library load its code).
+ * Results do not depend on timing: partial sums meet in a fixed order.
  *
  * 8-bit matrices
  * --------------
@@ -79,7 +80,8 @@ typedef struct gp_fp8_options {
                                     planner's choice; other values: GP_ERR_UNSUPPORTED) */
     int32_t no_split;            /* 1: never share a tile's K loop among CTAs */
     int32_t inject_lost_load;    /* test hook: the TMA producer skips the last tile load of the problem, so a
-                                    consumer wait runs out and the call reports GP_ERR_TIMEOUT (no GPU fault) */
+                                    consumer wait runs out and the call reports GP_ERR_TIMEOUT (no GPU fault); not
+                                    with bn 256 (GP_ERR_UNSUPPORTED), whose tiles two CTAs share */
 } gp_fp8_options;
 
 /*
@@ -89,7 +91,8 @@ typedef struct gp_fp8_options {
  *   addend   NULL, or a row-major M x N matrix of type out_type with ld_add elements between rows, added in FP32
  *            before the one rounding to out_type; may be C itself (same pointer and ld), not overlap it otherwise.
  * Products of 128 along K are summed by the tensor cores in FP32, scaled by
- * the two FP32 scales and added to FP32 sums.
+ * the product of the two scales (formed in FP32: where that overflows, so does
+ * the result) and added to FP32 sums.
  * M == 0 or N == 0: nothing is launched.  K == 0: C = addend, or zeros.
  * GP_ERR_ARG: NULL A, B or scales with K > 0, NULL C, bad enums, group not 1
  * or 128, an ld below the columns (K, or N for C and addend), a negative size.

@@ -414,8 +414,8 @@ __device__ __forceinline__ void write_out(const Fp8Params& g, const float (&acc)
 
 // The K loop split over a cluster: every CTA hands each of the others the
 // columns that are theirs, and writes its own.  Buffer of a CTA: for each
-// source, its columns of kXRow floats, one per row and one to keep the lanes of either walk off each
-// other's banks.
+// source, its columns of kXRow floats, one per row and one to keep the lanes of
+// either walk off each other's banks.
 constexpr int kXRow = 129;
 template <bool ADD, typename T>
 __device__ __forceinline__ void write_shared(const Fp8Params& g, const float* buf, int t, int ctas, int per_log,
@@ -933,6 +933,7 @@ int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int
   for (const TileCost& t : kTileCosts) known |= t.bn == want;
   if (!known) return GP_ERR_UNSUPPORTED;
   const bool one_cta = opts && opts->inject_lost_load;   // (a lost load is injected into whole tiles of one CTA)
+  if (one_cta && want == 256) return GP_ERR_UNSUPPORTED;
   const int64_t kt = (K + kBK - 1) / kBK;
   const int have = sms > 0 ? sms : 152;
   // Try every width with either operand on the MMA's N side (Q), and every

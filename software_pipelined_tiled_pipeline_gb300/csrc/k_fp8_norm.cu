@@ -4,9 +4,10 @@
 //   h = round(x + residual),  rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight
 //   g = dy * weight,  dx = rstd * (g - h * rstd * mean(g * h * rstd)) + dres,  dw = sum_rows dy * h * rstd
 //
-// Each input is read once and each output written once.  A row stays in the registers of its threads (NCH chunks of 8 values
-// each) from the load to the store, so the sum over the row costs one exchange
-// between warps and no second read.  Chunk i of thread t holds columns
+// Each input is read once and each output written once (the gradient of few
+// rows reads dy and h twice).  A row stays in the registers of its threads (NCH
+// chunks of 8 values each) from the load to the store, so the sum over the row
+// costs one exchange between warps and no second read.  Chunk i of thread t holds columns
 // 8 (i * threads + t) .., so a group of 128 columns is 16 neighbouring lanes
 // and its maximum four shuffles.  Rows too long for the registers
 // (kRowsMaxCols) are read twice.  Measured (BF16): the norm of 4096 x 8192 with

@@ -53,6 +53,7 @@ def test_gemm_null_matrix_and_forced_width(gp):
     f = gp.lib().gemm_fp8
     assert f(None, matrix(), PTR, 64, None, 0, 64, 64, 256, 1, None, None) == gp.GP_ERR_ARG
     assert gemm(gp, opts=b.GpFp8Options(0, 48, 0, 0)) == gp.GP_ERR_UNSUPPORTED
+    assert gemm(gp, opts=b.GpFp8Options(0, 256, 0, 1)) == gp.GP_ERR_UNSUPPORTED     # two CTAs share a tile
 
 
 def test_empty_output_needs_no_device(gp):
