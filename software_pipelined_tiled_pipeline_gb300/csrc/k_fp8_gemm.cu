@@ -11,7 +11,7 @@
 //   warp 1      allocates TMEM and issues the MMAs of a K block into the next
 //               TMEM buffer; their one commit both frees the ring slot and
 //               hands the buffer to the adding warps
-//   warps 4-11  bring the scales of kScaleBatch K blocks at a time into shared
+//   warps 4-11  bring the scales of 8 to 32 K blocks at a time into shared
 //               memory (cp.async), add each TMEM buffer, scaled, to the sums in
 //               their registers, and write C at a tile's end
 // Warp w may read TMEM lanes 32 (w mod 4) .. +31; the two warps of a quarter
@@ -38,7 +38,6 @@ constexpr int kMmaK = 32;                 // K of one kind::f8f6f4 instruction
 constexpr int kThreads = 384;
 constexpr int kAddWarps = 8;
 constexpr int kAddThreads = 32 * kAddWarps;
-constexpr int kScaleBatch = 8;            // K blocks whose scales are staged together (two batches in turn)
 constexpr int kStageWarpBytes = 32 * 128;   // output staging of one warp: 32 rows of 32 FP32
 constexpr int kLaunchRegs = 168;          // registers per thread at launch, where warps trade them
 constexpr int kMaxRing = 12;
@@ -70,7 +69,13 @@ struct Fp8Shape {
   static constexpr uint32_t TMEM_COLS = BUFS * BN;
   static constexpr int HALF = BN / 2;                  // columns per adding warp
   static constexpr int SCALES = P_ROWS + BN;           // floats per K block: P's, then Q's
-  static constexpr int FIXED = kAddWarps * kStageWarpBytes + 2 * kScaleBatch * SCALES * 4 + kFp8BarrierBytes + 1024;
+  // K blocks whose scales are staged together, in two batches in turn: as many
+  // as cost no ring slot.  The code between two batches is cold each time it
+  // comes: 8192 x 8192 x 4096 228 us with 8 together, 215 with 22; 4096 x 4096 x
+  // 8192 with row scales 206 with 8, 190 with 16.  (Three batches of 5 and 8
+  // with a barrier that nobody waits for: 223 and 202.)
+  static constexpr int BATCH = BN == 256 ? 11 : (BN >= 64 ? 16 : 8);
+  static constexpr int FIXED = kAddWarps * kStageWarpBytes + 2 * BATCH * SCALES * 4 + kFp8BarrierBytes + 1024;
   static constexpr int FIT = (kSmemPerCtaMax - FIXED) / STAGE;
   static constexpr int STAGES = FIT < kMaxRing ? FIT : kMaxRing;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
@@ -447,8 +452,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = ring + Sh::STAGES * Sh::STAGE;
   float* scales = reinterpret_cast<float*>(staging + kAddWarps * kStageWarpBytes);
-  Fp8Barriers* bar = reinterpret_cast<Fp8Barriers*>(scales + 2 * kScaleBatch * Sh::SCALES);
+  Fp8Barriers* bar = reinterpret_cast<Fp8Barriers*>(scales + 2 * Sh::BATCH * Sh::SCALES);
 
+  // K blocks whose scales are staged together; with one scale for 128 of Q's rows the same memory holds more.
+  constexpr int SCALES = QROWS ? Sh::SCALES : Sh::P_ROWS + 4;
+  constexpr int BATCH = Sh::BATCH * Sh::SCALES / SCALES;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // (uniform for the compiler too)
   const int lane = threadIdx.x & 31;
   const int k_ctas = PAIR ? 1 : 1 << g.k_log;                 // CTAs that share a tile's K blocks
@@ -615,15 +623,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int p_log = g.p.shift ? 0 : 7;                                   // log2 of P's values per K block
     constexpr int Q_LOG = QROWS ? LOG_BN : (BN == 256 ? 1 : 0);
     auto stage_scales = [&](int to, int pb, int qb, int kb, int n) {
-      const uint32_t dst = smem_u32(scales + to * kScaleBatch * Sh::SCALES);
+      const uint32_t slot = smem_u32(scales + to * BATCH * SCALES);
       auto one = [&](const ScaleView& v, int64_t first, int log, int step, int at) {
-        for (int i = t; i < n << log; i += kAddThreads) {
-          const int b = i >> log, r = i & ((1 << log) - 1);
-          const int64_t row = first + r * step;
-          const bool in = row < v.rows;
-          cp_async4(dst + (b * Sh::SCALES + at + r) * 4,
-                    v.base + (in ? (row >> v.shift) * v.stride_row + (kb + b) * v.stride_col : 0), in);
-        }
+        // (a thread's values lie in one row: their addresses differ by a stride)
+        const int r = t & ((1 << log) - 1), b0 = t >> log, by = kAddThreads >> log;
+        const int64_t row = first + r * step;
+        const bool in = row < v.rows;
+        const float* from = v.base + (in ? (row >> v.shift) * v.stride_row + (kb + b0) * v.stride_col : 0);
+        const int64_t next = in ? by * v.stride_col : 0;
+        uint32_t dst = slot + (b0 * SCALES + at + r) * 4;
+        for (int b = b0; b < n; b += by, from += next, dst += by * (SCALES * 4)) cp_async4(dst, from, in);
       };
       one(g.p, static_cast<int64_t>(pb) * Sh::TILE_P + rank * Sh::P_ROWS, p_log, 1, 0);
       one(g.q, static_cast<int64_t>(qb) * BN, Q_LOG, QROWS ? 1 : 128, Sh::P_ROWS);
@@ -634,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < Sh::HALF; ++i) acc[i] = 0.f;
       int pb, qb;
       tile_blocks(items.tile, p_blocks, q_blocks, g.raster_gp, pb, qb);
-      if (ok) stage_scales(batch, pb, qb, k0, min(kScaleBatch, k1 - k0));
+      if (ok && items.tile == worker) stage_scales(batch, pb, qb, k0, min(BATCH, k1 - k0));
       if (ADD && !g.swapped) {
         // this thread's row of the addend comes into L2 while the K loop runs
         const int size = g.out_type == GP_REAL_F32 ? 4 : 2;
@@ -647,16 +656,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * size));
         }
       }
-      for (int kc = k0; kc < k1; kc += kScaleBatch, batch ^= 1) {
-        const int end = min(kc + kScaleBatch, k1);
+      for (int kc = k0; kc < k1; kc += BATCH, batch ^= 1) {
+        const int end = min(kc + BATCH, k1);
         cp_async_wait_all();
         add_warps_sync();      // this batch is there for all, and all have read the one before
         if (!ok) continue;
-        if (end < k1) stage_scales(batch ^ 1, pb, qb, end, min(kScaleBatch, k1 - end));
-        const float* slot = scales + batch * kScaleBatch * Sh::SCALES;
+        if (end < k1) stage_scales(batch ^ 1, pb, qb, end, min(BATCH, k1 - end));
+        const float* slot = scales + batch * BATCH * SCALES;
         // A wait that gave up in here leaves wrong sums behind, which are never
         // written: the abort flag is looked at after each batch.
-        for (int kb = kc; kb < end; ++kb, slot += Sh::SCALES) {
+        for (int kb = kc; kb < end; ++kb, slot += SCALES) {
           const float sp = slot[g.p.shift ? 0 : row];
           const float* sq = slot + Sh::P_ROWS;
           const float one = QROWS ? sp : sp * sq[BN == 256 ? half : 0];
@@ -732,6 +741,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       if (!ok) continue;
+      if (items.tile + items.step < items.tiles) {
+        // the next tile's first scales come while this one is written
+        int pn, qn;
+        tile_blocks(items.tile + items.step, p_blocks, q_blocks, g.raster_gp, pn, qn);
+        stage_scales(batch, pn, qn, k0, min(BATCH, k1 - k0));
+      }
       const int64_t p0 = static_cast<int64_t>(pb) * Sh::TILE_P + rank * Sh::P_ROWS + quarter * 32;
       const int64_t q0 = static_cast<int64_t>(qb) * BN + half * Sh::HALF;
       if (g.out_type == GP_REAL_BF16)
@@ -916,8 +931,8 @@ struct TileCost {
 constexpr TileCost kTileCosts[] = {{16, 210, 210, 3200, 300, 800},
                                    {32, 270, 270, 3500, 400, 1200},
                                    {64, 350, 350, 4200, 600, 2000},
-                                   {128, 330, 480, 5000, 1000, 5000},
-                                   {256, 500, 850, 6500, 1800, 0}};
+                                   {128, 315, 400, 5000, 1000, 5000},
+                                   {256, 415, 790, 6500, 1800, 0}};
 constexpr double kReadGbs = 6500;        // operands from HBM
 constexpr double kStageGbs = 72;         // one CTA's ring
 constexpr int kSwappedNs = 13;           // a column of a swapped tile's epilogue
