@@ -21,9 +21,9 @@
 // What bounds it: with every K block, 128 x BN sums change hands between the
 // tensor cores and the adding warps (wait, TMEM read, FMA, release), about as
 // long as the block's MMAs; no unit is near its limit alone.  Measured: 8192 x
-// 8192 x 4096 (E4M3, row and block scales, BF16 out) 233 us in a graph, 2360
+// 8192 x 4096 (E4M3, row and block scales, BF16 out) 207 us in a graph, 2660
 // TFLOP/s, against 186 us when the hand-over is left out; 4096 x 4096 x 8192
-// with row scales on both sides 219 us.  For few rows the weights' bytes bound
+// with row scales on both sides 190 us.  For few rows the weights' bytes bound
 // it: 1 x 8192 x 8192 14.9 us, 4.5 TB/s with its start and end.
 #include <atomic>
 #include <cstring>
@@ -923,18 +923,17 @@ namespace {
 // tile, and the exchange where a cluster splits the K loop.  For example, unsplit
 // against two CTAs per tile: 48 x 8192 x 8192 25.6 -> 19.2 us (BN 64), 256 x
 // 4096 x 4096 14.0 -> 20.0 us (BN 128); BN 64 against 128 at 1000 x 776 x 2056
-// 9.5 and 9.8 us, BN 128 against 256 at 1024 x 4096 x 4096 25.8 and 20.1 us and
-// at 512 x 4096 x 4096 14.6 and 18.9 us.
+// 9.8 and 10.1 us, BN 128 against 256 at 1024 x 4096 x 4096 25.5 and 18.3 us and
+// at 512 x 4096 x 4096 14.6 and 16.7 us.
 struct TileCost {
   int bn, k_block, k_rows, call, more, exchange;
 };
-constexpr TileCost kTileCosts[] = {{16, 210, 210, 3200, 300, 800},
-                                   {32, 270, 270, 3500, 400, 1200},
+constexpr TileCost kTileCosts[] = {{16, 255, 255, 3200, 300, 800},
+                                   {32, 285, 285, 3500, 400, 1200},
                                    {64, 350, 350, 4200, 600, 2000},
-                                   {128, 315, 400, 5000, 1000, 5000},
-                                   {256, 415, 790, 6500, 1800, 0}};
+                                   {128, 315, 395, 5000, 1000, 8000},
+                                   {256, 385, 750, 6500, 1800, 0}};
 constexpr double kReadGbs = 6500;        // operands from HBM
-constexpr double kStageGbs = 72;         // one CTA's ring
 constexpr int kSwappedNs = 13;           // a column of a swapped tile's epilogue
 constexpr int kMinShare = 4;             // K blocks of each CTA of a cluster, at least
 
@@ -965,7 +964,6 @@ int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int
       if (want ? t.bn != want : (one_cta && t.bn == 256)) continue;
       const int ctas = t.bn == 256 ? 2 : 1;
       const int64_t tiles = (P + 128 * ctas - 1) / (128 * ctas) * ((Q + t.bn - 1) / t.bn);
-      const int stage = 128 * (128 + t.bn / ctas);
       for (int c = 1; c <= 8; c *= 2) {
         if (c > 1 && (ctas == 2 || one_cta || (opts && opts->no_split) || tiles * c > (c > 2 ? have * 7 / 8 : have) ||
                       kt < kMinShare * c))
@@ -973,8 +971,7 @@ int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int
         const int64_t workers = have / (ctas * c);
         if (workers < 1) break;
         const int64_t waves = (tiles + workers - 1) / workers, blocks = waves * ((kt + c - 1) / c);
-        const double k_block = q_rows ? t.k_rows : t.k_block, ring = stage / kStageGbs;
-        double ns = blocks * (k_block > ring ? k_block : ring);
+        double ns = blocks * static_cast<double>(q_rows ? t.k_rows : t.k_block);
         const double read = (M + N) * static_cast<double>(K) / kReadGbs;
         if (ns < read) ns = read;
         ns += t.call + (waves - 1) * t.more + (c > 1 ? t.exchange : 0) + (sw ? waves * t.bn * kSwappedNs : 0);
