@@ -12,7 +12,7 @@
 // and its maximum four shuffles.  Rows too long for the registers
 // (kRowsMaxCols) are read twice.  Measured (BF16): the norm of 4096 x 8192 with
 // a residual 46 us, 5.1 TB/s, 73 % of the issue slots (37 instructions per
-// value); the gradient of 8192 x 8192 92 us, 5.8 TB/s, bound by HBM.
+// value); the gradient of 8192 x 8192 91 us, 5.9 TB/s, bound by HBM.
 #include <cstring>
 #include "fp8_rows.cuh"
 
