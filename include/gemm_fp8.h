@@ -77,7 +77,7 @@ typedef struct gp_fp8_matrix {
 typedef struct gp_fp8_options {
     uint64_t timeout_ns;         /* limit of every bounded wait inside the kernel (0 = 1 s) */
     int32_t bn;                  /* force the tile width on the tensor cores' N side: 16, 32, 64, 128 or 256 (0 = the
-                                    planner's choice; other values: GP_ERR_UNSUPPORTED) */
+                                    planner's choice; other values, and 256 on one SM: GP_ERR_UNSUPPORTED) */
     int32_t no_split;            /* 1: never share a tile's K loop among CTAs */
     int32_t inject_lost_load;    /* test hook: the TMA producer skips the last tile load of the problem, so a
                                     consumer wait runs out and the call reports GP_ERR_TIMEOUT (no GPU fault); not

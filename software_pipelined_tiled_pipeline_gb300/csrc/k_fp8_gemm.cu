@@ -984,6 +984,7 @@ int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int
       }
     }
   }
+  if (!tile) return GP_ERR_UNSUPPORTED;   // (width 256 forced on one SM: a pair of CTAs does not fit)
   const int64_t p_rows = swapped ? N : M, q_rows = swapped ? M : N;
   p->dtype = GP_PLAN_FP8;
   p->layout = swapped;

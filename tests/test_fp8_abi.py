@@ -207,3 +207,21 @@ def test_few_tiles_share_their_k_loops_in_clusters(gp):
     # pairs run whole tiles
     p = gp.gemm_fp8_plan(4096, 4096, 4096, sms=152)
     assert (p["cta_pair"], p["bm"], p["bn"], p["k_splits"], p["grid"]) == (1, 256, 256, 1, 152)
+
+
+def test_plan_of_few_sms(gp):
+    # a plan that no SM count allows is refused: tiles of 256 take pairs of CTAs, so two SMs
+    from software_pipelined_tiled_pipeline_gb300 import _binding as b
+    p = b.GpPlan()
+    for sms in (1, 2, 3, 5, 8):
+        for bn in (0, 16, 32, 64, 128, 256):
+            for M, N, K in ((64, 64, 64), (1, 4096, 4096), (512, 512, 512), (5000, 3000, 700)):
+                for groups in ((1, 128), (1, 1), (128, 1)):
+                    rc = gp.lib().gemm_fp8_plan(M, N, K, *groups, sms, b.GpFp8Options(0, bn, 0, 0), p)
+                    if sms == 1 and bn == 256:
+                        assert rc == gp.GP_ERR_UNSUPPORTED
+                        continue
+                    assert rc == gp.GP_OK
+                    d = p.as_dict()
+                    assert 1 <= d["grid"] <= sms and d["grid"] % (2 if d["cta_pair"] else d["k_splits"]) == 0
+                    assert bn in (0, d["bn"])
