@@ -141,7 +141,8 @@ int fp8_quantize(const void* x, int64_t ldx, int64_t rows, int64_t cols, int typ
  *   y_out   y rounded to `type` (NULL: not written).
  *   q       NULL, or the 8-bit matrix to write (group 1).
  * The norm is of the rounded h, so that the gradient computed from the stored
- * h is that of the function that ran.  cols == 0 or rows == 0: nothing is launched.
+ * h is that of the function that ran.  rows == 0: nothing is launched.  cols == 0:
+rstd is filled with NaN (the mean of no values).
  * GP_ERR_SIZE: rows of 2^31 or more, cols above 2^30 (here and in the gradient).
  */
 int fp8_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ld_res, const void* weight, int weight_type,

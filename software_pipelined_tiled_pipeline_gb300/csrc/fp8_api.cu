@@ -2,6 +2,7 @@
 // checks and the per-thread last-call record.
 #include <cstring>
 #include <initializer_list>
+#include <limits>
 
 #include "fp8_internal.h"
 
@@ -159,7 +160,16 @@ int fp8_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ld_res
   if (rc == GP_OK && cols > kMaxNormCols) rc = GP_ERR_SIZE;
   if (rc == GP_OK && (!real_ok(type) || !real_ok(weight_type) || !(eps >= 0.f))) rc = GP_ERR_ARG;
   if (rc != GP_OK) return call_finish(rc);
-  if (rows == 0 || cols == 0) return call_finish(GP_OK);
+  if (rows == 0 || (cols == 0 && !rstd)) return call_finish(GP_OK);
+  if (cols == 0) {
+    // the mean of no values is NaN
+    if (!aligned(rstd, 4)) return call_finish(GP_ERR_UNSUPPORTED);
+    CallInfo info;
+    cudaError_t e = call_begin(0, &info);
+    if (e != cudaSuccess) return call_finish(GP_ERR_CUDA, e, GP_SITE_DEVICE);
+    e = launch_fp8_fill_f32(rstd, rows, std::numeric_limits<float>::quiet_NaN(), st);
+    return e == cudaSuccess ? call_finish(GP_OK) : call_finish(GP_ERR_CUDA, e);
+  }
   rc = first_error({check_real(x, ldx, cols, type, false), check_real(residual, ld_res, cols, type, true),
                     check_real(weight, cols, cols, weight_type, false), check_real(h_out, ld_h, cols, type, true),
                     check_real(y_out, ld_y, cols, type, true), q ? check_fp8(q, cols) : GP_OK,

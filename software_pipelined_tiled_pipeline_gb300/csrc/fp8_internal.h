@@ -53,6 +53,9 @@ struct NormArgs {
 };
 cudaError_t launch_fp8_rmsnorm(const NormArgs& a, int sm_count, cudaStream_t stream, const void** kernel, gp_plan* plan);
 
+// p[0 .. n - 1] = value.
+cudaError_t launch_fp8_fill_f32(float* p, int64_t n, float value, cudaStream_t stream);
+
 struct NormGradArgs {
   const void *dy, *h, *dres, *weight;
   const float* rstd;

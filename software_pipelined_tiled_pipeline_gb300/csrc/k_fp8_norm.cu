@@ -506,12 +506,12 @@ __global__ void __launch_bounds__(kSumCols * kSumWays) sum_parts_kernel(const fl
   dw[c] = v;
 }
 
-__global__ void __launch_bounds__(256) zero_kernel(float* p, int64_t n) {
+__global__ void __launch_bounds__(256) fill_f32_kernel(float* p, int64_t n, float value) {
   pdl_launch_dependents();
   pdl_wait();
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x)
-    p[i] = 0.f;
+    p[i] = value;
 }
 
 // Threads per row, chunks per thread and rows per block for a row of `cols`.
@@ -617,6 +617,12 @@ cudaError_t launch_fp8_rmsnorm(const NormArgs& a, int sm_count, cudaStream_t str
   }
 }
 
+cudaError_t launch_fp8_fill_f32(float* p, int64_t n, float value, cudaStream_t stream) {
+  const int64_t blocks = (n + 255) / 256;
+  return launch_dependent(fill_f32_kernel, dim3(static_cast<unsigned>(blocks < 1024 ? blocks : 1024)), dim3(256), 0, stream,
+                          p, n, value);
+}
+
 int64_t fp8_rmsnorm_backward_parts(int64_t rows, int64_t cols, int sm_count) {
   if (by_columns(rows, cols)) return 0;
   if (cols > kRowsMaxCols) return rows < kLongParts ? rows : kLongParts;
@@ -627,11 +633,7 @@ int64_t fp8_rmsnorm_backward_parts(int64_t rows, int64_t cols, int sm_count) {
 cudaError_t launch_fp8_rmsnorm_backward(const NormGradArgs& a, int sm_count, cudaStream_t stream, const void** kernel,
                                         gp_plan* plan) {
   plan->kernel = "fp8_rmsnorm_backward";
-  if (a.rows == 0) {
-    const int64_t blocks = (a.cols + 255) / 256;
-    return launch_dependent(zero_kernel, dim3(static_cast<unsigned>(blocks < 1024 ? blocks : 1024)), dim3(256), 0,
-                            stream, a.dw, a.cols);
-  }
+  if (a.rows == 0) return launch_fp8_fill_f32(a.dw, a.cols, 0.f, stream);
   cudaError_t e;
   switch (a.type) {
     case GP_REAL_F16: e = backward_type<__half>(a, sm_count, stream, kernel, plan); break;

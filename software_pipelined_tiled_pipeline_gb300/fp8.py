@@ -232,7 +232,7 @@ def rmsnorm_fp8(x, weight, residual=None, *, eps=1e-6, format="e4m3", normed=Fal
     h = x + residual (rounded to x's type), rstd = 1 / sqrt(mean(h^2) + eps),
     y = h * rstd * weight, and y in 8 bits with a scale for each row's 128 values.
     Returns (data, scales, h, rstd), and y rounded to x's type as a fifth with
-    ``normed``.  Without a residual h is x itself.
+    ``normed``.  Without a residual h is x itself.  Without columns rstd is NaN.
     """
     if _elsewhere(x, "x", stream):
         with _On(x.get_device(), stream):

@@ -339,3 +339,29 @@ def test_refusals():
             bad()
     with pytest.raises(gp.GemmError):
         gp.rmsnorm_fp8(x, w, eps=-1.0)
+
+
+@pytest.mark.parametrize("type", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("residual", [True, False])
+def test_rows_without_columns(type, residual):
+    # the mean of nothing is NaN, and so is rstd; the buffer it is written to held other values before
+    rows = 700
+    x = torch.empty((rows, 0), dtype=ref.REAL[type], device="cuda")
+    w = torch.empty(0, device="cuda")
+    for _ in range(3):
+        before = torch.full((rows,), 5.0, device="cuda")
+        del before                                      # (the allocator hands the same memory out again)
+        q, s, h, rstd, y = gp.rmsnorm_fp8(x, w, x.clone() if residual else None, normed=True)
+        assert q.shape == h.shape == y.shape == (rows, 0) and s.shape == (rows, 0) and rstd.shape == (rows,)
+        assert bool(torch.isnan(rstd).all())
+    dx, dw = gp.rmsnorm_backward(x, x, w, rstd)
+    assert dx.shape == (rows, 0) and dw.shape == (0,)
+    guard = torch.full((rows + 2,), 7.0, device="cuda")
+    assert gp.lib().fp8_rmsnorm(None, 0, None, 0, None, 0, 1e-6, rows, 0, 1, None, 0, guard[1:].data_ptr(), None, 0, None,
+                                None) == 0
+    torch.cuda.synchronize()
+    assert float(guard[0]) == float(guard[-1]) == 7.0 and bool(torch.isnan(guard[1:-1]).all())
+    for kind in ("rows", "blocks"):
+        q, s, qt, st = gp.quantize_fp8(x, kind, transpose=True)
+        groups = rows if kind == "rows" else -(-rows // 128)
+        assert q.shape == (rows, 0) and s.shape == (groups, 0) and qt.shape == (0, rows) and st.shape == (0, -(-rows // 128))
