@@ -175,15 +175,16 @@ def dequantize_fp8(data, scales, dtype=torch.float32):
     return data.to(dtype) * wide
 
 
-def gemm_fp8(A, A_scales, B, B_scales, *, out_dtype=torch.bfloat16, addend=None, out=None, stream=None, bn=0,
+def gemm_fp8(A, A_scales, B, B_scales, *, out_dtype=None, addend=None, out=None, stream=None, bn=0,
              no_split=False, timeout_ns=0, inject_lost_load=False):
     """C = A x B^T (+ addend) of two 8-bit matrices, A: M x K, B: N x K.
 
     The three products of a linear layer y = x W^T are
     ``gemm_fp8(x, W)``, ``gemm_fp8(dy, W^T)`` and ``gemm_fp8(dy^T, x^T, addend=dW)``
-    on what ``quantize_fp8`` gives.  ``addend``: an M x N tensor of ``out_dtype``
-    added in FP32 before the rounding; it may be ``out`` itself.  ``out``: where
-    to write (M x N, rows contiguous).  ``bn``, ``no_split``, ``timeout_ns``,
+    on what ``quantize_fp8`` gives.  ``out``: where to write (M x N, rows
+    contiguous); ``out_dtype``: the type of a new output (bfloat16 where neither
+    is given), or out's own.  ``addend``: an M x N tensor of the output's type
+    added in FP32 before the rounding; it may be ``out`` itself.  ``bn``, ``no_split``, ``timeout_ns``,
     ``inject_lost_load``: see gp_fp8_options.
     """
     if _elsewhere(A, "A", stream):
@@ -197,9 +198,11 @@ def gemm_fp8(A, A_scales, B, B_scales, *, out_dtype=torch.bfloat16, addend=None,
     if B.get_device() != A.get_device():
         raise ValueError("A is on %s and B on %s" % (A.device, B.device))
     if out is None:
-        out = _empty((M, N), (N, 1), dtype=out_dtype, device=A.device)
+        out = _empty((M, N), (N, 1), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=A.device)
         ldc = N
     else:
+        if out_dtype is not None and out.dtype is not out_dtype:
+            raise ValueError("out is %s: out_dtype %s asks for another type" % (out.dtype, out_dtype))
         rows, cols, ldc = _matrix(out, "out")
         if (rows, cols) != (M, N) or out.get_device() != A.get_device():
             raise ValueError("out has shape %s on %s: want %s on %s" % ((rows, cols), out.device, (M, N), A.device))

@@ -256,3 +256,25 @@ def test_refusals():
         gp.gemm_fp8(torch.empty(5, 250, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn), a.scales,
                     b.data[:, :250], b.scales)
     assert err.value.code == gp.GP_ERR_UNSUPPORTED
+
+
+def test_out_of_another_type_than_asked_for_is_refused():
+    rng = np.random.default_rng(16)
+    a, b = ref.Fp8(5, 256, "rows", "e4m3", rng), ref.Fp8(6, 256, "rows", "e4m3", rng)
+    args = (a.data, a.scales, b.data, b.scales)
+    for have in (torch.float16, torch.bfloat16, torch.float32):
+        out = torch.full((5, 6), 3.0, dtype=have, device="cuda")
+        for want in (torch.float16, torch.bfloat16, torch.float32):
+            if want is have:
+                continue
+            with pytest.raises(ValueError):
+                gp.gemm_fp8(*args, out=out, out_dtype=want)
+            with pytest.raises(ValueError):
+                gp.gemm_fp8(*args, out=out, out_dtype=want, stream=torch.cuda.Stream())
+        assert bool((out == 3).all())
+        fresh = gp.gemm_fp8(*args, out_dtype=have)
+        assert fresh.dtype is have
+        for kw in (dict(), dict(out_dtype=have)):       # out's own type, named or not
+            assert gp.gemm_fp8(*args, out=out, **kw) is out and torch.equal(out, fresh)
+            out.fill_(3.0)
+    assert gp.gemm_fp8(*args).dtype is torch.bfloat16
