@@ -79,8 +79,8 @@ typedef struct gp_fp8_options {
     int32_t bn;                  /* force the tile width on the tensor cores' N side: 16, 32, 64, 128 or 256 (0 = the
                                     planner's choice; other values, and 256 on one SM: GP_ERR_UNSUPPORTED) */
     int32_t no_split;            /* 1: never share a tile's K loop among CTAs */
-    int32_t inject_lost_load;    /* test hook: the TMA producer skips the last tile load of the problem, so a
-                                    consumer wait runs out and the call reports GP_ERR_TIMEOUT (no GPU fault); not
+    int32_t inject_lost_load;    /* test hook: the TMA producer skips the last tile load of the problem (2: the first),
+                                    so a consumer wait runs out and the call reports GP_ERR_TIMEOUT (no GPU fault); not
                                     with bn 256 (GP_ERR_UNSUPPORTED), whose tiles two CTAs share */
 } gp_fp8_options;
 
@@ -94,6 +94,8 @@ typedef struct gp_fp8_options {
  * the product of the two scales (formed in FP32: where that overflows, so does
  * the result) and added to FP32 sums.
  * M == 0 or N == 0: nothing is launched.  K == 0: C = addend, or zeros.
+ * After GP_ERR_TIMEOUT, C is incomplete: a tile whose K loop did not come to its
+ * end is not written, and which these are is not reported.
  * GP_ERR_ARG: NULL A, B or scales with K > 0, NULL C, bad enums, group not 1
  * or 128, an ld below the columns (K, or N for C and addend), a negative size.
  * GP_ERR_UNSUPPORTED: an 8-bit matrix not 16-byte aligned or with ld % 16 != 0;

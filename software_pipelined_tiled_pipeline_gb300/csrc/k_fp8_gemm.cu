@@ -161,6 +161,9 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
 }
 
 // Store 4 bytes into another CTA's shared memory (cluster-window address).
+__device__ __forceinline__ void st_cluster_s32(uint32_t cluster_addr, int v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void st_cluster_f1(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
@@ -184,9 +187,11 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 
 // Waits that come with every K block.  The try itself waits in hardware, up to
 // kTryNs; the clock is read only where that is not enough.  One that gives up
-// leaves its site in the CTA's abort flag, which makes every further wait
-// return at once and is reported when the kernel ends; code and registers here
-// are counted, as the K loop of the adding warps fills both.
+// leaves its site in the CTA's abort flag, which is reported when the kernel
+// ends and makes every further wait return after two tries: the producer and
+// the MMA issuer leave their loops at that, the adding warps after at most a
+// batch of K blocks (7 ms).  Code and registers here are counted, as the K loop
+// of the adding warps fills both.
 constexpr uint32_t kTryNs = 100000;
 constexpr uint64_t kMostWaitNs = 4000000000ull;   // the 32-bit clock wraps after 4.29 s
 __device__ __forceinline__ bool try_wait(uint32_t bar_addr, uint32_t parity) {
@@ -205,17 +210,18 @@ __device__ __forceinline__ uint32_t clock_ns() {
   asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
   return t;
 }
-__device__ __forceinline__ void ring_wait(uint32_t bar_addr, uint32_t parity, uint32_t limit_ns, CtaCtl* cta,
+__device__ __forceinline__ bool ring_wait(uint32_t bar_addr, uint32_t parity, uint32_t limit_ns, CtaCtl* cta,
                                           int site) {
-  if (try_wait(bar_addr, parity)) return;
+  if (try_wait(bar_addr, parity)) return true;
   const uint32_t t0 = clock_ns();
   while (!try_wait(bar_addr, parity)) {
-    if (cta->abort) return;
+    if (cta->abort) return false;
     if (clock_ns() - t0 > limit_ns) {
       cta->abort = site;
-      return;
+      return false;
     }
   }
+  return true;
 }
 
 // Pairs of FP32 values in one 64-bit register: a packed product is one
@@ -520,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   CtaCtl* cta = &bar->ctl;
   const uint32_t limit_ns = static_cast<uint32_t>(g.ctl.timeout_ns < kMostWaitNs ? g.ctl.timeout_ns : kMostWaitNs);
   const uint32_t full0 = smem_u32(&bar->full[0]), done0 = smem_u32(&bar->done[0]), free0 = smem_u32(&bar->acc_empty[0]);
-  int issued = 0;   // producer only
+  int issued = 0, lost = -1;   // producer only: loads so far, and the one that the test hook skipped
 
   if (warp < 4) {
     if (Sh::SPLIT_REGS) regs_decrease<Sh::OTHER_REGS>();
@@ -535,8 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int p_row = pb * Sh::TILE_P + rank * Sh::P_ROWS;
         const int q_row = qb * BN + rank * Sh::Q_ROWS;
         for (int kb = k0; kb < k1; ++kb) {
-          ring_wait(done0 + s * 8, ph ^ 1u, limit_ns, cta, kSiteProducerEmpty);
-          if (cta->abort) { ok = false; break; }
+          if (!ring_wait(done0 + s * 8, ph ^ 1u, limit_ns, cta, kSiteProducerEmpty) || cta->abort) { ok = false; break; }
           uint8_t* slot = ring + s * Sh::STAGE;
           if (PAIR) {
             // the even CTA's barrier counts the bytes of both CTAs' loads
@@ -544,13 +549,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t full = mapa_shared(smem_u32(&bar->full[s]), 0);
             tma_load_2d_pair(smem_u32(slot), &tmP, full, kb * kBK, p_row);
             tma_load_2d_pair(smem_u32(slot + Sh::P_BYTES), &tmQ, full, kb * kBK, q_row);
-            ++issued;
-          } else if (!(g.ctl.inject_lost_load && items.tile == items.tiles - 1 && kb == kt - 1)) {
+          } else if (g.ctl.inject_lost_load == 0 ||
+                     (g.ctl.inject_lost_load == 2 ? items.tile + kb != 0 : items.tile != items.tiles - 1 || kb != kt - 1)) {
             mbar_arrive_expect_tx(&bar->full[s], Sh::STAGE);
             tma_load_2d(smem_u32(slot), &tmP, &bar->full[s], kb * kBK, p_row);
             tma_load_2d(smem_u32(slot + Sh::P_BYTES), &tmQ, &bar->full[s], kb * kBK, q_row);
-            ++issued;
+          } else {
+            lost = issued;
           }
+          ++issued;
           if (++s == Sh::STAGES) { s = 0; ph ^= 1u; }
         }
       }
@@ -565,13 +572,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t desc0 = umma_desc_sw128(smem_u32(ring));
       while (ok && items.next()) {
         for (int kb = k0; kb < k1; ++kb) {
-          ring_wait(full0 + s * 8, ph, limit_ns, cta, kSiteConsumerFull);
-          ring_wait(free0 + a * 8, aph ^ 1u, limit_ns, cta, kSiteMmaAccEmpty);
-          tc_fence_after();   // (after a wait that gave up: MMAs of whatever the slot holds)
+          const bool there = ring_wait(full0 + s * 8, ph, limit_ns, cta, kSiteConsumerFull) &&
+                             ring_wait(free0 + a * 8, aph ^ 1u, limit_ns, cta, kSiteMmaAccEmpty);
+          tc_fence_after();
           const uint64_t dp = desc0 + static_cast<uint32_t>(s * Sh::STAGE) / 16;
           const uint64_t dq = dp + Sh::P_BYTES / 16;
           const uint32_t d = tmem + a * BN;
-          if (leader) {
+          if (leader && there) {   // (nothing of a slot that never came, in a pair for neither CTA)
 #pragma unroll
             for (int kk = 0; kk < kBK / kMmaK; ++kk) {   // 32 bytes along K: the start address field moves by 2
               if (PAIR)
@@ -581,11 +588,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (PAIR) umma_commit_pair(&bar->done[s], 0x3); else umma_commit(&bar->done[s]);
           }
-          __syncwarp();
+          // (the vote comes after the MMAs are issued, off their path)
+          if (!__all_sync(0xffffffffu, there)) { ok = false; break; }
           if (++s == Sh::STAGES) { s = 0; ph ^= 1u; }
           if (++a == Sh::BUFS) { a = 0; aph ^= 1u; }
         }
-        if (__any_sync(0xffffffffu, cta->abort)) ok = false;
       }
       if (leader) {
         // fires when every MMA issued above has completed
@@ -664,7 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (end < k1) stage_scales(batch ^ 1, pb, qb, end, min(BATCH, k1 - end));
         const float* slot = scales + batch * BATCH * SCALES;
         // A wait that gave up in here leaves wrong sums behind, which are never
-        // written: the abort flag is looked at after each batch.
+        // written: the abort flag is looked at after each batch, and the CTAs of
+        // a cluster tell each other.
         for (int kb = kc; kb < end; ++kb, slot += SCALES) {
           const float sp = slot[g.p.shift ? 0 : row];
           const float* sq = slot + Sh::P_ROWS;
@@ -727,8 +735,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int col = half * Sh::HALF + i;
           st_cluster_f1(mapa_shared(at + (col & (per - 1)) * (kXRow * 4), static_cast<uint32_t>(col >> per_log)), acc[i]);
         }
+        if (!ok && lane < k_ctas)   // none of the cluster writes what this CTA's sums are missing from
+          st_cluster_s32(mapa_shared(smem_u32(const_cast<int*>(&cta->abort)), lane), kSiteEpilogueAccFull);
         cluster_sync();
-        if (ok) {
+        if (!cta->abort) {
           const float* buf = reinterpret_cast<const float*>(ring);
           const int64_t p0 = static_cast<int64_t>(pb) * Sh::TILE_P, q0 = static_cast<int64_t>(qb) * BN + in_cluster * per;
           if (g.out_type == GP_REAL_BF16)
@@ -769,9 +779,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // loads still in flight land in shared memory: wait for them before exit
       CtaCtl never_abort{0};
-      for (int i = issued > Sh::STAGES ? issued - Sh::STAGES : 0; i < issued; ++i)
+      for (int i = issued > Sh::STAGES ? issued - Sh::STAGES : 0; i < issued; ++i) {
+        if (i == lost) continue;
         mbar_wait(&bar->full[i % Sh::STAGES], static_cast<uint32_t>((i / Sh::STAGES) & 1), g.ctl, &never_abort,
                   kSiteDrain);
+      }
     }
   }
   if (PAIR) {
@@ -946,8 +958,8 @@ int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int
   bool known = want == 0;
   for (const TileCost& t : kTileCosts) known |= t.bn == want;
   if (!known) return GP_ERR_UNSUPPORTED;
-  const bool one_cta = opts && opts->inject_lost_load;   // (a lost load is injected into whole tiles of one CTA)
-  if (one_cta && want == 256) return GP_ERR_UNSUPPORTED;
+  const bool no_pair = opts && opts->inject_lost_load;   // (a lost load is not injected into pairs)
+  if (no_pair && want == 256) return GP_ERR_UNSUPPORTED;
   const int64_t kt = (K + kBK - 1) / kBK;
   const int have = sms > 0 ? sms : 152;
   // Try every width with either operand on the MMA's N side (Q), and every
@@ -961,11 +973,11 @@ int fp8_plan_impl(int64_t M, int64_t N, int64_t K, int a_group, int b_group, int
     const int64_t P = sw ? N : M, Q = sw ? M : N;
     const bool q_rows = (sw ? a_group : b_group) == 1;
     for (const TileCost& t : kTileCosts) {
-      if (want ? t.bn != want : (one_cta && t.bn == 256)) continue;
+      if (want ? t.bn != want : (no_pair && t.bn == 256)) continue;
       const int ctas = t.bn == 256 ? 2 : 1;
       const int64_t tiles = (P + 128 * ctas - 1) / (128 * ctas) * ((Q + t.bn - 1) / t.bn);
       for (int c = 1; c <= 8; c *= 2) {
-        if (c > 1 && (ctas == 2 || one_cta || (opts && opts->no_split) || tiles * c > (c > 2 ? have * 7 / 8 : have) ||
+        if (c > 1 && (ctas == 2 || (opts && opts->no_split) || tiles * c > (c > 2 ? have * 7 / 8 : have) ||
                       kt < kMinShare * c))
           break;
         const int64_t workers = have / (ctas * c);

@@ -278,3 +278,66 @@ def test_out_of_another_type_than_asked_for_is_refused():
             assert gp.gemm_fp8(*args, out=out, **kw) is out and torch.equal(out, fresh)
             out.fill_(3.0)
     assert gp.gemm_fp8(*args).dtype is torch.bfloat16
+
+
+def tile_regions(M, N, plan):
+    """(rows, columns) of C of each output tile, in the kernel's order."""
+    P, Q = (N, M) if plan["layout"] else (M, N)
+    bm, bn, group = plan["bm"], plan["bn"], plan["raster_gm"]
+    p_blocks, q_blocks = -(-P // bm), -(-Q // bn)
+    for first in range(0, p_blocks, group):
+        for qb in range(q_blocks):
+            for pb in range(first, min(first + group, p_blocks)):
+                p, q = slice(pb * bm, (pb + 1) * bm), slice(qb * bn, (qb + 1) * bn)
+                yield (q, p) if plan["layout"] else (p, q)
+
+
+@pytest.mark.parametrize("which", [1, 2])
+@pytest.mark.parametrize("M,N,K,bn", [(3, 512, 4096, 0), (3, 1024, 2048, 0), (20, 4096, 1024, 0), (200, 300, 1024, 16),
+                                      (200, 300, 1024, 32), (200, 300, 1024, 64), (200, 300, 1024, 128),
+                                      (2100, 2300, 512, 64)])
+def test_a_tile_with_a_lost_load_is_not_written(M, N, K, bn, which):
+    # the first or last tile, whose K loop may be shared by a cluster: none of its CTAs writes sums that lack a share
+    rng = np.random.default_rng(17)
+    a, b = ref.Fp8(M, K, "rows", "e4m3", rng), ref.Fp8(N, K, "blocks", "e4m3", rng)
+    C, buf = guarded(M, N, "f32")
+    gp.gemm_fp8(a.data, a.scales, b.data, b.scales, out=C, bn=bn, timeout_ns=20_000_000, inject_lost_load=which)
+    st = gp.gemm_stats(sync=True)
+    assert st["status"] == gp.GP_ERR_TIMEOUT
+    assert outside_untouched(buf, M, N, N)
+    if bn == 0:
+        assert st["plan"]["k_splits"] == {512: 8, 1024: 4, 4096: 2}[N]
+    x, y = a.values, b.values
+    want = x @ y.T
+    near = np.abs(ref.f64(C) - want) <= ref.gemm_bound(x, y, want, "f32")
+    regions = list(tile_regions(M, N, st["plan"]))
+    assert len(regions) == st["plan"]["tiles"]
+    for i, at in enumerate(regions):
+        untouched = bool(torch.isnan(C[at]).all())
+        if i == (0 if which == 2 else len(regions) - 1):
+            assert untouched, "the tile without a load was written"
+        else:
+            assert untouched or near[at].all()
+
+
+@pytest.mark.parametrize("no_split", [True, False])
+def test_a_lost_load_does_not_hold_the_gpu_for_the_rest_of_a_long_k_loop(no_split):
+    # the first of 1024 K blocks never comes: each later wait would take its tries' 100 us again
+    M, N, K = 3, 128, 131072
+    q = torch.zeros((M + N, K), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    s = torch.ones((M + N, K // 128), device="cuda")
+    args = (q[:M], s[:M], q[M:], s[M:])
+    out = torch.full((M, N), float("nan"), device="cuda")
+    gp.gemm_fp8(*args, out=out, no_split=no_split)
+    torch.cuda.synchronize()
+    assert bool((out == 0).all())
+    out.fill_(float("nan"))
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    gp.gemm_fp8(*args, out=out, no_split=no_split, timeout_ns=20_000_000, inject_lost_load=2)
+    end.record()
+    st = gp.gemm_stats(sync=True)
+    assert st["status"] == gp.GP_ERR_TIMEOUT and st["plan"]["k_splits"] == (1 if no_split else 8)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(out[next(tile_regions(M, N, st["plan"]))]).all())
+    assert 20 <= begin.elapsed_time(end) <= 80           # ms: the limit, and a batch of tries after it
