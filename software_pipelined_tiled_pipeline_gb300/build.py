@@ -8,6 +8,7 @@ no libcuda is needed at link time).  Host code is portable C++17: the same
 sources build on x86_64 and on aarch64.
 """
 import os
+import re
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -23,6 +24,28 @@ SOURCES = ["api.cu", "fp8_api.cu", "k_ffma.cu", "k_fp8_gemm.cu", "k_fp8_norm.cu"
            "k_umma.cu", "probe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
+
+# Kernels whose warps trade registers count on an exact number per thread at launch, and are refused at run time with
+# any other: {source: (kernel, registers)}.  ptxas says what it gave them.
+LAUNCH_REGISTERS = {"k_fp8_gemm.cu": (r"fp8_ring_kernelILi(128|256)E", 168), "k_umma.cu": (r"umma_i8_overlap_kernel", 128)}
+
+
+def check_launch_registers(src, ptxas):
+    """Raise if a kernel of `src` in ptxas's -v output has other registers than its register split counts on."""
+    if src not in LAUNCH_REGISTERS:
+        return
+    kernel, want = LAUNCH_REGISTERS[src]
+    seen = 0
+    for part in ptxas.split("Compiling entry function '")[1:]:
+        name, used = part.split("'", 1)[0], re.search(r"Used (\d+) registers", part)
+        if not re.search(kernel, name):
+            continue
+        seen += 1
+        if used is None or int(used.group(1)) != want:
+            raise RuntimeError("%s: %s was compiled to %s registers, its register split counts on %d" % (
+                src, name, used.group(1) if used else "an unknown number of", want))
+    if not seen:
+        raise RuntimeError("%s: no kernel like %s in ptxas's output" % (src, kernel))
 
 
 def nvcc() -> str:
@@ -56,7 +79,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
 
     def compile_one(src):
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        cmd = [cc] + ARCH + CFLAGS + (["-Xptxas", "-v"] if ptxas_verbose else []) + [
+        cmd = [cc] + ARCH + CFLAGS + (["-Xptxas", "-v"] if ptxas_verbose or src in LAUNCH_REGISTERS else []) + [
             "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, cmd, r
@@ -71,6 +94,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
                 print(r.stderr, file=sys.stderr)
         if r.returncode != 0:
             raise RuntimeError("nvcc failed on %s:\n%s%s" % (src, r.stdout, r.stderr))
+        check_launch_registers(src, r.stderr)
         objs.append(obj)
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs

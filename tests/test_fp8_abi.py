@@ -3,6 +3,7 @@ reported before anything is launched, struct layouts match the header, the
 plan follows its rules, and the tests' own plain formats agree with torch's."""
 import ctypes
 import os
+import re
 import shutil
 import subprocess
 
@@ -225,3 +226,29 @@ def test_plan_of_few_sms(gp):
                     d = p.as_dict()
                     assert 1 <= d["grid"] <= sms and d["grid"] % (2 if d["cta_pair"] else d["k_splits"]) == 0
                     assert bn in (0, d["bn"])
+
+
+PTXAS = """ptxas info    : Compiling entry function '_ZN2gp15fp8_ring_kernelILi256ELb0ELb1ELb0EEEv' for 'sm_103a'
+ptxas info    : Function properties for _ZN2gp15fp8_ring_kernelILi256ELb0ELb1ELb0EEEv
+    0 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads
+ptxas info    : Used %d registers, used 2 barriers
+ptxas info    : Compiling entry function '_ZN2gp15fp8_ring_kernelILi16ELb1ELb0ELb0EEEv' for 'sm_103a'
+ptxas info    : Used 122 registers, used 2 barriers
+"""
+
+
+def test_build_refuses_a_register_split_that_cannot_launch():
+    # the wide kernels' warps trade registers; with others than 168 at launch every call would be refused
+    gbuild.check_launch_registers("k_fp8_gemm.cu", PTXAS % 168)
+    gbuild.check_launch_registers("k_fp8_quant.cu", "")              # (no such kernel there)
+    for wrong in (160, 128):
+        with pytest.raises(RuntimeError, match="compiled to %d registers" % wrong):
+            gbuild.check_launch_registers("k_fp8_gemm.cu", PTXAS % wrong)
+    with pytest.raises(RuntimeError):
+        gbuild.check_launch_registers("k_umma.cu", PTXAS % 128)      # its kernel is missing from the output
+    for src, constant, threads in (("k_fp8_gemm.cu", r"kLaunchRegs = (\d+);", None),
+                                   ("k_umma.cu", r"kOvLaunchRegs = 65536 / kOvThreads;", r"kOvThreads = (\d+);")):
+        text = open(os.path.join(gbuild.CSRC, src)).read()
+        found = re.search(constant, text)
+        regs = int(found.group(1)) if threads is None else 65536 // int(re.search(threads, text).group(1))
+        assert regs == gbuild.LAUNCH_REGISTERS[src][1]
