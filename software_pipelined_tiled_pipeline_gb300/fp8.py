@@ -130,6 +130,15 @@ def _new_fp8(rows, cols, fmt, group, device):
     return data, scales, _pack(data.data_ptr(), scales.data_ptr(), ld, 1, groups, fmt, group)
 
 
+def _group(scales):
+    """Rows that share a scale."""
+    if scales == "rows":
+        return 1
+    if scales == "blocks":
+        return GROUP
+    raise ValueError("unknown scales %r" % (scales,))
+
+
 def quantize_fp8(x, scales="rows", *, format="e4m3", transpose=False, stream=None):
     """x (rows x cols; float16, bfloat16 or float32) to 8 bits.
 
@@ -146,12 +155,7 @@ def quantize_fp8(x, scales="rows", *, format="e4m3", transpose=False, stream=Non
             return quantize_fp8(x, scales, format=format, transpose=transpose)
     rows, cols, ld = _matrix(x, "x")
     real = _real(x, "x")
-    if scales == "rows":
-        group = 1
-    elif scales == "blocks":
-        group = GROUP
-    else:
-        raise ValueError("unknown scales %r" % (scales,))
+    group = _group(scales)
     if transpose not in (False, True, "only"):
         raise ValueError("unknown transpose %r" % (transpose,))
     fmt = _binding._enum(format, FP8_FORMATS, "format")
@@ -222,10 +226,9 @@ def gemm_fp8(A, A_scales, B, B_scales, *, out_dtype=None, addend=None, out=None,
 
 def gemm_fp8_plan(M, N, K, A_scales="rows", B_scales="blocks", *, sms=0, bn=0, no_split=False) -> dict:
     """The tile, ring and split that gemm_fp8 would choose (see gemm_fp8_plan in the C header)."""
-    group = {"rows": 1, "blocks": GROUP}
     p = GpPlan()
     opts = GpFp8Options(0, int(bn), int(no_split), 0)
-    _check(lib().gemm_fp8_plan(M, N, K, group[A_scales], group[B_scales], sms, opts, p), "gemm_fp8_plan")
+    _check(lib().gemm_fp8_plan(M, N, K, _group(A_scales), _group(B_scales), sms, opts, p), "gemm_fp8_plan")
     return p.as_dict()
 
 

@@ -252,3 +252,9 @@ def test_build_refuses_a_register_split_that_cannot_launch():
         found = re.search(constant, text)
         regs = int(found.group(1)) if threads is None else 65536 // int(re.search(threads, text).group(1))
         assert regs == gbuild.LAUNCH_REGISTERS[src][1]
+
+
+@pytest.mark.parametrize("kinds", [("columns", "blocks"), ("rows", "tiles"), (128, "rows")])
+def test_plan_refuses_unknown_scales(gp, kinds):
+    with pytest.raises(ValueError):
+        gp.gemm_fp8_plan(64, 64, 64, *kinds)
