@@ -75,7 +75,8 @@ typedef struct gp_fp8_matrix {
 
 /* Options of gemm_fp8.  Zero-initialise and set what you need. */
 typedef struct gp_fp8_options {
-    uint64_t timeout_ns;         /* limit of every bounded wait inside the kernel (0 = 1 s) */
+    uint64_t timeout_ns;         /* limit of every bounded wait inside the kernel (0 = 1 s; waits of the K loop count
+                                    with a 32-bit clock, and give up after 4 s where it is longer) */
     int32_t bn;                  /* force the tile width on the tensor cores' N side: 16, 32, 64, 128 or 256 (0 = the
                                     planner's choice; other values, and 256 on one SM: GP_ERR_UNSUPPORTED) */
     int32_t no_split;            /* 1: never share a tile's K loop among CTAs */
