@@ -341,3 +341,80 @@ def test_a_lost_load_does_not_hold_the_gpu_for_the_rest_of_a_long_k_loop(no_spli
     torch.cuda.synchronize()
     assert bool(torch.isnan(out[next(tile_regions(M, N, st["plan"]))]).all())
     assert 20 <= begin.elapsed_time(end) <= 80           # ms: the limit, and a batch of tries after it
+
+
+def check_with_addend(a, b, out, ld, rng, **kw):
+    """The product with an addend of its own and with the output as addend: the same bits, and within the bound."""
+    M, N = a.code.shape[0], b.code.shape[0]
+    add = rng.standard_normal((M, N)) * 5
+    apart, plan = check(a, b, out, addend=add, ld=ld, **kw)
+    C, buf = guarded(M, N, out, ld)
+    C.copy_(torch.from_numpy(add).cuda())
+    assert gp.gemm_fp8(a.data, a.scales, b.data, b.scales, out=C, addend=C, **kw) is C
+    assert torch.equal(C, apart) and outside_untouched(buf, M, N, ld)
+    return plan
+
+
+@pytest.mark.parametrize("bn", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("kinds,K,swapped", [(("rows", "blocks"), 700, (0, 0)), (("rows", "rows"), 300, (0, 0)),
+                                             (("blocks", "rows"), 4100, (1, 1))])
+def test_addends_at_every_width(bn, out, kinds, K, swapped):
+    # whole tiles and ragged ones, rows on and off the alignment of whole stores; the operand with block scales takes
+    # the N side of wide tiles, so that both roles come about
+    rng = np.random.default_rng(bn + K)
+    M, N = 300, 520
+    a, b = ref.Fp8(M, K, kinds[0], "e4m3", rng, spread_log2=0.5), ref.Fp8(N, K, kinds[1], "e5m2", rng, spread_log2=0.5)
+    for ld in (N, N + 2, N + 3):
+        plan = check_with_addend(a, b, out, ld, rng, bn=bn, no_split=True)
+        assert plan["bn"] == bn and plan["k_splits"] == 1 and plan["cta_pair"] == (bn == 256)
+        if bn >= 128:
+            assert plan["layout"] == swapped[bn == 256]
+
+
+# (M, N, K): the plan on 152 SMs -- 1 where B takes the M side, width, CTAs per tile
+FEW_ROWS = [((1, 4096, 4096), (1, 16, 4)), ((1, 300, 4096), (1, 16, 8)), ((9, 2048, 1024), (1, 16, 2)),
+            ((33, 4000, 1024), (1, 16, 1)), ((50, 8192, 1024), (1, 32, 1)), ((5, 130, 1024), (0, 16, 2)),
+            ((200, 9, 4096), (0, 16, 8)), ((640, 33, 2056), (0, 16, 4)), ((1030, 60, 4096), (0, 32, 4)),
+            ((1, 128, 512), (0, 16, 1))]
+
+
+@pytest.mark.parametrize("shape,plan", FEW_ROWS)
+@pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
+def test_few_rows_in_every_plan(shape, plan, out):
+    M, N, K = shape
+    rng = np.random.default_rng(M + N)
+    a = ref.Fp8(M, K, "rows", "e4m3", rng, spread_log2=0.5)
+    b = ref.Fp8(N, K, "blocks" if M % 2 else "rows", "e4m3", rng, spread_log2=0.5)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for ld in (N, N + 3):
+        got = check(a, b, out, ld=ld)[1], check_with_addend(a, b, out, ld, rng)
+        for p in got:
+            assert sms != 152 or (p["layout"], p["bn"], p["k_splits"]) == plan
+    whole = check(a, b, out, no_split=True)[1]
+    assert whole["k_splits"] == 1
+
+
+# width forced, kinds of scales, (M, N, K): the plan on 152 SMs -- 1 where B takes the M side, CTAs per tile
+CLUSTERS = [(16, "rb", (100, 200, 8192), (0, 8)), (16, "rb", (700, 150, 8192), (0, 2)), (16, "rb", (20, 2400, 8192), (1, 2)),
+            (32, "rb", (100, 200, 8192), (0, 8)), (32, "rr", (700, 150, 8192), (0, 4)), (32, "rb", (300, 500, 8192), (0, 2)),
+            (32, "rb", (20, 1100, 8192), (1, 8)), (32, "rb", (20, 2400, 8192), (1, 4)), (32, "rr", (260, 1000, 8192), (1, 2)),
+            (64, "rb", (100, 200, 8192), (0, 8)), (64, "rb", (300, 500, 8192), (0, 4)), (64, "rr", (260, 1000, 8192), (0, 2)),
+            (64, "rb", (60, 2000, 8192), (1, 8)), (64, "rb", (20, 2400, 8192), (1, 4)), (64, "rb", (60, 9000, 8192), (1, 2)),
+            (128, "rb", (100, 200, 8192), (0, 8)), (128, "rb", (260, 1000, 8192), (0, 4)), (128, "rb", (60, 9000, 8192), (0, 2)),
+            (128, "br", (300, 500, 32768), (1, 8)), (128, "br", (500, 600, 16384), (1, 4)), (128, "br", (900, 1100, 8192), (1, 2))]
+
+
+@pytest.mark.parametrize("bn,kinds,shape,plan", CLUSTERS)
+def test_clusters_of_every_width_and_role(bn, kinds, shape, plan):
+    M, N, K = shape
+    rng = np.random.default_rng(bn + M)
+    kind = {"r": "rows", "b": "blocks"}
+    a = ref.Fp8(M, K, kind[kinds[0]], "e4m3", rng, spread_log2=0.5)
+    b = ref.Fp8(N, K, kind[kinds[1]], "e4m3", rng, spread_log2=0.5)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for out in ("f16", "bf16", "f32"):
+        got = check(a, b, out, bn=bn)[1], check_with_addend(a, b, out, N + (out == "f16"), rng, bn=bn)
+        for p in got:
+            assert p["bn"] == bn
+            assert sms != 152 or (p["layout"], p["k_splits"]) == plan

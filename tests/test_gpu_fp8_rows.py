@@ -365,3 +365,23 @@ def test_rows_without_columns(type, residual):
         q, s, qt, st = gp.quantize_fp8(x, kind, transpose=True)
         groups = rows if kind == "rows" else -(-rows // 128)
         assert q.shape == (rows, 0) and s.shape == (groups, 0) and qt.shape == (0, rows) and st.shape == (0, -(-rows // 128))
+
+
+@pytest.mark.parametrize("cols", [200, 1000, 5000, 17000])
+@pytest.mark.parametrize("type", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("wtype", ["f16", "bf16", "f32"])
+def test_weights_of_every_type_on_and_off_alignment(cols, type, wtype):
+    rng = np.random.default_rng(cols)
+    rows = 6
+    x, dy = matrix(rows, cols, type, rng), matrix(rows, cols, type, rng)
+    wide = torch.from_numpy(1 + 0.2 * rng.standard_normal(cols + 1)).cuda().to(ref.REAL[wtype])
+    for w in (wide[:-1], wide[1:]):                     # the second begins one element past a 16-byte boundary
+        q, s, h, rstd, y = gp.rmsnorm_fp8(x, w, eps=1e-5, normed=True)
+        check_norm(q, s, rstd, y, h, w, 1e-5, type, "e4m3")
+        same = w.to(torch.float32)                      # the same values in 32 bits: the same bits come out
+        again = gp.rmsnorm_fp8(x, same, eps=1e-5, normed=True)
+        assert torch.equal(q.view(torch.uint8), again[0].view(torch.uint8))
+        assert torch.equal(s, again[1]) and torch.equal(rstd, again[3]) and torch.equal(y, again[4])
+        dx, dw = gp.rmsnorm_backward(dy, x, w, rstd)
+        dx2, dw2 = gp.rmsnorm_backward(dy, x, same, rstd)
+        assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
