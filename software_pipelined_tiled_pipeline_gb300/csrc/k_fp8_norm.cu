@@ -267,28 +267,61 @@ __device__ __forceinline__ void column_sums(const NormGradArgs& a, float (*s)[kS
   const int cols = static_cast<int>(a.cols), c = blockIdx.x * kStripCols + (t & 7) * 8;
   const bool vec = a.vec != 0;
   const int64_t step = threads >> 3;
-  constexpr int BATCH = 4;   // rows whose loads are under way together
+  const Eight e = eight_columns(c, vec);
   float dw[8] = {};
-  for (int64_t row = t >> 3; row < a.rows; row += BATCH * step) {
-    Raw8<T> rdy[BATCH], rh[BATCH];
-    float rstd[BATCH];
+  // A thread has `batch` rows under way together, and their loads carry no
+  // branch: past the last row the thread's first one is read again and not
+  // added, past the last column the first one is (those sums go nowhere).  whole:
+  // the eight columns are one aligned run.
+  auto walk = [&](auto whole, auto batch) {
+    constexpr int BATCH = batch.value;
+    for (int64_t row = t >> 3; row < a.rows; row += BATCH * step) {
+      Raw8<T> rdy[BATCH], rh[BATCH];
+      float rstd[BATCH];
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const int64_t at = row + u * step;
-      const bool in = at < a.rows;
-      load8(rdy[u], static_cast<const T*>(a.dy) + at * a.ld_dy, c, in ? cols : 0, vec);
-      load8(rh[u], static_cast<const T*>(a.h) + at * a.ld_h, c, in ? cols : 0, vec);
-      rstd[u] = in ? a.rstd[at] : 0.f;
+      for (int u = 0; u < BATCH; ++u) {
+        const bool in = row + u * step < a.rows;
+        const int64_t at = in ? row + u * step : row;
+        const T* dy = static_cast<const T*>(a.dy) + at * a.ld_dy;
+        const T* h = static_cast<const T*>(a.h) + at * a.ld_h;
+        if constexpr (whole.value) {
+#pragma unroll
+          for (int i = 0; i < Raw8<T>::WORDS; ++i) {
+            rdy[u].w[i] = reinterpret_cast<const uint4*>(dy + c)[i];
+            rh[u].w[i] = reinterpret_cast<const uint4*>(h + c)[i];
+          }
+        } else {
+          T x[8], y[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int col = e.first + k * e.stride < cols ? e.first + k * e.stride : e.first;
+            x[k] = dy[col];
+            y[k] = h[col];
+          }
+          memcpy(&rdy[u], x, sizeof(x));
+          memcpy(&rh[u], y, sizeof(y));
+        }
+        rstd[u] = a.rstd[at];
+      }
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        float dy[8], h[8];
+        unpack8(rdy[u], dy);
+        unpack8(rh[u], h);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float p = dy[k] * (h[k] * rstd[u]);
+          dw[k] += row + u * step < a.rows ? p : 0.f;
+        }
+      }
     }
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      float dy[8], h[8];
-      unpack8(rdy[u], dy);
-      unpack8(rh[u], h);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) dw[k] += dy[k] * (h[k] * rstd[u]);
-    }
-  }
+  };
+  // (threads past the row's end have nothing to add; the shuffles below need them)
+  if (vec && c + 8 <= cols)
+    walk(std::true_type(), std::integral_constant<int, 4>());
+  else if (e.first < cols)
+    walk(std::false_type(), std::integral_constant<int, 2>());
+  __syncwarp();
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], 8);
@@ -299,8 +332,8 @@ __device__ __forceinline__ void column_sums(const NormGradArgs& a, float (*s)[kS
   if (t >= kStripCols) return;
   float v = s[0][t];
   for (int w = 1; w < threads >> 5; ++w) v += s[w][t];
-  const Eight e = eight_columns(blockIdx.x * kStripCols + (t & ~7), vec);
-  const int col = e.first + (t & 7) * e.stride;
+  const Eight own = eight_columns(blockIdx.x * kStripCols + (t & ~7), vec);
+  const int col = own.first + (t & 7) * own.stride;
   if (col < cols) a.dw[col] = v;
 }
 
@@ -557,10 +590,14 @@ cudaError_t forward_type(const NormArgs& a, int sm_count, cudaStream_t stream, c
 }
 
 // Rows up to which the weight's gradient is worked out by columns (see
-// rmsnorm_grad_kernel).  Measured against partial sums and their kernel, BF16,
-// device time (a call saves 5 us of host time besides): 256 rows of 8192
-// 7.2 against 9.3 us, 512 rows 10.5 against 12.0, 1024 rows 16.5 against 15.7;
-// 512 rows of 4096 7.2 against 9.9, of 2056 12.1 against 9.0.
+// rmsnorm_grad_kernel).  Measured against partial sums and their kernel, us of
+// device time, columns | partials, 512 rows (a call saves 5 us of host time
+// besides): BF16 64 columns 4.0 | 6.8, 512 4.3 | 7.2, 1000 5.4 | 7.8, 2056 6.3 | 9.0,
+// 8192 10.0 | 11.9, 16384 21.1 | 24.2; FP32 64 4.6 | 6.1, 2056 9.3 | 12.4, 8192
+// 17.6 | 18.7, 16384 40.9 | 42.5.  At 1024 rows of 16384 47.0 | 43.6 (FP32 84 | 72).
+// With rows off 16-byte boundaries up to 200 rows (BF16 1001 columns 6.1 | 6.4, 65
+// 4.6 | 5.1); at 512 rows 65 columns take 9.1 | 7.1, FP32 1001 11.3 | 7.4, as a call
+// 16 | 21.  The alignment is no part of the rule: the workspace goes by sizes alone.
 constexpr int64_t kFewRows = 512;
 bool by_columns(int64_t rows, int64_t cols) { return rows <= kFewRows && cols <= kRowsMaxCols; }
 

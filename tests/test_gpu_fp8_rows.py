@@ -385,3 +385,23 @@ def test_weights_of_every_type_on_and_off_alignment(cols, type, wtype):
         dx, dw = gp.rmsnorm_backward(dy, x, w, rstd)
         dx2, dw2 = gp.rmsnorm_backward(dy, x, same, rstd)
         assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("rows,cols,pad", [(5, 200, 0), (77, 1000, 0), (133, 65, 0), (200, 2056, 0), (90, 1004, 4), (512, 130, 1)])
+def test_weight_gradient_of_few_rows_with_values_that_are_not_finite(rows, cols, pad):
+    # each stays in its own column, where the rows' number is no multiple of what a block takes at a time too
+    rng = np.random.default_rng(rows + cols)
+    for type in ("bf16", "f32"):
+        dy, h = matrix(rows, cols, type, rng, ld=cols + pad), matrix(rows, cols, type, rng, ld=cols + pad)
+        w = torch.ones(cols, device="cuda")
+        rstd = torch.rsqrt(h.float().square().mean(1) + 1e-6)
+        want = gp.rmsnorm_backward(dy, h, w, rstd)[1]
+        assert bool(torch.isfinite(want).all())
+        dy[rows - 1, 3] = float("inf")
+        h[0, cols - 1] = float("nan")
+        h[rows // 2, cols // 2] = -float("inf")
+        dw = gp.rmsnorm_backward(dy, h, w, rstd)[1]
+        bad = {3: torch.isinf(dw[3]), cols - 1: torch.isnan(dw[cols - 1]), cols // 2: torch.isinf(dw[cols // 2])}
+        assert all(bool(v) for v in bad.values())
+        keep = [c for c in range(cols) if c not in bad]
+        assert torch.equal(dw[keep], want[keep])
