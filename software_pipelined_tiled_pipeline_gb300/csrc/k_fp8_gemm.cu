@@ -532,6 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (Sh::SPLIT_REGS) regs_decrease<Sh::OTHER_REGS>();
     if (warp == 0 && lane == 0) {
       // ---------------- producer (every CTA) ----------------
+      const int lose = g.ctl.inject_lost_load;   // test hook: the load of this tile and K block never comes
+      const int lose_tile = lose == 0 ? -1 : (lose == 2 ? 0 : items.tiles - 1), lose_kb = lose == 2 ? 0 : kt - 1;
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -549,8 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t full = mapa_shared(smem_u32(&bar->full[s]), 0);
             tma_load_2d_pair(smem_u32(slot), &tmP, full, kb * kBK, p_row);
             tma_load_2d_pair(smem_u32(slot + Sh::P_BYTES), &tmQ, full, kb * kBK, q_row);
-          } else if (g.ctl.inject_lost_load == 0 ||
-                     (g.ctl.inject_lost_load == 2 ? items.tile + kb != 0 : items.tile != items.tiles - 1 || kb != kt - 1)) {
+          } else if (items.tile != lose_tile || kb != lose_kb) {
             mbar_arrive_expect_tx(&bar->full[s], Sh::STAGE);
             tma_load_2d(smem_u32(slot), &tmP, &bar->full[s], kb * kBK, p_row);
             tma_load_2d(smem_u32(slot + Sh::P_BYTES), &tmQ, &bar->full[s], kb * kBK, q_row);
@@ -602,9 +603,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!PAIR && k_ctas > 1 && worker < items.tiles) {
-      // the adding warps' two barriers around their exchange (below)
+      // the adding warps' two barriers around their exchange (below); between
+      // them a CTA that gave up tells the others, so that none of them writes
+      // what its sums are missing from
       __syncwarp();
       cluster_sync();
+      if (warp == 2 && lane < k_ctas && cta->abort)
+        st_cluster_s32(mapa_shared(smem_u32(const_cast<int*>(&cta->abort)), lane), kSiteEpilogueAccFull);
+      __syncwarp();
       cluster_sync();
     }
   } else {
@@ -735,8 +741,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int col = half * Sh::HALF + i;
           st_cluster_f1(mapa_shared(at + (col & (per - 1)) * (kXRow * 4), static_cast<uint32_t>(col >> per_log)), acc[i]);
         }
-        if (!ok && lane < k_ctas)   // none of the cluster writes what this CTA's sums are missing from
-          st_cluster_s32(mapa_shared(smem_u32(const_cast<int*>(&cta->abort)), lane), kSiteEpilogueAccFull);
         cluster_sync();
         if (!cta->abort) {
           const float* buf = reinterpret_cast<const float*>(ring);
