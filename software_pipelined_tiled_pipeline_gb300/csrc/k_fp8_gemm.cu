@@ -21,10 +21,13 @@
 // What bounds it: with every K block, 128 x BN sums change hands between the
 // tensor cores and the adding warps (wait, TMEM read, FMA, release), about as
 // long as the block's MMAs; no unit is near its limit alone.  Measured: 8192 x
-// 8192 x 4096 (E4M3, row and block scales, BF16 out) 207 us in a graph, 2660
-// TFLOP/s, against 186 us when the hand-over is left out; 4096 x 4096 x 8192
-// with row scales on both sides 190 us.  For few rows the weights' bytes bound
-// it: 1 x 8192 x 8192 14.9 us, 4.5 TB/s with its start and end.
+// 8192 x 4096 (E4M3, row and block scales, BF16 out) 207 us, 2660 TFLOP/s, for
+// some tens of calls in a row, as calls or in a graph, and 220 to 232 us where
+// they go on for a second, as the power limit then takes the SM clock from 2070
+// to 1870-1950 MHz; 186 us when the hand-over is left out.  4096 x 4096 x 8192
+// with row scales on both sides 195 us, 227 with an FP32 addend.  For few rows
+// the weights' bytes bound it: 1 x 8192 x 8192 15.3 us, 4.4 TB/s with its start
+// and end.
 #include <atomic>
 #include <cstring>
 #include "fp8_internal.h"
@@ -71,8 +74,9 @@ struct Fp8Shape {
   static constexpr int SCALES = P_ROWS + BN;           // floats per K block: P's, then Q's
   // K blocks whose scales are staged together, in two batches in turn: as many
   // as cost no ring slot.  The code between two batches is cold each time it
-  // comes: 8192 x 8192 x 4096 228 us with 8 together, 215 with 22; 4096 x 4096 x
-  // 8192 with row scales 206 with 8, 190 with 16.  (Three batches of 5 and 8
+  // comes: 8192 x 8192 x 4096 228 us with 8 together, 215 with 22, 207 with the 32
+  // that 11 times a tile's scales hold; 4096 x 4096 x 8192 with row scales 206
+  // with 8, 190 with 16.  (Three batches of 5 and 8
   // with a barrier that nobody waits for: 223 and 202.)
   static constexpr int BATCH = BN == 256 ? 11 : (BN >= 64 ? 16 : 8);
   static constexpr int FIXED = kAddWarps * kStageWarpBytes + 2 * BATCH * SCALES * 4 + kFp8BarrierBytes + 1024;

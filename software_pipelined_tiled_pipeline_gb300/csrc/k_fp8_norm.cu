@@ -172,7 +172,9 @@ __global__ void __launch_bounds__(kRowThreads<NCH>, kForwardBlocks<T, NCH>)
   }
 }
 
-// Rows longer than kRowsMaxCols: one block per row, two passes over it.  The
+// Rows longer than kRowsMaxCols: one block per row, two passes over it (2048 x
+// 32768 with a residual, BF16 159 us, FP32 192 us: 3.0 and 4.5 TB/s of what has to
+// move; one row of 20480 6.9 us).  The
 // second pass takes h from where the first stored it (x or the residual may be
 // that place), else forms it again.
 template <typename T>
@@ -355,8 +357,10 @@ __global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_grad_kernel(const __
   const int block = blockIdx.x - a.col_blocks, blocks = gridDim.x - a.col_blocks;
   const bool vec = a.vec != 0;
   const float inv_cols = 1.0f / static_cast<float>(a.cols);
-  // The weight stays in registers where they suffice (the loads of four chunks
-  // would spill), else each row reads it again from the L1 cache.
+  // The weight of up to two chunks stays in registers; with four, each row reads
+  // it again from the L1 cache.  (512 threads have 128 registers each: four chunks
+  // spill all the same, 180 bytes stored per thread in 16-bit types and 292 in
+  // FP32, and so do two of FP32, 92 bytes.)
   constexpr bool KEEP_W = NCH <= 2;
   const int cols = static_cast<int>(a.cols);
   const int col0 = threadIdx.x * 8, chunk = blockDim.x * 8;    // column of chunk i: col0 + i * chunk
@@ -447,7 +451,9 @@ __global__ void __launch_bounds__(kRowThreads<NCH>) rmsnorm_grad_kernel(const __
   for (int i = 0; i < NCH; ++i) store_sums(part, dw[i], col0 + i * chunk, cols, vec);
 }
 
-// Rows longer than kRowsMaxCols: dx in two passes over the row, dw by columns.
+// Rows longer than kRowsMaxCols: dx in two passes over the row, dw by columns
+// (2048 x 32768, BF16 207 us, FP32 295 us: 2.6 and 3.6 TB/s, as dy and h are read
+// three times; one row of 20480 8.4 us).
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_long_kernel(const __grid_constant__ NormGradArgs a) {
   __shared__ float slots[32];
