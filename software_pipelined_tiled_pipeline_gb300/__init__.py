@@ -6,8 +6,9 @@ in-tree build (``build.py``), a thin ctypes binding (``_binding``) with the same
 entry-point names, and a torch convenience wrapper ``gemm`` that only
 allocates the output and passes pointers.  ``fp8`` does the same for the 8-bit
 operators (``include/gemm_fp8.h``): quantisation, the scaled product, and the
-RMS norm with its gradient.  ``synth`` generates the seeded
-synthetic operands.
+RMS norm with its gradient; ``ffn`` for the feed-forward operators in 16 bits
+(``include/gemm_ffn.h``): the product with its epilogue, the gated product, and
+their gradients.  ``synth`` generates the seeded synthetic operands.
 """
 from ._binding import (  # noqa: F401
     DTYPES, LAYOUTS, VARIANTS, GP_OK, GP_ERR_ARG, GP_ERR_UNSUPPORTED, GP_ERR_SMEM, GP_ERR_CUDA, GP_ERR_TIMEOUT,
@@ -16,15 +17,21 @@ from ._binding import (  # noqa: F401
 )
 
 
-# the operators of fp8.py, which needs torch: loaded when first used
+# the operators of fp8.py and ffn.py, which need torch: loaded when first used
 _FP8 = ("dequantize_fp8", "gemm_fp8", "gemm_fp8_plan", "quantize_fp8", "rmsnorm_backward", "rmsnorm_fp8")
+_FFN = ("ffn_plan", "gated", "gated_backward", "linear", "linear_backward")
 
 
 def __getattr__(name):
-    if name not in _FP8:
+    if name in _FP8:
+        from . import fp8 as module
+        names = _FP8
+    elif name in _FFN:
+        from . import ffn as module
+        names = _FFN
+    else:
         raise AttributeError("module %r has no attribute %r" % (__name__, name))
-    from . import fp8
-    globals().update({f: getattr(fp8, f) for f in _FP8})
+    globals().update({f: getattr(module, f) for f in names})
     return globals()[name]
 
 

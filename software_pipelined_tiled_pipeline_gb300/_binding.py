@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in include/gemm_pipelined.h, gemm_probe.h and gemm_fp8.h.
+"""ctypes binding of the C ABI in include/gemm_pipelined.h, gemm_probe.h, gemm_fp8.h and gemm_ffn.h.
 
 Argument marshalling only: every step of the GEMM runs in the CUDA kernels of
 libgemmpipe.so.  If the library is missing the first call raises -- there is
@@ -40,6 +40,9 @@ DTYPES = {"i8": GP_I8_I32, "f16": GP_F16_F32ACC_F16OUT, "bf16": GP_BF16_F32ACC_B
 FP8_FORMATS = {"e4m3": 0, "e5m2": 1}
 REALS = {"f16": 0, "bf16": 1, "f32": 2}
 GP_PLAN_FP8 = 16      # gp_plan.dtype of a gemm_fp8 call
+# gp_activation
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "sigmoid": 5}
+GP_PLAN_FFN = 17      # gp_plan.dtype of the feed-forward calls
 
 LAYOUTS = {"row_col": GP_A_ROW_B_COL, "row_row": GP_A_ROW_B_ROW}
 VARIANTS = {"pingpong": GP_PINGPONG, "pipelined": GP_PIPELINED, "nopipe": GP_NOPIPE}
@@ -48,7 +51,8 @@ VARIANTS = {"pingpong": GP_PINGPONG, "pipelined": GP_PIPELINED, "nopipe": GP_NOP
 SYMBOLS = ["gemm_pipelined", "gemm_pipelined_ex", "gemm_plan", "gemm_plan_ex", "gemm_stats", "gemm_strerror",
            "gemm_abi_version", "gemm_release", "gemm_pipelined_noalloc", "gemm_probe_peak",
            "gemm_probe_hbm", "gemm_fp8", "gemm_fp8_plan", "fp8_quantize", "fp8_rmsnorm", "fp8_rmsnorm_backward",
-           "fp8_rmsnorm_backward_workspace"]
+           "fp8_rmsnorm_backward_workspace", "gemm_linear", "gemm_gated", "gemm_input_grad", "gemm_weight_grad",
+           "gemm_ffn_plan", "ffn_act_backward", "ffn_act_backward_workspace", "ffn_gated_backward", "ffn_pack_rows"]
 
 
 class GpPlan(ctypes.Structure):
@@ -109,6 +113,48 @@ class GpFp8Options(ctypes.Structure):
     ]
 
 
+class GpFfnOptions(ctypes.Structure):
+    _fields_ = [
+        ("timeout_ns", ctypes.c_uint64), ("tile", ctypes.c_int32), ("no_split", ctypes.c_int32),
+        ("inject_lost_load", ctypes.c_int32),
+    ]
+
+
+def _fields(pointers="", matrices="", sizes="", ints=""):
+    """ctypes fields of an argument struct, "name" or "name:count" each."""
+    out = []
+    for names, kind in ((pointers, ctypes.c_void_p), (matrices, GpFp8Matrix), (sizes, ctypes.c_int64), (ints, ctypes.c_int32)):
+        for name in names.split():
+            name, _, n = name.partition(":")
+            out.append((name, kind * int(n) if n else kind))
+    return out
+
+
+class GpLinear(ctypes.Structure):
+    _fields_ = _fields("x weight bias residual y z", "q", "M N K ldx ldw ld_res ldy ldz", "type out_type bias_type activation")
+
+
+class GpGated(ctypes.Structure):
+    _fields_ = _fields("x gate up h z_gate z_up", "q_gate q_up", "M N K ldx ld_gate ld_up ldh ld_zg ld_zu", "type activation")
+
+
+class GpInputGrad(ctypes.Structure):
+    _fields_ = _fields("dz:2 weight:2 dx", "", "M N K ld_dz:2 ldw:2 ld_dx", "type out_type count reserved")
+
+
+class GpWeightGrad(ctypes.Structure):
+    _fields_ = _fields("dz:2 x addend:2 dw:2", "", "M N K ld_dz:2 ldx ld_add:2 ld_dw:2", "type out_type count reserved")
+
+
+class GpActBackward(ctypes.Structure):
+    _fields_ = _fields("dy z", "q") + _fields("dz dbias workspace", "", "workspace_bytes M N ld_dy ldz ld_dz", "type activation")
+
+
+class GpGatedBackward(ctypes.Structure):
+    _fields_ = _fields("dh z_gate z_up", "q_gate q_up") + _fields(
+        "dgate dup h", "", "M N ld_dh ld_zg ld_zu ld_dgate ld_dup ldh", "type activation")
+
+
 _lib = None
 
 
@@ -162,6 +208,20 @@ def lib():
     L.fp8_rmsnorm_backward.restype = ci
     L.fp8_rmsnorm_backward_workspace.argtypes = [i64, i64, ci, ctypes.POINTER(i64)]
     L.fp8_rmsnorm_backward_workspace.restype = ci
+    opt, plan = ctypes.POINTER(GpFfnOptions), ctypes.POINTER(GpPlan)
+    for name, args in (("linear", GpLinear), ("gated", GpGated), ("input_grad", GpInputGrad), ("weight_grad", GpWeightGrad)):
+        f = getattr(L, "gemm_" + name)
+        f.argtypes, f.restype = [ctypes.POINTER(args), vp, opt], ci
+    L.gemm_ffn_plan.argtypes = [ci, i64, i64, i64, ci, ci, ci, opt, plan]
+    L.gemm_ffn_plan.restype = ci
+    L.ffn_act_backward.argtypes = [ctypes.POINTER(GpActBackward), vp]
+    L.ffn_act_backward.restype = ci
+    L.ffn_act_backward_workspace.argtypes = [i64, i64, ci, ctypes.POINTER(i64)]
+    L.ffn_act_backward_workspace.restype = ci
+    L.ffn_gated_backward.argtypes = [ctypes.POINTER(GpGatedBackward), vp]
+    L.ffn_gated_backward.restype = ci
+    L.ffn_pack_rows.argtypes = [vp, i64, vp, i64, i64, i64, vp]
+    L.ffn_pack_rows.restype = ci
     _lib = L
     return L
 
@@ -177,6 +237,29 @@ class _Fp8Calls:
             f.restype = ctypes.c_int
             f.argtypes = [vp if i in mats else t for i, t in enumerate(getattr(L, symbol).argtypes)]
             setattr(self, name, f)
+
+
+class _FfnCalls:
+    """The feed-forward entry points taking their argument structs as packed bytes."""
+
+    def __init__(self):
+        L, vp = lib(), ctypes.c_void_p
+        for name in ("gemm_linear", "gemm_gated", "gemm_input_grad", "gemm_weight_grad", "ffn_act_backward",
+                     "ffn_gated_backward", "ffn_pack_rows"):
+            f = L[name]                # a function object of its own
+            f.restype = ctypes.c_int
+            f.argtypes = [vp] + list(getattr(L, name).argtypes[1:])
+            setattr(self, name[5:] if name.startswith("gemm_") else name[4:].replace("pack_rows", "pack"), f)
+
+
+_ffn_calls = None
+
+
+def ffn_calls():
+    global _ffn_calls
+    if _ffn_calls is None:
+        _ffn_calls = _FfnCalls()
+    return _ffn_calls
 
 
 _fp8_calls = None

@@ -1,0 +1,87 @@
+// ffn_internal.h -- declarations shared by the feed-forward entry points and kernels.
+#pragma once
+#include "fp8_internal.h"
+#include "gemm_ffn.h"
+
+namespace gp {
+
+enum FfnOp { kFfnLinear = 0, kFfnGated = 1, kFfnInputGrad = 2, kFfnWeightGrad = 3 };
+
+constexpr int kFfnBK = 64;             // summed axis per ring slot: 128 bytes of 16-bit values
+constexpr int kFfnRestart = 8;         // K blocks between restarts of the accumulator where more than 16 bits leave
+constexpr int64_t kFfnMaxTiles = int64_t(1) << 30;   // tile numbers plus a grid stay below 2^31
+
+// 8-bit codes with a scale for each row's 128 values, as the kernels see them.
+struct FfnCodes {
+  uint8_t* data;         // NULL: none
+  float* scales;
+  int64_t ld, stride_row, stride_col;
+};
+
+// What becomes of a product's sums.  Index 1: the second weight of a gated
+// product, or the second of two products in one launch.
+struct FfnOut {
+  void* out[2];
+  const void* add[2];    // addend (residual), NULL: none
+  const void* bias;
+  void* keep[2];         // sums as they are, NULL: not kept
+  FfnCodes codes[2];
+  int64_t ld_out[2], ld_add[2], ld_keep[2];
+  int32_t bf16;          // the 16-bit type
+  int32_t out_f32;
+  int32_t bias_f32;
+  int32_t act;
+  int32_t vec;           // rows of out, add and keep are on 16-byte boundaries
+};
+
+// A product: out[r][c] = sum over s of a[r][s] * b[c][s].
+struct FfnProduct {
+  int32_t op;
+  const void* a[2];      // second ones: input gradient (more of the summed axis), weight gradient (a second product)
+  const void* b[2];      // ... input gradient, or the second weight of a gated product
+  int64_t lda[2], ldb[2];
+  int64_t rows, cols, summed;
+  int32_t count;
+  FfnOut out;
+  gp_plan plan;
+  cudaStream_t stream;
+  KernelCtl ctl;
+};
+
+int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count, bool wide_sums, bool codes, int sms,
+                  const gp_ffn_options* opts, gp_plan* p);
+cudaError_t ffn_fit_pairs(gp_plan* plan);
+cudaError_t launch_ffn_linear(FfnProduct& a, const void** kernel);
+cudaError_t launch_ffn_gated(FfnProduct& a, const void** kernel);
+cudaError_t launch_ffn_input_grad(FfnProduct& a, const void** kernel);
+cudaError_t launch_ffn_weight_grad(FfnProduct& a, const void** kernel);
+cudaError_t launch_ffn_few(FfnProduct& a, const void** kernel);
+// Ring depth, stage bytes and shared memory of the kernel that a plan of this tile runs.
+void ffn_few_shape(gp_plan* p, int bn, bool gated);
+
+// ---------------------------------------------------------------------------
+// element by element
+// ---------------------------------------------------------------------------
+struct FfnActArgs {
+  const void* dy;
+  const void* z[2];      // [1]: the second of a gated product
+  FfnCodes codes[2];
+  int32_t e5m2;          // format of the codes
+  void* dz[2];
+  void* h;
+  float* dbias;
+  float* partials;       // parts x N sums of it
+  int64_t ld_dy, ldz[2], ld_dz[2], ldh;
+  int64_t M, N;
+  int32_t type, act;
+  int32_t vec;
+};
+// Row parts of a call of this size (partial sums of dbias: that many x N floats).
+int64_t ffn_act_parts(int64_t M, int64_t N, int sm_count);
+cudaError_t launch_ffn_act_backward(const FfnActArgs& a, int sm_count, cudaStream_t stream, const void** kernel, gp_plan* plan);
+cudaError_t launch_ffn_gated_backward(const FfnActArgs& a, int sm_count, cudaStream_t stream, const void** kernel,
+                                      gp_plan* plan);
+cudaError_t launch_ffn_pack(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_t rows, int64_t cols,
+                            cudaStream_t stream, const void** kernel, gp_plan* plan);
+
+}  // namespace gp

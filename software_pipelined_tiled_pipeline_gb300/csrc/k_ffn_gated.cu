@@ -1,0 +1,128 @@
+// k_ffn_gated.cu -- the ring's kernels of the gated product and of the gradients of weights, and the planner.
+#include "ffn_ring.cuh"
+
+namespace gp {
+
+cudaError_t launch_ffn_gated(FfnProduct& p, const void** kernel) {
+  return p.plan.cta_pair ? launch_ring<256, true, true, false, false>(p, kernel)
+                         : launch_ring<128, false, true, false, false>(p, kernel);
+}
+
+// Both operands are stored summed axis (tokens) first.
+cudaError_t launch_ffn_weight_grad(FfnProduct& p, const void** kernel) {
+  return p.plan.cta_pair ? launch_ring<256, true, false, true, true>(p, kernel)
+                         : launch_ring<128, false, false, true, true>(p, kernel);
+}
+
+namespace {
+
+// Pairs that fit on the device at once (cached per device).
+cudaError_t pair_capacity(int* pairs) {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && (*pairs = cached[dev].load()) > 0) return cudaSuccess;
+  using Sh = RingShape<256, true>;
+  const void* k = reinterpret_cast<const void*>(ffn_ring_kernel<256, true, true, false, false>);
+  if ((e = ensure_smem_attr(k, Sh::SMEM)) != cudaSuccess) return e;
+  RingConfig c(2, Sh::THREADS, 2, Sh::SMEM, nullptr);
+  if ((e = cudaOccupancyMaxActiveClusters(pairs, k, &c.cfg)) != cudaSuccess) return e;
+  if (*pairs < 1) return cudaErrorLaunchOutOfResources;
+  if (dev >= 0 && dev < 64) cached[dev].store(*pairs);
+  return cudaSuccess;
+}
+
+template <int BN, bool PAIR>
+void ring_shape_of(gp_plan* p) {
+  using Sh = RingShape<BN, PAIR>;
+  p->stages = Sh::STAGES;
+  p->stage_bytes = Sh::STAGE;
+  p->ring_bytes = Sh::STAGES * Sh::STAGE;
+  p->smem_bytes = Sh::SMEM;
+  p->tmem_cols = Sh::TMEM_COLS;
+  p->threads = Sh::THREADS;
+}
+
+int64_t blocks(int64_t n, int64_t of) { return (n + of - 1) / of; }
+
+}  // namespace
+
+int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count, bool wide_sums, bool codes, int sms,
+                  const gp_ffn_options* opts, gp_plan* p) {
+  std::memset(p, 0, sizeof(*p));
+  const int want = opts ? opts->tile : 0;
+  if (want != 0 && want != 16 && want != 32 && want != 64 && want != 128 && want != 256) return GP_ERR_UNSUPPORTED;
+  const bool forward = op == kFfnLinear || op == kFfnGated, gated = op == kFfnGated;
+  const bool lose = opts && opts->inject_lost_load;
+  const int have = sms > 0 ? sms : 152;
+  const bool can_pair = have >= 2 && !lose, can_one = !(gated && codes), can_few = forward && !codes;
+  const int64_t kt = blocks(summed, kFfnBK) * (op == kFfnInputGrad ? count : 1);
+  const int64_t problems = op == kFfnWeightGrad ? count : 1;
+  int tile = want;
+  if (tile == 0) {
+    if (can_few && rows <= 128) {
+      tile = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+    } else if (!can_one) {
+      tile = 256;
+    } else if (!can_pair) {
+      tile = 128;
+    } else {
+      // K blocks one after another on the busiest SM, times what one takes there
+      const int64_t pairs = problems * blocks(rows, 256) * blocks(cols, gated ? 128 : 256);
+      const int64_t ones = problems * blocks(rows, 128) * blocks(cols, gated ? 64 : 128);
+      const int64_t pair_time = blocks(pairs, have / 2) * (kt * 520 + 3000), one_time = blocks(ones, have) * (kt * 300 + 2500);
+      tile = pair_time <= one_time ? 256 : 128;
+    }
+  }
+  if ((tile == 256 && !can_pair) || (tile == 128 && !can_one) || (tile < 128 && !can_few)) return GP_ERR_UNSUPPORTED;
+  p->dtype = GP_PLAN_FFN;
+  p->variant = GP_PIPELINED;
+  p->bk = kFfnBK;
+  p->k_tiles = kt;
+  p->k_splits = 1;
+  p->raster_gm = 8;
+  if (tile < 128) {
+    p->kernel = gated ? "ffn_few_gated" : "ffn_few";
+    p->layout = 1;
+    p->bm = 128;
+    p->bn = tile;
+    ffn_few_shape(p, tile, gated);
+    p->tiles = blocks(cols, 128) * blocks(rows, tile);
+    // CTAs that share a tile's K blocks: as many as the SMs take at once, with four K blocks each at least
+    int c = 1;
+    if (!(opts && opts->no_split))
+      while (c < 8 && p->tiles * c * 2 <= have && kt >= 4 * c * 2) c *= 2;
+    p->k_splits = c;
+    if (p->tiles > kFfnMaxTiles / 8) return GP_ERR_SIZE;
+    p->grid = sms > 0 ? static_cast<int32_t>(p->tiles * c) : 0;
+  } else {
+    p->kernel = tile == 256 ? "ffn_pair_ring" : "ffn_ring";
+    p->persistent = 1;
+    p->cta_pair = tile == 256;
+    p->bm = tile;
+    p->bn = gated ? tile / 2 : tile;
+    if (tile == 256)
+      ring_shape_of<256, true>(p);
+    else
+      ring_shape_of<128, false>(p);
+    const int64_t r = blocks(rows, p->bm), c = blocks(cols, p->bn);
+    if (r > kFfnMaxTiles / c / problems) return GP_ERR_SIZE;
+    p->tiles = r * c * problems;
+    const int64_t ctas = p->cta_pair ? 2 : 1, workers = sms / ctas;
+    p->grid = static_cast<int32_t>(ctas * (p->tiles < workers ? p->tiles : workers));
+  }
+  p->dp_tiles = static_cast<int32_t>(p->tiles);
+  p->compute_load_ratio = 2.0 * p->bm * p->bn / (p->bm + p->bn);
+  return GP_OK;
+}
+
+cudaError_t ffn_fit_pairs(gp_plan* plan) {
+  if (!plan->cta_pair) return cudaSuccess;
+  int pairs = 0;
+  const cudaError_t e = pair_capacity(&pairs);
+  if (e == cudaSuccess && 2 * pairs < plan->grid) plan->grid = 2 * pairs;
+  return e;
+}
+
+}  // namespace gp

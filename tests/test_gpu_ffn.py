@@ -1,0 +1,391 @@
+"""The feed-forward operators against their formulas in float64, element by
+element within bounds derived from the arithmetic (ffn_ref): sizes around the
+tiles, both types, every activation, what is kept, strides, addends, values that
+are not finite, every tile, refusals, streams and graphs."""
+import numpy as np
+import pytest
+import torch
+
+import ffn_ref as ref
+import fp8_ref
+import software_pipelined_tiled_pipeline_gb300 as gp
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+def status_ok():
+    st = gp.gemm_stats(sync=True)
+    assert st["status"] == 0, (gp.strerror(st["status"]), st["device_status"], st["cuda_error"], st["cuda_error_site"])
+    return st["plan"]
+
+
+def check_linear(M, N, K, dtype=BF16, act=None, bias=None, residual=False, keep=None, out_dtype=None, seed=0, pads=(0, 0, 0),
+                 whole=None, ld=None, **kw):
+    rng = np.random.default_rng(seed + 7 * M + 3 * N + K)
+    x, w = ref.matrix(rng, M, K, dtype, pad=pads[0], whole=whole), ref.matrix(rng, N, K, dtype, 1.2 * max(K, 1) ** -0.5,
+                                                                             pad=pads[1], whole=whole)
+    out_dtype = out_dtype or dtype
+    b = ref.matrix(rng, 1, N, bias, whole=whole)[0] if bias else None
+    r = ref.matrix(rng, M, N, out_dtype, 2.0, pad=pads[2], whole=whole) if residual else None
+    out, buf = ref.guarded(M, N, out_dtype, ld)
+    got = gp.linear(x, w, b, activation=act, residual=r, keep=keep, out=out, **kw)
+    kept = None
+    if keep:
+        got, kept = got
+    assert got is out
+    plan = status_ok()
+    a, c = ref.f64(x), ref.f64(w)
+    z = a @ c.T + (ref.f64(b) if b is not None else 0)
+    wide = out_dtype is F32 or keep == "fp8"
+    err = ref.sum_error(ref.magnitudes(a, c), K, wide) + 2.0 ** -24 * (np.abs(z) + np.abs(a @ c.T))
+    y = ref.value(z, act)
+    yerr = 1.2 * err + ref.steps(z) * 2.0 ** -24 * np.abs(y) if act else err      # (no activation's slope is above 1.13)
+    if r is not None:
+        y = y + ref.f64(r)
+        yerr = yerr + 2.0 ** -24 * np.abs(y)
+    worst = ref.worst(ref.f64(out), y, ref.rounded(y, yerr, out_dtype), out_dtype)
+    assert worst <= 1.0, "%g of the bound (plan %s)" % (worst, plan)
+    assert ref.outside_untouched(buf, M, N, ld or N), "write outside of the output"
+    if keep == "real":
+        assert ref.kept_real(z, err, kept[0]) <= 1.0, plan
+    elif keep == "fp8":
+        assert ref.kept_codes(z, err, *kept) <= 1.0, plan
+    if whole:       # every sum is exact in FP32 in any order: so is what the epilogue starts from
+        if act is None:
+            assert torch.equal(out.cpu(), torch.from_numpy(y).to(out_dtype))
+        if keep == "fp8":
+            code, s = fp8_ref.quantize(z, "rows", "e4m3")
+            assert np.array_equal(ref.f64(kept[1]).astype(np.float32), s)
+            assert fp8_ref.same_codes(fp8_ref.codes(kept[0]), code, "e4m3")
+    return plan
+
+
+def check_gated(M, N, K, dtype=BF16, act="silu", keep=None, seed=0, pads=(0, 0, 0), ld=None, whole=None, **kw):
+    rng = np.random.default_rng(seed + 5 * M + 3 * N + K)
+    x = ref.matrix(rng, M, K, dtype, pad=pads[0], whole=whole)
+    wg, wu = (ref.matrix(rng, N, K, dtype, 1.2 * max(K, 1) ** -0.5, pad=p, whole=whole) for p in pads[1:])
+    out, buf = ref.guarded(M, N, dtype, ld)
+    got = gp.gated(x, wg, wu, activation=act, keep=keep, out=out, **kw)
+    kept = None
+    if keep:
+        got, kept = got
+    assert got is out
+    plan = status_ok()
+    a, b, c = ref.f64(x), ref.f64(wg), ref.f64(wu)
+    g, u = a @ b.T, a @ c.T
+    eg, eu = (ref.sum_error(ref.magnitudes(a, w), K, keep == "fp8") for w in (b, c))
+    v = ref.value(g, act)
+    ev = 1.2 * eg + ref.steps(g) * 2.0 ** -24 * np.abs(v)
+    h = v * u
+    err = ev * (np.abs(u) + eu) + np.abs(v) * eu + 2.0 ** -24 * np.abs(h)
+    worst = ref.worst(ref.f64(out), h, ref.rounded(h, err, dtype), dtype)
+    assert worst <= 1.0, "%g of the bound (plan %s)" % (worst, plan)
+    assert ref.outside_untouched(buf, M, N, ld or N), "write outside of the output"
+    if keep == "real":
+        assert ref.kept_real(g, eg, kept[0]) <= 1.0 and ref.kept_real(u, eu, kept[1]) <= 1.0, plan
+    elif keep == "fp8":
+        assert ref.kept_codes(g, eg, *kept[:2]) <= 1.0 and ref.kept_codes(u, eu, *kept[2:]) <= 1.0, plan
+        if whole:
+            for z, (data, s) in ((g, kept[:2]), (u, kept[2:])):
+                code, want = fp8_ref.quantize(z, "rows", "e4m3")
+                assert np.array_equal(ref.f64(s).astype(np.float32), want)
+                assert fp8_ref.same_codes(fp8_ref.codes(data), code, "e4m3")
+    return plan
+
+
+SHAPES = [(1, 1, 1), (1, 16, 16), (1, 300, 4096), (2, 129, 128), (16, 128, 130), (17, 127, 257), (31, 1000, 520), (33, 257, 129),
+          (64, 640, 1024), (65, 200, 384), (128, 128, 128), (129, 130, 1000), (300, 70, 257), (70, 300, 2057), (511, 385, 640),
+          (260, 1030, 300), (1000, 776, 2056), (5, 4096, 8192), (500, 600, 4100), (2100, 2300, 256), (3, 700, 513),
+          (1, 41, 20001), (200, 8, 64)]
+
+
+# ---------------------------------------------------------------------------
+# forward
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_linear_shapes(M, N, K, dtype):
+    check_linear(M, N, K, dtype, act="gelu" if M % 2 else None, bias=dtype, residual=N % 2 == 0)
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_linear_whole_numbers_are_exact(M, N, K):
+    check_linear(M, N, K, F16, whole=2 if K < 3000 else 1, bias=F16, residual=True, out_dtype=F32)
+    check_linear(M, N, K, BF16, whole=2 if K < 3000 else 1, bias=F32, keep="fp8", out_dtype=F32)
+
+
+@pytest.mark.parametrize("act", ref.ACTS)
+@pytest.mark.parametrize("M", [3, 200, 700])
+@pytest.mark.parametrize("dtype,out", [(F16, F16), (F16, F32), (BF16, BF16), (BF16, F32)])
+def test_linear_activations_and_types(act, M, dtype, out):
+    check_linear(M, 264, 200, dtype, act, bias=F32, residual=True, out_dtype=out)
+    check_linear(M, 260, 200, dtype, act, out_dtype=out, keep="real")
+
+
+@pytest.mark.parametrize("tile", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("M,N,K", [(1, 200, 700), (100, 1000, 333), (513, 700, 1300)])
+def test_linear_every_tile(tile, M, N, K):
+    for split in (False, True):
+        check_linear(M, N, K, BF16, "silu", bias=BF16, residual=True, tile=tile, no_split=split)
+        check_linear(M, N, K, F16, None, keep="real", out_dtype=F32, tile=tile, no_split=split)
+    if tile >= 128:
+        check_linear(M, N, K, BF16, "gelu", bias=BF16, keep="fp8", tile=tile)
+
+
+@pytest.mark.parametrize("M", [1, 40, 130, 600])
+@pytest.mark.parametrize("pads,ld", [((0, 8, 0), None), ((1, 3, 5), 301), ((8, 8, 4), 308), ((7, 0, 1), 304)])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_linear_strides(M, pads, ld, out):
+    check_linear(M, 300, 264, BF16, "relu", bias=BF16, residual=True, pads=pads, ld=ld, out_dtype=out)
+    check_linear(M, 300, 263, BF16, "relu", bias=BF16, residual=True, pads=pads, ld=ld, out_dtype=out)
+
+
+@pytest.mark.parametrize("M,N", [(3, 200), (300, 301), (300, 304)])
+@pytest.mark.parametrize("out", [F16, F32])
+def test_linear_residual_in_place(M, N, out):
+    rng = np.random.default_rng(4)
+    x, w = ref.matrix(rng, M, 260, F16), ref.matrix(rng, N, 260, F16)
+    r = ref.matrix(rng, M, N, out, pad=8)
+    apart = gp.linear(x, w, residual=r, out_dtype=out)
+    here = r.clone(memory_format=torch.preserve_format)
+    wide = torch.zeros((M, N + 8), dtype=out, device="cuda")
+    wide[:, :N] = r
+    here = wide[:, :N]
+    assert gp.linear(x, w, residual=here, out=here) is here
+    assert torch.equal(here, apart) and bool((wide[:, N:] == 0).all())
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_gated_shapes(M, N, K, dtype):
+    check_gated(M, N, K, dtype, keep=[None, "real", "fp8"][(M + N) % 3])
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES[:20])
+def test_gated_whole_numbers_kept_in_8_bits(M, N, K):
+    check_gated(M, N, K, BF16, keep="fp8", whole=2 if K < 3000 else 1)
+
+
+@pytest.mark.parametrize("act", ref.ACTS)
+@pytest.mark.parametrize("M", [3, 200, 700])
+@pytest.mark.parametrize("keep", [None, "real", "fp8"])
+def test_gated_activations(act, M, keep):
+    check_gated(M, 264, 200, F16, act, keep)
+    check_gated(M, 333, 200, BF16, act, keep)
+
+
+@pytest.mark.parametrize("tile", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("M,N,K", [(1, 200, 700), (100, 1000, 333), (513, 700, 1300)])
+def test_gated_every_tile(tile, M, N, K):
+    check_gated(M, N, K, BF16, tile=tile)
+    check_gated(M, N, K, F16, keep="real", tile=tile, no_split=True)
+
+
+@pytest.mark.parametrize("M", [1, 40, 130, 600])
+@pytest.mark.parametrize("pads,ld", [((0, 8, 0), None), ((1, 3, 5), 301), ((8, 8, 8), 304)])
+def test_gated_strides(M, pads, ld):
+    check_gated(M, 300, 264, BF16, keep="real", pads=pads, ld=ld)
+    check_gated(M, 300, 263, F16, keep="fp8", pads=pads, ld=ld)
+
+
+def test_few_tokens_alone_and_together():
+    """A token's outputs do not depend on what else is in the batch (the same tile, so the same order of sums)."""
+    rng = np.random.default_rng(2)
+    x, w, u = ref.matrix(rng, 16, 1030, BF16), ref.matrix(rng, 500, 1030, BF16, 0.03), ref.matrix(rng, 500, 1030, BF16, 0.03)
+    whole = gp.linear(x, w, activation="gelu")
+    both = gp.gated(x, w, u)
+    for i in (0, 7, 15):
+        assert torch.equal(gp.linear(x[i:i + 1], w, activation="gelu"), whole[i:i + 1])
+        assert torch.equal(gp.gated(x[i:i + 1], w, u), both[i:i + 1])
+
+
+@pytest.mark.parametrize("M", [2, 300, 600])
+def test_values_that_are_not_finite(M):
+    """A NaN or an infinity reaches the outputs of its own row or column alone, and the scale of its own groups."""
+    rng = np.random.default_rng(3)
+    N, K = 300, 200
+    x, w, u = ref.matrix(rng, M, K, BF16), ref.matrix(rng, N, K, BF16, 0.1), ref.matrix(rng, N, K, BF16, 0.1)
+    x[1, 5] = float("nan")
+    x[0, 7] = float("inf")
+    w[4, 9] = float("nan")
+    y = gp.linear(x, w)
+    want = x.double().cpu() @ w.double().cpu().t()
+    assert torch.equal(torch.isnan(y).cpu(), torch.isnan(want)) and torch.equal(torch.isinf(y).cpu(), torch.isinf(want))
+    h = gp.gated(x, w, u, activation="sigmoid")
+    assert bool(torch.isnan(h[1]).all()) and bool(torch.isnan(h[:, 4]).all())
+    assert M < 3 or bool(torch.isfinite(h[2:, torch.arange(N) != 4]).all())
+    y, (data, s) = gp.linear(x, w, keep="fp8")
+    z = want.float()
+    assert torch.equal(torch.isnan(s).cpu(), torch.stack([torch.isnan(z[:, j:j + 128]).any(1) for j in (0, 128, 256)], 1))
+    inf = torch.stack([torch.isinf(z[:, j:j + 128]).any(1) & ~torch.isnan(z[:, j:j + 128]).any(1) for j in (0, 128, 256)], 1)
+    assert torch.equal(torch.isinf(s).cpu(), inf)
+
+
+@pytest.mark.parametrize("M,N,K", [(4, 8, 0), (300, 129, 0), (0, 64, 64), (64, 0, 64)])
+def test_empty(M, N, K):
+    x, w = torch.ones(M, K, dtype=BF16, device="cuda"), torch.ones(N, K, dtype=BF16, device="cuda")
+    b, r = torch.full((N,), 0.5, dtype=BF16, device="cuda"), torch.full((M, N), 2.0, dtype=BF16, device="cuda")
+    y, kept = gp.linear(x, w, b, activation="relu", residual=r, keep="real")
+    assert y.shape == (M, N) and bool((y == 2.5).all()) and bool((kept[0] == 0.5).all())
+    h = gp.gated(x, w, w)
+    assert h.shape == (M, N) and bool((h == 0).all())
+    dx, dw, db = gp.linear_backward(r, x, w, bias_grad=True)
+    assert dx.shape == (M, K) and dw.shape == (N, K) and bool((db == 2.0 * M).all())
+    assert bool((dx == (2.0 * N if K else 0)).all()) and bool((dw == 2.0 * M).all())
+    add = torch.full((N, K), 3.0, dtype=F32, device="cuda")
+    _, dw, _ = gp.linear_backward(r, x, w, addend=add, out_dtype=F32)
+    assert bool((dw == 2.0 * M + 3).all())
+    dx, dg, du, h = gp.gated_backward(r, x, w, w, (r, r), product=True)
+    assert dx.shape == (M, K) and dg.shape == du.shape == (N, K) and h.shape == (M, N)
+
+
+# ---------------------------------------------------------------------------
+# backward
+# ---------------------------------------------------------------------------
+def make_kept(rng, M, N, dtype, keep, pad=0, fmt="e4m3"):
+    z = ref.matrix(rng, M, N, dtype, 1.5, pad=pad)
+    if keep == "real":
+        return (z,)
+    return gp.quantize_fp8(z, format=fmt)
+
+
+def check_products(dz, edz, x, w, dx, dw, addend=None):
+    """dx = sum dz w and dw = dz^T x, from gradients dz that the kernel rounded to x's type, off by edz before that."""
+    dtype = x.dtype
+    a = ref.f64(x)
+    want, err = 0.0, 0.0
+    summed = 0
+    for z, e, weight, got in zip(dz, edz, w, dw):
+        e = ref.rounded(z, e, dtype)
+        b = ref.f64(weight)
+        want = want + z @ b
+        err = err + e @ np.abs(b) + 0 * want
+        summed += z.shape[1]
+        if got is not None:
+            g, ge = z.T @ a, e.T @ np.abs(a)
+            ge = ge + ref.sum_error((np.abs(z) + e).T @ np.abs(a), len(a), got.dtype is F32)
+            if addend is not None:
+                i = [j for j, t in enumerate(dw) if t is got][0]
+                g = g + ref.f64(addend[i])
+                ge = ge + 2.0 ** -24 * np.abs(g)
+            far = ref.worst(ref.f64(got), g, ref.rounded(g, ge, got.dtype), got.dtype)
+            assert far <= 1.0, "weight gradient: %g of the bound" % far
+    if dx is not None:
+        mag = sum((np.abs(z) + ref.rounded(z, e, dtype)) @ np.abs(ref.f64(weight)) for z, e, weight in zip(dz, edz, w))
+        err = err + ref.sum_error(mag, summed, False)
+        far = ref.worst(ref.f64(dx), want, ref.rounded(want, err, dtype), dtype)
+        assert far <= 1.0, "input gradient: %g of the bound" % far
+
+
+def check_linear_backward(M, N, K, dtype=BF16, act=None, keep="real", out_dtype=None, add=False, pads=(0, 0, 0, 0), seed=0, **kw):
+    rng = np.random.default_rng(seed + M + 3 * N + 5 * K)
+    dy, x = ref.matrix(rng, M, N, dtype, 0.1, pad=pads[0]), ref.matrix(rng, M, K, dtype, pad=pads[1])
+    w = ref.matrix(rng, N, K, dtype, 0.05, pad=pads[2])
+    kept = make_kept(rng, M, N, dtype, keep, pads[3]) if act else None
+    addend = ref.matrix(rng, N, K, out_dtype or dtype) if add else None
+    dx, dw, db = gp.linear_backward(dy, x, w, activation=act, kept=kept, bias_grad=True, out_dtype=out_dtype, addend=addend, **kw)
+    status_ok()
+    assert dx.dtype is dtype and dw.dtype is (out_dtype or dtype) and db.dtype is F32
+    d = ref.f64(dy)
+    if act:
+        z = ref.held(kept, dtype)
+        s = ref.slope(z, act)
+        es = ref.steps(z) * 2.0 ** -23 * (1 + np.abs(z)) * (z != 0 if act == "relu" else 1)
+        dz, e = d * s, np.abs(d) * (es + 2.0 ** -24 * np.abs(s))
+    else:
+        dz, e = d, np.zeros_like(d)
+    # without an activation dy itself is the operand: it is in its type already
+    check_products([dz], [e], x, [w], dx, [dw], None if addend is None else [addend])
+    want = dz.sum(0)
+    bound = e.sum(0) + M * 2.0 ** -24 * (np.abs(dz) + e).sum(0) + 2.0 ** -150
+    assert ref.worst(ref.f64(db), want, bound) <= 1.0
+
+
+BACK = [(1, 1, 1), (1, 300, 130), (16, 128, 64), (17, 127, 257), (130, 129, 131), (200, 2056, 776), (333, 1000, 776),
+        (260, 70, 1030), (1000, 264, 520), (2100, 300, 256), (5, 4096, 1000), (4100, 65, 72)]
+
+
+@pytest.mark.parametrize("M,N,K", BACK)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_linear_backward_shapes(M, N, K, dtype):
+    check_linear_backward(M, N, K, dtype)
+    check_linear_backward(M, N, K, dtype, out_dtype=F32, add=True)
+    check_linear_backward(M, N, K, dtype, act="gelu", keep="fp8" if M % 2 else "real")
+
+
+@pytest.mark.parametrize("act", ref.ACTS[1:])
+@pytest.mark.parametrize("keep", ["real", "fp8"])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_linear_backward_activations(act, keep, dtype):
+    check_linear_backward(150, 264, 200, dtype, act, keep, add=True)
+    check_linear_backward(150, 261, 200, dtype, act, keep)
+
+
+@pytest.mark.parametrize("tile", [128, 256])
+@pytest.mark.parametrize("M,N,K", [(100, 333, 700), (700, 513, 300), (300, 1300, 520)])
+def test_backward_every_tile(tile, M, N, K):
+    check_linear_backward(M, N, K, BF16, tile=tile, out_dtype=F32, add=True)
+    check_linear_backward(M, N, K, F16, "silu", "fp8", tile=tile)
+    check_gated_backward(M, N, K, BF16, tile=tile)
+
+
+@pytest.mark.parametrize("pads", [(1, 3, 5, 7), (8, 8, 8, 8), (0, 1, 0, 0), (4, 0, 0, 1)])
+@pytest.mark.parametrize("M,N,K", [(40, 300, 264), (300, 129, 333)])
+def test_backward_strides(pads, M, N, K):
+    check_linear_backward(M, N, K, F16, "gelu_tanh", pads=pads)
+    check_linear_backward(M, N, K, F16, pads=pads)
+    check_gated_backward(M, N, K, BF16, pads=pads)
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 200, 64), (300, 264, 520), (700, 300, 1024)])
+def test_backward_whole_numbers_are_exact(M, N, K):
+    rng = np.random.default_rng(6)
+    dy, x, w = (ref.matrix(rng, r, c, BF16, whole=2) for r, c in ((M, N), (M, K), (N, K)))
+    a, b, c = (t.cpu().double() for t in (dy, x, w))
+    for tile in (0, 128, 256):
+        dx, dw, db = gp.linear_backward(dy, x, w, bias_grad=True, out_dtype=F32, tile=tile)
+        assert torch.equal(dw.cpu().double(), a.t() @ b) and torch.equal(db.cpu().double(), a.sum(0))
+        assert torch.equal(dx.cpu(), (a @ c).to(BF16))
+        # both weights' gradients in one launch, with addends in place
+        relu = torch.ones(M, N, dtype=BF16, device="cuda")
+        acc = [torch.full((N, K), float(i + 1), dtype=F32, device="cuda") for i in range(2)]
+        dx, dg, du = gp.gated_backward(dy, x, w, w, (relu, relu + 1), activation="relu", addend=acc, out=acc, tile=tile)
+        assert dg is acc[0] and du is acc[1]
+        assert torch.equal(dg.cpu().double(), 2 * (a.t() @ b) + 1) and torch.equal(du.cpu().double(), a.t() @ b + 2)
+        assert torch.equal(dx.cpu(), (3 * (a @ c)).to(BF16))
+
+
+def check_gated_backward(M, N, K, dtype=BF16, act="silu", keep="real", product=True, pads=(0, 0, 0, 0), seed=0, fmt="e4m3", **kw):
+    rng = np.random.default_rng(seed + M + 3 * N + 5 * K)
+    dh, x = ref.matrix(rng, M, N, dtype, 0.1, pad=pads[0]), ref.matrix(rng, M, K, dtype, pad=pads[1])
+    wg, wu = ref.matrix(rng, N, K, dtype, 0.05, pad=pads[2]), ref.matrix(rng, N, K, dtype, 0.05)
+    kg, ku = (make_kept(rng, M, N, dtype, keep, pads[3], fmt) for _ in range(2))
+    got = gp.gated_backward(dh, x, wg, wu, kg + ku, activation=act, product=product, **kw)
+    status_ok()
+    d, g, u = ref.f64(dh), ref.held(kg, dtype), ref.held(ku, dtype)
+    s, v = ref.slope(g, act), ref.value(g, act)
+    es = ref.steps(g) * 2.0 ** -23 * (1 + np.abs(g)) * (g != 0 if act == "relu" else 1)
+    ev = ref.steps(g) * 2.0 ** -24 * np.abs(v)
+    dg, du = d * u * s, d * v
+    eg = np.abs(d * u) * (es + 2.0 ** -22 * np.abs(s))
+    eu = np.abs(d) * (ev + 2.0 ** -23 * np.abs(v))
+    check_products([dg, du], [eg, eu], x, [wg, wu], got[0], list(got[1:3]))
+    if product:
+        h = v * u
+        err = np.abs(u) * ev + 2.0 ** -22 * np.abs(h)
+        assert ref.worst(ref.f64(got[3]), h, ref.rounded(h, err, dtype), dtype) <= 1.0
+
+
+@pytest.mark.parametrize("M,N,K", BACK)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_gated_backward_shapes(M, N, K, dtype):
+    check_gated_backward(M, N, K, dtype, keep="fp8" if M % 2 else "real", product=bool(N % 2))
+
+
+@pytest.mark.parametrize("act", ref.ACTS)
+@pytest.mark.parametrize("keep,fmt", [("real", ""), ("fp8", "e4m3"), ("fp8", "e5m2")])
+def test_gated_backward_activations(act, keep, fmt):
+    check_gated_backward(150, 264, 200, F16, act, keep, fmt=fmt)
+    check_gated_backward(150, 261, 200, BF16, act, keep, fmt=fmt)
