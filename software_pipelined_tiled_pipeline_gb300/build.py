@@ -21,14 +21,15 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgemmpipe.so")
 
 SOURCES = ["api.cu", "ffn_api.cu", "fp8_api.cu", "k_ffma.cu", "k_ffn_act.cu", "k_ffn_few.cu", "k_ffn_gated.cu",
-           "k_ffn_linear.cu", "k_fp8_gemm.cu", "k_fp8_norm.cu", "k_fp8_quant.cu", "k_imma.cu", "k_umma.cu", "probe.cu"]
+           "k_ffn_input_grad.cu", "k_ffn_linear.cu", "k_ffn_weight_grad.cu", "k_fp8_gemm.cu", "k_fp8_norm.cu", "k_fp8_quant.cu", "k_imma.cu", "k_umma.cu", "probe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 
 # Kernels whose warps trade registers count on an exact number per thread at launch, and are refused at run time with
 # any other: {source: (kernel, registers)}.  ptxas says what it gave them.
 LAUNCH_REGISTERS = {"k_fp8_gemm.cu": (r"fp8_ring_kernelILi(128|256)E", 168),
-                    "k_ffn_gated.cu": (r"ffn_ring_kernelILi256E", 168), "k_ffn_linear.cu": (r"ffn_ring_kernelILi256E", 168),
+                    **{"k_ffn_%s.cu" % f: (r"ffn_ring_kernelILi256ELb1ELNS_7RingOutE1", 96)
+                       for f in ("gated", "input_grad", "linear", "weight_grad")},
                     "k_umma.cu": (r"umma_i8_overlap_kernel", 128)}
 
 

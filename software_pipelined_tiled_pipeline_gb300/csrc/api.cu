@@ -66,9 +66,12 @@ struct TmapKey {
   uint64_t inner, outer, row_bytes;
   uint32_t box_inner, box_outer;
   int swizzle;
+  uint64_t planes, plane_bytes;   // third dimension (planes 0: there is none)
+  uint32_t box_planes;
   bool operator==(const TmapKey& o) const {
     return dev == o.dev && base == o.base && type == o.type && inner == o.inner && outer == o.outer &&
-           row_bytes == o.row_bytes && box_inner == o.box_inner && box_outer == o.box_outer && swizzle == o.swizzle;
+           row_bytes == o.row_bytes && box_inner == o.box_inner && box_outer == o.box_outer && swizzle == o.swizzle &&
+           planes == o.planes && plane_bytes == o.plane_bytes && box_planes == o.box_planes;
   }
 };
 
@@ -755,14 +758,14 @@ int call_finish(int status, cudaError_t error, int site) {
 // ---------------------------------------------------------------------------
 // helpers used by the kernel translation units
 // ---------------------------------------------------------------------------
-cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type, uint64_t inner,
-                         uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
-                         CUtensorMapSwizzle swizzle) {
+namespace {
+
+// The map of `key` (its device filled in here), from the cache or encoded.
+cudaError_t make_tmap(CUtensorMap* map, TmapKey key) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  TmapKey key{dev, base, static_cast<int>(type), inner, outer, row_bytes, box_inner, box_outer,
-              static_cast<int>(swizzle)};
+  key.dev = dev;
   std::lock_guard<std::mutex> lk(g_mu);
   for (auto& t : g_tmaps) {
     if (t.used && t.key == key) {
@@ -792,13 +795,14 @@ cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType
     }
     ctx_dev = dev;
   }
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
+  const cuuint64_t dims[3] = {key.inner, key.outer, key.planes};
+  const cuuint64_t strides[2] = {key.row_bytes, key.plane_bytes};
+  const cuuint32_t box[3] = {key.box_inner, key.box_outer, key.box_planes};
+  const cuuint32_t estr[3] = {1, 1, 1};
   CUtensorMap m;
-  const CUresult r = g_encode(&m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUresult r = g_encode(&m, static_cast<CUtensorMapDataType>(key.type), key.planes ? 3 : 2,
+                              const_cast<void*>(key.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              static_cast<CUtensorMapSwizzle>(key.swizzle), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     t_fail_site = GP_SITE_TENSOR_MAP;
@@ -815,6 +819,22 @@ cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType
   victim->used = true;
   *map = m;
   return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type, uint64_t inner,
+                         uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+                         CUtensorMapSwizzle swizzle) {
+  return make_tmap(map, TmapKey{0, base, static_cast<int>(type), inner, outer, row_bytes, box_inner, box_outer,
+                                static_cast<int>(swizzle), 0, 0, 1});
+}
+
+cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType type, uint64_t inner,
+                         uint64_t outer, uint64_t row_bytes, uint64_t planes, uint64_t plane_bytes, uint32_t box_inner,
+                         uint32_t box_outer, uint32_t box_planes, CUtensorMapSwizzle swizzle) {
+  return make_tmap(map, TmapKey{0, base, static_cast<int>(type), inner, outer, row_bytes, box_inner, box_outer,
+                                static_cast<int>(swizzle), planes, plane_bytes, box_planes});
 }
 
 cudaError_t ensure_smem_attr(const void* kernel, int bytes) {

@@ -48,6 +48,19 @@ int check_codes(const gp_fp8_matrix& m, int64_t cols, bool e5m2) {
   return aligned(m.data, 16) && m.ld % 16 == 0 && aligned(m.scales, 4) ? GP_OK : GP_ERR_UNSUPPORTED;
 }
 
+// Boundaries that the rows of a matrix begin on: 32 bytes (2), 16 (1), or neither; one that is not there, on any.
+int align_of(const void* p, int64_t ld, int type) {
+  if (!p) return 2;
+  const int64_t at = reinterpret_cast<intptr_t>(p) | (ld * real_bytes(type));
+  return at % 32 == 0 ? 2 : (at % 16 == 0 ? 1 : 0);
+}
+
+int least(std::initializer_list<int> v) {
+  int m = 2;
+  for (int x : v) m = x < m ? x : m;
+  return m;
+}
+
 FfnCodes codes_of(const gp_fp8_matrix& m) {
   return FfnCodes{static_cast<uint8_t*>(m.data), m.scales, m.ld, m.stride_row, m.stride_col};
 }
@@ -151,8 +164,8 @@ int gemm_linear(const gp_linear* a, void* stream, const gp_ffn_options* opts) {
   o.out_f32 = a->out_type == GP_REAL_F32;
   o.bias_f32 = a->bias_type == GP_REAL_F32;
   o.act = a->activation;
-  const int size = real_bytes(a->out_type);
-  o.vec = vec16(a->y, a->ldy, size) && (!a->residual || vec16(a->residual, a->ld_res, size)) && (!a->z || vec16(a->z, a->ldz, 2));
+  o.vec = least({align_of(a->y, a->ldy, a->out_type), align_of(a->residual, a->ld_res, a->out_type),
+                 align_of(a->z, a->ldz, a->type)});
   return run_product(p, opts);
 }
 
@@ -199,7 +212,7 @@ int gemm_gated(const gp_gated* a, void* stream, const gp_ffn_options* opts) {
   o.codes[1] = codes_of(a->q_up);
   o.bf16 = a->type == GP_REAL_BF16;
   o.act = a->activation;
-  o.vec = vec16(a->h, a->ldh, 2) && (!a->z_gate || (vec16(a->z_gate, a->ld_zg, 2) && vec16(a->z_up, a->ld_zu, 2)));
+  o.vec = least({align_of(a->h, a->ldh, a->type), align_of(a->z_gate, a->ld_zg, a->type), align_of(a->z_up, a->ld_zu, a->type)});
   return run_product(p, opts);
 }
 
@@ -233,7 +246,7 @@ int gemm_input_grad(const gp_input_grad* a, void* stream, const gp_ffn_options* 
   o.ld_out[0] = a->ld_dx;
   o.bf16 = a->type == GP_REAL_BF16;
   o.out_f32 = a->out_type == GP_REAL_F32;
-  o.vec = vec16(a->dx, a->ld_dx, real_bytes(a->out_type));
+  o.vec = align_of(a->dx, a->ld_dx, a->out_type);
   return run_product(p, opts);
 }
 
@@ -254,9 +267,8 @@ int gemm_weight_grad(const gp_weight_grad* a, void* stream, const gp_ffn_options
   if (rc != GP_OK) return call_finish(rc);
   FfnProduct p = {};
   p.op = kFfnWeightGrad;
-  const int size = real_bytes(a->out_type);
   FfnOut& o = p.out;
-  o.vec = 1;
+  o.vec = 2;
   for (int i = 0; i < a->count; ++i) {
     p.a[i] = a->dz[i];
     p.lda[i] = a->ld_dz[i];
@@ -264,7 +276,7 @@ int gemm_weight_grad(const gp_weight_grad* a, void* stream, const gp_ffn_options
     o.ld_out[i] = a->ld_dw[i];
     o.add[i] = a->addend[i];
     o.ld_add[i] = a->ld_add[i];
-    o.vec = o.vec && vec16(a->dw[i], a->ld_dw[i], size) && (!a->addend[i] || vec16(a->addend[i], a->ld_add[i], size));
+    o.vec = least({o.vec, align_of(a->dw[i], a->ld_dw[i], a->out_type), align_of(a->addend[i], a->ld_add[i], a->out_type)});
   }
   p.b[0] = a->x;
   p.ldb[0] = a->ldx;

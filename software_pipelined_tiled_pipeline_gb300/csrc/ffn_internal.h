@@ -8,7 +8,7 @@ namespace gp {
 enum FfnOp { kFfnLinear = 0, kFfnGated = 1, kFfnInputGrad = 2, kFfnWeightGrad = 3 };
 
 constexpr int kFfnBK = 64;             // summed axis per ring slot: 128 bytes of 16-bit values
-constexpr int kFfnRestart = 8;         // K blocks between restarts of the accumulator where more than 16 bits leave
+constexpr int kFfnRestart = 12;        // K blocks between restarts of the accumulator where more than 16 bits leave
 constexpr int64_t kFfnMaxTiles = int64_t(1) << 30;   // tile numbers plus a grid stay below 2^31
 
 // 8-bit codes with a scale for each row's 128 values, as the kernels see them.
@@ -31,7 +31,7 @@ struct FfnOut {
   int32_t out_f32;
   int32_t bias_f32;
   int32_t act;
-  int32_t vec;           // rows of out, add and keep are on 16-byte boundaries
+  int32_t vec;           // rows of out, add and keep are on boundaries of 32 bytes (2), 16 (1), or neither (0)
 };
 
 // A product: out[r][c] = sum over s of a[r][s] * b[c][s].

@@ -11,9 +11,8 @@
 // Persistent and warp-specialised:
 //   warp 0     TMA producer: one ring slot = 64 of the summed axis
 //   warp 1     allocates TMEM and issues tcgen05.mma (kind::f16, FP32 in TMEM)
-//   warps 4+   take a tile's sums to registers, 32 rows x 128 columns per warp, hand
-//              the TMEM buffer back and write the outputs while the next tile's
-//              products run into the other buffer
+//   warps 4+   write the outputs from one TMEM buffer while the next tile's products
+//              run into the other
 // PAIR: a cluster of two CTAs shares a 256 x 256 tile (M = 256 instructions).
 //
 // The tensor cores cut their FP32 sums instead of rounding them, always towards
@@ -30,8 +29,7 @@
 
 namespace gp {
 
-constexpr int kRingWarpStage = 32 * 256;   // output staging of one warp: 32 rows of 64 FP32
-constexpr int kRingLaunchRegs = 168;       // registers per thread at launch, where warps trade them
+constexpr int kRingLaunchRegs = 96;        // registers per thread at launch, where warps trade them
 constexpr int kRingMax = 8;
 
 struct RingBarriers {
@@ -46,7 +44,16 @@ struct RingBarriers {
 constexpr int kRingBarrierBytes = 256;
 static_assert(sizeof(RingBarriers) <= kRingBarrierBytes, "barrier region too small");
 
-template <int BN, bool PAIR>
+// How the sums leave.  A lane has 32 columns of its own row at a time in
+// registers, and reads and writes the row's memory itself, a whole 32-byte sector
+// per access: no shared memory, whose bandwidth the operands take (through it, a
+// 256 x 256 tile of BF16 took 8000 cycles to leave, beside 16,400 of products at K
+// = 2048).  kStream: straight from TMEM, in a loop.  kHold: a warp takes 64 sums
+// per lane to registers, hands the buffer back and works on them: it can add up
+// several hand-overs, and sees half of a group of 128 columns.
+enum RingOut { kStream = 0, kHold = 1 };
+
+template <int BN, bool PAIR, RingOut OUT>
 struct RingShape {
   static constexpr int CTAS = PAIR ? 2 : 1;
   static constexpr int A_ROWS = 128;                     // per CTA
@@ -55,17 +62,19 @@ struct RingShape {
   static constexpr int TILE_ROWS = A_ROWS * CTAS;
   static constexpr int A_BYTES = A_ROWS * kFfnBK * 2;
   static constexpr int STAGE = (A_ROWS + B_ROWS) * kFfnBK * 2;
-  static constexpr int EPI_WARPS = BN / 32;              // 32 rows x 128 columns each
+  static constexpr int EPI_WARPS = OUT == kHold ? BN / 16 : 8;
+  static constexpr int EPI_COLS = 4 * BN / EPI_WARPS;    // TMEM columns of each, over 32 rows
+  static_assert(OUT == kStream || EPI_COLS == 64, "held sums");
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
-  static constexpr int FIXED = EPI_WARPS * kRingWarpStage + kRingBarrierBytes + kSmemAlignSlack;
+  static constexpr int SHARED_MAX = OUT == kHold ? EPI_WARPS * 32 * 8 : 0;   // maxima that warps show each other
+  static constexpr int FIXED = SHARED_MAX + kRingBarrierBytes + kSmemAlignSlack;
   static constexpr int FIT = (kSmemPerCtaMax - FIXED) / STAGE;
   static constexpr int STAGES = FIT < kRingMax ? FIT : kRingMax;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
-  // The warps that write hold 128 sums per thread, and take registers for them
-  // from the other four (of a 384-thread launch).
-  static constexpr bool SPLIT_REGS = THREADS == 384;
-  static constexpr int EPI_REGS = 216, OTHER_REGS = 72;
+  // Sixteen warps that hold 64 sums per thread take registers for them from the other four.
+  static constexpr bool SPLIT_REGS = THREADS == 640;
+  static constexpr int EPI_REGS = 104, OTHER_REGS = 64;
   static_assert(!SPLIT_REGS || THREADS * kRingLaunchRegs == 32 * (EPI_WARPS * EPI_REGS + 4 * OTHER_REGS), "register split");
 };
 
@@ -78,6 +87,7 @@ struct RingParams {
   int32_t restart;           // K blocks per hand-over of the accumulator
   int32_t raster;            // row blocks per raster group
   uint32_t idesc;
+  int32_t a_planes, b_planes;   // an MN-major operand's 128 rows come as one box of two planes of 64
   KernelCtl ctl;
 };
 
@@ -93,6 +103,22 @@ __device__ __forceinline__ uint64_t umma_desc_mn(uint32_t smem_addr) {
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
+}
+
+// Loads of a box of three dimensions, as tma_load_2d and tma_load_2d_pair.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster_addr, int32_t x,
+                                                 int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];" ::"r"(dst),
+      "l"(map), "r"(bar_cluster_addr), "r"(x), "r"(y), "r"(z)
+      : "memory");
 }
 
 // Instruction descriptor bits 15 and 16: operand A, B is MN-major.
@@ -127,305 +153,303 @@ __device__ __forceinline__ void ring_tile(int tile, int row_blocks, int col_bloc
 }
 
 // ---------------------------------------------------------------------------
-// sums to outputs: one warp, 32 rows; a thread holds 128 sums of one row
+// sums to outputs: a warp has 32 rows, a lane one of them
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, float a, float b, float c, float d) {
-  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ void ld_shared_v4(uint32_t addr, float& a, float& b, float& c, float& d) {
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a), "=f"(b), "=f"(c), "=f"(d) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint4& v) {
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-}
-
-// 16-byte chunk `chunk` of 256-byte row `row` of a warp's staging: rows 0 to 7 at
-// one chunk, and chunks at one row, fall on different banks.
-__device__ __forceinline__ uint32_t stage_at(uint32_t base, int row, int chunk) {
-  return base + static_cast<uint32_t>(row * 256 + ((chunk ^ (row & 15)) << 4));
+__device__ __forceinline__ void ld_global_v8(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
 }
 
-// N neighbouring values of a row on a boundary of their size (16 bytes at most).
-template <typename T, int N>
-struct alignas(16) RawN {
-  T e[N];
+// The values of a row that 32 bytes hold (16 or 8), in memory's form; `n` of them exist (that many or less), `align` says
+// whether rows begin on boundaries of 32 bytes (2), 16 (1) or their own size (0).
+template <typename T>
+struct Sector {
+  static constexpr int N = 32 / static_cast<int>(sizeof(T));
+  uint32_t w[8];
 };
-template <typename T, int N>
-__device__ __forceinline__ void load_n(RawN<T, N>& r, const T* p) {
-  if constexpr (sizeof(T) * N >= 16) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) * N / 16); ++i)
-      reinterpret_cast<uint4*>(r.e)[i] = reinterpret_cast<const uint4*>(p)[i];
-  } else {
-    *reinterpret_cast<uint2*>(r.e) = *reinterpret_cast<const uint2*>(p);
-  }
-}
-template <typename T, int N>
-__device__ __forceinline__ void store_n(T* p, const float (&v)[N]) {
-  RawN<T, N> r;
-#pragma unroll
-  for (int i = 0; i < N; ++i) from_f32(v[i], r.e[i]);
-  if constexpr (sizeof(T) * N >= 16) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) * N / 16); ++i)
-      reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(r.e)[i];
-  } else {
-    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(r.e);
-  }
-}
-
-// Sixteen codes of a row, as far as its columns go.
-__device__ __forceinline__ void store_codes16(uint8_t* row, uint4 v, int64_t col, int64_t cols) {
-  if (col + 16 <= cols) {
-    *reinterpret_cast<uint4*>(row + col) = v;
+template <typename T>
+__device__ __forceinline__ void load_sector(Sector<T>& r, const T* p, int n, int align) {
+  constexpr int PER16 = Sector<T>::N / 2;
+  if (n >= Sector<T>::N && align == 2) {
+    ld_global_v8(p, r.w);
     return;
   }
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = i * PER16;
+    if (align && at + PER16 <= n) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + at);
+      memcpy(r.w + 4 * i, &v, 16);
+      continue;
+    }
+    T t[PER16];
+#pragma unroll
+    for (int k = 0; k < PER16; ++k) {
+      from_f32(0.f, t[k]);
+      if (at + k < n) t[k] = p[at + k];
+    }
+    memcpy(r.w + 4 * i, t, 16);
+  }
+}
+template <typename T>
+__device__ __forceinline__ float sector_value(const Sector<T>& r, int i) {
+  if constexpr (sizeof(T) == 4) return word_lo<T>(r.w[i]);
+  return i & 1 ? word_hi<T>(r.w[i / 2]) : word_lo<T>(r.w[i / 2]);
+}
+template <typename T>
+__device__ __forceinline__ void store_sector(T* p, const float* v, int n, int align) {
+  constexpr int N = Sector<T>::N, PER16 = N / 2;
+  T t[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) from_f32(v[i], t[i]);
+  uint32_t w[8];
+  memcpy(w, t, 32);
+  if (n >= N && align == 2) {
+    st_global_v8(p, w);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (align && (i + 1) * PER16 <= n) {
+      *reinterpret_cast<uint4*>(p + i * PER16) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      continue;
+    }
+#pragma unroll
+    for (int k = i * PER16; k < (i + 1) * PER16; ++k)
+      if (k < n) p[k] = t[k];
+  }
+}
+// 32 neighbouring values.
+template <typename T>
+__device__ __forceinline__ void store_row(T* p, const float* v, int n, int align) {
+#pragma unroll
+  for (int i = 0; i < 32; i += Sector<T>::N) store_sector(p + i, v + i, n - i, align);
+}
+
+// Sixteen codes of a row, `n` of which exist.
+__device__ __forceinline__ void store_codes16(uint8_t* p, const uint32_t* w, int n) {
+  if (n >= 16) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    if (col + i < cols) row[col + i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
+    if (i < n) p[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
 }
 
-// out = act(s + bias) + addend of 32 rows x 128 columns.  `rows`: rows of the output (0: nothing is written).
-template <typename T, typename O>
-__device__ __forceinline__ void finish_linear(const RingParams& g, int p, float (&acc)[128], uint8_t* stage, int lane,
-                                              int64_t row0, int64_t col0, int64_t rows) {
-  const FfnOut& o = g.o;
-  const uint32_t base = smem_u32(stage);
-  const int64_t cols = g.cols;
-  if (col0 >= cols) return;
-  if (o.bias) {
-    // a lane fetches four columns' bias, all read all of it
-    float b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t c = col0 + 4 * lane + i;
-      b[i] = 0.f;
-      if (c < cols) b[i] = o.bias_f32 ? static_cast<const float*>(o.bias)[c] : to_f32(static_cast<const T*>(o.bias)[c]);
-    }
-    __syncwarp();
-    st_shared_v4(base + lane * 16, b[0], b[1], b[2], b[3]);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      float x, y, z, w;
-      ld_shared_v4(base + i * 16, x, y, z, w);
-      acc[4 * i] += x;
-      acc[4 * i + 1] += y;
-      acc[4 * i + 2] += z;
-      acc[4 * i + 3] += w;
-    }
-  }
-  if (o.codes[0].data) {
-    // the thread's row has its group of 128 columns to itself
-    if (col0 + 128 > cols) {   // (an infinity times a column that is not there is NaN)
-#pragma unroll
-      for (int i = 0; i < 128; ++i)
-        if (col0 + i >= cols) acc[i] = 0.f;
-    }
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < 128; ++i) most = max(most, abs_bits(acc[i]));
-    const GroupScale s = group_scale(most, 448.f);
-    const FfnCodes& q = o.codes[0];
-    if (row0 + lane < rows) q.scales[(row0 + lane) * q.stride_row + (col0 >> 7) * q.stride_col] = s.scale;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float* v = acc + 16 * i + 4 * j;
-        w[j] = fp8x4<false>(v[0] * s.inv, v[1] * s.inv, v[2] * s.inv, v[3] * s.inv);
-      }
-      st_shared_v4(base + sw128_offset(lane, i), w[0], w[1], w[2], w[3]);
-    }
-    __syncwarp();
-#pragma unroll 4
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + lane / 8;
-      uint4 v;
-      ld_shared_v4(base + sw128_offset(r, lane % 8), v);
-      if (row0 + r < rows) store_codes16(q.data + (row0 + r) * q.ld, v, col0 + lane % 8 * 16, cols);
-    }
-  }
-  const int lr = lane >> 3, lc = lane & 7;
-  const O* const add = static_cast<const O*>(o.add[p]);
-  O* const out = static_cast<O*>(o.out[p]);
-  T* const keep = static_cast<T*>(o.keep[0]);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float* x = acc + j * 64 + 4 * i;
-      st_shared_v4(stage_at(base, lane, i), x[0], x[1], x[2], x[3]);
-    }
-    __syncwarp();
-    const int64_t first = col0 + j * 64;
-    // eight lanes to a row, eight columns each, where rows are on 16-byte boundaries
-    const int64_t col = first + lc * 8;
-    const bool mine = o.vec && col + 8 <= cols;
-    constexpr int AHEAD = sizeof(O) == 4 ? 2 : 4;   // (more, and registers spill)
-#pragma unroll 1
-    for (int r0 = lr; r0 < 32; r0 += 4 * AHEAD) {
-      RawN<O, 8> was[AHEAD];
-      if (add) {
-        // addends are asked for before the first of these outputs is written: they may be the same memory
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
-          if (mine && row0 + r0 + 4 * u < rows) load_n(was[u], add + (row0 + r0 + 4 * u) * o.ld_add[p] + col);
-      }
-#pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        const int r = r0 + 4 * u;
-        float v[8], t[8];
-        // (the first of the two chunks alternates, so that eight lanes meet eight banks)
-        const int odd = lc >> 2;
-        ld_shared_v4(stage_at(base, r, 2 * lc + odd), t[0], t[1], t[2], t[3]);
-        ld_shared_v4(stage_at(base, r, 2 * lc + 1 - odd), t[4], t[5], t[6], t[7]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = odd ? t[4 + i] : t[i];
-          v[4 + i] = odd ? t[i] : t[4 + i];
-        }
-        if (!mine || row0 + r >= rows) continue;
-        if (keep) store_n(keep + (row0 + r) * o.ld_keep[0] + col, v);
-        activate_all(v, o.act);
-        if (add) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += to_f32(was[u].e[i]);
-        }
-        store_n(out + (row0 + r) * o.ld_out[p] + col, v);
-      }
-    }
-    // what is left of a row one by one, a lane to a column
-    const int64_t rest = o.vec ? (cols & ~int64_t(7)) : 0, end = cols < first + 64 ? cols : first + 64;
-    for (int64_t c = (rest > first ? rest : first) + lane; c < end; c += 32) {
-      const int at = static_cast<int>(c - first);
-#pragma unroll 4
-      for (int r = 0; r < 32; ++r) {
-        if (row0 + r >= rows) break;
-        float v;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(stage_at(base, r, at >> 2) + (at & 3) * 4) : "memory");
-        if (keep) from_f32(v, keep[(row0 + r) * o.ld_keep[0] + c]);
-        v = activate(v, o.act);
-        if (add) v += to_f32(add[(row0 + r) * o.ld_add[p] + c]);
-        from_f32(v, out[(row0 + r) * o.ld_out[p] + c]);
-      }
-    }
-  }
-  __syncwarp();
-}
-
-// out = act(g) * u of 32 rows x 64 columns: acc[0 .. 63] are g's sums, the others u's.  The other warp of the same
-// rows (`half`) holds the other 64 columns of a group of 128.
+// Adds 32 columns' bias, of which a lane fetches one.
 template <typename T>
-__device__ __forceinline__ void finish_gated(const RingParams& g, float (&acc)[128], uint8_t* stage, int lane, int quarter,
-                                             int half, int64_t row0, int64_t col0, int64_t rows) {
+__device__ __forceinline__ void add_bias(float* v, const FfnOut& o, int lane, int64_t first, int64_t cols) {
+  const int64_t c = first + lane;
+  float b = 0.f;
+  if (c < cols) b = o.bias_f32 ? static_cast<const float*>(o.bias)[c] : to_f32(static_cast<const T*>(o.bias)[c]);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, b, i);
+}
+
+// out = act(v) + addend, and v itself where it is kept: a lane's 32 columns.
+template <typename T, typename O>
+__device__ __forceinline__ void emit_row(const FfnOut& o, int p, float (&v)[32], int64_t row, int64_t first, int n) {
+  constexpr int N = Sector<O>::N;
+  O* const out = static_cast<O*>(o.out[p]) + row * o.ld_out[p] + first;
+  if (o.keep[0]) store_row(static_cast<T*>(o.keep[0]) + row * o.ld_keep[0] + first, v, n, o.vec);
+  activate_all(v, o.act);
+  if (o.add[p]) {
+    // 16-bit addends all at once, FP32 ones sector by sector, as registers allow; each before its output is written, which
+    // may be the same memory
+    const O* const add = static_cast<const O*>(o.add[p]) + row * o.ld_add[p] + first;
+    constexpr int AT_ONCE = sizeof(O) == 2 ? 2 : 1;
+#pragma unroll
+    for (int i = 0; i < 32; i += AT_ONCE * N) {
+      Sector<O> was[AT_ONCE];
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k) load_sector(was[k], add + i + k * N, n - i - k * N, o.vec);
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) v[i + k * N + c] += sector_value(was[k], c);
+        store_sector(out + i + k * N, v + i + k * N, n - i - k * N, o.vec);
+      }
+    }
+    return;
+  }
+  store_row(out, v, n, o.vec);
+}
+
+// h = act(g) * u, and g and u themselves where they are kept: a lane's 32 columns.
+template <typename T>
+__device__ __forceinline__ void emit_gated(const FfnOut& o, float (&g)[32], const float* u, int64_t row, int64_t first, int n) {
+  if (o.keep[0]) {
+    store_row(static_cast<T*>(o.keep[0]) + row * o.ld_keep[0] + first, g, n, o.vec);
+    store_row(static_cast<T*>(o.keep[1]) + row * o.ld_keep[1] + first, u, n, o.vec);
+  }
+  activate_all(g, o.act);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) g[i] *= u[i];
+  store_row(static_cast<T*>(o.out[0]) + row * o.ld_out[0] + first, g, n, o.vec);
+}
+
+__device__ __forceinline__ int columns_left(int64_t first, int64_t cols) {
+  return cols - first < 32 ? static_cast<int>(cols - first) : 32;
+}
+
+// 32 columns of TMEM, or zeros.
+__device__ __forceinline__ void load_sums(float (&v)[32], uint32_t src, bool sums) {
+  uint32_t s[32];
+  if (sums) {
+    tmem_ld_32x32b_x32(src, s);
+    tmem_wait_ld();
+    regs_after_wait(s);
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = sums ? __uint_as_float(s[i]) : 0.f;
+}
+
+// A tile's outputs straight from TMEM: OUTS columns of the warp's rows, 32 at a time.  `src`: the first sum's address (sums
+// false: there are none, all are 0); `other`: how far behind it the second weight's lie; release(): called when the last
+// has been read.
+template <int OUTS, bool GATED, typename T, typename Release>
+__device__ __forceinline__ void stream_out(const RingParams& g, int p, uint32_t src, uint32_t other, bool sums, Release release,
+                                           int lane, int64_t row, int64_t col0) {
   const FfnOut& o = g.o;
-  const uint32_t base = smem_u32(stage);
   const int64_t cols = g.cols;
+  if (col0 >= cols) {
+    if (sums) release();
+    return;
+  }
+#pragma unroll 1
+  for (int j = 0; j < OUTS / 32; ++j) {
+    const int64_t first = col0 + j * 32;
+    if (first >= cols) break;
+    float v[32], u[GATED ? 32 : 1];
+    load_sums(v, src + j * 32, sums);
+    if constexpr (GATED) load_sums(u, src + other + j * 32, sums);
+    if (sums && (j + 1 == OUTS / 32 || first + 32 >= cols)) release();
+    if (!GATED && o.bias) add_bias<T>(v, o, lane, first, cols);
+    if (row < g.rows) {
+      if constexpr (GATED)
+        emit_gated<T>(o, v, u, row, first, columns_left(first, cols));
+      else
+        emit_row<T, T>(o, p, v, row, first, columns_left(first, cols));
+    }
+    __syncwarp();
+  }
+}
+
+// The larger magnitude, a NaN before any number.
+__device__ __forceinline__ float max_abs(float m, float x) {
+  asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %1;\n\tmax.NaN.f32 %0, %0, t;\n\t}" : "+f"(m) : "f"(x));
+  return m;
+}
+
+template <int N>
+__device__ __forceinline__ float max_abs_of(const float (&v)[N]) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};   // four chains
+#pragma unroll
+  for (int i = 0; i < N; ++i) m[i & 3] = max_abs(m[i & 3], v[i]);
+  return max_abs(max_abs(m[0], m[1]), max_abs(m[2], m[3]));
+}
+
+// The largest over the `warps` warps that hold a group of 128 columns together: their slots of shared memory lie 4 warps
+// apart, this one's is the `which`-th.  All of them come here for every tile that is kept in 8 bits.
+constexpr int kMaxSlot = 32 * 8;
+template <int N>
+__device__ __forceinline__ void share_max(float (&m)[N], uint32_t slot, int lane, int which, int warps, int barrier) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(slot + (i * 32 + lane) * 4), "f"(m[i]) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * warps) : "memory");
+  for (int w = 0; w < warps; ++w) {
+    if (w == which) continue;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float x;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(slot + (w - which) * 4 * kMaxSlot + (i * 32 + lane) * 4) : "memory");
+      m[i] = max_abs(m[i], x);
+    }
+  }
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * warps) : "memory");   // (read before the next tile's)
+}
+
+// 32 values as codes, to a row's columns from `first` on, n of which exist.
+__device__ __forceinline__ void emit_codes(const FfnCodes& q, const float* v, float inv, int64_t row, int64_t first, int n) {
+  uint8_t* const p = q.data + row * q.ld + first;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float* x = v + 16 * i + 4 * k;
+      w[k] = fp8x4<false>(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    }
+    store_codes16(p + 16 * i, w, n - 16 * i);
+  }
+}
+
+// out = act(s + bias) + addend of a lane's 64 columns; `part`: which 64 of the tile's columns.  write false: nothing is
+// written (the row does not exist, or its sums did not come).
+template <typename T, typename O>
+__device__ __forceinline__ void finish_linear(const RingParams& g, int p, float (&acc)[2][32], uint32_t slot, int lane,
+                                              int quarter, int part, int64_t row, int64_t col0, bool write) {
+  const FfnOut& o = g.o;
+  const int64_t cols = g.cols;
+  if (o.bias) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) add_bias<T>(acc[j], o, lane, col0 + 32 * j, cols);
+  }
   if (o.codes[0].data) {
     if (col0 + 64 > cols) {   // (an infinity times a column that is not there is NaN)
 #pragma unroll
       for (int i = 0; i < 64; ++i)
-        if (col0 + i >= cols) acc[i] = acc[64 + i] = 0.f;
+        if (col0 + i >= cols) acc[i >> 5][i & 31] = 0.f;
     }
-    uint32_t mg = 0, mu = 0;
+    float most[1] = {max_abs(max_abs_of(acc[0]), max_abs_of(acc[1]))};
+    share_max(most, slot, lane, part & 1, 2, 2 + quarter * 2 + (part >> 1));
+    const GroupScale s = group_scale(__float_as_uint(most[0]), 448.f);
+    const FfnCodes& q = o.codes[0];
+    if (write && col0 < cols) {
+      if ((part & 1) == 0) q.scales[row * q.stride_row + (col0 >> 7) * q.stride_col] = s.scale;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) {
-      mg = max(mg, abs_bits(acc[i]));
-      mu = max(mu, abs_bits(acc[64 + i]));
-    }
-    // the two warps that share the group show each other their maxima (both come here for every tile)
-    const uint32_t mine = base + lane * 8, theirs = half ? mine - 4 * kRingWarpStage : mine + 4 * kRingWarpStage;
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(mine), "r"(mg), "r"(mu) : "memory");
-    asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory");
-    uint32_t og, ou;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(og), "=r"(ou) : "r"(theirs) : "memory");
-    asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory");
-    const GroupScale sg = group_scale(max(mg, og), 448.f), su = group_scale(max(mu, ou), 448.f);
-    if (row0 + lane < rows && col0 < cols) {
-      if (half == 0) o.codes[0].scales[(row0 + lane) * o.codes[0].stride_row + (col0 >> 7) * o.codes[0].stride_col] = sg.scale;
-      if (half == 0) o.codes[1].scales[(row0 + lane) * o.codes[1].stride_row + (col0 >> 7) * o.codes[1].stride_col] = su.scale;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float inv = i < 4 ? sg.inv : su.inv;
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float* v = acc + 16 * i + 4 * j;
-        w[j] = fp8x4<false>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-      }
-      st_shared_v4(base + sw128_offset(lane, i), w[0], w[1], w[2], w[3]);
-    }
-    __syncwarp();
-#pragma unroll 4
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + lane / 8, c = lane % 8;
-      uint4 v;
-      ld_shared_v4(base + sw128_offset(r, c), v);
-      const FfnCodes& q = o.codes[c >> 2];
-      if (row0 + r < rows) store_codes16(q.data + (row0 + r) * q.ld, v, col0 + (c & 3) * 16, cols);
+      for (int j = 0; j < 2; ++j) emit_codes(q, acc[j], s.inv, row, col0 + 32 * j, columns_left(col0 + 32 * j, cols));
     }
   }
-  const int lr = lane >> 3, lc = lane & 7;
-  T* const out = static_cast<T*>(o.out[0]);
-  T* const kg = static_cast<T*>(o.keep[0]);
-  T* const ku = static_cast<T*>(o.keep[1]);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    __syncwarp();
+  for (int j = 0; j < 2; ++j)
+    if (write && col0 + 32 * j < cols) emit_row<T, O>(o, p, acc[j], row, col0 + 32 * j, columns_left(col0 + 32 * j, cols));
+  __syncwarp();
+}
+
+// h = act(g) * u of a lane's 32 columns: acc[0] are g's sums, acc[1] u's.  `part`: which 32 of the tile's columns, four of
+// which are a group of 128.
+template <typename T>
+__device__ __forceinline__ void finish_gated(const RingParams& g, float (&acc)[2][32], uint32_t slot, int lane, int quarter,
+                                             int part, int64_t row, int64_t col0, bool write) {
+  const FfnOut& o = g.o;
+  const int64_t cols = g.cols;
+  if (col0 + 32 > cols) {   // (an infinity times a column that is not there is NaN)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float *x = acc + j * 32 + 4 * i, *y = x + 64;
-      st_shared_v4(stage_at(base, lane, i), x[0], x[1], x[2], x[3]);
-      st_shared_v4(stage_at(base, lane, 8 + i), y[0], y[1], y[2], y[3]);
-    }
-    __syncwarp();
-    const int64_t first = col0 + j * 32;
-    // eight lanes to a row, four columns each, where rows are on 16-byte boundaries
-    const int64_t col = first + lc * 4;
-    const bool mine = o.vec && col + 4 <= cols;
-#pragma unroll 4
-    for (int r = lr; r < 32; r += 4) {
-      float v[4], u[4];
-      ld_shared_v4(stage_at(base, r, lc), v[0], v[1], v[2], v[3]);
-      ld_shared_v4(stage_at(base, r, 8 + lc), u[0], u[1], u[2], u[3]);
-      if (!mine || row0 + r >= rows) continue;
-      if (kg) {
-        store_n(kg + (row0 + r) * o.ld_keep[0] + col, v);
-        store_n(ku + (row0 + r) * o.ld_keep[1] + col, u);
-      }
-      activate_all(v, o.act);
+    for (int i = 0; i < 32; ++i)
+      if (col0 + i >= cols) acc[0][i] = acc[1][i] = 0.f;
+  }
+  float most[2] = {max_abs_of(acc[0]), max_abs_of(acc[1])};
+  share_max(most, slot, lane, part, 4, 2 + quarter);
+  if (write && col0 < cols) {
+    const int n = columns_left(col0, cols);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] *= u[i];
-      store_n(out + (row0 + r) * o.ld_out[0] + col, v);
+    for (int j = 0; j < 2; ++j) {
+      const GroupScale s = group_scale(__float_as_uint(most[j]), 448.f);
+      const FfnCodes& q = o.codes[j];
+      if (part == 0) q.scales[row * q.stride_row + (col0 >> 7) * q.stride_col] = s.scale;
+      emit_codes(q, acc[j], s.inv, row, col0, n);
     }
-    // what is left of a row one by one, a lane to a column
-    const int64_t rest = o.vec ? (cols & ~int64_t(3)) : 0, end = cols < first + 32 ? cols : first + 32;
-    const int64_t c = (rest > first ? rest : first) + lane;
-    if (c < end) {
-      const int at = static_cast<int>(c - first);
-#pragma unroll 4
-      for (int r = 0; r < 32; ++r) {
-        if (row0 + r >= rows) break;
-        float v, u;
-        const uint32_t in = (at & 3) * 4;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(stage_at(base, r, at >> 2) + in) : "memory");
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(u) : "r"(stage_at(base, r, 8 + (at >> 2)) + in) : "memory");
-        if (kg) {
-          from_f32(v, kg[(row0 + r) * o.ld_keep[0] + c]);
-          from_f32(u, ku[(row0 + r) * o.ld_keep[1] + c]);
-        }
-        from_f32(activate(v, o.act) * u, out[(row0 + r) * o.ld_out[0] + c]);
-      }
-    }
+    emit_gated<T>(o, acc[0], acc[1], row, col0, n);
   }
   __syncwarp();
 }
@@ -438,14 +462,14 @@ struct RingMaps {
   CUtensorMap a[2], b[2];
 };
 
-template <int BN, bool PAIR, bool GATED, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(RingShape<BN, PAIR>::THREADS, 1)
+template <int BN, bool PAIR, RingOut OUT, bool GATED, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
     ffn_ring_kernel(const __grid_constant__ RingMaps maps, const __grid_constant__ RingParams g) {
-  using Sh = RingShape<BN, PAIR>;
+  using Sh = RingShape<BN, PAIR, OUT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* staging = ring + Sh::STAGES * Sh::STAGE;
-  RingBarriers* bar = reinterpret_cast<RingBarriers*>(staging + Sh::EPI_WARPS * kRingWarpStage);
+  uint8_t* maxima = ring + Sh::STAGES * Sh::STAGE;
+  RingBarriers* bar = reinterpret_cast<RingBarriers*>(maxima + Sh::SHARED_MAX);
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // (uniform for the compiler too)
   const int lane = threadIdx.x & 31;
@@ -514,26 +538,36 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR>::THREADS, 1)
           const CUtensorMap* ma = &maps.a[problem | second];
           const CUtensorMap* mb = &maps.b[GATED ? static_cast<int>(rank) : second];   // (two products share b)
           const uint32_t a_at = smem_u32(ring + s * Sh::STAGE), b_at = a_at + Sh::A_BYTES;
+          const uint32_t full = PAIR ? mapa_shared(smem_u32(&bar->full[s]), 0) : 0u;
           auto load = [&](uint32_t at, const CUtensorMap* m, int x, int y) {
             if (PAIR)
-              tma_load_2d_pair(at, m, mapa_shared(smem_u32(&bar->full[s]), 0), x, y);
+              tma_load_2d_pair(at, m, full, x, y);
             else
               tma_load_2d(at, m, &bar->full[s], x, y);
+          };
+          // Two boxes of 8 KB where one of 16 KB would do cost time in the TMA unit: 4096 x 8192 x 4096 142 us with two
+          // boxes per slot, 161 with four.
+          auto load_mn = [&](uint32_t at, const CUtensorMap* m, bool planes, int row, int k) {
+            if (!planes) {
+              load(at, m, row, k);
+              load(at + 8192, m, row + 64, k);
+            } else if (PAIR) {
+              tma_load_3d_pair(at, m, full, 0, k, row >> 6);
+            } else {
+              tma_load_3d(at, m, &bar->full[s], 0, k, row >> 6);
+            }
           };
           if (tile == lose_tile && kb == kt - 1) {
             lost = issued;
           } else {
             // (the even CTA's barrier counts the bytes of both CTAs' loads)
             if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], Sh::CTAS * Sh::STAGE);
-            if (A_MN) {
-              load(a_at, ma, a_row, k);
-              load(a_at + 8192, ma, a_row + 64, k);
-            } else {
+            if (A_MN)
+              load_mn(a_at, ma, g.a_planes, a_row, k);
+            else
               load(a_at, ma, k, a_row);
-            }
             if (B_MN) {
-              load(b_at, mb, b_row, k);
-              load(b_at + 8192, mb, b_row + 64, k);
+              load_mn(b_at, mb, g.b_planes, b_row, k);
             } else if (GATED && !PAIR) {
               load(b_at, mb, k, b_row);
               load(b_at + 8192, &maps.b[1], k, b_row);
@@ -603,11 +637,11 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR>::THREADS, 1)
     if (Sh::SPLIT_REGS) regs_increase<Sh::EPI_REGS>();
     const int e = warp - 4;
     const int quarter = warp & 3;          // TMEM lanes this warp may access
-    const int half = e >> 2;               // which half of the tile's columns
-    uint8_t* my_stage = staging + e * kRingWarpStage;
+    const int part = e >> 2;               // which of the tile's columns
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    // TMEM columns of a thread's sums 0 .. 63 and 64 .. 127
-    const uint32_t lo = GATED ? half * 64 : half * 128, hi = GATED ? BN / 2 + half * 64 : half * 128 + 64;
+    // its output columns, and the TMEM columns of their sums: a gated product's second weight has its own BN / 2 further on
+    constexpr int OUTS = GATED ? Sh::EPI_COLS / 2 : Sh::EPI_COLS;
+    const uint32_t lo = part * OUTS, other = BN / 2;
     int a = 0;
     uint32_t aph = 0;
     bool ok = true;   // after a wait that gave up: nothing is written any more
@@ -615,65 +649,80 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR>::THREADS, 1)
       int rb, cb;
       const int problem = tile >= per_problem ? 1 : 0;
       ring_tile(tile - problem * per_problem, row_blocks, col_blocks, g.raster, rb, cb);
-      const int64_t row0 = static_cast<int64_t>(rb) * Sh::TILE_ROWS + rank * Sh::A_ROWS + quarter * 32;
-      const int64_t col0 = static_cast<int64_t>(cb) * TILE_COLS + half * (GATED ? 64 : 128);
-      float acc[128];
-#pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      if (!GATED && g.o.add[problem] && row0 + lane < g.rows) {
+      const int64_t row = static_cast<int64_t>(rb) * Sh::TILE_ROWS + rank * Sh::A_ROWS + quarter * 32 + lane;
+      const int64_t col0 = static_cast<int64_t>(cb) * TILE_COLS + part * OUTS;
+      if (!GATED && g.o.add[problem] && row < g.rows) {
         // this thread's row of the addend comes into L2 while the products run
         const int size = g.o.out_f32 ? 4 : 2;
-        const uint8_t* at = static_cast<const uint8_t*>(g.o.add[problem]) + ((row0 + lane) * g.o.ld_add[problem] + col0) * size;
+        const uint8_t* at = static_cast<const uint8_t*>(g.o.add[problem]) + (row * g.o.ld_add[problem] + col0) * size;
 #pragma unroll 1
-        for (int i = 0; i < 128 && col0 + i < g.cols; i += 128 / size) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * size));
+        for (int i = 0; i < OUTS && col0 + i < g.cols; i += 128 / size) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * size));
       }
-#pragma unroll 1
-      for (int kc = 0; kc < kt; kc += g.restart) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bar->acc_full[a], aph, g.ctl, cta, kSiteEpilogueAccFull));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t src = tmem + lanes + a * BN;
-        uint32_t v[2][32];
-        tmem_ld_32x32b_x32(src + lo, v[0]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          tmem_wait_ld();
-          regs_after_wait(v[j & 1]);
-          if (j < 3) {
-            tmem_ld_32x32b_x32(src + (j + 1 < 2 ? lo + 32 : hi + (j - 1) * 32), v[(j + 1) & 1]);
-          } else {
-            // the buffer is in registers: hand it back to the MMA issuer
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (PAIR)
-                ring_arrive_cluster_relaxed(mapa_shared(smem_u32(&bar->acc_empty[a]), 0));
-              else
-                mbar_arrive(&bar->acc_empty[a]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[j * 32 + i] += __uint_as_float(v[j & 1][i]);
+      auto hand_back = [&]() {
+        // the buffer has been read: back to the MMA issuer
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            ring_arrive_cluster_relaxed(mapa_shared(smem_u32(&bar->acc_empty[a]), 0));
+          else
+            mbar_arrive(&bar->acc_empty[a]);
         }
-        if (++a == 2) { a = 0; aph ^= 1u; }
-      }
-      const int64_t rows = ok ? g.rows : 0;
-      if constexpr (GATED) {
+      };
+      if constexpr (OUT == kStream) {
+        const bool sums = kt > 0;
+        if (sums) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bar->acc_full[a], aph, g.ctl, cta, kSiteEpilogueAccFull));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t src = tmem + lanes + a * BN + lo;
         if (g.o.bf16)
-          finish_gated<__nv_bfloat16>(g, acc, my_stage, lane, quarter, half, row0, col0, rows);
+          stream_out<OUTS, GATED, __nv_bfloat16>(g, problem, src, other, sums, hand_back, lane, row, col0);
         else
-          finish_gated<__half>(g, acc, my_stage, lane, quarter, half, row0, col0, rows);
+          stream_out<OUTS, GATED, __half>(g, problem, src, other, sums, hand_back, lane, row, col0);
+        if (sums && ++a == 2) { a = 0; aph ^= 1u; }
       } else {
-        if (g.o.bf16) {
-          if (g.o.out_f32)
-            finish_linear<__nv_bfloat16, float>(g, problem, acc, my_stage, lane, row0, col0, rows);
+        float acc[2][32];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) acc[i >> 5][i & 31] = 0.f;
+#pragma unroll 1
+        for (int kc = 0; kc < kt; kc += g.restart) {
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bar->acc_full[a], aph, g.ctl, cta, kSiteEpilogueAccFull));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t src = tmem + lanes + a * BN + lo;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(src + (j >> 1) * (GATED ? other : 32u) + (j & 1) * 16, v);
+            tmem_wait_ld();
+            regs_after_wait(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[j >> 1][(j & 1) * 16 + i] += __uint_as_float(v[i]);
+          }
+          hand_back();
+          if (++a == 2) { a = 0; aph ^= 1u; }
+        }
+        const bool write = ok && row < g.rows;
+        const uint32_t slot = smem_u32(maxima) + e * kMaxSlot;
+        if constexpr (GATED) {
+          if (g.o.bf16)
+            finish_gated<__nv_bfloat16>(g, acc, slot, lane, quarter, part, row, col0, write);
           else
-            finish_linear<__nv_bfloat16, __nv_bfloat16>(g, problem, acc, my_stage, lane, row0, col0, rows);
+            finish_gated<__half>(g, acc, slot, lane, quarter, part, row, col0, write);
         } else {
-          if (g.o.out_f32)
-            finish_linear<__half, float>(g, problem, acc, my_stage, lane, row0, col0, rows);
-          else
-            finish_linear<__half, __half>(g, problem, acc, my_stage, lane, row0, col0, rows);
+          if (g.o.bf16) {
+            if (g.o.out_f32)
+              finish_linear<__nv_bfloat16, float>(g, problem, acc, slot, lane, quarter, part, row, col0, write);
+            else
+              finish_linear<__nv_bfloat16, __nv_bfloat16>(g, problem, acc, slot, lane, quarter, part, row, col0, write);
+          } else {
+            if (g.o.out_f32)
+              finish_linear<__half, float>(g, problem, acc, slot, lane, quarter, part, row, col0, write);
+            else
+              finish_linear<__half, __half>(g, problem, acc, slot, lane, quarter, part, row, col0, write);
+          }
         }
       }
     }
@@ -738,10 +787,14 @@ inline CUtensorMapDataType ffn_map_type(const FfnOut& o) {
   return o.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
-// Map of an operand of `rows` x `summed`, stored summed axis first where `mn`, whose boxes hold box_rows of its rows.
+// Map of an operand of `rows` x `summed`, whose boxes hold box_rows of its rows; stored summed axis first where `mn`: 64 of
+// its rows, or two planes of 64.
 inline cudaError_t ffn_map(CUtensorMap* m, const FfnProduct& p, const void* base, int64_t ld, int64_t rows, bool mn,
                            int box_rows) {
   const uint64_t row_bytes = static_cast<uint64_t>(ld) * 2;
+  if (mn && rows % 64 == 0)   // (otherwise the last plane would end outside of its rows)
+    return make_tmap_3d(m, base, ffn_map_type(p.out), 64, p.summed, row_bytes, rows / 64, 128, 64, kFfnBK, 2,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
   return mn ? make_tmap_2d(m, base, ffn_map_type(p.out), rows, p.summed, row_bytes, 64, kFfnBK, CU_TENSOR_MAP_SWIZZLE_128B)
             : make_tmap_2d(m, base, ffn_map_type(p.out), p.summed, rows, row_bytes, kFfnBK, box_rows,
                            CU_TENSOR_MAP_SWIZZLE_128B);
@@ -758,10 +811,10 @@ inline cudaError_t check_launch_regs(std::atomic<int>& regs, const void* kernel)
   return regs.load() == kRingLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
-template <int BN, bool PAIR, bool GATED, bool A_MN, bool B_MN>
+template <int BN, bool PAIR, RingOut OUT, bool GATED, bool A_MN, bool B_MN>
 cudaError_t launch_ring(FfnProduct& p, const void** kernel) {
-  using Sh = RingShape<BN, PAIR>;
-  auto k = ffn_ring_kernel<BN, PAIR, GATED, A_MN, B_MN>;
+  using Sh = RingShape<BN, PAIR, OUT>;
+  auto k = ffn_ring_kernel<BN, PAIR, OUT, GATED, A_MN, B_MN>;
   *kernel = reinterpret_cast<const void*>(k);
   const bool sum = p.op == kFfnInputGrad && p.count == 2, both = p.op == kFfnWeightGrad && p.count == 2;
   RingMaps maps = {};
@@ -784,6 +837,8 @@ cudaError_t launch_ring(FfnProduct& p, const void** kernel) {
   g.restart = wide ? kFfnRestart : (g.kt > 0 ? g.kt * g.sources : 1);
   g.raster = p.plan.raster_gm;
   g.idesc = umma_idesc_f16(p.out.bf16 != 0, Sh::TILE_ROWS, BN) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
+  g.a_planes = A_MN && p.rows % 64 == 0;
+  g.b_planes = B_MN && p.cols % 64 == 0;
   g.ctl = p.ctl;
   if (Sh::SPLIT_REGS) {
     static std::atomic<int> regs{-1};
@@ -792,6 +847,22 @@ cudaError_t launch_ring(FfnProduct& p, const void** kernel) {
   if ((e = ensure_smem_attr(*kernel, Sh::SMEM)) != cudaSuccess) return e;
   RingConfig c(p.plan.grid, Sh::THREADS, Sh::CTAS, Sh::SMEM, p.stream);
   return cudaLaunchKernelEx(&c.cfg, k, maps, g);
+}
+
+// The tile of the plan; sums are held where FP32 or 8-bit codes leave.
+template <bool GATED, bool A_MN, bool B_MN>
+cudaError_t launch_tile(FfnProduct& p, const void** kernel) {
+  const bool wide = p.out.out_f32 || p.out.codes[0].data;
+  if constexpr (GATED) {   // (8 bits on pairs alone)
+    if (wide) return launch_ring<256, true, kHold, true, A_MN, B_MN>(p, kernel);
+    return p.plan.cta_pair ? launch_ring<256, true, kStream, true, A_MN, B_MN>(p, kernel)
+                           : launch_ring<128, false, kStream, true, A_MN, B_MN>(p, kernel);
+  } else if (p.plan.cta_pair)
+    return wide ? launch_ring<256, true, kHold, false, A_MN, B_MN>(p, kernel)
+                : launch_ring<256, true, kStream, false, A_MN, B_MN>(p, kernel);
+  else
+    return wide ? launch_ring<128, false, kHold, false, A_MN, B_MN>(p, kernel)
+                : launch_ring<128, false, kStream, false, A_MN, B_MN>(p, kernel);
 }
 
 }  // namespace gp

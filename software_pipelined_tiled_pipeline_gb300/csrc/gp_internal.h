@@ -185,6 +185,10 @@ cudaError_t launch_zero_fill(void* C, int64_t bytes, cudaStream_t stream);
 cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type, uint64_t inner,
                          uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                          CUtensorMapSwizzle swizzle);
+// The same with a third dimension of `planes` planes, plane_bytes apart (which may be less than a row).
+cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType type, uint64_t inner,
+                         uint64_t outer, uint64_t row_bytes, uint64_t planes, uint64_t plane_bytes, uint32_t box_inner,
+                         uint32_t box_outer, uint32_t box_planes, CUtensorMapSwizzle swizzle);
 
 // Opt a kernel into more than 48 KB of dynamic shared memory (cached per device).
 cudaError_t ensure_smem_attr(const void* kernel, int bytes);

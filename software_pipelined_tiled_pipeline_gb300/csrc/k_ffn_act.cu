@@ -5,11 +5,13 @@
 //   gated:  dg = dh * u * act'(g), du = dh * act(g), h = act(g) * u
 //
 // z, g and u come in 16 bits or as 8-bit codes with a scale for each row's 128
-// values.  A block takes a strip of 256 columns and a part of the rows, a warp
-// every eighth of these, a lane eight columns; the bias gradient is summed in
-// FP32 per lane, over the block's warps and, by a second kernel, over the parts,
-// each in a fixed order.  HBM bounds it: two bytes in and out per value, one
-// for each 8-bit one.
+// values.  A block takes a strip of 128 columns (one group of codes per row) and a
+// part of the rows, a warp every eighth of these, a lane four columns; the bias
+// gradient is summed in FP32 per lane, over the block's warps and, by a second
+// kernel, over the parts, each in a fixed order.  HBM bounds it: two bytes in and
+// out per value, one for each 8-bit one.  Four values per lane and three rows under
+// way keep it within 64 registers, so 48 KB of loads are under way on an SM (with
+// eight values it took 255, and 4096 x 8192 with codes 111 us).
 #include <algorithm>
 #include "ffn_math.cuh"
 #include "fp8_rows.cuh"
@@ -17,7 +19,8 @@
 namespace gp {
 namespace {
 
-constexpr int kActThreads = 256, kActWarps = 8, kActStrip = 256;
+constexpr int kActThreads = 256, kActWarps = 8, kActStrip = 128;
+constexpr int kAtOnce = 3;   // rows whose loads a warp has under way
 
 // Two 8-bit codes (the lower first) as FP32.
 __device__ __forceinline__ float2 decode2(uint32_t codes, bool e5m2) {
@@ -32,71 +35,82 @@ __device__ __forceinline__ float2 decode2(uint32_t codes, bool e5m2) {
   return __half22float2(v);
 }
 
-// Eight kept values of a row, as they lie in memory and (below) as FP32.
+// A lane's four columns of its strip: side by side where rows are on 16-byte
+// boundaries, else every 32nd, so that a warp reads neighbouring values either way.
+// All four exist with VEC; a block's last strip and rows off 16-byte boundaries go without.
+template <bool VEC>
+struct Four {
+  int first, stride, cols;   // columns c = first + i * stride; `cols` there are
+  __device__ __forceinline__ bool has(int i) const { return first + i * stride < cols; }
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ uint2 load4(const T* row, const Four<VEC>& f) {
+  if (VEC) return *reinterpret_cast<const uint2*>(row + f.first);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = f.has(i) ? reinterpret_cast<const uint16_t*>(row)[f.first + i * f.stride] : 0u;
+  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+template <typename T>
+__device__ __forceinline__ void unpack4(float (&v)[4], uint2 w) {
+  v[0] = word_lo<T>(w.x);
+  v[1] = word_hi<T>(w.x);
+  v[2] = word_lo<T>(w.y);
+  v[3] = word_hi<T>(w.y);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store4(T* row, const float (&v)[4], const Four<VEC>& f) {
+  T t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) from_f32(v[i], t[i]);
+  if (VEC) {
+    uint2 w;
+    memcpy(&w, t, 8);
+    *reinterpret_cast<uint2*>(row + f.first) = w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (f.has(i)) row[f.first + i * f.stride] = t[i];
+}
+
+// Four kept values of a row, as they lie in memory and as FP32.
 template <typename T, bool FP8>
 struct Kept {
-  Raw8<T> r;
+  uint2 w;               // FP8: the codes, and their scale
 };
-template <typename T>
-struct Kept<T, true> {
-  uint2 c;
-  float scale;
-};
-
-template <typename T, bool FP8>
-__device__ __forceinline__ void load_kept(Kept<T, FP8>& k, const void* z, int64_t ldz, const FfnCodes& q, int64_t row, int c,
-                                          int cols, bool vec) {
+template <typename T, bool FP8, bool VEC>
+__device__ __forceinline__ Kept<T, FP8> load_kept(const void* z, int64_t ldz, const FfnCodes& q, int64_t row, int strip,
+                                                  const Four<VEC>& f) {
+  Kept<T, FP8> k;
   if constexpr (FP8) {
     const uint8_t* p = q.data + row * q.ld;
-    // (with rows off 16-byte boundaries a lane past the end still holds columns of its group)
-    k.scale = (c & ~127) < cols ? q.scales[row * q.stride_row + (c >> 7) * q.stride_col] : 0.f;
-    if (vec && c + 8 <= cols) {
-      k.c = *reinterpret_cast<const uint2*>(p + c);
+    k.w.y = __float_as_uint(q.scales[row * q.stride_row + strip * q.stride_col]);
+    if (VEC) {
+      k.w.x = *reinterpret_cast<const uint32_t*>(p + f.first);
     } else {
-      const Eight e = eight_columns(c, vec);
-      uint32_t w[2] = {0, 0};
+      k.w.x = 0u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (e.first + i * e.stride < cols) w[i >> 2] |= static_cast<uint32_t>(p[e.first + i * e.stride]) << (8 * (i & 3));
-      k.c = make_uint2(w[0], w[1]);
+      for (int i = 0; i < 4; ++i)
+        if (f.has(i)) k.w.x |= static_cast<uint32_t>(p[f.first + i * f.stride]) << (8 * i);
     }
   } else {
-    load8(k.r, static_cast<const T*>(z) + row * ldz, c, cols, vec);
+    k.w = load4(static_cast<const T*>(z) + row * ldz, f);
   }
+  return k;
 }
 template <typename T, bool FP8>
-__device__ __forceinline__ void widen_kept(float (&v)[8], const Kept<T, FP8>& k, bool e5m2) {
+__device__ __forceinline__ void widen_kept(float (&v)[4], const Kept<T, FP8>& k, bool e5m2) {
   if constexpr (FP8) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = decode2((i < 2 ? k.c.x : k.c.y) >> (16 * (i & 1)), e5m2);
-      v[2 * i] = f.x * k.scale;
-      v[2 * i + 1] = f.y * k.scale;
-    }
+    const float scale = __uint_as_float(k.w.y);
+    const float2 a = decode2(k.w.x, e5m2), b = decode2(k.w.x >> 16, e5m2);
+    v[0] = a.x * scale;
+    v[1] = a.y * scale;
+    v[2] = b.x * scale;
+    v[3] = b.y * scale;
   } else {
-    unpack8(k.r, v);
-  }
-}
-
-__device__ __forceinline__ void slopes(float (&z)[8], float (&d)[8], int act) {
-  switch (act) {
-#define GP_SLOPE_LOOP(A)                          \
-  case A:                                         \
-    _Pragma("unroll") for (int i = 0; i < 8; ++i) { \
-      const ActSlope s = activate_slope(z[i], A); \
-      z[i] = s.a;                                 \
-      d[i] = s.d;                                 \
-    }                                             \
-    break;
-    GP_SLOPE_LOOP(GP_ACT_RELU)
-    GP_SLOPE_LOOP(GP_ACT_GELU)
-    GP_SLOPE_LOOP(GP_ACT_GELU_TANH)
-    GP_SLOPE_LOOP(GP_ACT_SILU)
-    GP_SLOPE_LOOP(GP_ACT_SIGMOID)
-    default:
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = 1.f;
-#undef GP_SLOPE_LOOP
+    unpack4<T>(v, k.w);
   }
 }
 
@@ -110,64 +124,84 @@ __device__ __forceinline__ Rows rows_of(int64_t M, int part, int parts) {
   return Rows{from, from + per < M ? from + per : M};
 }
 
-constexpr int kAtOnce = 2;   // rows whose loads a warp has under way
+template <bool VEC>
+__device__ __forceinline__ Four<VEC> columns_of(const FfnActArgs& a, int strip, int lane) {
+  return Four<VEC>{strip * kActStrip + (VEC ? 4 * lane : lane), VEC ? 1 : 32, static_cast<int>(a.N)};
+}
 
-template <typename T, bool FP8>
-__global__ void __launch_bounds__(kActThreads) act_backward_kernel(const __grid_constant__ FfnActArgs a, int parts) {
-  __shared__ float sums[kActWarps][kActStrip];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int cols = static_cast<int>(a.N), first = static_cast<int>(blockIdx.x) * kActStrip, c = first + lane * 8;
-  const bool vec = a.vec;
-  const Rows in = rows_of(a.M, blockIdx.y, parts);
-  const bool act = a.act != GP_ACT_NONE;
-  float sum[8];
+template <typename T, bool FP8, int ACT, bool VEC>
+__device__ __forceinline__ void act_backward_rows(const FfnActArgs& a, const Rows& in, int strip, const Four<VEC>& f, int warp,
+                                                  float (&sum)[4]) {
+  constexpr int AT_ONCE = VEC ? kAtOnce : 1;
+  for (int64_t r0 = in.from + warp; r0 < in.to; r0 += AT_ONCE * kActWarps) {
+    uint2 dy[AT_ONCE];
+    Kept<T, FP8> z[AT_ONCE];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-  for (int64_t r0 = in.from + warp; r0 < in.to; r0 += kAtOnce * kActWarps) {
-    Raw8<T> dy[kAtOnce];
-    Kept<T, FP8> z[kAtOnce];
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
+    for (int u = 0; u < AT_ONCE; ++u) {
       const int64_t r = r0 + u * kActWarps;
-      if (r >= in.to) break;
-      load8(dy[u], static_cast<const T*>(a.dy) + r * a.ld_dy, c, cols, vec);
-      if (act) load_kept<T, FP8>(z[u], a.z[0], a.ldz[0], a.codes[0], r, c, cols, vec);
+      if (r < in.to) {
+        dy[u] = load4(static_cast<const T*>(a.dy) + r * a.ld_dy, f);
+        if (ACT != GP_ACT_NONE) z[u] = load_kept<T, FP8, VEC>(a.z[0], a.ldz[0], a.codes[0], r, strip, f);
+      }
     }
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
+    for (int u = 0; u < AT_ONCE; ++u) {
       const int64_t r = r0 + u * kActWarps;
-      if (r >= in.to) break;
-      float v[8], d[8];
-      unpack8(dy[u], v);
-      if (act) {
-        float y[8];
-        widen_kept<T, FP8>(y, z[u], a.e5m2);
-        slopes(y, d, a.act);
+      if (r < in.to) {
+        float v[4];
+        unpack4<T>(v, dy[u]);
+        if (ACT != GP_ACT_NONE) {
+          float y[4];
+          widen_kept<T, FP8>(y, z[u], a.e5m2);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= d[i];
-      }
+          for (int i = 0; i < 4; ++i) v[i] *= activate_slope(y[i], ACT).d;
+        }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += v[i];
-      if (a.dz[0]) {
-        Raw8<T> o;
-        pack8(v, o);
-        store8(static_cast<T*>(a.dz[0]) + r * a.ld_dz[0], o, c, cols, vec);
+        for (int i = 0; i < 4; ++i) sum[i] += v[i];
+        if (a.dz[0]) store4(static_cast<T*>(a.dz[0]) + r * a.ld_dz[0], v, f);
       }
     }
   }
+}
+
+#define GP_ACT_SWITCH(act, CALL)                            \
+  switch (act) {                                            \
+    case GP_ACT_RELU: CALL(GP_ACT_RELU); break;             \
+    case GP_ACT_GELU: CALL(GP_ACT_GELU); break;             \
+    case GP_ACT_GELU_TANH: CALL(GP_ACT_GELU_TANH); break;   \
+    case GP_ACT_SILU: CALL(GP_ACT_SILU); break;             \
+    case GP_ACT_SIGMOID: CALL(GP_ACT_SIGMOID); break;       \
+    default: CALL(GP_ACT_NONE); break;                      \
+  }
+
+template <typename T, bool FP8>
+__global__ void __launch_bounds__(kActThreads, 4) act_backward_kernel(const __grid_constant__ FfnActArgs a, int parts) {
+  __shared__ float sums[kActWarps][kActStrip];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, strip = blockIdx.x;
+  const Rows in = rows_of(a.M, blockIdx.y, parts);
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  const bool vec = a.vec && (strip + 1) * kActStrip <= a.N;
+  if (vec) {
+    const Four<true> f = columns_of<true>(a, strip, lane);
+#define GP_CALL(ACT) act_backward_rows<T, FP8, ACT>(a, in, strip, f, warp, sum)
+    GP_ACT_SWITCH(a.act, GP_CALL)
+  } else {
+    const Four<false> f = columns_of<false>(a, strip, lane);
+    GP_ACT_SWITCH(a.act, GP_CALL)
+#undef GP_CALL
+  }
   if (!a.dbias) return;
-  const Eight e = eight_columns(c, vec);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sums[warp][e.first + i * e.stride - first] = sum[i];
+  for (int i = 0; i < 4; ++i) sums[warp][vec ? 4 * lane + i : lane + 32 * i] = sum[i];
   __syncthreads();
-  const int col = first + static_cast<int>(threadIdx.x);
-  if (col >= cols) return;
+  const int col = strip * kActStrip + static_cast<int>(threadIdx.x);
+  if (threadIdx.x >= kActStrip || col >= a.N) return;
   float total = 0.f;
 #pragma unroll
   for (int w = 0; w < kActWarps; ++w) total += sums[w][threadIdx.x];
-  (parts > 1 ? a.partials + static_cast<int64_t>(blockIdx.y) * cols : a.dbias)[col] = total;
+  (parts > 1 ? a.partials + static_cast<int64_t>(blockIdx.y) * a.N : a.dbias)[col] = total;
 }
 
 // dbias = sum of the parts, in their order.
@@ -182,50 +216,58 @@ __global__ void __launch_bounds__(kActThreads) sum_parts_kernel(const float* par
   dbias[c] = total;
 }
 
-template <typename T, bool FP8>
-__global__ void __launch_bounds__(kActThreads) gated_backward_kernel(const __grid_constant__ FfnActArgs a, int parts) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int cols = static_cast<int>(a.N), c = static_cast<int>(blockIdx.x) * kActStrip + lane * 8;
-  const bool vec = a.vec;
-  const Rows in = rows_of(a.M, blockIdx.y, parts);
-  for (int64_t r0 = in.from + warp; r0 < in.to; r0 += kAtOnce * kActWarps) {
-    Raw8<T> dh[kAtOnce];
-    Kept<T, FP8> kg[kAtOnce], ku[kAtOnce];
+template <typename T, bool FP8, int ACT, bool VEC>
+__device__ __forceinline__ void gated_backward_rows(const FfnActArgs& a, const Rows& in, int strip, const Four<VEC>& f, int warp) {
+  constexpr int AT_ONCE = VEC ? kAtOnce : 1;
+  for (int64_t r0 = in.from + warp; r0 < in.to; r0 += AT_ONCE * kActWarps) {
+    uint2 dh[AT_ONCE];
+    Kept<T, FP8> kg[AT_ONCE], ku[AT_ONCE];
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
+    for (int u = 0; u < AT_ONCE; ++u) {
       const int64_t r = r0 + u * kActWarps;
-      if (r >= in.to) break;
-      load8(dh[u], static_cast<const T*>(a.dy) + r * a.ld_dy, c, cols, vec);
-      load_kept<T, FP8>(kg[u], a.z[0], a.ldz[0], a.codes[0], r, c, cols, vec);
-      load_kept<T, FP8>(ku[u], a.z[1], a.ldz[1], a.codes[1], r, c, cols, vec);
-    }
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      const int64_t r = r0 + u * kActWarps;
-      if (r >= in.to) break;
-      float v[8], g[8], d[8], up[8], t[8];
-      unpack8(dh[u], v);
-      widen_kept<T, FP8>(g, kg[u], a.e5m2);
-      widen_kept<T, FP8>(up, ku[u], a.e5m2);
-      slopes(g, d, a.act);
-      Raw8<T> o;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = v[i] * up[i] * d[i];
-      pack8(t, o);
-      store8(static_cast<T*>(a.dz[0]) + r * a.ld_dz[0], o, c, cols, vec);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = v[i] * g[i];
-      pack8(t, o);
-      store8(static_cast<T*>(a.dz[1]) + r * a.ld_dz[1], o, c, cols, vec);
-      if (a.h) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = g[i] * up[i];
-        pack8(t, o);
-        store8(static_cast<T*>(a.h) + r * a.ldh, o, c, cols, vec);
+      if (r < in.to) {
+        dh[u] = load4(static_cast<const T*>(a.dy) + r * a.ld_dy, f);
+        kg[u] = load_kept<T, FP8, VEC>(a.z[0], a.ldz[0], a.codes[0], r, strip, f);
+        ku[u] = load_kept<T, FP8, VEC>(a.z[1], a.ldz[1], a.codes[1], r, strip, f);
       }
     }
+#pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) {
+      const int64_t r = r0 + u * kActWarps;
+      if (r < in.to) {
+        float v[4], g[4], up[4], dg[4], du[4], h[4];
+        unpack4<T>(v, dh[u]);
+        widen_kept<T, FP8>(g, kg[u], a.e5m2);
+        widen_kept<T, FP8>(up, ku[u], a.e5m2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const ActSlope s = activate_slope(g[i], ACT);
+          dg[i] = v[i] * up[i] * s.d;
+          du[i] = v[i] * s.a;
+          h[i] = s.a * up[i];
+        }
+        store4(static_cast<T*>(a.dz[0]) + r * a.ld_dz[0], dg, f);
+        store4(static_cast<T*>(a.dz[1]) + r * a.ld_dz[1], du, f);
+        if (a.h) store4(static_cast<T*>(a.h) + r * a.ldh, h, f);
+      }
+    }
+  }
+}
+
+template <typename T, bool FP8>
+__global__ void __launch_bounds__(kActThreads, 4) gated_backward_kernel(const __grid_constant__ FfnActArgs a, int parts) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, strip = blockIdx.x;
+  const Rows in = rows_of(a.M, blockIdx.y, parts);
+  if (a.vec && (strip + 1) * kActStrip <= a.N) {
+    const Four<true> f = columns_of<true>(a, strip, lane);
+#define GP_CALL(ACT) gated_backward_rows<T, FP8, ACT>(a, in, strip, f, warp)
+    GP_ACT_SWITCH(a.act, GP_CALL)
+  } else {
+    const Four<false> f = columns_of<false>(a, strip, lane);
+    GP_ACT_SWITCH(a.act, GP_CALL)
+#undef GP_CALL
   }
 }
 
@@ -258,9 +300,9 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint16_t* src, int64_t 
 }  // namespace
 
 int64_t ffn_act_parts(int64_t M, int64_t N, int sm_count) {
-  // four blocks for each SM, and a row or two for each warp at least
+  // eight blocks for each SM (four at a time), and two rows for each warp at least
   const int64_t strips = (N + kActStrip - 1) / kActStrip, most = (M + 2 * kActWarps - 1) / (2 * kActWarps);
-  return std::max<int64_t>(1, std::min(most, (4 * sm_count + strips - 1) / strips));
+  return std::max<int64_t>(1, std::min(most, (8 * sm_count + strips - 1) / strips));
 }
 
 namespace {

@@ -1,18 +1,9 @@
-// k_ffn_gated.cu -- the ring's kernels of the gated product and of the gradients of weights, and the planner.
+// k_ffn_gated.cu -- the ring's kernels of the gated product, and the planner of all products.
 #include "ffn_ring.cuh"
 
 namespace gp {
 
-cudaError_t launch_ffn_gated(FfnProduct& p, const void** kernel) {
-  return p.plan.cta_pair ? launch_ring<256, true, true, false, false>(p, kernel)
-                         : launch_ring<128, false, true, false, false>(p, kernel);
-}
-
-// Both operands are stored summed axis (tokens) first.
-cudaError_t launch_ffn_weight_grad(FfnProduct& p, const void** kernel) {
-  return p.plan.cta_pair ? launch_ring<256, true, false, true, true>(p, kernel)
-                         : launch_ring<128, false, false, true, true>(p, kernel);
-}
+cudaError_t launch_ffn_gated(FfnProduct& p, const void** kernel) { return launch_tile<true, false, false>(p, kernel); }
 
 namespace {
 
@@ -23,8 +14,8 @@ cudaError_t pair_capacity(int* pairs) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 0 && dev < 64 && (*pairs = cached[dev].load()) > 0) return cudaSuccess;
-  using Sh = RingShape<256, true>;
-  const void* k = reinterpret_cast<const void*>(ffn_ring_kernel<256, true, true, false, false>);
+  using Sh = RingShape<256, true, kHold>;
+  const void* k = reinterpret_cast<const void*>(ffn_ring_kernel<256, true, kHold, true, false, false>);
   if ((e = ensure_smem_attr(k, Sh::SMEM)) != cudaSuccess) return e;
   RingConfig c(2, Sh::THREADS, 2, Sh::SMEM, nullptr);
   if ((e = cudaOccupancyMaxActiveClusters(pairs, k, &c.cfg)) != cudaSuccess) return e;
@@ -33,9 +24,9 @@ cudaError_t pair_capacity(int* pairs) {
   return cudaSuccess;
 }
 
-template <int BN, bool PAIR>
+template <int BN, bool PAIR, RingOut OUT>
 void ring_shape_of(gp_plan* p) {
-  using Sh = RingShape<BN, PAIR>;
+  using Sh = RingShape<BN, PAIR, OUT>;
   p->stages = Sh::STAGES;
   p->stage_bytes = Sh::STAGE;
   p->ring_bytes = Sh::STAGES * Sh::STAGE;
@@ -102,10 +93,11 @@ int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count,
     p->cta_pair = tile == 256;
     p->bm = tile;
     p->bn = gated ? tile / 2 : tile;
+    const bool hold = wide_sums;
     if (tile == 256)
-      ring_shape_of<256, true>(p);
+      hold ? ring_shape_of<256, true, kHold>(p) : ring_shape_of<256, true, kStream>(p);
     else
-      ring_shape_of<128, false>(p);
+      hold ? ring_shape_of<128, false, kHold>(p) : ring_shape_of<128, false, kStream>(p);
     const int64_t r = blocks(rows, p->bm), c = blocks(cols, p->bn);
     if (r > kFfnMaxTiles / c / problems) return GP_ERR_SIZE;
     p->tiles = r * c * problems;
