@@ -61,11 +61,13 @@ typedef enum {
 /* Options of the products.  Zero-initialise and set what you need; NULL: all zero. */
 typedef struct gp_ffn_options {
     uint64_t timeout_ns;         /* limit of every bounded wait inside the kernel (0 = 1 s) */
-    int32_t tile;                /* force the tile: 256 (256 x 256 of two CTAs), 128 (128 x 128), or 16, 32, 64 (128 rows
-                                    of the weight x so many tokens; forward calls that keep nothing in 8 bits); 0 = the
-                                    planner's choice.  Other values, and tiles that the call does not have:
-                                    GP_ERR_UNSUPPORTED */
-    int32_t no_split;            /* 1: never share a tile's K loop among CTAs */
+    int32_t tile;                /* force the tile: 256 (256 x 256 of two CTAs), 128 (128 x 128), or so many rows of the
+                                    output x 128 columns by a cluster that may share the K loop: 16, 32, 64 (gemm_gated
+                                    up to here, gemm_weight_grad from here on) or 129 (128 rows); these not where values
+                                    are kept in 8 bits.  0 = the planner's choice.  Other values, and tiles that the
+                                    call does not have: GP_ERR_UNSUPPORTED */
+    int32_t k_splits;            /* tiles of a cluster: the CTAs that share a tile's K loop, 1, 2, 4 or 8 (at most 4
+                                    with 16); 0 = the planner's choice.  Others: GP_ERR_UNSUPPORTED */
     int32_t inject_lost_load;    /* test hook: the TMA producer skips the last tile load of the problem, so a consumer
                                     wait runs out and the call reports GP_ERR_TIMEOUT (no GPU fault); not with tile 256
                                     (GP_ERR_UNSUPPORTED), and the planner does not choose that then */
@@ -157,7 +159,7 @@ int gemm_weight_grad(const gp_weight_grad* args, void* stream, const gp_ffn_opti
  * gemm_ffn_plan -- the kernel and tile that a call would choose on a device with `sms` SMs (0: the current device;
  * without one, as on 152 SMs with gp_plan.grid left 0).  op: 0 gemm_linear, 1 gemm_gated, 2 gemm_input_grad,
  * 3 gemm_weight_grad; M, N, K and count as in that call; kept: 1 where values are kept in 8 bits, or FP32 is written.
- * gp_plan.bm x bn is the tile (bm: rows of the weight where layout is 1, else tokens); k_splits CTAs, one cluster,
+ * gp_plan.bm x bn is the tile (where layout is 1, bm counts columns of the output and bn rows); k_splits CTAs, one cluster,
  * share each tile's K loop.
  */
 int gemm_ffn_plan(int op, int64_t M, int64_t N, int64_t K, int count, int kept, int sms, const gp_ffn_options* opts,

@@ -57,7 +57,8 @@ cudaError_t launch_ffn_input_grad(FfnProduct& a, const void** kernel);
 cudaError_t launch_ffn_weight_grad(FfnProduct& a, const void** kernel);
 cudaError_t launch_ffn_few(FfnProduct& a, const void** kernel);
 // Ring depth, stage bytes and shared memory of the kernel that a plan of this tile runs.
-void ffn_few_shape(gp_plan* p, int bn, bool gated);
+void ffn_few_shape(gp_plan* p, int rows, bool gated);
+int ffn_few_most_ctas(int rows);   // that may share a tile's K blocks
 
 // ---------------------------------------------------------------------------
 // element by element

@@ -9,7 +9,9 @@
 //            columns side by side: "MN major"), so that nothing is transposed in memory
 //
 // Persistent and warp-specialised:
-//   warp 0     TMA producer: one ring slot = 64 of the summed axis
+//   warps 0, 2, 3   TMA producers, each of every third ring slot (a slot is 64 of the
+//              summed axis): one thread issues a slot's loads in about 230 ns, which
+//              is longer than the products of a 128 x 128 tile's slot take
 //   warp 1     allocates TMEM and issues tcgen05.mma (kind::f16, FP32 in TMEM)
 //   warps 4+   write the outputs from one TMEM buffer while the next tile's products
 //              run into the other
@@ -31,6 +33,7 @@ namespace gp {
 
 constexpr int kRingLaunchRegs = 96;        // registers per thread at launch, where warps trade them
 constexpr int kRingMax = 8;
+constexpr int kRingProducers = 3;          // threads that issue loads
 
 struct RingBarriers {
   uint64_t full[kRingMax];
@@ -72,6 +75,7 @@ struct RingShape {
   static constexpr int FIT = (kSmemPerCtaMax - FIXED) / STAGE;
   static constexpr int STAGES = FIT < kRingMax ? FIT : kRingMax;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
+  static_assert(STAGES > kRingProducers, "a slot for each producer");
   // Sixteen warps that hold 64 sums per thread take registers for them from the other four.
   static constexpr bool SPLIT_REGS = THREADS == 640;
   static constexpr int EPI_REGS = 104, OTHER_REGS = 64;
@@ -139,6 +143,31 @@ __device__ __forceinline__ bool ring_elect_one() {
 __device__ __forceinline__ void ring_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+
+// One of the threads that issue loads: every kRingProducers-th ring slot is its own.
+struct RingProducer {
+  int which;               // 0 .. kRingProducers - 1, or -1
+  int slot;
+  uint32_t phase = 0;
+  int issued = 0, lost = -1;   // slots so far, and the one whose load the test hook skipped
+  __device__ __forceinline__ explicit RingProducer(int warp)
+      : which(warp == 0 ? 0 : (warp == 2 || warp == 3 ? warp - 1 : -1)), slot(which) {}
+  __device__ __forceinline__ void advance(int stages) {
+    ++issued;
+    if ((slot += kRingProducers) >= stages) {
+      slot -= stages;
+      phase ^= 1u;
+    }
+  }
+  // Loads still in flight land in shared memory: wait for them before exit.
+  __device__ __forceinline__ void drain(uint64_t* full, int stages, const KernelCtl& ctl) {
+    CtaCtl never_abort{0};
+    for (int i = max(0, issued - stages / kRingProducers - 1); i < issued; ++i) {
+      const int n = which + i * kRingProducers;
+      if (i != lost) mbar_wait(full + n % stages, static_cast<uint32_t>((n / stages) & 1), ctl, &never_abort, kSiteDrain);
+    }
+  }
+};
 
 // Output tile -> its row and column blocks: groups of `gp` row blocks, each
 // swept over all column blocks, so that CTAs at work at one time share operands in L2.
@@ -515,24 +544,24 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
   pdl_wait();
   const uint32_t tmem = bar->tmem_base;
   CtaCtl* cta = &bar->ctl;
-  int issued = 0, lost = -1;   // producer only: loads so far, and the one that the test hook skipped
+  RingProducer prod(warp);
 
   if (warp < 4) {
     if (Sh::SPLIT_REGS) regs_decrease<Sh::OTHER_REGS>();
-    if (warp == 0 && lane == 0) {
-      // ---------------- producer (every CTA) ----------------
+    if (warp != 1 && lane == 0) {
+      // ---------------- producers (every CTA) ----------------
       const int lose_tile = g.ctl.inject_lost_load ? tiles - 1 : -1;   // test hook: this tile's last load never comes
-      int s = 0;
-      uint32_t ph = 0;
       bool ok = true;
-      for (int tile = worker; ok && tile < tiles; tile += workers) {
+      int kb = prod.which;
+      for (int tile = worker; ok && tile < tiles; tile += workers, kb -= kt) {
         int rb, cb;
         const int problem = tile >= per_problem ? 1 : 0;
         ring_tile(tile - problem * per_problem, row_blocks, col_blocks, g.raster, rb, cb);
         const int a_row = rb * Sh::TILE_ROWS + static_cast<int>(rank) * Sh::A_ROWS;
         const int b_row = GATED ? cb * TILE_COLS : cb * BN + static_cast<int>(rank) * Sh::B_ROWS;
-        for (int kb = 0; kb < kt; ++kb) {
-          if (!mbar_wait(&bar->empty[s], ph ^ 1u, g.ctl, cta, kSiteProducerEmpty) || cta->abort) { ok = false; break; }
+        for (; kb < kt; kb += kRingProducers) {
+          const int s = prod.slot;
+          if (!mbar_wait(&bar->empty[s], prod.phase ^ 1u, g.ctl, cta, kSiteProducerEmpty) || cta->abort) { ok = false; break; }
           const int second = kb >= g.kt ? 1 : 0;      // the second source
           const int k = (kb - second * g.kt) * kFfnBK;
           const CUtensorMap* ma = &maps.a[problem | second];
@@ -558,7 +587,7 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
             }
           };
           if (tile == lose_tile && kb == kt - 1) {
-            lost = issued;
+            prod.lost = prod.issued;
           } else {
             // (the even CTA's barrier counts the bytes of both CTAs' loads)
             if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], Sh::CTAS * Sh::STAGE);
@@ -575,8 +604,7 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
               load(b_at, mb, k, b_row);
             }
           }
-          ++issued;
-          if (++s == Sh::STAGES) { s = 0; ph ^= 1u; }
+          prod.advance(Sh::STAGES);
         }
       }
     } else if (warp == 1 && rank == 0) {
@@ -729,20 +757,14 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
   }
 
   __syncthreads();
-  if (cta->abort && warp == 0 && lane == 0) {
+  if (cta->abort && prod.which >= 0 && lane == 0) {
     if (PAIR) {
       // this CTA's loads count on the even CTA's barrier: give any still in
       // flight time to land before the pair tears down
       const uint64_t t0 = global_timer_ns();
       while (global_timer_ns() - t0 < 200000ull) __nanosleep(1000);
     } else {
-      // loads still in flight land in shared memory: wait for them before exit
-      CtaCtl never_abort{0};
-      for (int i = issued > Sh::STAGES ? issued - Sh::STAGES : 0; i < issued; ++i) {
-        if (i == lost) continue;
-        mbar_wait(&bar->full[i % Sh::STAGES], static_cast<uint32_t>((i / Sh::STAGES) & 1), g.ctl, &never_abort,
-                  kSiteDrain);
-      }
+      prod.drain(bar->full, Sh::STAGES, g.ctl);
     }
   }
   if (PAIR) {

@@ -1,14 +1,17 @@
-// k_ffn_few.cu -- the forward products for few tokens: the weight fills the
-// tensor cores' M side (128 rows per CTA), the tokens their N side (16, 32 or
-// 64), and a cluster of 1 to 8 CTAs shares a tile's K blocks.
+// k_ffn_few.cu -- the products of small problems: for few tokens, and where the
+// ring's tiles would leave SMs idle.  The operand whose rows are the output's
+// columns (a weight, or x in a weight's gradient) fills the tensor cores' M side,
+// 128 rows per CTA, the other one their N side (16, 32 or 64 rows), and a cluster
+// of 1 to 8 CTAs shares a tile's K blocks.
 //
-//   s[n][m] = sum over k of w[n][k] * x[m][k]
-//   linear: out = act(s + bias) + addend;  gated: out = act(g) * u, with a second weight and sums u
+//   s[c][r] = sum over k of p[c][k] * q[r][k];  then as in ffn_ring.cuh
 //
-// The sums of a cluster meet in distributed shared memory: each CTA is handed
-// its share of the token columns by all, adds them in K order and writes them.
-// What bounds it: the weights' bytes, and for one token the launch, the first
-// loads and the exchange.
+// The sums of a cluster meet in distributed shared memory: each CTA is handed its
+// share of q's rows by all, adds them in K order and writes them, neighbouring
+// lanes along a row of the output.
+// What bounds it: for few tokens the weight's bytes (1 x 8192 x 4096 twice, gated:
+// 134 MB in 17.8 us from the first load to the last), and for one token and a
+// small weight the launch, the first loads and the exchange: 3.5 of 9 us.
 #include "ffn_ring.cuh"
 
 namespace gp {
@@ -17,7 +20,6 @@ namespace {
 constexpr int kFewThreads = 384;
 constexpr int kFewAddThreads = 256;      // eight warps: 32 rows of the weight x half of the tokens each
 constexpr int kFewMaxRing = 12;
-constexpr int kFewXRow = 129;            // floats per column of the exchange: keeps either walk off each other's banks
 
 struct FewBarriers {
   uint64_t full[kFewMaxRing];
@@ -31,34 +33,39 @@ struct FewBarriers {
 constexpr int kFewBarrierBytes = 256;
 static_assert(sizeof(FewBarriers) <= kFewBarrierBytes, "barrier region too small");
 
+constexpr int kFewRow = 128 + 4;         // floats of a row of the exchange: rows begin on other banks
+
 template <int BN, bool GATED>
 struct FewShape {
   static constexpr int PARTS = GATED ? 2 : 1;
-  static constexpr int W_BYTES = 128 * kFfnBK * 2;
-  static constexpr int STAGE = PARTS * W_BYTES + BN * kFfnBK * 2;
+  static constexpr int P_BYTES = 128 * kFfnBK * 2;
+  static constexpr int STAGE = PARTS * P_BYTES + BN * kFfnBK * 2;
   static constexpr int FIXED = kFewBarrierBytes + kSmemAlignSlack;
   static constexpr int FIT = (kSmemPerCtaMax - FIXED) / STAGE;
   static constexpr int STAGES = FIT < kFewMaxRing ? FIT : kFewMaxRing;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
   static constexpr uint32_t TMEM_COLS = 2 * PARTS * BN;
   static constexpr int HALF = BN / 2;
-  static_assert(PARTS * BN * kFewXRow * 4 <= STAGES * STAGE, "the exchange takes the ring's memory");
+  // The exchange: for each CTA of the cluster its sums of the rows of q that are this one's share, kFewRow floats each.
+  static_assert(PARTS * BN * kFewRow * 4 <= STAGES * STAGE, "the exchange takes the ring's memory");
   static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS >= 32 && TMEM_COLS <= 512, "TMEM columns");
 };
 
 struct FewParams {
   FfnOut o;
-  int32_t tokens, n;         // rows and columns of the output
-  int32_t kt;
+  int32_t rows, cols;        // of the output
+  int32_t kt;                // K blocks of one source
+  int32_t sources, problems;
   int32_t restart;
   int32_t k_log;             // log2 of the CTAs that share a tile's K blocks
-  int32_t token_blocks;
+  int32_t row_blocks, per_problem;
   uint32_t idesc;
+  int32_t p_planes, q_planes;  // an MN-major operand's 128 rows come as one box of two planes of 64
   KernelCtl ctl;
 };
 
 struct FewMaps {
-  CUtensorMap x, w[2];
+  CUtensorMap q[2], p[2];
 };
 
 __device__ __forceinline__ void tmem_ld_few(uint32_t taddr, uint32_t (&r)[8]) {
@@ -68,51 +75,129 @@ __device__ __forceinline__ void tmem_ld_few(uint32_t taddr, uint32_t (&r)[8]) {
                : "memory");
 }
 
-__device__ __forceinline__ void st_cluster_float(uint32_t cluster_addr, float v) {
+__device__ __forceinline__ void st_shared_f1(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_f1(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 __device__ __forceinline__ void st_cluster_int(uint32_t cluster_addr, int v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
-// The tokens col0 .. of a tile from the exchanged sums of `ctas` CTAs.
+// Eight neighbouring values of a row in 16 bits or FP32, `n` of which exist (8 or less).
+template <typename T>
+__device__ __forceinline__ void load_eight(T (&t)[8], const T* p, int n, bool vec) {
+  if (vec && n >= 8) {
+    uint4 w[sizeof(T) / 2];
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    memcpy(t, w, sizeof(t));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    from_f32(0.f, t[i]);
+    if (i < n) t[i] = p[i];
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_eight(T* p, const float (&v)[8], int n, bool vec) {
+  T t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) from_f32(v[i], t[i]);
+  if (vec && n >= 8) {
+    uint4 w[sizeof(T) / 2];
+    memcpy(w, t, sizeof(t));
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) p[i] = t[i];
+}
+
+__device__ __forceinline__ void add_eight(float (&v)[8], const float* from) {
+  const float4 x = reinterpret_cast<const float4*>(from)[0], y = reinterpret_cast<const float4*>(from)[1];
+  v[0] += x.x;
+  v[1] += x.y;
+  v[2] += x.z;
+  v[3] += x.w;
+  v[4] += y.x;
+  v[5] += y.y;
+  v[6] += y.z;
+  v[7] += y.w;
+}
+
+// The `per` output rows from row0 on, 128 columns from col0 on, of the exchanged sums of `ctas` CTAs: sixteen threads to a
+// row, eight columns each.
 template <int BN, bool GATED, typename T, typename O>
-__device__ __forceinline__ void finish_few(const FewParams& g, const float* buf, int t, int ctas, int per, int64_t n0,
-                                           int64_t m0) {
+__device__ __forceinline__ void finish_few(const FewParams& g, int problem, const float* buf, int t, int ctas, int per,
+                                           int64_t row0, int64_t col0) {
   const FfnOut& o = g.o;
-  const O* const add = static_cast<const O*>(o.add[0]);
-  O* const out = static_cast<O*>(o.out[0]);
+  const O* const add = static_cast<const O*>(o.add[problem]);
+  O* const out = static_cast<O*>(o.out[problem]);
   T* const keep0 = static_cast<T*>(o.keep[0]);
   T* const keep1 = static_cast<T*>(o.keep[1]);
-  const int row = t & 127;
-  const int64_t n = n0 + row;
-  if (n >= g.n) return;
-  float bias = 0.f;
-  if (!GATED && o.bias) bias = o.bias_f32 ? static_cast<const float*>(o.bias)[n] : to_f32(static_cast<const T*>(o.bias)[n]);
-#pragma unroll 2
-  for (int c = t >> 7; c < per; c += kFewAddThreads / 128) {
-    const int64_t m = m0 + c;
-    if (m >= g.tokens) return;
-    float v[1] = {0.f}, u = 0.f;
-    O was;
-    if (!GATED && add) was = add[m * o.ld_add[0] + n];
-    for (int s = 0; s < ctas; ++s) {   // in K order
-      v[0] += buf[(s * per + c) * kFewXRow + row];
-      if (GATED) u += buf[(BN + s * per + c) * kFewXRow + row];
+  const int lane = t & 15;
+  const int64_t c = col0 + 8 * lane;
+  const int n = g.cols - c < 8 ? static_cast<int>(g.cols - c) : 8;
+  if (n <= 0) return;
+  const bool vec = o.vec != 0;
+  float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (!GATED && o.bias) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) bias[i] = o.bias_f32 ? static_cast<const float*>(o.bias)[c + i] : to_f32(static_cast<const T*>(o.bias)[c + i]);
+  }
+  const int64_t left = g.rows - row0;
+  const int rows = left < per ? static_cast<int>(left) : per;      // (may be < 0)
+  constexpr int STEP = kFewAddThreads / 16;
+  const float* const mine = buf + 8 * lane;
+  // Short code, run a few times: an instruction that runs once costs more to fetch than the loop does (four rows
+  // unrolled: 1000 x 776 x 2056 15.5 us).  The next row's addend is under way meanwhile.
+  O was[8];
+  const int i0 = t >> 4;
+  if (!GATED && add && i0 < rows) load_eight(was, add + (row0 + i0) * o.ld_add[problem] + c, n, vec);
+#pragma unroll 1
+  for (int i = i0; i < rows; i += STEP) {
+    O next[8];
+    if (!GATED && add && i + STEP < rows) load_eight(next, add + (row0 + i + STEP) * o.ld_add[problem] + c, n, vec);
+    float v[8], u[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[k] = 0.f;
+      u[k] = 0.f;
     }
-    v[0] += bias;
+#pragma unroll 1
+    for (int s = 0; s < ctas; ++s) {   // in K order
+      add_eight(v, mine + (s * per + i) * kFewRow);
+      if (GATED) add_eight(u, mine + (BN + s * per + i) * kFewRow);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += bias[k];
     if (keep0) {
-      from_f32(v[0], keep0[m * o.ld_keep[0] + n]);
-      if (GATED) from_f32(u, keep1[m * o.ld_keep[1] + n]);
+      store_eight(keep0 + (row0 + i) * o.ld_keep[0] + c, v, n, vec);
+      if (GATED) store_eight(keep1 + (row0 + i) * o.ld_keep[1] + c, u, n, vec);
     }
     activate_all(v, o.act);
-    if (GATED) v[0] *= u;
-    if (!GATED && add) v[0] += to_f32(was);
-    from_f32(v[0], out[m * o.ld_out[0] + n]);
+    if (GATED) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= u[k];
+    } else if (add) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] += to_f32(was[k]);
+        was[k] = next[k];
+      }
+    }
+    store_eight(out + (row0 + i) * o.ld_out[problem] + c, v, n, vec);
   }
 }
 
-template <int BN, bool GATED>
+// P_MN, Q_MN: the operand is stored summed axis first.
+template <int BN, bool GATED, bool P_MN, bool Q_MN>
 __global__ void __launch_bounds__(kFewThreads, 1)
     ffn_few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewParams g) {
   using Sh = FewShape<BN, GATED>;
@@ -124,10 +209,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int ctas = 1 << g.k_log;
   const uint32_t rank = ctas > 1 ? cluster_ctarank() : 0u;
   const int tile = static_cast<int>(blockIdx.x) >> g.k_log;
-  // token blocks of one weight block side by side: its rows are read from L2 after the first
-  const int wb = tile / g.token_blocks, mb = tile - wb * g.token_blocks;
-  const int k0 = static_cast<int>((static_cast<int64_t>(g.kt) * rank) >> g.k_log);
-  const int k1 = static_cast<int>((static_cast<int64_t>(g.kt) * (rank + 1)) >> g.k_log);
+  // row blocks of one column block side by side: p's rows are read from L2 after the first
+  const int problem = tile >= g.per_problem ? 1 : 0, in = tile - problem * g.per_problem;
+  const int pb = in / g.row_blocks, qb = in - pb * g.row_blocks;
+  const int kt = g.kt * g.sources;
+  const int k0 = static_cast<int>((static_cast<int64_t>(kt) * rank) >> g.k_log);
+  const int k1 = static_cast<int>((static_cast<int64_t>(kt) * (rank + 1)) >> g.k_log);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Sh::STAGES; ++s) {
@@ -152,37 +239,53 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   pdl_launch_dependents();
   // While the work before this kernel finishes, its first boxes come into L2:
   // a prefetch writes nothing, and L2 stays coherent with what is still written.
-  if (warp == 0 && lane == 0) {
+  if (!P_MN && warp == 0 && lane == 0) {
     for (int kb = k0; kb < k1 && kb < k0 + Sh::STAGES; ++kb) {
-      tma_prefetch_l2_2d(&maps.w[0], kb * kFfnBK, wb * 128);
-      if (GATED) tma_prefetch_l2_2d(&maps.w[1], kb * kFfnBK, wb * 128);
-      tma_prefetch_l2_2d(&maps.x, kb * kFfnBK, mb * BN);
+      tma_prefetch_l2_2d(&maps.p[0], kb * kFfnBK, pb * 128);
+      if (GATED) tma_prefetch_l2_2d(&maps.p[1], kb * kFfnBK, pb * 128);
+      tma_prefetch_l2_2d(&maps.q[0], kb * kFfnBK, qb * BN);
     }
   }
   pdl_wait();
   const uint32_t tmem = bar->tmem_base;
   CtaCtl* cta = &bar->ctl;
-  int issued = 0, lost = -1;
+  RingProducer prod(warp);
 
   if (warp < 4) {
-    if (warp == 0 && lane == 0) {
-      // ---------------- producer ----------------
+    if (warp != 1 && lane == 0) {
+      // ---------------- producers ----------------
       const bool lose = g.ctl.inject_lost_load && tile == static_cast<int>(gridDim.x >> g.k_log) - 1;
-      int s = 0;
-      uint32_t ph = 0;
-      for (int kb = k0; kb < k1; ++kb) {
-        if (!mbar_wait(&bar->empty[s], ph ^ 1u, g.ctl, cta, kSiteProducerEmpty) || cta->abort) break;
+      for (int kb = k0 + prod.which; kb < k1; kb += kRingProducers) {
+        const int s = prod.slot;
+        if (!mbar_wait(&bar->empty[s], prod.phase ^ 1u, g.ctl, cta, kSiteProducerEmpty) || cta->abort) break;
         const uint32_t at = smem_u32(ring + s * Sh::STAGE);
-        if (lose && kb == g.kt - 1) {   // test hook: this load never comes
-          lost = issued;
+        if (lose && kb == kt - 1) {   // test hook: this load never comes
+          prod.lost = prod.issued;
         } else {
+          const int second = kb >= g.kt ? 1 : 0, k = (kb - second * g.kt) * kFfnBK;
+          const CUtensorMap* mp = &maps.p[second];
+          const CUtensorMap* mq = &maps.q[problem | second];
           mbar_arrive_expect_tx(&bar->full[s], Sh::STAGE);
-          tma_load_2d(at, &maps.w[0], &bar->full[s], kb * kFfnBK, wb * 128);
-          if (GATED) tma_load_2d(at + Sh::W_BYTES, &maps.w[1], &bar->full[s], kb * kFfnBK, wb * 128);
-          tma_load_2d(at + Sh::PARTS * Sh::W_BYTES, &maps.x, &bar->full[s], kb * kFfnBK, mb * BN);
+          if (!P_MN) {
+            tma_load_2d(at, mp, &bar->full[s], k, pb * 128);
+            if (GATED) tma_load_2d(at + Sh::P_BYTES, &maps.p[1], &bar->full[s], k, pb * 128);
+          } else if (g.p_planes) {
+            tma_load_3d(at, mp, &bar->full[s], 0, k, pb * 2);
+          } else {
+            tma_load_2d(at, mp, &bar->full[s], pb * 128, k);
+            tma_load_2d(at + 8192, mp, &bar->full[s], pb * 128 + 64, k);
+          }
+          const uint32_t q_at = at + Sh::PARTS * Sh::P_BYTES;
+          if (!Q_MN) {
+            tma_load_2d(q_at, mq, &bar->full[s], k, qb * BN);
+          } else if (BN == 128 && g.q_planes) {
+            tma_load_3d(q_at, mq, &bar->full[s], 0, k, qb * 2);
+          } else {
+            tma_load_2d(q_at, mq, &bar->full[s], qb * BN, k);
+            if (BN == 128) tma_load_2d(q_at + 8192, mq, &bar->full[s], qb * BN + 64, k);
+          }
         }
-        ++issued;
-        if (++s == Sh::STAGES) { s = 0; ph ^= 1u; }
+        prod.advance(Sh::STAGES);
       }
     } else if (warp == 1) {
       // ---------------- MMA issuer ----------------
@@ -190,7 +293,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       uint32_t ph = 0, aph = 0;
       bool ok = true;
       const bool leader = ring_elect_one();
-      const uint64_t desc0 = umma_desc_sw128(smem_u32(ring));
+      const uint32_t ring0 = smem_u32(ring);
+      const uint64_t p0 = P_MN ? umma_desc_mn(ring0) : umma_desc_sw128(ring0);
+      const uint64_t q0 = (Q_MN ? umma_desc_mn(ring0) : umma_desc_sw128(ring0)) + Sh::PARTS * Sh::P_BYTES / 16;
+      constexpr uint32_t P_STEP = P_MN ? 128 : 2, Q_STEP = Q_MN ? 128 : 2;   // 16 along K, as in the ring
       for (int kc = k0; ok && kc < k1; kc += g.restart) {
         const int end = min(kc + g.restart, k1);
         if (!__all_sync(0xffffffffu, mbar_wait(&bar->acc_empty[a], aph ^ 1u, g.ctl, cta, kSiteMmaAccEmpty))) break;
@@ -199,14 +305,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int kb = kc; kb < end; ++kb) {
           const bool there = mbar_wait(&bar->full[s], ph, g.ctl, cta, kSiteConsumerFull);
           tc_fence_after();
-          const uint64_t dw = desc0 + static_cast<uint32_t>(s * Sh::STAGE) / 16;
-          const uint64_t dx = dw + Sh::PARTS * Sh::W_BYTES / 16;
-          if (leader && there) {
+          const uint64_t dp = p0 + static_cast<uint32_t>(s * Sh::STAGE) / 16;
+          const uint64_t dq = q0 + static_cast<uint32_t>(s * Sh::STAGE) / 16;
+          if (leader && there) {   // (nothing of a slot that never came)
 #pragma unroll
             for (int kk = 0; kk < kFfnBK / 16; ++kk) {
               const uint32_t more = kb > kc || kk > 0;
-              umma_f16(d, dw + 2 * kk, dx + 2 * kk, g.idesc, more);
-              if (GATED) umma_f16(d + BN, dw + Sh::W_BYTES / 16 + 2 * kk, dx + 2 * kk, g.idesc, more);
+              umma_f16(d, dp + P_STEP * kk, dq + Q_STEP * kk, g.idesc, more);
+              if (GATED) umma_f16(d + BN, dp + Sh::P_BYTES / 16 + P_STEP * kk, dq + Q_STEP * kk, g.idesc, more);
             }
             umma_commit(&bar->empty[s]);
           }
@@ -244,6 +350,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     for (int p = 0; p < Sh::PARTS; ++p)
 #pragma unroll
       for (int i = 0; i < Sh::HALF; ++i) acc[p][i] = 0.f;
+    if (!GATED && g.o.add[problem]) {
+      // this CTA's part of the addend comes into L2 while the products run: a thread takes half of a row's 128 columns
+      const int size = g.o.out_f32 ? 4 : 2, t = threadIdx.x - 128, per = BN >> g.k_log;
+      const int64_t r = static_cast<int64_t>(qb) * BN + rank * per + (t >> 1), c = static_cast<int64_t>(pb) * 128 + (t & 1) * 64;
+      if ((t >> 1) < per && r < g.rows && c < g.cols) {
+        const uint8_t* at = static_cast<const uint8_t*>(g.o.add[problem]) + (r * g.o.ld_add[problem] + c) * size;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+        if (size == 4 && c + 32 < g.cols) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128));
+      }
+    }
     int a = 0;
     uint32_t aph = 0;
     bool ok = true;
@@ -276,18 +392,21 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       cluster_sync();
     else
       asm volatile("bar.sync 1, %0;" ::"n"(kFewAddThreads) : "memory");
-    const int per = BN >> g.k_log;    // token columns per CTA
-    const uint32_t at = smem_u32(ring) + (rank * per * kFewXRow + row) * 4;
+    const int per = BN >> g.k_log;    // of q's rows per CTA
+    const uint32_t at = smem_u32(ring) + (static_cast<int>(rank) * per * kFewRow + row) * 4;
+    const int there = g.rows - qb * BN;   // of q's rows
+    // 32 lanes' sums of one of q's rows lie side by side
 #pragma unroll
     for (int p = 0; p < Sh::PARTS; ++p) {
 #pragma unroll
       for (int i = 0; i < Sh::HALF; ++i) {
         const int col = half * Sh::HALF + i;
-        const uint32_t here = at + (p * BN + (col & (per - 1))) * (kFewXRow * 4);
+        if (col >= there) break;
+        const uint32_t here = at + (p * BN + (col & (per - 1))) * (kFewRow * 4);
         if (ctas > 1)
-          st_cluster_float(mapa_shared(here, static_cast<uint32_t>(col / per)), acc[p][i]);
+          st_cluster_f1(mapa_shared(here, static_cast<uint32_t>(col / per)), acc[p][i]);
         else
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(here), "f"(acc[p][i]) : "memory");
+          st_shared_f1(here, acc[p][i]);
       }
     }
     if (ctas > 1)
@@ -297,30 +416,23 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (ok && !cta->abort) {
       const float* buf = reinterpret_cast<const float*>(ring);
       const int t = threadIdx.x - 128;
-      const int64_t n0 = static_cast<int64_t>(wb) * 128, m0 = static_cast<int64_t>(mb) * BN + rank * per;
+      const int64_t col0 = static_cast<int64_t>(pb) * 128, row0 = static_cast<int64_t>(qb) * BN + rank * per;
       if (g.o.bf16) {
         if (!GATED && g.o.out_f32)
-          finish_few<BN, GATED, __nv_bfloat16, float>(g, buf, t, ctas, per, n0, m0);
+          finish_few<BN, GATED, __nv_bfloat16, float>(g, problem, buf, t, ctas, per, row0, col0);
         else
-          finish_few<BN, GATED, __nv_bfloat16, __nv_bfloat16>(g, buf, t, ctas, per, n0, m0);
+          finish_few<BN, GATED, __nv_bfloat16, __nv_bfloat16>(g, problem, buf, t, ctas, per, row0, col0);
       } else {
         if (!GATED && g.o.out_f32)
-          finish_few<BN, GATED, __half, float>(g, buf, t, ctas, per, n0, m0);
+          finish_few<BN, GATED, __half, float>(g, problem, buf, t, ctas, per, row0, col0);
         else
-          finish_few<BN, GATED, __half, __half>(g, buf, t, ctas, per, n0, m0);
+          finish_few<BN, GATED, __half, __half>(g, problem, buf, t, ctas, per, row0, col0);
       }
     }
   }
 
   __syncthreads();
-  if (cta->abort && warp == 0 && lane == 0) {
-    // loads still in flight land in shared memory: wait for them before exit
-    CtaCtl never_abort{0};
-    for (int i = issued > Sh::STAGES ? issued - Sh::STAGES : 0; i < issued; ++i) {
-      if (i == lost) continue;
-      mbar_wait(&bar->full[i % Sh::STAGES], static_cast<uint32_t>((i / Sh::STAGES) & 1), g.ctl, &never_abort, kSiteDrain);
-    }
-  }
+  if (cta->abort && prod.which >= 0 && lane == 0) prod.drain(bar->full, Sh::STAGES, g.ctl);
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -328,27 +440,41 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
 }
 
-template <int BN, bool GATED>
+template <int BN, bool GATED, bool P_MN, bool Q_MN>
 cudaError_t launch_as(FfnProduct& p, const void** kernel) {
   using Sh = FewShape<BN, GATED>;
-  auto k = ffn_few_kernel<BN, GATED>;
+  static_assert(!Q_MN || BN >= 64, "a row of an MN-major box is 64 of the operand's rows");
+  auto k = ffn_few_kernel<BN, GATED, P_MN, Q_MN>;
   *kernel = reinterpret_cast<const void*>(k);
+  const bool sum = p.op == kFfnInputGrad && p.count == 2, both = p.op == kFfnWeightGrad && p.count == 2;
   FewMaps maps = {};
   cudaError_t e;
   if (p.summed > 0) {
-    if ((e = ffn_map(&maps.x, p, p.a[0], p.lda[0], p.rows, false, BN)) != cudaSuccess) return e;
-    if ((e = ffn_map(&maps.w[0], p, p.b[0], p.ldb[0], p.cols, false, 128)) != cudaSuccess) return e;
-    if (GATED && (e = ffn_map(&maps.w[1], p, p.b[1], p.ldb[1], p.cols, false, 128)) != cudaSuccess) return e;
+    // (64 rows are one plane of the MN-major form, 128 as the ring has them)
+    auto q_map = [&](int i) {
+      return Q_MN && BN == 64 ? make_tmap_2d(&maps.q[i], p.a[i], ffn_map_type(p.out), p.rows, p.summed, static_cast<uint64_t>(p.lda[i]) * 2,
+                                 64, kFfnBK, CU_TENSOR_MAP_SWIZZLE_128B)
+                  : ffn_map(&maps.q[i], p, p.a[i], p.lda[i], p.rows, Q_MN, BN);
+    };
+    if ((e = q_map(0)) != cudaSuccess) return e;
+    if ((e = ffn_map(&maps.p[0], p, p.b[0], p.ldb[0], p.cols, P_MN, 128)) != cudaSuccess) return e;
+    if ((sum || both) && (e = q_map(1)) != cudaSuccess) return e;
+    if ((sum || GATED) && (e = ffn_map(&maps.p[1], p, p.b[1], p.ldb[1], p.cols, P_MN, 128)) != cudaSuccess) return e;
   }
   FewParams g = {};
   g.o = p.out;
-  g.tokens = static_cast<int32_t>(p.rows);
-  g.n = static_cast<int32_t>(p.cols);
+  g.rows = static_cast<int32_t>(p.rows);
+  g.cols = static_cast<int32_t>(p.cols);
   g.kt = static_cast<int32_t>((p.summed + kFfnBK - 1) / kFfnBK);
-  g.restart = p.out.out_f32 ? kFfnRestart : (g.kt > 0 ? g.kt : 1);
+  g.sources = sum ? 2 : 1;
+  g.problems = both ? 2 : 1;
+  g.restart = p.out.out_f32 ? kFfnRestart : (g.kt > 0 ? g.kt * g.sources : 1);
   g.k_log = p.plan.k_splits == 8 ? 3 : (p.plan.k_splits == 4 ? 2 : (p.plan.k_splits == 2 ? 1 : 0));
-  g.token_blocks = (g.tokens + BN - 1) / BN;
-  g.idesc = umma_idesc_f16(p.out.bf16 != 0, 128, BN);
+  g.row_blocks = (g.rows + BN - 1) / BN;
+  g.per_problem = g.row_blocks * ((g.cols + 127) / 128);
+  g.idesc = umma_idesc_f16(p.out.bf16 != 0, 128, BN) | (P_MN ? kIdescAMn : 0u) | (Q_MN ? kIdescBMn : 0u);
+  g.p_planes = P_MN && p.cols % 64 == 0;
+  g.q_planes = Q_MN && BN == 128 && p.rows % 64 == 0;
   g.ctl = p.ctl;
   if ((e = ensure_smem_attr(*kernel, Sh::SMEM)) != cudaSuccess) return e;
   RingConfig c(p.plan.grid, kFewThreads, p.plan.k_splits, Sh::SMEM, p.stream);
@@ -368,19 +494,40 @@ void shape_of(gp_plan* p) {
 
 }  // namespace
 
-void ffn_few_shape(gp_plan* p, int bn, bool gated) {
-  if (gated)
-    bn == 16 ? shape_of<16, true>(p) : bn == 32 ? shape_of<32, true>(p) : shape_of<64, true>(p);
-  else
-    bn == 16 ? shape_of<16, false>(p) : bn == 32 ? shape_of<32, false>(p) : shape_of<64, false>(p);
+int ffn_few_most_ctas(int rows) { return rows == 16 ? 4 : 8; }
+
+void ffn_few_shape(gp_plan* p, int rows, bool gated) {
+  switch (rows) {
+    case 16: return gated ? shape_of<16, true>(p) : shape_of<16, false>(p);
+    case 32: return gated ? shape_of<32, true>(p) : shape_of<32, false>(p);
+    case 64: return gated ? shape_of<64, true>(p) : shape_of<64, false>(p);
+    default: return shape_of<128, false>(p);
+  }
 }
 
-cudaError_t launch_ffn_few(FfnProduct& p, const void** kernel) {
-  const bool gated = p.op == kFfnGated;
+namespace {
+
+template <bool P_MN>
+cudaError_t launch_rows(FfnProduct& p, const void** kernel) {
   switch (p.plan.bn) {
-    case 16: return gated ? launch_as<16, true>(p, kernel) : launch_as<16, false>(p, kernel);
-    case 32: return gated ? launch_as<32, true>(p, kernel) : launch_as<32, false>(p, kernel);
-    default: return gated ? launch_as<64, true>(p, kernel) : launch_as<64, false>(p, kernel);
+    case 16: return launch_as<16, false, P_MN, false>(p, kernel);
+    case 32: return launch_as<32, false, P_MN, false>(p, kernel);
+    case 64: return launch_as<64, false, P_MN, false>(p, kernel);
+    default: return launch_as<128, false, P_MN, false>(p, kernel);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_ffn_few(FfnProduct& p, const void** kernel) {
+  switch (p.op) {
+    case kFfnLinear: return launch_rows<false>(p, kernel);
+    case kFfnInputGrad: return launch_rows<true>(p, kernel);
+    case kFfnGated:
+      return p.plan.bn == 16   ? launch_as<16, true, false, false>(p, kernel)
+             : p.plan.bn == 32 ? launch_as<32, true, false, false>(p, kernel)
+                               : launch_as<64, true, false, false>(p, kernel);
+    default: return p.plan.bn == 64 ? launch_as<64, false, true, true>(p, kernel) : launch_as<128, false, true, true>(p, kernel);
   }
 }
 

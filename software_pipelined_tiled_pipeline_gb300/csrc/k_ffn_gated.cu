@@ -1,4 +1,5 @@
 // k_ffn_gated.cu -- the ring's kernels of the gated product, and the planner of all products.
+#include <initializer_list>
 #include "ffn_ring.cuh"
 
 namespace gp {
@@ -43,47 +44,69 @@ int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count,
                   const gp_ffn_options* opts, gp_plan* p) {
   std::memset(p, 0, sizeof(*p));
   const int want = opts ? opts->tile : 0;
-  if (want != 0 && want != 16 && want != 32 && want != 64 && want != 128 && want != 256) return GP_ERR_UNSUPPORTED;
-  const bool forward = op == kFfnLinear || op == kFfnGated, gated = op == kFfnGated;
+  constexpr int kSplit128 = 129;   // 128 x 128 by a cluster; 128: by the ring
+  bool known = false;
+  for (int t : {0, 16, 32, 64, 128, kSplit128, 256}) known |= want == t;
+  if (!known) return GP_ERR_UNSUPPORTED;
+  const bool gated = op == kFfnGated;
   const bool lose = opts && opts->inject_lost_load;
   const int have = sms > 0 ? sms : 152;
-  const bool can_pair = have >= 2 && !lose, can_one = !(gated && codes), can_few = forward && !codes;
+  const bool can_pair = have >= 2 && !lose, can_one = !(gated && codes), can_few = !codes;
   const int64_t kt = blocks(summed, kFfnBK) * (op == kFfnInputGrad ? count : 1);
   const int64_t problems = op == kFfnWeightGrad ? count : 1;
+  auto few_tiles = [&](int bn) { return problems * blocks(cols, 128) * blocks(rows, bn); };
+  const int want_splits = opts ? opts->k_splits : 0;
+  if (want_splits != 0 && want_splits != 1 && want_splits != 2 && want_splits != 4 && want_splits != 8) return GP_ERR_UNSUPPORTED;
+  // CTAs that share a tile's K blocks: as many as the SMs take at once, with four K blocks each at least
+  auto few_ctas = [&](int bn) {
+    if (want_splits) return want_splits;
+    int c = 1;
+    while (c < ffn_few_most_ctas(bn) && few_tiles(bn) * c * 2 <= have && kt >= 4 * c * 2) c *= 2;
+    return c;
+  };
   int tile = want;
   if (tile == 0) {
-    if (can_few && rows <= 128) {
-      tile = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
-    } else if (!can_one) {
-      tile = 256;
-    } else if (!can_pair) {
-      tile = 128;
-    } else {
-      // K blocks one after another on the busiest SM, times what one takes there
-      const int64_t pairs = problems * blocks(rows, 256) * blocks(cols, gated ? 128 : 256);
-      const int64_t ones = problems * blocks(rows, 128) * blocks(cols, gated ? 64 : 128);
-      const int64_t pair_time = blocks(pairs, have / 2) * (kt * 520 + 3000), one_time = blocks(ones, have) * (kt * 300 + 2500);
-      tile = pair_time <= one_time ? 256 : 128;
+    // Estimates in ns: K blocks one after another on the busiest SM, and the rest of a call.
+    double best = 0;
+    auto take = [&](int t, double ns) {
+      if (tile == 0 || ns < best) {
+        tile = t;
+        best = ns;
+      }
+    };
+    if (can_few) {
+      for (int bn = op == kFfnWeightGrad ? 64 : 16; bn <= (gated ? 64 : 128); bn *= 2) {
+        const int64_t t = few_tiles(bn);
+        const int c = few_ctas(bn);
+        take(bn == 128 ? kSplit128 : bn, static_cast<double>(blocks(t * c, have)) * (blocks(kt, c) * (gated ? 300 : 200) + 2500 + bn * 25) + (c > 1 ? 1500 : 0));
+      }
     }
+    const int64_t pairs = problems * blocks(rows, 256) * blocks(cols, gated ? 128 : 256);
+    const int64_t ones = problems * blocks(rows, 128) * blocks(cols, gated ? 64 : 128);
+    if (can_one) take(128, static_cast<double>(blocks(ones, have)) * kt * 260 + 6000);
+    if (can_pair) take(256, static_cast<double>(blocks(pairs, have / 2)) * kt * 280 + 8000);
+    if (tile == 0) return GP_ERR_UNSUPPORTED;   // (kept in 8 bits on one SM: a pair of CTAs does not fit)
   }
-  if ((tile == 256 && !can_pair) || (tile == 128 && !can_one) || (tile < 128 && !can_few)) return GP_ERR_UNSUPPORTED;
+  const bool few = tile < 128 || tile == kSplit128;
+  if ((tile == 256 && !can_pair) || (tile == 128 && !can_one) || (few && !can_few) || (tile < 64 && op == kFfnWeightGrad) ||
+      (tile == kSplit128 && gated))
+    return GP_ERR_UNSUPPORTED;
   p->dtype = GP_PLAN_FFN;
   p->variant = GP_PIPELINED;
   p->bk = kFfnBK;
   p->k_tiles = kt;
   p->k_splits = 1;
   p->raster_gm = 8;
-  if (tile < 128) {
+  if (few) {
+    if (tile == kSplit128) tile = 128;
     p->kernel = gated ? "ffn_few_gated" : "ffn_few";
     p->layout = 1;
     p->bm = 128;
     p->bn = tile;
     ffn_few_shape(p, tile, gated);
-    p->tiles = blocks(cols, 128) * blocks(rows, tile);
-    // CTAs that share a tile's K blocks: as many as the SMs take at once, with four K blocks each at least
-    int c = 1;
-    if (!(opts && opts->no_split))
-      while (c < 8 && p->tiles * c * 2 <= have && kt >= 4 * c * 2) c *= 2;
+    p->tiles = few_tiles(tile);
+    const int c = few_ctas(tile);
+    if (c > ffn_few_most_ctas(tile)) return GP_ERR_UNSUPPORTED;
     p->k_splits = c;
     if (p->tiles > kFfnMaxTiles / 8) return GP_ERR_SIZE;
     p->grid = sms > 0 ? static_cast<int32_t>(p->tiles * c) : 0;

@@ -39,9 +39,9 @@ _gated_backward = struct.Struct("3P48s48s3P8q2i").pack
 _codes = struct.Struct("PPqqqii").pack
 
 
-def _options(tile, no_split, timeout_ns, inject_lost_load):
-    if tile or no_split or timeout_ns or inject_lost_load:
-        return GpFfnOptions(int(timeout_ns), int(tile), int(no_split), int(inject_lost_load))
+def _options(tile, k_splits, timeout_ns, inject_lost_load):
+    if tile or k_splits or timeout_ns or inject_lost_load:
+        return GpFfnOptions(int(timeout_ns), int(tile), int(k_splits), int(inject_lost_load))
     return None
 
 
@@ -131,7 +131,7 @@ def _kept(kept, weights, rows, cols, dtype, device):
 
 
 def linear(x, weight, bias=None, *, activation=None, residual=None, keep=None, out=None, out_dtype=None, stream=None,
-           tile=0, no_split=False, timeout_ns=0, inject_lost_load=False):
+           tile=0, k_splits=0, timeout_ns=0, inject_lost_load=False):
     """y = act(x W^T + bias) + residual, rounded once.  x: M x K, weight: N x K, float16 or bfloat16.
 
     ``activation``: None, "relu", "gelu", "gelu_tanh", "silu" or "sigmoid".
@@ -139,7 +139,7 @@ def linear(x, weight, bias=None, *, activation=None, residual=None, keep=None, o
     output's type; it may be ``out`` itself.  ``out``: where to write;
     ``out_dtype``: x's type or float32.  ``keep``: "real" or "fp8" also returns
     the values before the activation, as ``kept`` of ``linear_backward``: (z,)
-    in x's type, or (codes, scales).  ``tile``, ``no_split``, ``timeout_ns``,
+    in x's type, or (codes, scales).  ``tile``, ``k_splits``, ``timeout_ns``,
     ``inject_lost_load``: see gp_ffn_options.
 
     Returns y, or (y, kept) with ``keep``.
@@ -147,7 +147,7 @@ def linear(x, weight, bias=None, *, activation=None, residual=None, keep=None, o
     if _elsewhere(x, "x", stream):
         with _On(x.get_device(), stream):
             return linear(x, weight, bias, activation=activation, residual=residual, keep=keep, out=out, out_dtype=out_dtype,
-                          tile=tile, no_split=no_split, timeout_ns=timeout_ns, inject_lost_load=inject_lost_load)
+                          tile=tile, k_splits=k_splits, timeout_ns=timeout_ns, inject_lost_load=inject_lost_load)
     real = _type(x, "x")
     act = _activation(activation)
     M, K, ldx, x = _operand(x, "x")
@@ -183,12 +183,12 @@ def linear(x, weight, bias=None, *, activation=None, residual=None, keep=None, o
             raise ValueError("unknown keep %r" % (keep,))
     args = _linear(x.data_ptr(), weight.data_ptr(), b_ptr or 0, r_ptr or 0, out.data_ptr(), z_ptr or 0, q, M, N, K, ldx, ldw,
                    ld_res, ldy, ldz, real, _REAL_OF[out.dtype], b_type, act)
-    _check(ffn_calls().linear(args, _raw_stream(device), _options(tile, no_split, timeout_ns, inject_lost_load)),
+    _check(ffn_calls().linear(args, _raw_stream(device), _options(tile, k_splits, timeout_ns, inject_lost_load)),
            "gemm_linear")
     return out if kept is None else (out, kept)
 
 
-def gated(x, w_gate, w_up, *, activation="silu", keep=None, out=None, stream=None, tile=0, no_split=False, timeout_ns=0,
+def gated(x, w_gate, w_up, *, activation="silu", keep=None, out=None, stream=None, tile=0, k_splits=0, timeout_ns=0,
           inject_lost_load=False):
     """h = act(x Wg^T) * (x Wu^T), both products in one kernel, rounded once.  x: M x K, weights: N x K.
 
@@ -200,7 +200,7 @@ def gated(x, w_gate, w_up, *, activation="silu", keep=None, out=None, stream=Non
     """
     if _elsewhere(x, "x", stream):
         with _On(x.get_device(), stream):
-            return gated(x, w_gate, w_up, activation=activation, keep=keep, out=out, tile=tile, no_split=no_split,
+            return gated(x, w_gate, w_up, activation=activation, keep=keep, out=out, tile=tile, k_splits=k_splits,
                          timeout_ns=timeout_ns, inject_lost_load=inject_lost_load)
     real = _type(x, "x")
     act = _activation(activation)
@@ -228,7 +228,7 @@ def gated(x, w_gate, w_up, *, activation="silu", keep=None, out=None, stream=Non
             raise ValueError("unknown keep %r" % (keep,))
     args = _gated(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(), zg, zu, qg, qu, M, N, K, ldx, ld_gate,
                   ld_up, ldh, ldz, ldz, real, act)
-    _check(ffn_calls().gated(args, _raw_stream(device), _options(tile, no_split, timeout_ns, inject_lost_load)), "gemm_gated")
+    _check(ffn_calls().gated(args, _raw_stream(device), _options(tile, k_splits, timeout_ns, inject_lost_load)), "gemm_gated")
     return out if kept is None else (out, kept)
 
 
@@ -295,7 +295,7 @@ def linear_backward(dy, x, weight, *, activation=None, kept=None, bias_grad=Fals
         raise ValueError("without an activation nothing is kept")
     if not weight_grad and (addend is not None or out is not None):
         raise ValueError("addend and out are for dweight")
-    opts = _options(tile, False, timeout_ns, False)
+    opts = _options(tile, 0, timeout_ns, False)
     M, N, ldd = _matrix(dy, "dy")
     device = dy.get_device()
     if act or bias_grad:
@@ -353,7 +353,7 @@ def gated_backward(dh, x, w_gate, w_up, kept, *, activation="silu", product=Fals
     act = _activation(activation)
     if not weight_grad and (addend is not None or out is not None):
         raise ValueError("addend and out are for the weights' gradients")
-    opts = _options(tile, False, timeout_ns, False)
+    opts = _options(tile, 0, timeout_ns, False)
     M, N, ldd = _matrix(dh, "dh")
     device = dh.get_device()
     mx, K, ldx, x = _operand(x, "x", dh)
@@ -386,9 +386,9 @@ def gated_backward(dh, x, w_gate, w_up, kept, *, activation="silu", product=Fals
 OPERATORS = {"linear": 0, "gated": 1, "input_grad": 2, "weight_grad": 3}
 
 
-def ffn_plan(op, M, N, K, *, count=1, kept=False, sms=0, tile=0, no_split=False) -> dict:
+def ffn_plan(op, M, N, K, *, count=1, kept=False, sms=0, tile=0, k_splits=0) -> dict:
     """The kernel and tile that a product of ``linear``, ``gated`` or a backward pass would take (see gemm_ffn_plan)."""
     p = GpPlan()
-    opts = GpFfnOptions(0, int(tile), int(no_split), 0)
+    opts = GpFfnOptions(0, int(tile), int(k_splits), 0)
     _check(lib().gemm_ffn_plan(_binding._enum(op, OPERATORS, "op"), M, N, K, count, int(kept), sms, opts, p), "gemm_ffn_plan")
     return p.as_dict()

@@ -129,14 +129,15 @@ def test_null_arguments(gp):
 
 
 def test_forced_tiles(gp):
-    def opts(tile, lose=0):
-        return b.GpFfnOptions(0, tile, 0, lose)
+    def opts(tile, lose=0, splits=0):
+        return b.GpFfnOptions(0, tile, splits, lose)
+    assert linear(gp, opts(32, splits=3)) == gp.GP_ERR_UNSUPPORTED and linear(gp, opts(16, splits=8)) == gp.GP_ERR_UNSUPPORTED
     assert linear(gp, opts(48)) == gp.GP_ERR_UNSUPPORTED and linear(gp, opts(256, 1)) == gp.GP_ERR_UNSUPPORTED
     assert linear(gp, opts(16), q=codes()) == gp.GP_ERR_UNSUPPORTED
     assert gated(gp, opts(128), q_gate=codes(), q_up=codes()) == gp.GP_ERR_UNSUPPORTED
     assert gated(gp, opts(0, 1), q_gate=codes(), q_up=codes()) == gp.GP_ERR_UNSUPPORTED
-    for call in (input_grad, weight_grad):
-        assert call(gp, opts(64)) == gp.GP_ERR_UNSUPPORTED
+    assert weight_grad(gp, opts(32)) == gp.GP_ERR_UNSUPPORTED and weight_grad(gp, opts(16)) == gp.GP_ERR_UNSUPPORTED
+    assert input_grad(gp, opts(96)) == gp.GP_ERR_UNSUPPORTED
 
 
 def test_empty_outputs_need_no_device(gp):
@@ -216,8 +217,9 @@ def test_plan_invariants(gp, op):
         p = gp.ffn_plan(op, M, N, K, count=count, kept=kept, sms=sms)
         rows, cols = (N, K) if op == "weight_grad" else (M, K if op == "input_grad" else N)
         if p["layout"]:
-            assert op in ("linear", "gated") and not kept
-            assert p["tiles"] == -(-cols // p["bm"]) * -(-rows // p["bn"]) and p["grid"] == p["tiles"] * p["k_splits"]
+            assert not kept or op in ("input_grad", "weight_grad")
+            assert p["tiles"] == -(-cols // p["bm"]) * -(-rows // p["bn"]) * (count if op == "weight_grad" else 1)
+            assert p["grid"] == p["tiles"] * p["k_splits"] and (p["bn"] == 64 or op != "weight_grad")
             assert p["k_splits"] == 1 or (p["grid"] <= sms and p["k_tiles"] >= 4 * p["k_splits"])
         else:
             assert p["tiles"] == -(-rows // p["bm"]) * -(-cols // p["bn"]) * (count if op == "weight_grad" else 1)

@@ -127,9 +127,9 @@ def test_linear_activations_and_types(act, M, dtype, out):
 @pytest.mark.parametrize("tile", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("M,N,K", [(1, 200, 700), (100, 1000, 333), (513, 700, 1300)])
 def test_linear_every_tile(tile, M, N, K):
-    for split in (False, True):
-        check_linear(M, N, K, BF16, "silu", bias=BF16, residual=True, tile=tile, no_split=split)
-        check_linear(M, N, K, F16, None, keep="real", out_dtype=F32, tile=tile, no_split=split)
+    for splits in (0, 1, 2, 4, 8) if 16 < tile < 128 else (0, 1, 4) if tile == 16 else (0,):
+        check_linear(M, N, K, BF16, "silu", bias=BF16, residual=True, tile=tile, k_splits=splits)
+        check_linear(M, N, K, F16, None, keep="real", out_dtype=F32, tile=tile, k_splits=splits)
     if tile >= 128:
         check_linear(M, N, K, BF16, "gelu", bias=BF16, keep="fp8", tile=tile)
 
@@ -180,7 +180,8 @@ def test_gated_activations(act, M, keep):
 @pytest.mark.parametrize("M,N,K", [(1, 200, 700), (100, 1000, 333), (513, 700, 1300)])
 def test_gated_every_tile(tile, M, N, K):
     check_gated(M, N, K, BF16, tile=tile)
-    check_gated(M, N, K, F16, keep="real", tile=tile, no_split=True)
+    for splits in (1, 2, 4) if tile < 128 else ():
+        check_gated(M, N, K, F16, keep="real", tile=tile, k_splits=splits)
 
 
 @pytest.mark.parametrize("M", [1, 40, 130, 600])
@@ -287,7 +288,7 @@ def check_linear_backward(M, N, K, dtype=BF16, act=None, keep="real", out_dtype=
     addend = ref.matrix(rng, N, K, out_dtype or dtype) if add else None
     dx, dw, db = gp.linear_backward(dy, x, w, activation=act, kept=kept, bias_grad=True, out_dtype=out_dtype, addend=addend, **kw)
     status_ok()
-    assert dx.dtype is dtype and dw.dtype is (out_dtype or dtype) and db.dtype is F32
+    assert dx.dtype is dtype and db.dtype is F32 and (dw is None or dw.dtype is (out_dtype or dtype))
     d = ref.f64(dy)
     if act:
         z = ref.held(kept, dtype)
@@ -323,12 +324,13 @@ def test_linear_backward_activations(act, keep, dtype):
     check_linear_backward(150, 261, 200, dtype, act, keep)
 
 
-@pytest.mark.parametrize("tile", [128, 256])
-@pytest.mark.parametrize("M,N,K", [(100, 333, 700), (700, 513, 300), (300, 1300, 520)])
+@pytest.mark.parametrize("tile", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("M,N,K", [(100, 333, 700), (700, 513, 300), (300, 1300, 520), (20, 2000, 128), (1000, 64, 192)])
 def test_backward_every_tile(tile, M, N, K):
-    check_linear_backward(M, N, K, BF16, tile=tile, out_dtype=F32, add=True)
-    check_linear_backward(M, N, K, F16, "silu", "fp8", tile=tile)
-    check_gated_backward(M, N, K, BF16, tile=tile)
+    weight = tile >= 64            # (a weight's gradient has no narrower one)
+    check_linear_backward(M, N, K, BF16, tile=tile, out_dtype=F32, add=weight, weight_grad=weight)
+    check_linear_backward(M, N, K, F16, "silu", "fp8", tile=tile, weight_grad=weight)
+    check_gated_backward(M, N, K, BF16, tile=tile, weight_grad=weight)
 
 
 @pytest.mark.parametrize("pads", [(1, 3, 5, 7), (8, 8, 8, 8), (0, 1, 0, 0), (4, 0, 0, 1)])
@@ -344,7 +346,7 @@ def test_backward_whole_numbers_are_exact(M, N, K):
     rng = np.random.default_rng(6)
     dy, x, w = (ref.matrix(rng, r, c, BF16, whole=2) for r, c in ((M, N), (M, K), (N, K)))
     a, b, c = (t.cpu().double() for t in (dy, x, w))
-    for tile in (0, 128, 256):
+    for tile in (0, 64, 128, 256):
         dx, dw, db = gp.linear_backward(dy, x, w, bias_grad=True, out_dtype=F32, tile=tile)
         assert torch.equal(dw.cpu().double(), a.t() @ b) and torch.equal(db.cpu().double(), a.sum(0))
         assert torch.equal(dx.cpu(), (a @ c).to(BF16))
