@@ -287,47 +287,43 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         prod.advance(Sh::STAGES);
       }
-    } else if (warp == 1) {
-      // ---------------- MMA issuer ----------------
+    } else if (warp == 1 && ring_elect_one()) {
+      // ---------------- MMA issuer (one lane) ----------------
       int s = 0, a = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
-      const bool leader = ring_elect_one();
       const uint32_t ring0 = smem_u32(ring);
       const uint64_t p0 = P_MN ? umma_desc_mn(ring0) : umma_desc_sw128(ring0);
       const uint64_t q0 = (Q_MN ? umma_desc_mn(ring0) : umma_desc_sw128(ring0)) + Sh::PARTS * Sh::P_BYTES / 16;
       constexpr uint32_t P_STEP = P_MN ? 128 : 2, Q_STEP = Q_MN ? 128 : 2;   // 16 along K, as in the ring
       for (int kc = k0; ok && kc < k1; kc += g.restart) {
         const int end = min(kc + g.restart, k1);
-        if (!__all_sync(0xffffffffu, mbar_wait(&bar->acc_empty[a], aph ^ 1u, g.ctl, cta, kSiteMmaAccEmpty))) break;
+        if (!mbar_wait(&bar->acc_empty[a], aph ^ 1u, g.ctl, cta, kSiteMmaAccEmpty)) break;
         tc_fence_after();
         const uint32_t d = tmem + a * Sh::PARTS * BN;
         for (int kb = kc; kb < end; ++kb) {
-          const bool there = mbar_wait(&bar->full[s], ph, g.ctl, cta, kSiteConsumerFull);
+          // (nothing is issued of a slot that never came)
+          if (!mbar_wait(&bar->full[s], ph, g.ctl, cta, kSiteConsumerFull)) { ok = false; break; }
           tc_fence_after();
           const uint64_t dp = p0 + static_cast<uint32_t>(s * Sh::STAGE) / 16;
           const uint64_t dq = q0 + static_cast<uint32_t>(s * Sh::STAGE) / 16;
-          if (leader && there) {   // (nothing of a slot that never came)
 #pragma unroll
-            for (int kk = 0; kk < kFfnBK / 16; ++kk) {
-              const uint32_t more = kb > kc || kk > 0;
-              umma_f16(d, dp + P_STEP * kk, dq + Q_STEP * kk, g.idesc, more);
-              if (GATED) umma_f16(d + BN, dp + Sh::P_BYTES / 16 + P_STEP * kk, dq + Q_STEP * kk, g.idesc, more);
-            }
-            umma_commit(&bar->empty[s]);
+          for (int kk = 0; kk < kFfnBK / 16; ++kk) {
+            const uint32_t more = kb > kc || kk > 0;
+            umma_f16(d, dp + P_STEP * kk, dq + Q_STEP * kk, g.idesc, more);
+            if (GATED) umma_f16(d + BN, dp + Sh::P_BYTES / 16 + P_STEP * kk, dq + Q_STEP * kk, g.idesc, more);
           }
-          if (!__all_sync(0xffffffffu, there)) { ok = false; break; }
+          umma_commit(&bar->empty[s]);
           if (++s == Sh::STAGES) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
-        if (leader) umma_commit(&bar->acc_full[a]);
+        umma_commit(&bar->acc_full[a]);
         if (++a == 2) { a = 0; aph ^= 1u; }
       }
-      if (leader) {
-        umma_commit(&bar->drain);
-        CtaCtl never_abort{0};
-        mbar_wait(&bar->drain, 0, g.ctl, &never_abort, kSiteDrain);
-      }
+      // fires when every MMA issued above has completed
+      umma_commit(&bar->drain);
+      CtaCtl never_abort{0};
+      mbar_wait(&bar->drain, 0, g.ctl, &never_abort, kSiteDrain);
     }
     __syncwarp();
     if (ctas > 1) {
