@@ -239,29 +239,6 @@ class _Fp8Calls:
             setattr(self, name, f)
 
 
-class _FfnCalls:
-    """The feed-forward entry points taking their argument structs as packed bytes."""
-
-    def __init__(self):
-        L, vp = lib(), ctypes.c_void_p
-        for name in ("gemm_linear", "gemm_gated", "gemm_input_grad", "gemm_weight_grad", "ffn_act_backward",
-                     "ffn_gated_backward", "ffn_pack_rows"):
-            f = L[name]                # a function object of its own
-            f.restype = ctypes.c_int
-            f.argtypes = [vp] + list(getattr(L, name).argtypes[1:])
-            setattr(self, name[5:] if name.startswith("gemm_") else name[4:].replace("pack_rows", "pack"), f)
-
-
-_ffn_calls = None
-
-
-def ffn_calls():
-    global _ffn_calls
-    if _ffn_calls is None:
-        _ffn_calls = _FfnCalls()
-    return _ffn_calls
-
-
 _fp8_calls = None
 
 

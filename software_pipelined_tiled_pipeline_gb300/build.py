@@ -4,13 +4,16 @@ Each CUDA translation unit is compiled to an object in parallel under
 ``_build/`` and the objects are linked into
 ``software_pipelined_tiled_pipeline_gb300/libgemmpipe.so`` (CUDA runtime linked
 statically; the driver is reached through the runtime's entry-point query, so
-no libcuda is needed at link time).  Host code is portable C++17: the same
-sources build on x86_64 and on aarch64.
+no libcuda is needed at link time).  Beside it ``_torch_ffn.so``, the CPython
+extension that takes torch tensors to the feed-forward calls, is compiled with
+g++ against the installed torch.  Host code is portable C++17: the same sources
+build on x86_64 and on aarch64.
 """
 import os
 import re
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgemmpipe.so")
+TORCH_SOURCE = "torch_ffn.cpp"
+TORCH_LIB = os.path.join(PKG, "_torch_ffn.so")
 
 SOURCES = ["api.cu", "ffn_api.cu", "fp8_api.cu", "k_ffma.cu", "k_ffn_act.cu", "k_ffn_few.cu", "k_ffn_gated.cu",
            "k_ffn_input_grad.cu", "k_ffn_linear.cu", "k_ffn_weight_grad.cu", "k_fp8_gemm.cu", "k_fp8_norm.cu", "k_fp8_quant.cu", "k_imma.cu", "k_umma.cu", "probe.cu"]
@@ -59,7 +64,7 @@ def nvcc() -> str:
 
 
 def _deps():
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))]
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".cpp", ".h"))]
     deps += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     deps.append(os.path.abspath(__file__))
     return deps
@@ -72,10 +77,29 @@ def _stale(target, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_torch_extension():
+    """The CPython extension on torch tensors: host code only, against the torch that is installed."""
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    include = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(base, "include"),
+               os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include") if os.path.sep in nvcc() else "/usr/local/cuda/include"]
+    tmp = TORCH_LIB + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", os.path.join(CSRC, TORCH_SOURCE), "-o", tmp]
+    cmd += ["-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)] + ["-I" + i for i in include]
+    lib = os.path.join(base, "lib")
+    cmd += ["-L" + lib, "-Wl,-rpath," + lib, "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on %s:\n%s%s" % (TORCH_SOURCE, r.stdout, r.stderr))
+    os.replace(tmp, TORCH_LIB)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     """Compile and link the library if any source is newer than it; return its path."""
     deps = _deps()
-    if not force and not _stale(LIB, deps):
+    if not force and not _stale(LIB, deps) and not _stale(TORCH_LIB, deps):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -87,8 +111,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, cmd, r
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        extension = ex.submit(_build_torch_extension)
         results = list(ex.map(compile_one, SOURCES))
+        extension.result()
     objs = []
     for src, obj, cmd, r in results:
         if verbose or ptxas_verbose:

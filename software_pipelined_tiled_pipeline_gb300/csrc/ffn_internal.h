@@ -77,7 +77,7 @@ struct FfnActArgs {
   int32_t type, act;
   int32_t vec;
 };
-// Row parts of a call of this size (partial sums of dbias: that many x N floats).
+// Rows of partial sums of dbias that a call of this size leaves (1: none, it adds them up itself).
 int64_t ffn_act_parts(int64_t M, int64_t N, int sm_count);
 cudaError_t launch_ffn_act_backward(const FfnActArgs& a, int sm_count, cudaStream_t stream, const void** kernel, gp_plan* plan);
 cudaError_t launch_ffn_gated_backward(const FfnActArgs& a, int sm_count, cudaStream_t stream, const void** kernel,

@@ -6,10 +6,10 @@
 //
 // z, g and u come in 16 bits or as 8-bit codes with a scale for each row's 128
 // values.  A block takes a strip of 128 columns (one group of codes per row) and a
-// part of the rows, a warp every eighth of these, a lane four columns; the bias
-// gradient is summed in FP32 per lane, over the block's warps and, by a second
-// kernel, over the parts, each in a fixed order.  HBM bounds it: two bytes in and
-// out per value, one for each 8-bit one.  Four values per lane and three rows under
+// part of the rows, a warp every eighth of these, a lane four columns.  The bias
+// gradient is summed in FP32 per lane, over the block's warps, over the up to eight
+// parts of a cluster and, by a second kernel, over the clusters, each in a fixed
+// order.  HBM bounds it: two bytes in and out per value, one for each 8-bit one.  Four values per lane and three rows under
 // way keep it within 64 registers, so 48 KB of loads are under way on an SM (with
 // eight values it took 255, and 4096 x 8192 with codes 111 us).
 #include <algorithm>
@@ -175,7 +175,7 @@ __device__ __forceinline__ void act_backward_rows(const FfnActArgs& a, const Row
   }
 
 template <typename T, bool FP8>
-__global__ void __launch_bounds__(kActThreads, 4) act_backward_kernel(const __grid_constant__ FfnActArgs a, int parts) {
+__global__ void __launch_bounds__(kActThreads, 4) act_backward_kernel(const __grid_constant__ FfnActArgs a, int parts, int cluster) {
   __shared__ float sums[kActWarps][kActStrip];
   pdl_launch_dependents();
   pdl_wait();
@@ -196,12 +196,30 @@ __global__ void __launch_bounds__(kActThreads, 4) act_backward_kernel(const __gr
 #pragma unroll
   for (int i = 0; i < 4; ++i) sums[warp][vec ? 4 * lane + i : lane + 32 * i] = sum[i];
   __syncthreads();
-  const int col = strip * kActStrip + static_cast<int>(threadIdx.x);
-  if (threadIdx.x >= kActStrip || col >= a.N) return;
+  const int at = static_cast<int>(threadIdx.x), col = strip * kActStrip + at;
   float total = 0.f;
+  if (at < kActStrip) {
 #pragma unroll
-  for (int w = 0; w < kActWarps; ++w) total += sums[w][threadIdx.x];
-  (parts > 1 ? a.partials + static_cast<int64_t>(blockIdx.y) * a.N : a.dbias)[col] = total;
+    for (int w = 0; w < kActWarps; ++w) total += sums[w][at];
+    sums[0][at] = total;
+  }
+  if (cluster > 1) {
+    // the cluster's first block adds up what the others hold
+    __syncwarp();
+    cluster_sync();
+    if (cluster_ctarank() == 0 && at < kActStrip) {
+      for (int r = 1; r < cluster; ++r) {
+        float x;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(mapa_shared(smem_u32(&sums[0][at]), r)) : "memory");
+        total += x;
+      }
+    }
+    __syncwarp();
+    cluster_sync();   // nobody leaves before its sums are read
+    if (cluster_ctarank() != 0) return;
+  }
+  if (at >= kActStrip || col >= a.N) return;
+  (parts > cluster ? a.partials + static_cast<int64_t>(blockIdx.y / cluster) * a.N : a.dbias)[col] = total;
 }
 
 // dbias = sum of the parts, in their order.
@@ -299,51 +317,73 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint16_t* src, int64_t 
 
 }  // namespace
 
-int64_t ffn_act_parts(int64_t M, int64_t N, int sm_count) {
-  // eight blocks for each SM (four at a time), and two rows for each warp at least
-  const int64_t strips = (N + kActStrip - 1) / kActStrip, most = (M + 2 * kActWarps - 1) / (2 * kActWarps);
-  return std::max<int64_t>(1, std::min(most, (8 * sm_count + strips - 1) / strips));
-}
-
 namespace {
 
-template <typename Kernel>
-cudaError_t launch_act(Kernel k, const FfnActArgs& a, int parts, cudaStream_t stream, const void** kernel, gp_plan* plan) {
+// Parts of the rows: eight blocks for each SM (four at a time), and two rows for each warp at least; a power of two up to
+// eight, or a multiple of eight, so that clusters of up to eight share them.
+int64_t row_parts(int64_t M, int64_t N, int sm_count) {
+  const int64_t strips = (N + kActStrip - 1) / kActStrip, most = (M + 2 * kActWarps - 1) / (2 * kActWarps);
+  const int64_t parts = std::min(most, (8 * sm_count + strips - 1) / strips);
+  if (parts >= 8) return parts / 8 * 8;
+  return parts >= 4 ? 4 : (parts >= 2 ? 2 : 1);
+}
+
+template <typename Kernel, typename... Args>
+cudaError_t launch_act(Kernel k, const FfnActArgs& a, int parts, int cluster, cudaStream_t stream, const void** kernel,
+                       gp_plan* plan, Args... args) {
   *kernel = reinterpret_cast<const void*>(k);
-  const dim3 grid(static_cast<unsigned>((a.N + kActStrip - 1) / kActStrip), static_cast<unsigned>(parts));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.N + kActStrip - 1) / kActStrip), static_cast<unsigned>(parts));
+  cfg.blockDim = dim3(kActThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   plan->threads = kActThreads;
-  plan->grid = static_cast<int32_t>(grid.x * grid.y);
-  return launch_dependent(k, grid, dim3(kActThreads), 0, stream, a, parts);
+  plan->grid = static_cast<int32_t>(cfg.gridDim.x * cfg.gridDim.y);
+  return cudaLaunchKernelEx(&cfg, k, a, parts, args...);
 }
 
 }  // namespace
 
+int64_t ffn_act_parts(int64_t M, int64_t N, int sm_count) {
+  const int64_t parts = row_parts(M, N, sm_count);
+  return parts > 8 ? parts / 8 : 1;
+}
+
 cudaError_t launch_ffn_act_backward(const FfnActArgs& a, int sm_count, cudaStream_t stream, const void** kernel,
                                     gp_plan* plan) {
-  const int parts = static_cast<int>(ffn_act_parts(a.M, a.N, sm_count));
+  const int parts = static_cast<int>(row_parts(a.M, a.N, sm_count)), cluster = a.dbias ? std::min(parts, 8) : 1;
   plan->dtype = GP_PLAN_FFN;
   plan->kernel = "ffn_act_backward";
+  plan->k_splits = cluster;
   const bool bf16 = a.type == GP_REAL_BF16, codes = a.codes[0].data != nullptr;
   const cudaError_t e =
-      bf16 ? (codes ? launch_act(act_backward_kernel<__nv_bfloat16, true>, a, parts, stream, kernel, plan)
-                    : launch_act(act_backward_kernel<__nv_bfloat16, false>, a, parts, stream, kernel, plan))
-           : (codes ? launch_act(act_backward_kernel<__half, true>, a, parts, stream, kernel, plan)
-                    : launch_act(act_backward_kernel<__half, false>, a, parts, stream, kernel, plan));
-  if (e != cudaSuccess || !a.dbias || parts == 1) return e;
+      bf16 ? (codes ? launch_act(act_backward_kernel<__nv_bfloat16, true>, a, parts, cluster, stream, kernel, plan, cluster)
+                    : launch_act(act_backward_kernel<__nv_bfloat16, false>, a, parts, cluster, stream, kernel, plan, cluster))
+           : (codes ? launch_act(act_backward_kernel<__half, true>, a, parts, cluster, stream, kernel, plan, cluster)
+                    : launch_act(act_backward_kernel<__half, false>, a, parts, cluster, stream, kernel, plan, cluster));
+  if (e != cudaSuccess || !a.dbias || parts <= 8) return e;
   return launch_dependent(sum_parts_kernel, dim3(static_cast<unsigned>((a.N + kActThreads - 1) / kActThreads)),
-                          dim3(kActThreads), 0, stream, a.partials, a.dbias, a.N, parts);
+                          dim3(kActThreads), 0, stream, a.partials, a.dbias, a.N, parts / 8);
 }
 
 cudaError_t launch_ffn_gated_backward(const FfnActArgs& a, int sm_count, cudaStream_t stream, const void** kernel,
                                       gp_plan* plan) {
-  const int parts = static_cast<int>(ffn_act_parts(a.M, a.N, sm_count));
+  const int parts = static_cast<int>(row_parts(a.M, a.N, sm_count));
   plan->dtype = GP_PLAN_FFN;
   plan->kernel = "ffn_gated_backward";
   const bool bf16 = a.type == GP_REAL_BF16, codes = a.codes[0].data != nullptr;
-  return bf16 ? (codes ? launch_act(gated_backward_kernel<__nv_bfloat16, true>, a, parts, stream, kernel, plan)
-                       : launch_act(gated_backward_kernel<__nv_bfloat16, false>, a, parts, stream, kernel, plan))
-              : (codes ? launch_act(gated_backward_kernel<__half, true>, a, parts, stream, kernel, plan)
-                       : launch_act(gated_backward_kernel<__half, false>, a, parts, stream, kernel, plan));
+  return bf16 ? (codes ? launch_act(gated_backward_kernel<__nv_bfloat16, true>, a, parts, 1, stream, kernel, plan)
+                       : launch_act(gated_backward_kernel<__nv_bfloat16, false>, a, parts, 1, stream, kernel, plan))
+              : (codes ? launch_act(gated_backward_kernel<__half, true>, a, parts, 1, stream, kernel, plan)
+                       : launch_act(gated_backward_kernel<__half, false>, a, parts, 1, stream, kernel, plan));
 }
 
 cudaError_t launch_ffn_pack(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_t rows, int64_t cols,

@@ -57,34 +57,50 @@ int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count,
   auto few_tiles = [&](int bn) { return problems * blocks(cols, 128) * blocks(rows, bn); };
   const int want_splits = opts ? opts->k_splits : 0;
   if (want_splits != 0 && want_splits != 1 && want_splits != 2 && want_splits != 4 && want_splits != 8) return GP_ERR_UNSUPPORTED;
-  // CTAs that share a tile's K blocks: as many as the SMs take at once, with four K blocks each at least
+  // CTAs that share a tile's K blocks: as many as the SMs take at once (16 clusters of 8 do not fit on 152: 128 rows of a
+  // weight gradient by 8 CTAs 20.7 us, by 4 13.3), with four K blocks each at least
   auto few_ctas = [&](int bn) {
     if (want_splits) return want_splits;
     int c = 1;
-    while (c < ffn_few_most_ctas(bn) && few_tiles(bn) * c * 2 <= have && kt >= 4 * c * 2) c *= 2;
+    while (c < ffn_few_most_ctas(bn) && few_tiles(bn) * c * 2 <= (c == 4 ? have * 3 / 4 : have) && kt >= 4 * c * 2) c *= 2;
     return c;
   };
   int tile = want;
   if (tile == 0) {
-    // Estimates in ns: K blocks one after another on the busiest SM, and the rest of a call.
+    // The least estimate, in ns, as measured on a 152-SM GB300 (device time of calls in a graph): a call with one K
+    // block, each further one on the busiest SM, and each further round of tiles; but not less than the operands take
+    // from HBM.  For example 1000 x 776 x 2048: 64 rows 10.5 us, 128 rows by two CTAs 11.0, 128 x 128 13; 512 x 4096 x
+    // 4096: 128 x 128 20.6, 128 rows 22.1, 256 x 256 29; gated 333 x 1000 x 776: 128 x 128 8.7, 256 x 256 10.0, 64 rows by
+    // two CTAs 10.0; weight gradient of 8192 x 512 x 512: 64 rows by four CTAs 10.5, by one 21.1, 128 x 128 26.4.
+    const double read = 2.0 * (static_cast<double>(rows) * summed + (gated ? 2.0 : 1.0) * cols * summed) * (kt > 0 ? count : 0) / 6500;
+    // Rows of a box off 128-byte boundaries, and boxes of 64 of a stored row, take longer to load.
+    const double slow = (op == kFfnLinear || gated ? summed : cols) % 64 ? 1.6 : 1.0;
     double best = 0;
-    auto take = [&](int t, double ns) {
+    auto take = [&](int t, double once, double k_blocks) {
+      const double ns = once + (k_blocks > read ? k_blocks : read);
       if (tile == 0 || ns < best) {
         tile = t;
         best = ns;
       }
     };
     if (can_few) {
-      for (int bn = op == kFfnWeightGrad ? 64 : 16; bn <= (gated ? 64 : 128); bn *= 2) {
-        const int64_t t = few_tiles(bn);
-        const int c = few_ctas(bn);
-        take(bn == 128 ? kSplit128 : bn, static_cast<double>(blocks(t * c, have)) * (blocks(kt, c) * (gated ? 300 : 200) + 2500 + bn * 25) + (c > 1 ? 1500 : 0));
+      constexpr int kRows[4] = {16, 32, 64, 128}, kBlock[2][4] = {{130, 110, 150, 220}, {217, 230, 265, 0}};
+      for (int i = op == kFfnWeightGrad ? 2 : 0; i < (gated ? 3 : 4); ++i) {
+        const int bn = kRows[i], c = few_ctas(bn);
+        const double rounds = static_cast<double>(blocks(few_tiles(bn) * c, have));
+        const double again = (blocks(rows, bn) - 1) * (bn < 64 ? 1500 : 0);   // the other operand once more from L2
+        const double once = 4500 + bn * 15 + (gated ? 2000 : 0) + (c > 1 ? 700 : 0) + again;
+        take(bn == 128 ? kSplit128 : bn, once + (rounds - 1) * once, rounds * blocks(kt, c) * kBlock[gated][i] * slow);
       }
     }
     const int64_t pairs = problems * blocks(rows, 256) * blocks(cols, gated ? 128 : 256);
     const int64_t ones = problems * blocks(rows, 128) * blocks(cols, gated ? 64 : 128);
-    if (can_one) take(128, static_cast<double>(blocks(ones, have)) * kt * 260 + 6000);
-    if (can_pair) take(256, static_cast<double>(blocks(pairs, have / 2)) * kt * 280 + 8000);
+    const double one_rounds = static_cast<double>(blocks(ones, have)), pair_rounds = static_cast<double>(blocks(pairs, have / 2 > 0 ? have / 2 : 1));
+    // (few rows leave most of an operand's slot empty, and the loads under way are too few: gated 1 x 8192 x 4096 36.6 us
+    // by 128 x 128, 22.6 by 16 rows)
+    const bool whole = rows > 64 || !can_few;
+    if (can_one && whole) take(128, 5500 + (one_rounds - 1) * 800, one_rounds * kt * 210 * slow);
+    if (can_pair && (whole || !can_one)) take(256, 6500 + (pair_rounds - 1) * 1500, pair_rounds * kt * 285 * slow);
     if (tile == 0) return GP_ERR_UNSUPPORTED;   // (kept in 8 bits on one SM: a pair of CTAs does not fit)
   }
   const bool few = tile < 128 || tile == kSplit128;

@@ -160,12 +160,12 @@ def test_pack_refusals(gp):
 def test_bias_workspace(gp):
     size = ctypes.c_int64(-1)
     f = gp.lib().ffn_act_backward_workspace
-    for M, N in [(0, 64), (64, 0), (1, 1), (16, 5000)]:       # one part of rows needs none
+    for M, N in [(0, 64), (64, 0), (1, 1), (16, 5000), (200, 2056), (128, 100)]:       # what a cluster adds up needs none
         assert f(M, N, 152, size) == gp.GP_OK and size.value == 0
-    for M, N in [(1000, 1), (200, 2056), (8192, 8192), (4096, 100)]:
+    for M, N in [(1000, 1), (8192, 1000), (4096, 100)]:
         assert f(M, N, 152, size) == gp.GP_OK
         parts, left = divmod(size.value, 4 * N)
-        assert left == 0 and 2 <= parts <= (M + 15) // 16        # at least a row or two for each warp of a part
+        assert left == 0 and 2 <= parts <= (M + 127) // 128        # eight parts of two rows for each warp at least
     assert f(-1, 4, 152, size) == gp.GP_ERR_ARG and f(4, 4, -1, size) == gp.GP_ERR_ARG and f(4, 4, 152, None) == gp.GP_ERR_ARG
 
 
@@ -187,13 +187,6 @@ def test_struct_layout_matches_the_header(tmp_path):
     subprocess.run([cc, "-std=c99", "-I", os.path.join(ROOT, "include"), str(src), "-o", exe], check=True)
     out = subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split()
     assert [int(v) for v in out] == want
-
-
-def test_packed_arguments_match_the_structs():
-    from software_pipelined_tiled_pipeline_gb300 import ffn
-    for name, cls in (("_linear", b.GpLinear), ("_gated", b.GpGated), ("_input_grad", b.GpInputGrad), ("_weight_grad", b.GpWeightGrad),
-                      ("_act_backward", b.GpActBackward), ("_gated_backward", b.GpGatedBackward)):
-        assert getattr(ffn, name).__self__.size == ctypes.sizeof(cls)
 
 
 def test_header_constants():
@@ -219,7 +212,7 @@ def test_plan_invariants(gp, op):
         if p["layout"]:
             assert not kept or op in ("input_grad", "weight_grad")
             assert p["tiles"] == -(-cols // p["bm"]) * -(-rows // p["bn"]) * (count if op == "weight_grad" else 1)
-            assert p["grid"] == p["tiles"] * p["k_splits"] and (p["bn"] == 64 or op != "weight_grad")
+            assert p["grid"] == p["tiles"] * p["k_splits"] and (p["bn"] >= 64 or op != "weight_grad")
             assert p["k_splits"] == 1 or (p["grid"] <= sms and p["k_tiles"] >= 4 * p["k_splits"])
         else:
             assert p["tiles"] == -(-rows // p["bm"]) * -(-cols // p["bn"]) * (count if op == "weight_grad" else 1)
