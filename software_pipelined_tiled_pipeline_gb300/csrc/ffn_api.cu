@@ -85,7 +85,7 @@ int run_product(FfnProduct& p, const gp_ffn_options* opts) {
   if (e != cudaSuccess) return call_finish(GP_ERR_CUDA, e, GP_SITE_DEVICE);
   rc = ffn_plan_impl(p.op, p.rows, p.cols, p.summed, p.count, wide, codes, info.sm_count, opts, &p.plan);
   if (rc != GP_OK) return call_finish(rc);
-  e = ffn_fit_pairs(&p.plan);
+  e = ffn_fit_pairs(&p.plan, codes && p.op == kFfnGated);
   if (e != cudaSuccess) return call_finish(GP_ERR_CUDA, e, GP_SITE_CAPACITY);
   p.ctl = info.ctl;
   p.ctl.inject_lost_load = opts ? opts->inject_lost_load : 0;

@@ -50,7 +50,8 @@ struct FfnProduct {
 
 int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count, bool wide_sums, bool codes, int sms,
                   const gp_ffn_options* opts, gp_plan* p);
-cudaError_t ffn_fit_pairs(gp_plan* plan);
+// Pairs must sit on one TPC each: where fewer fit at once than the plan counted on, launch those.
+cudaError_t ffn_fit_pairs(gp_plan* plan, bool whole_groups);
 cudaError_t launch_ffn_linear(FfnProduct& a, const void** kernel);
 cudaError_t launch_ffn_gated(FfnProduct& a, const void** kernel);
 cudaError_t launch_ffn_input_grad(FfnProduct& a, const void** kernel);

@@ -15,7 +15,10 @@
 //   warp 1     allocates TMEM and issues tcgen05.mma (kind::f16, FP32 in TMEM)
 //   warps 4+   write the outputs from one TMEM buffer while the next tile's products
 //              run into the other
-// PAIR: a cluster of two CTAs shares a 256 x 256 tile (M = 256 instructions).
+// PAIR: a cluster of two CTAs shares a 256 x 256 tile (M = 256 instructions).  The
+// tiles after the last full round go as two halves of their columns each, where all
+// of those make one round: 4096 x 4096 outputs are 256 tiles, 3.37 rounds of 76
+// pairs, and take 3.5 instead of 4.
 //
 // The tensor cores cut their FP32 sums instead of rounding them, always towards
 // zero (measured on normal operands: 1.0e-6 relative after 1024 of K, 9e-6 after
@@ -90,7 +93,9 @@ struct RingParams {
   int32_t problems;          // products in this launch, with operands and outputs of their own
   int32_t restart;           // K blocks per hand-over of the accumulator
   int32_t raster;            // row blocks per raster group
-  uint32_t idesc;
+  int32_t whole;             // tiles that are not cut in halves: the first ones
+  int32_t items;             // these, and the halves
+  uint32_t idesc, idesc_half;
   int32_t a_planes, b_planes;   // an MN-major operand's 128 rows come as one box of two planes of 64
   KernelCtl ctl;
 };
@@ -179,6 +184,25 @@ __device__ __forceinline__ void ring_tile(int tile, int row_blocks, int col_bloc
   const int in = tile - group * per;
   rb = first + in % n;
   cb = in / n;
+}
+
+// What a worker works on: a tile, or half of its columns.
+struct RingItem {
+  int problem, rb, cb;
+  int half;              // 0 or 1, or -1: the whole tile
+};
+__device__ __forceinline__ RingItem ring_item(int item, const RingParams& g, int row_blocks, int col_blocks) {
+  RingItem t;
+  int tile = item;
+  t.half = -1;
+  if (item >= g.whole) {
+    tile = g.whole + ((item - g.whole) >> 1);
+    t.half = (item - g.whole) & 1;
+  }
+  const int per = row_blocks * col_blocks;
+  t.problem = tile >= per ? 1 : 0;
+  ring_tile(tile - t.problem * per, row_blocks, col_blocks, g.raster, t.rb, t.cb);
+  return t;
 }
 
 // ---------------------------------------------------------------------------
@@ -341,11 +365,11 @@ __device__ __forceinline__ void load_sums(float (&v)[32], uint32_t src, bool sum
   for (int i = 0; i < 32; ++i) v[i] = sums ? __uint_as_float(s[i]) : 0.f;
 }
 
-// A tile's outputs straight from TMEM: OUTS columns of the warp's rows, 32 at a time.  `src`: the first sum's address (sums
+// A tile's outputs straight from TMEM: `outs` columns of the warp's rows, 32 at a time.  `src`: the first sum's address (sums
 // false: there are none, all are 0); `other`: how far behind it the second weight's lie; release(): called when the last
 // has been read.
-template <int OUTS, bool GATED, typename T, typename Release>
-__device__ __forceinline__ void stream_out(const RingParams& g, int p, uint32_t src, uint32_t other, bool sums, Release release,
+template <bool GATED, typename T, typename Release>
+__device__ __forceinline__ void stream_out(const RingParams& g, int p, int outs, uint32_t src, uint32_t other, bool sums, Release release,
                                            int lane, int64_t row, int64_t col0) {
   const FfnOut& o = g.o;
   const int64_t cols = g.cols;
@@ -354,13 +378,13 @@ __device__ __forceinline__ void stream_out(const RingParams& g, int p, uint32_t 
     return;
   }
 #pragma unroll 1
-  for (int j = 0; j < OUTS / 32; ++j) {
+  for (int j = 0; j < outs / 32; ++j) {
     const int64_t first = col0 + j * 32;
     if (first >= cols) break;
     float v[32], u[GATED ? 32 : 1];
     load_sums(v, src + j * 32, sums);
     if constexpr (GATED) load_sums(u, src + other + j * 32, sums);
-    if (sums && (j + 1 == OUTS / 32 || first + 32 >= cols)) release();
+    if (sums && (j + 1 == outs / 32 || first + 32 >= cols)) release();
     if (!GATED && o.bias) add_bias<T>(v, o, lane, first, cols);
     if (row < g.rows) {
       if constexpr (GATED)
@@ -488,7 +512,7 @@ __device__ __forceinline__ void finish_gated(const RingParams& g, float (&acc)[2
 // ---------------------------------------------------------------------------
 // Maps: a of the first and second source or product, b likewise, or of the two weights of a gated product.
 struct RingMaps {
-  CUtensorMap a[2], b[2];
+  CUtensorMap a[2], b[2], b_half[2];   // (b in boxes of 64 of its rows, for half tiles)
 };
 
 template <int BN, bool PAIR, RingOut OUT, bool GATED, bool A_MN, bool B_MN>
@@ -508,8 +532,7 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
   constexpr int TILE_COLS = GATED ? BN / 2 : BN;
   const int row_blocks = (g.rows + Sh::TILE_ROWS - 1) / Sh::TILE_ROWS;
   const int col_blocks = (g.cols + TILE_COLS - 1) / TILE_COLS;
-  const int per_problem = row_blocks * col_blocks;
-  const int tiles = per_problem * g.problems;
+  const int items = g.items;
   const int kt = g.kt * g.sources;
 
   if (threadIdx.x == 0) {
@@ -550,22 +573,23 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
     if (Sh::SPLIT_REGS) regs_decrease<Sh::OTHER_REGS>();
     if (warp != 1 && lane == 0) {
       // ---------------- producers (every CTA) ----------------
-      const int lose_tile = g.ctl.inject_lost_load ? tiles - 1 : -1;   // test hook: this tile's last load never comes
+      const int lose_item = g.ctl.inject_lost_load ? items - 1 : -1;   // test hook: this tile's last load never comes
       bool ok = true;
       int kb = prod.which;
-      for (int tile = worker; ok && tile < tiles; tile += workers, kb -= kt) {
-        int rb, cb;
-        const int problem = tile >= per_problem ? 1 : 0;
-        ring_tile(tile - problem * per_problem, row_blocks, col_blocks, g.raster, rb, cb);
-        const int a_row = rb * Sh::TILE_ROWS + static_cast<int>(rank) * Sh::A_ROWS;
-        const int b_row = GATED ? cb * TILE_COLS : cb * BN + static_cast<int>(rank) * Sh::B_ROWS;
+      for (int item = worker; ok && item < items; item += workers, kb -= kt) {
+        const RingItem t = ring_item(item, g, row_blocks, col_blocks);
+        const int a_row = t.rb * Sh::TILE_ROWS + static_cast<int>(rank) * Sh::A_ROWS;
+        const bool half = PAIR && t.half >= 0;
+        const int b_row = !half ? (GATED ? t.cb * TILE_COLS : t.cb * BN + static_cast<int>(rank) * Sh::B_ROWS)
+                                : t.cb * TILE_COLS + t.half * (TILE_COLS / 2) + (GATED ? 0 : static_cast<int>(rank) * 64);
         for (; kb < kt; kb += kRingProducers) {
           const int s = prod.slot;
           if (!mbar_wait(&bar->empty[s], prod.phase ^ 1u, g.ctl, cta, kSiteProducerEmpty) || cta->abort) { ok = false; break; }
           const int second = kb >= g.kt ? 1 : 0;      // the second source
           const int k = (kb - second * g.kt) * kFfnBK;
-          const CUtensorMap* ma = &maps.a[problem | second];
-          const CUtensorMap* mb = &maps.b[GATED ? static_cast<int>(rank) : second];   // (two products share b)
+          const CUtensorMap* ma = &maps.a[t.problem | second];
+          const int which_b = GATED ? static_cast<int>(rank) : second;   // (two products share b)
+          const CUtensorMap* mb = &maps.b[which_b];
           const uint32_t a_at = smem_u32(ring + s * Sh::STAGE), b_at = a_at + Sh::A_BYTES;
           const uint32_t full = PAIR ? mapa_shared(smem_u32(&bar->full[s]), 0) : 0u;
           auto load = [&](uint32_t at, const CUtensorMap* m, int x, int y) {
@@ -586,16 +610,18 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
               tma_load_3d(at, m, &bar->full[s], 0, k, row >> 6);
             }
           };
-          if (tile == lose_tile && kb == kt - 1) {
+          if (item == lose_item && kb == kt - 1) {
             prod.lost = prod.issued;
           } else {
             // (the even CTA's barrier counts the bytes of both CTAs' loads)
-            if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], Sh::CTAS * Sh::STAGE);
+            if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], Sh::CTAS * (half ? Sh::STAGE - 8192 : Sh::STAGE));
             if (A_MN)
               load_mn(a_at, ma, g.a_planes, a_row, k);
             else
               load(a_at, ma, k, a_row);
-            if (B_MN) {
+            if (half) {
+              load(b_at, &maps.b_half[which_b], B_MN ? b_row : k, B_MN ? k : b_row);
+            } else if (B_MN) {
               load_mn(b_at, mb, g.b_planes, b_row, k);
             } else if (GATED && !PAIR) {
               load(b_at, mb, k, b_row);
@@ -620,7 +646,8 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
         const uint64_t b0 = (B_MN ? umma_desc_mn(ring0) : umma_desc_sw128(ring0)) + Sh::A_BYTES / 16;
         // 16 along K: 32 bytes of a K-major row, 16 rows of 128 bytes of an MN-major tile
         constexpr uint32_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;
-        for (int tile = worker; ok && tile < tiles; tile += workers) {
+        for (int item = worker; ok && item < items; item += workers) {
+          const uint32_t idesc = item < g.whole ? g.idesc : g.idesc_half;
           for (int kc = 0; ok && kc < kt; kc += g.restart) {
             const int end = min(kc + g.restart, kt);
             if (!mbar_wait(&bar->acc_empty[a], aph ^ 1u, g.ctl, cta, kSiteMmaAccEmpty)) { ok = false; break; }
@@ -636,9 +663,9 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
               for (int kk = 0; kk < kFfnBK / 16; ++kk) {
                 const uint32_t more = kb > kc || kk > 0;
                 if (PAIR)
-                  umma_f16_pair(d, da + A_STEP * kk, db + B_STEP * kk, g.idesc, more);
+                  umma_f16_pair(d, da + A_STEP * kk, db + B_STEP * kk, idesc, more);
                 else
-                  umma_f16(d, da + A_STEP * kk, db + B_STEP * kk, g.idesc, more);
+                  umma_f16(d, da + A_STEP * kk, db + B_STEP * kk, idesc, more);
               }
               if (PAIR) umma_commit_pair(&bar->empty[s], 0x3); else umma_commit(&bar->empty[s]);
               if (++s == Sh::STAGES) { s = 0; ph ^= 1u; }
@@ -662,24 +689,27 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
     const int quarter = warp & 3;          // TMEM lanes this warp may access
     const int part = e >> 2;               // which of the tile's columns
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    // its output columns, and the TMEM columns of their sums: a gated product's second weight has its own BN / 2 further on
+    // its output columns, and the TMEM columns of their sums: a gated product's second weight has its own half of a tile
+    // further on.  Of a half tile the streaming warps take half of their columns each, the holding ones all or none.
     constexpr int OUTS = GATED ? Sh::EPI_COLS / 2 : Sh::EPI_COLS;
-    const uint32_t lo = part * OUTS, other = BN / 2;
     int a = 0;
     uint32_t aph = 0;
     bool ok = true;   // after a wait that gave up: nothing is written any more
-    for (int tile = worker; tile < tiles; tile += workers) {
-      int rb, cb;
-      const int problem = tile >= per_problem ? 1 : 0;
-      ring_tile(tile - problem * per_problem, row_blocks, col_blocks, g.raster, rb, cb);
-      const int64_t row = static_cast<int64_t>(rb) * Sh::TILE_ROWS + rank * Sh::A_ROWS + quarter * 32 + lane;
-      const int64_t col0 = static_cast<int64_t>(cb) * TILE_COLS + part * OUTS;
-      if (!GATED && g.o.add[problem] && row < g.rows) {
+    for (int item = worker; item < items; item += workers) {
+      const RingItem t = ring_item(item, g, row_blocks, col_blocks);
+      const int problem = t.problem;
+      const bool cut = PAIR && t.half >= 0;
+      const int outs = cut && OUT == kStream ? OUTS / 2 : OUTS;
+      const bool idle = cut && part * outs >= TILE_COLS / 2;
+      const uint32_t lo = part * outs, other = cut ? BN / 4 : BN / 2;
+      const int64_t row = static_cast<int64_t>(t.rb) * Sh::TILE_ROWS + rank * Sh::A_ROWS + quarter * 32 + lane;
+      const int64_t col0 = static_cast<int64_t>(t.cb) * TILE_COLS + (cut ? t.half * (TILE_COLS / 2) : 0) + part * outs;
+      if (!GATED && g.o.add[problem] && row < g.rows && !idle) {
         // this thread's row of the addend comes into L2 while the products run
         const int size = g.o.out_f32 ? 4 : 2;
         const uint8_t* at = static_cast<const uint8_t*>(g.o.add[problem]) + (row * g.o.ld_add[problem] + col0) * size;
 #pragma unroll 1
-        for (int i = 0; i < OUTS && col0 + i < g.cols; i += 128 / size) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * size));
+        for (int i = 0; i < outs && col0 + i < g.cols; i += 128 / size) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * size));
       }
       auto hand_back = [&]() {
         // the buffer has been read: back to the MMA issuer
@@ -701,9 +731,9 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
         }
         const uint32_t src = tmem + lanes + a * BN + lo;
         if (g.o.bf16)
-          stream_out<OUTS, GATED, __nv_bfloat16>(g, problem, src, other, sums, hand_back, lane, row, col0);
+          stream_out<GATED, __nv_bfloat16>(g, problem, outs, src, other, sums, hand_back, lane, row, col0);
         else
-          stream_out<OUTS, GATED, __half>(g, problem, src, other, sums, hand_back, lane, row, col0);
+          stream_out<GATED, __half>(g, problem, outs, src, other, sums, hand_back, lane, row, col0);
         if (sums && ++a == 2) { a = 0; aph ^= 1u; }
       } else {
         float acc[2][32];
@@ -717,6 +747,7 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
           const uint32_t src = tmem + lanes + a * BN + lo;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
+            if (idle) break;
             uint32_t v[16];
             tmem_ld_32x32b_x16(src + (j >> 1) * (GATED ? other : 32u) + (j & 1) * 16, v);
             tmem_wait_ld();
@@ -727,7 +758,7 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
           hand_back();
           if (++a == 2) { a = 0; aph ^= 1u; }
         }
-        const bool write = ok && row < g.rows;
+        const bool write = ok && row < g.rows && !idle;
         const uint32_t slot = smem_u32(maxima) + e * kMaxSlot;
         if constexpr (GATED) {
           if (g.o.bf16)
@@ -817,6 +848,13 @@ inline cudaError_t ffn_map(CUtensorMap* m, const FfnProduct& p, const void* base
                            CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// The same in boxes of 64 of its rows.
+inline cudaError_t ffn_map64(CUtensorMap* m, const FfnProduct& p, const void* base, int64_t ld, int64_t rows, bool mn) {
+  const uint64_t row_bytes = static_cast<uint64_t>(ld) * 2;
+  return mn ? make_tmap_2d(m, base, ffn_map_type(p.out), rows, p.summed, row_bytes, 64, kFfnBK, CU_TENSOR_MAP_SWIZZLE_128B)
+            : make_tmap_2d(m, base, ffn_map_type(p.out), p.summed, rows, row_bytes, kFfnBK, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 // With a register split, a kernel must have exactly kRingLaunchRegs at launch: with fewer, the increase would wait for ever.
 inline cudaError_t check_launch_regs(std::atomic<int>& regs, const void* kernel) {
   if (regs.load() < 0) {
@@ -842,6 +880,8 @@ cudaError_t launch_ring(FfnProduct& p, const void** kernel) {
     if ((e = ffn_map(&maps.b[0], p, p.b[0], p.ldb[0], p.cols, B_MN, b_box)) != cudaSuccess) return e;
     if ((sum || both) && (e = ffn_map(&maps.a[1], p, p.a[1], p.lda[1], p.rows, A_MN, 128)) != cudaSuccess) return e;
     if ((sum || GATED) && (e = ffn_map(&maps.b[1], p, p.b[1], p.ldb[1], p.cols, B_MN, b_box)) != cudaSuccess) return e;
+    for (int i = 0; PAIR && p.plan.half_tiles && i < (sum || GATED ? 2 : 1); ++i)
+      if ((e = ffn_map64(&maps.b_half[i], p, p.b[i], p.ldb[i], p.cols, B_MN)) != cudaSuccess) return e;
   }
   RingParams g = {};
   g.o = p.out;
@@ -854,6 +894,9 @@ cudaError_t launch_ring(FfnProduct& p, const void** kernel) {
   g.restart = wide ? kFfnRestart : (g.kt > 0 ? g.kt * g.sources : 1);
   g.raster = p.plan.raster_gm;
   g.idesc = umma_idesc_f16(p.out.bf16 != 0, Sh::TILE_ROWS, BN) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
+  g.idesc_half = umma_idesc_f16(p.out.bf16 != 0, Sh::TILE_ROWS, BN / 2) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
+  g.whole = static_cast<int32_t>(p.plan.tiles) - p.plan.half_tiles;
+  g.items = g.whole + 2 * p.plan.half_tiles;
   g.a_planes = A_MN && p.rows % 64 == 0;
   g.b_planes = B_MN && p.cols % 64 == 0;
   g.ctl = p.ctl;

@@ -38,6 +38,14 @@ void ring_shape_of(gp_plan* p) {
 
 int64_t blocks(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
+// The tiles of pairs behind the last full round are cut in halves where those make one round at most (not where a group
+// of 128 columns kept in 8 bits would be cut: whole_groups).
+void ffn_cut_tail(gp_plan* p, bool whole_groups) {
+  const int64_t pairs = p->grid / 2, rest = p->cta_pair && pairs > 0 ? p->tiles % pairs : 0;
+  p->half_tiles = !whole_groups && p->tiles > pairs && 2 * rest <= pairs ? static_cast<int32_t>(rest) : 0;
+  p->dp_tiles = static_cast<int32_t>(p->tiles) - p->half_tiles;
+}
+
 }  // namespace
 
 int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count, bool wide_sums, bool codes, int sms,
@@ -143,16 +151,19 @@ int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count,
     const int64_t ctas = p->cta_pair ? 2 : 1, workers = sms / ctas;
     p->grid = static_cast<int32_t>(ctas * (p->tiles < workers ? p->tiles : workers));
   }
-  p->dp_tiles = static_cast<int32_t>(p->tiles);
+  ffn_cut_tail(p, gated && codes);
   p->compute_load_ratio = 2.0 * p->bm * p->bn / (p->bm + p->bn);
   return GP_OK;
 }
 
-cudaError_t ffn_fit_pairs(gp_plan* plan) {
+cudaError_t ffn_fit_pairs(gp_plan* plan, bool whole_groups) {
   if (!plan->cta_pair) return cudaSuccess;
   int pairs = 0;
   const cudaError_t e = pair_capacity(&pairs);
-  if (e == cudaSuccess && 2 * pairs < plan->grid) plan->grid = 2 * pairs;
+  if (e == cudaSuccess && 2 * pairs < plan->grid) {
+    plan->grid = 2 * pairs;
+    ffn_cut_tail(plan, whole_groups);
+  }
   return e;
 }
 

@@ -134,6 +134,28 @@ def test_linear_every_tile(tile, M, N, K):
         check_linear(M, N, K, BF16, "gelu", bias=BF16, keep="fp8", tile=tile)
 
 
+@pytest.mark.parametrize("M,N", [(2560, 2304), (2300, 2500), (5000, 1100)])
+def test_tiles_cut_in_halves(M, N):
+    """More tiles of two CTAs than pairs, and few enough in the last round: those are cut in halves of their columns."""
+    for K in (64, 200):
+        plan = check_linear(M, N, K, BF16, "relu", bias=BF16, residual=True, whole=2, tile=256)
+        assert plan["half_tiles"] > 0 and plan["dp_tiles"] + plan["half_tiles"] == plan["tiles"]
+        check_linear(M, N, K, F16, whole=2, out_dtype=F32, residual=True, tile=256)
+        check_linear(M, N, K, F16, whole=2, keep="fp8", tile=256)
+        assert check_gated(M, N // 2, K, BF16, keep="real", tile=256)["half_tiles"] > 0
+        assert check_gated(M, N // 2, K, BF16, keep="fp8", tile=256)["half_tiles"] == 0
+    rng = np.random.default_rng(1)
+    for K in (64, 200):
+        dy, x, w = (ref.matrix(rng, r, c, BF16, whole=1) for r, c in ((K, M), (K, N), (M, N)))
+        _, dw, _ = gp.linear_backward(dy, x, w, input_grad=False, out_dtype=F32, tile=256)       # M x N of K tokens
+        assert gp.gemm_stats()["plan"]["half_tiles"] > 0
+        assert torch.equal(dw.cpu().double(), dy.cpu().double().t() @ x.cpu().double())
+        dy, w = ref.matrix(rng, M, K, BF16, whole=1), ref.matrix(rng, K, N, BF16, whole=1)
+        dx, _, _ = gp.linear_backward(dy, ref.matrix(rng, M, N, BF16), w, weight_grad=False, tile=256)
+        assert gp.gemm_stats()["plan"]["half_tiles"] > 0
+        assert torch.equal(dx.cpu(), (dy.cpu().double() @ w.cpu().double()).to(BF16))
+
+
 @pytest.mark.parametrize("M", [1, 40, 130, 600])
 @pytest.mark.parametrize("pads,ld", [((0, 8, 0), None), ((1, 3, 5), 301), ((8, 8, 4), 308), ((7, 0, 1), 304)])
 @pytest.mark.parametrize("out", [BF16, F32])
