@@ -24,7 +24,7 @@
  *
  * Products are summed in FP32 by the tensor cores, which cut instead of
  * rounding; where an output is FP32, or 8-bit codes with FP32 scales, that sum
- * is restarted every 512 of the summed axis and the parts are added in FP32.
+ * is restarted every 768 of the summed axis and the parts are added in FP32.
  * Everything up to an output's one rounding is FP32.
  *
  * Activations (act'(0) of relu is 0):

@@ -24,7 +24,7 @@
 // zero (measured on normal operands: 1.0e-6 relative after 1024 of K, 9e-6 after
 // 8192).  For 16-bit outputs that is far below their rounding (2^-9 on average
 // for BF16).  Where FP32 leaves, or the scales of 8-bit codes, the accumulator is
-// handed over every kFfnRestart slots (512 of K) and added to sums in registers.
+// handed over every kFfnRestart slots (768 of K) and added to sums in registers.
 #pragma once
 #include <atomic>
 #include <cstring>
@@ -309,12 +309,13 @@ __device__ __forceinline__ void add_bias(float* v, const FfnOut& o, int lane, in
 
 // out = act(v) + addend, and v itself where it is kept: a lane's 32 columns.
 template <typename T, typename O>
-__device__ __forceinline__ void emit_row(const FfnOut& o, int p, float (&v)[32], int64_t row, int64_t first, int n) {
+__device__ __forceinline__ void emit_row(const FfnOut& o, int p, float (&v)[32], int64_t row, int64_t first, int n,
+                                         bool with_addend = true) {
   constexpr int N = Sector<O>::N;
   O* const out = static_cast<O*>(o.out[p]) + row * o.ld_out[p] + first;
   if (o.keep[0]) store_row(static_cast<T*>(o.keep[0]) + row * o.ld_keep[0] + first, v, n, o.vec);
   activate_all(v, o.act);
-  if (o.add[p]) {
+  if (o.add[p] && with_addend) {
     // 16-bit addends all at once, FP32 ones sector by sector, as registers allow; each before its output is written, which
     // may be the same memory
     const O* const add = static_cast<const O*>(o.add[p]) + row * o.ld_add[p] + first;
@@ -334,6 +335,19 @@ __device__ __forceinline__ void emit_row(const FfnOut& o, int p, float (&v)[32],
     return;
   }
   store_row(out, v, n, o.vec);
+}
+
+// An FP32 addend's 64 columns, where the sums begin.
+__device__ __forceinline__ void load_addend(float (&acc)[2][32], const FfnOut& o, int p, int64_t row, int64_t col0, int64_t cols) {
+  const float* const add = static_cast<const float*>(o.add[p]) + row * o.ld_add[p] + col0;
+  const int n = cols - col0 < 64 ? static_cast<int>(cols - col0) : 64;   // (may be < 0)
+#pragma unroll
+  for (int i = 0; i < 64; i += 8) {
+    Sector<float> s;
+    load_sector(s, add + i, n - i, o.vec);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[i >> 5][(i & 31) + k] = sector_value(s, k);
+  }
 }
 
 // h = act(g) * u, and g and u themselves where they are kept: a lane's 32 columns.
@@ -447,10 +461,10 @@ __device__ __forceinline__ void emit_codes(const FfnCodes& q, const float* v, fl
 }
 
 // out = act(s + bias) + addend of a lane's 64 columns; `part`: which 64 of the tile's columns.  write false: nothing is
-// written (the row does not exist, or its sums did not come).
+// written (the row does not exist, or its sums did not come); `added`: the sums began with the addend.
 template <typename T, typename O>
 __device__ __forceinline__ void finish_linear(const RingParams& g, int p, float (&acc)[2][32], uint32_t slot, int lane,
-                                              int quarter, int part, int64_t row, int64_t col0, bool write) {
+                                              int quarter, int part, int64_t row, int64_t col0, bool write, bool added) {
   const FfnOut& o = g.o;
   const int64_t cols = g.cols;
   if (o.bias) {
@@ -475,7 +489,8 @@ __device__ __forceinline__ void finish_linear(const RingParams& g, int p, float 
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    if (write && col0 + 32 * j < cols) emit_row<T, O>(o, p, acc[j], row, col0 + 32 * j, columns_left(col0 + 32 * j, cols));
+    if (write && col0 + 32 * j < cols)
+      emit_row<T, O>(o, p, acc[j], row, col0 + 32 * j, columns_left(col0 + 32 * j, cols), !added);
   __syncwarp();
 }
 
@@ -695,6 +710,8 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
     int a = 0;
     uint32_t aph = 0;
     bool ok = true;   // after a wait that gave up: nothing is written any more
+    const bool add_first = OUT == kHold && !GATED && g.o.out_f32 && g.o.add[0] && g.o.act == GP_ACT_NONE && !g.o.keep[0] &&
+                           !g.o.codes[0].data;
     for (int item = worker; item < items; item += workers) {
       const RingItem t = ring_item(item, g, row_blocks, col_blocks);
       const int problem = t.problem;
@@ -704,7 +721,7 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
       const uint32_t lo = part * outs, other = cut ? BN / 4 : BN / 2;
       const int64_t row = static_cast<int64_t>(t.rb) * Sh::TILE_ROWS + rank * Sh::A_ROWS + quarter * 32 + lane;
       const int64_t col0 = static_cast<int64_t>(t.cb) * TILE_COLS + (cut ? t.half * (TILE_COLS / 2) : 0) + part * outs;
-      if (!GATED && g.o.add[problem] && row < g.rows && !idle) {
+      if (!GATED && g.o.add[problem] && row < g.rows && !idle && !add_first) {
         // this thread's row of the addend comes into L2 while the products run
         const int size = g.o.out_f32 ? 4 : 2;
         const uint8_t* at = static_cast<const uint8_t*>(g.o.add[problem]) + (row * g.o.ld_add[problem] + col0) * size;
@@ -739,6 +756,10 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
         float acc[2][32];
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i >> 5][i & 31] = 0.f;
+        if constexpr (!GATED) {
+          // an FP32 addend with nothing between it and the sums is what they are added to: it comes while the products run
+          if (add_first && row < g.rows && !idle) load_addend(acc, g.o, problem, row, col0, g.cols);
+        }
 #pragma unroll 1
         for (int kc = 0; kc < kt; kc += g.restart) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bar->acc_full[a], aph, g.ctl, cta, kSiteEpilogueAccFull));
@@ -768,14 +789,14 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
         } else {
           if (g.o.bf16) {
             if (g.o.out_f32)
-              finish_linear<__nv_bfloat16, float>(g, problem, acc, slot, lane, quarter, part, row, col0, write);
+              finish_linear<__nv_bfloat16, float>(g, problem, acc, slot, lane, quarter, part, row, col0, write, add_first);
             else
-              finish_linear<__nv_bfloat16, __nv_bfloat16>(g, problem, acc, slot, lane, quarter, part, row, col0, write);
+              finish_linear<__nv_bfloat16, __nv_bfloat16>(g, problem, acc, slot, lane, quarter, part, row, col0, write, false);
           } else {
             if (g.o.out_f32)
-              finish_linear<__half, float>(g, problem, acc, slot, lane, quarter, part, row, col0, write);
+              finish_linear<__half, float>(g, problem, acc, slot, lane, quarter, part, row, col0, write, add_first);
             else
-              finish_linear<__half, __half>(g, problem, acc, slot, lane, quarter, part, row, col0, write);
+              finish_linear<__half, __half>(g, problem, acc, slot, lane, quarter, part, row, col0, write, false);
           }
         }
       }

@@ -13,7 +13,7 @@ UNIT = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8, torch.float32: 2.0
 LEAST = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134, torch.float32: 2.0 ** -150}
 LARGEST = {torch.float16: 65520.0, torch.bfloat16: math.inf, torch.float32: math.inf}
 ACTS = [None, "relu", "gelu", "gelu_tanh", "silu", "sigmoid"]
-RESTART = 512          # of the summed axis per accumulator where FP32 leaves
+RESTART = 768          # of the summed axis per accumulator where FP32 leaves
 
 
 def f64(t):
@@ -61,9 +61,9 @@ def steps(z):
 def sum_error(mag, summed, wide):
     """Largest error of a sum of `summed` products whose magnitudes add up to `mag`: the tensor cores cut each product's
     addition by 2^-23 of the sum of magnitudes so far at most; where FP32 leaves, they do so over RESTART products at a
-    time, and those parts are added with 2^-24."""
+    time, and those parts, and an addend that the sum may begin with, are added with 2^-24 each."""
     if wide:
-        return (min(summed, RESTART) * 2.0 ** -23 + (summed // RESTART + 1) * 2.0 ** -24) * mag
+        return (min(summed, RESTART) * 2.0 ** -23 + (summed // RESTART + 2) * 2.0 ** -24) * mag
     return (summed * 2.0 ** -23 + 2.0 ** -24) * mag
 
 

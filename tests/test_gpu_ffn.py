@@ -44,7 +44,7 @@ def check_linear(M, N, K, dtype=BF16, act=None, bias=None, residual=False, keep=
     yerr = 1.2 * err + ref.steps(z) * 2.0 ** -24 * np.abs(y) if act else err      # (no activation's slope is above 1.13)
     if r is not None:
         y = y + ref.f64(r)
-        yerr = yerr + 2.0 ** -24 * np.abs(y)
+        yerr = yerr + (K // ref.RESTART + 2) * 2.0 ** -24 * (np.abs(y) + np.abs(ref.f64(r)))
     worst = ref.worst(ref.f64(out), y, ref.rounded(y, yerr, out_dtype), out_dtype)
     assert worst <= 1.0, "%g of the bound (plan %s)" % (worst, plan)
     assert ref.outside_untouched(buf, M, N, ld or N), "write outside of the output"
@@ -291,8 +291,8 @@ def check_products(dz, edz, x, w, dx, dw, addend=None):
             ge = ge + ref.sum_error((np.abs(z) + e).T @ np.abs(a), len(a), got.dtype is F32)
             if addend is not None:
                 i = [j for j, t in enumerate(dw) if t is got][0]
+                ge = ge + (len(a) // ref.RESTART + 2) * 2.0 ** -24 * (np.abs(g) + np.abs(ref.f64(addend[i])))
                 g = g + ref.f64(addend[i])
-                ge = ge + 2.0 ** -24 * np.abs(g)
             far = ref.worst(ref.f64(got), g, ref.rounded(g, ge, got.dtype), got.dtype)
             assert far <= 1.0, "weight gradient: %g of the bound" % far
     if dx is not None:
