@@ -434,14 +434,19 @@ PyObject* linear_backward(PyObject* const* a) {
   const Matrix md = matrix(dy, "dy");
   const int64_t M = md.rows, N = md.cols;
   // everything is looked over before the first launch
-  const at::Tensor &x = tensor(a[1], "x"), &w = tensor(a[2], "weight");
-  const Matrix vx = matrix(x, "x"), vw = matrix(w, "weight");
-  if (vx.rows != M || vw.rows != N || vw.cols != vx.cols)
-    throw Refused{"dy is " + shape_of(dy) + " and x " + shape_of(x) + ": the weight is " + shape_of(w)};
+  const at::Tensor& w = tensor(a[2], "weight");
+  const Matrix vw = matrix(w, "weight");
+  if (vw.rows != N) throw Refused{"dy is " + shape_of(dy) + ": the weight is " + shape_of(w)};
+  Operand mx, mw;
+  if (want_w || a[1] != Py_None) {
+    const at::Tensor& x = tensor(a[1], "x");
+    const Matrix vx = matrix(x, "x");
+    if (vx.rows != M || vw.cols != vx.cols)
+      throw Refused{"dy is " + shape_of(dy) + " and x " + shape_of(x) + ": the weight is " + shape_of(w)};
+    if (want_w) mx = operand(x, "x", &dy, call);
+  }
   Kept kept;
   if (act != GP_ACT_NONE) read_kept(a[4], 1, M, N, dy, &kept);
-  Operand mx, mw;
-  if (want_x || want_w) mx = operand(x, "x", &dy, call);
   if (want_x) mw = operand(w, "weight", &dy, call);
   at::Tensor dz, dbias, work, dx, dw;
   Operand md16;
@@ -479,7 +484,7 @@ PyObject* linear_backward(PyObject* const* a) {
     } else {
       md16 = operand(dy, "dy", nullptr, call);
     }
-    if (want_x) dx = input_gradient(1, &md16, &mw, M, N, vx.cols, real, dy, call, opts);
+    if (want_x) dx = input_gradient(1, &md16, &mw, M, N, vw.cols, real, dy, call, opts);
     if (want_w) weight_gradients(1, &md16, mx, N, real, a[8], a[9], a[10], dy, call, opts, &dw);
   }
   return tuple({dx, dw, dbias});
@@ -498,14 +503,20 @@ PyObject* gated_backward(PyObject* const* a) {
     throw Refused{"addend takes 2 matrices"};
   const Matrix md = matrix(dh, "dh");
   const int64_t M = md.rows, N = md.cols;
-  const at::Tensor &x = tensor(a[1], "x"), &wg = tensor(a[2], "w_gate"), &wu = tensor(a[3], "w_up");
-  const Matrix vx = matrix(x, "x"), vg = matrix(wg, "w_gate"), vu = matrix(wu, "w_up");
-  if (vx.rows != M || vg.rows != N || vu.rows != N || vg.cols != vx.cols || vu.cols != vx.cols)
-    throw Refused{"dh is " + shape_of(dh) + " and x " + shape_of(x) + ": the weights are " + shape_of(wg) + " and " + shape_of(wu)};
+  const at::Tensor &wg = tensor(a[2], "w_gate"), &wu = tensor(a[3], "w_up");
+  const Matrix vg = matrix(wg, "w_gate"), vu = matrix(wu, "w_up");
+  if (vg.rows != N || vu.rows != N || vu.cols != vg.cols)
+    throw Refused{"dh is " + shape_of(dh) + ": the weights are " + shape_of(wg) + " and " + shape_of(wu)};
+  Operand mx, mw[2];
+  if (want_w || a[1] != Py_None) {
+    const at::Tensor& x = tensor(a[1], "x");
+    const Matrix vx = matrix(x, "x");
+    if (vx.rows != M || vx.cols != vg.cols)
+      throw Refused{"dh is " + shape_of(dh) + " and x " + shape_of(x) + ": the weights are " + shape_of(wg) + " and " + shape_of(wu)};
+    if (want_w) mx = operand(x, "x", &dh, call);
+  }
   Kept kept[2];
   read_kept(a[4], 2, M, N, dh, kept);
-  Operand mx, mw[2];
-  if (want_w) mx = operand(x, "x", &dh, call);
   if (want_x) {
     mw[0] = operand(wg, "w_gate", &dh, call);
     mw[1] = operand(wu, "w_up", &dh, call);
@@ -537,7 +548,7 @@ PyObject* gated_backward(PyObject* const* a) {
   g.type = real;
   g.activation = static_cast<int32_t>(PyLong_AsLong(a[5]));
   check(lib.gated_backward(&g, call.stream), "ffn_gated_backward");
-  if (want_x) dx = input_gradient(2, dz, mw, M, N, vx.cols, real, dh, call, opts);
+  if (want_x) dx = input_gradient(2, dz, mw, M, N, vg.cols, real, dh, call, opts);
   if (want_w) weight_gradients(2, dz, mx, N, real, a[9], a[10], a[11], dh, call, opts, dw);
   return product ? tuple({dx, dw[0], dw[1], h}) : tuple({dx, dw[0], dw[1]});
 }

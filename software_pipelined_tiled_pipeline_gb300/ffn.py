@@ -115,7 +115,8 @@ def linear_backward(dy, x, weight, *, activation=None, kept=None, bias_grad=Fals
     dx has x's type, dweight x's type or ``out_dtype`` (float32), and is written
     to ``out`` if given; ``addend`` (of dweight's type, may be ``out`` itself) is
     added to it in FP32.  dbias (float32) is summed from dz before its rounding.
-    What is not asked for (``input_grad``, ``weight_grad``, ``bias_grad``) is None.
+    What is not asked for (``input_grad``, ``weight_grad``, ``bias_grad``) is None;
+    without ``weight_grad`` x may be None too.
     """
     if stream is not None:
         with _On(_device_of(dy, "dy"), stream):
@@ -135,6 +136,7 @@ def gated_backward(dh, x, w_gate, w_up, kept, *, activation="silu", product=Fals
     products are rounded to x's type for the products behind them.  ``out_dtype``,
     ``addend``, ``out`` as in ``linear_backward``, the last two a pair each.
     h, for the gradient of the weight that reads it, need not have been kept.
+    Without ``weight_grad`` x may be None.
     """
     if stream is not None:
         with _On(_device_of(dh, "dh"), stream):

@@ -413,3 +413,241 @@ def test_gated_backward_shapes(M, N, K, dtype):
 def test_gated_backward_activations(act, keep, fmt):
     check_gated_backward(150, 264, 200, F16, act, keep, fmt=fmt)
     check_gated_backward(150, 261, 200, BF16, act, keep, fmt=fmt)
+
+
+# ---------------------------------------------------------------------------
+# calls together: streams, graphs, threads, refusals, waits that run out
+# ---------------------------------------------------------------------------
+def block_pass(x, w, wd, b, r):
+    """A gated block forward and backward, as a program calls it."""
+    h, kept = gp.gated(x, w[0], w[1], keep="fp8")
+    y, z = gp.linear(h, wd, b, activation="gelu", residual=r, keep="real")
+    dh, dwd, db = gp.linear_backward(y, h, wd, activation="gelu", kept=z, bias_grad=True)
+    dx, dg, du, again = gp.gated_backward(dh, x, w[0], w[1], kept, product=True)
+    return h, y, dh, dwd, db, dx, dg, du, again, kept[0].view(torch.uint8), kept[1]
+
+
+def block_operands(M, N, K, seed):
+    rng = np.random.default_rng(seed)
+    x, r = ref.matrix(rng, M, K, BF16), ref.matrix(rng, M, K, BF16)
+    w = [ref.matrix(rng, N, K, BF16, 0.05) for _ in range(2)]
+    return x, w, ref.matrix(rng, K, N, BF16, 0.05), ref.matrix(rng, 1, K, BF16)[0], r
+
+
+SIZES = [(1, 200, 136), (48, 520, 264), (300, 640, 333), (2000, 1100, 520)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_repeated_calls_give_the_same_bits(M, N, K):
+    ops = block_operands(M, N, K, 3)
+    first = [t.clone() for t in block_pass(*ops)]
+    for _ in range(3):
+        for a, b in zip(first, block_pass(*ops)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_chained_calls_in_a_graph(M, N, K):
+    """A captured pass replayed on new inputs, and two graphs that share what can be shared, give what the calls give."""
+    ops, other = block_operands(M, N, K, 1), block_operands(M, N, K, 2)
+    want, want_other = [[t.clone() for t in block_pass(*o)] for o in (ops, other)]
+    stream = torch.cuda.Stream()
+    graphs, outs = [], []
+    for o in (ops, other):
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            block_pass(*o)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            outs.append(block_pass(*o))
+        graphs.append(g)
+    for _ in range(2):
+        for g in graphs:
+            g.replay()
+    block_pass(*ops)                      # an eager call between replays
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    for got, w in ((outs[0], want), (outs[1], want_other)):
+        for a, b in zip(got, w):
+            assert torch.equal(a, b)
+    ops[0].copy_(other[0])                # new inputs in the same memory
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    for a, b in zip(outs[0], block_pass(*ops)):
+        assert torch.equal(a, b)
+
+
+def test_streams():
+    """Calls on a stream of their own, given as an argument or made current, after work on another one."""
+    x, w, wd, b, r = block_operands(300, 640, 264, 5)
+    want = gp.gated(x, *w)
+    side = torch.cuda.Stream()
+    late = torch.empty_like(x)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(x)
+        got = gp.gated(late, *w)          # after the copy on the same stream
+    side.synchronize()
+    assert torch.equal(got, want)
+    late.zero_()
+    torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(x)
+    got = gp.gated(late, *w, stream=side)
+    y = gp.linear(got, wd, b, stream=side)
+    d = gp.linear_backward(y, got, wd, bias_grad=True, stream=side)
+    e = gp.gated_backward(got, late, *w, (want, want), stream=side)
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(y, gp.linear(want, wd, b))
+    for a, c in zip(d, gp.linear_backward(y, got, wd, bias_grad=True)):
+        assert torch.equal(a, c)
+    for a, c in zip(e, gp.gated_backward(want, x, *w, (want, want))):
+        assert torch.equal(a, c)
+
+
+def test_two_threads():
+    """Two host threads on streams of their own."""
+    import threading
+    sizes = [(40, 520, 264), (700, 640, 520)]
+    ops = [block_operands(*s, 7 + i) for i, s in enumerate(sizes)]
+    want = [[t.clone() for t in block_pass(*o)] for o in ops]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got = block_pass(*ops[i])
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+@pytest.mark.parametrize("tile,splits", [(16, 1), (32, 4), (64, 2), (129, 2), (128, 0)])
+def test_a_lost_load_is_reported(tile, splits):
+    """A load that never comes: the waits give up, the status says so, and the next call is right."""
+    x, w, _, _, _ = block_operands(100, 384, 1500, 4)
+    want = gp.linear(x, w[0], tile=tile, k_splits=splits)
+    got = torch.full_like(want, 7.0)
+    gp.linear(x, w[0], out=got, tile=tile, k_splits=splits, timeout_ns=5_000_000, inject_lost_load=True)
+    assert gp.gemm_stats(sync=True)["status"] == gp.GP_ERR_TIMEOUT
+    # tiles that came to their end are right, the others are as they were
+    assert bool(((got == want) | (got == 7.0)).all()) and bool((got == 7.0).any())
+    if tile != 129:
+        h = torch.full((100, 384), 7.0, dtype=BF16, device="cuda")
+        gp.gated(x, *w, out=h, tile=tile, k_splits=splits, timeout_ns=5_000_000, inject_lost_load=True)
+        assert gp.gemm_stats(sync=True)["status"] == gp.GP_ERR_TIMEOUT
+    assert torch.equal(gp.linear(x, w[0], tile=tile, k_splits=splits), want)
+    status_ok()
+
+
+def test_lost_load_not_where_two_ctas_share_a_tile():
+    x, w, _, _, _ = block_operands(600, 384, 200, 4)
+    with pytest.raises(gp.GemmError):
+        gp.linear(x, w[0], tile=256, inject_lost_load=True)
+    with pytest.raises(gp.GemmError):
+        gp.gated(x, *w, keep="fp8", inject_lost_load=True)
+
+
+def test_input_gradient_without_x():
+    x, w, wd, b, r = block_operands(70, 200, 136, 6)
+    z = torch.ones(70, 200, dtype=BF16, device="cuda")
+    dx, none, _ = gp.linear_backward(z, None, w[0], weight_grad=False)
+    assert none is None and torch.equal(dx, gp.linear_backward(z, x, w[0])[0])
+    got = gp.gated_backward(z, None, *w, (z, z), weight_grad=False)
+    assert got[1] is None and got[2] is None and torch.equal(got[0], gp.gated_backward(z, x, *w, (z, z))[0])
+    none, dw, _ = gp.linear_backward(z, x, w[0], input_grad=False)
+    assert none is None and torch.equal(dw, gp.linear_backward(z, x, w[0])[1])
+    assert gp.linear_backward(z, None, w[0], input_grad=False, weight_grad=False) == (None, None, None)
+
+
+def test_refusals():
+    x, w, wd, b, r = block_operands(20, 64, 40, 6)
+    z = torch.zeros(20, 64, dtype=BF16, device="cuda")
+    data, scales = gp.quantize_fp8(z)
+    blocks = gp.quantize_fp8(z, "blocks")
+    cases = [
+        lambda: gp.linear(x.float(), w[0]), lambda: gp.linear(x, w[0].half()), lambda: gp.linear(x, w[0].cpu()),
+        lambda: gp.linear(x, wd), lambda: gp.linear(x[0], w[0]), lambda: gp.linear(x.t(), w[0].t()),
+        lambda: gp.linear(x, w[0], b), lambda: gp.linear(x, w[0], z[0].half()), lambda: gp.linear(x, w[0], activation="tanh"),
+        lambda: gp.linear(x, w[0], keep="fp16"), lambda: gp.linear(x, w[0], residual=r), lambda: gp.linear(x, w[0], residual=z.float()),
+        lambda: gp.linear(x, w[0], out_dtype=F16), lambda: gp.linear(x, w[0], out=z, out_dtype=F32),
+        lambda: gp.linear(x, w[0], out=z.half()), lambda: gp.linear(x, w[0], out=z[:10]),
+        lambda: gp.gated(x, w[0], wd), lambda: gp.gated(x, w[0], w[1][:10]), lambda: gp.gated(x, *w, activation="swish"),
+        lambda: gp.gated(x, *w, out=z.float()), lambda: gp.gated(x, *w, keep=1),
+        lambda: gp.linear_backward(z, x, wd), lambda: gp.linear_backward(z, x[:4], w[0], weight_grad=False),
+        lambda: gp.linear_backward(z, wd, w[0], weight_grad=False), lambda: gp.linear_backward(z[:4], x, w[0]),
+        lambda: gp.linear_backward(z, x, w[0], activation="gelu"), lambda: gp.linear_backward(z, x, w[0], kept=(z,)),
+        lambda: gp.linear_backward(z, x, w[0], activation="gelu", kept=(z.half(),)),
+        lambda: gp.linear_backward(z, x, w[0], activation="gelu", kept=(z[:, :32],)),
+        lambda: gp.linear_backward(z, x, w[0], activation="gelu", kept=(data, scales[:1])),
+        lambda: gp.linear_backward(z, x, w[0], activation="gelu", kept=(data, blocks[1])),
+        lambda: gp.linear_backward(z, x, w[0], activation="gelu", kept=(z, scales)),
+        lambda: gp.linear_backward(z, x, w[0], activation="gelu", kept=(data, scales, data)),
+        lambda: gp.linear_backward(z, x, w[0], weight_grad=False, addend=w[0]),
+        lambda: gp.linear_backward(z, x, w[0], addend=w[0], out_dtype=F32), lambda: gp.linear_backward(z, x, w[0], out=wd),
+        lambda: gp.linear_backward(z, x.half(), w[0]), lambda: gp.linear_backward(z, x, w[0], addend=(w[0], w[1])),
+        lambda: gp.gated_backward(z, x, *w, None), lambda: gp.gated_backward(z, x, *w, (z,)), lambda: gp.gated_backward(z, x, *w, z),
+        lambda: gp.gated_backward(z, x, *w, (data, scales, z, scales)), lambda: gp.gated_backward(z, x, w[0], wd, (z, z)),
+        lambda: gp.gated_backward(z, x, *w, (z, z), addend=w[0]), lambda: gp.gated_backward(z, x, *w, (z, z), addend=(w[0], None)),
+        lambda: gp.gated_backward(z, x, *w, (z, z), out=[w[0]]), lambda: gp.gated_backward(z, x, *w, (z, z), weight_grad=False, out=w),
+    ]
+    for i, call in enumerate(cases):
+        with pytest.raises(ValueError):
+            call()
+            print("case", i)
+    for call in (lambda: gp.linear(None, w[0]), lambda: gp.linear_backward(z, None, w[0]), lambda: gp.gated_backward(z, None, *w, (z, z)), lambda: gp.linear(x, "w"), lambda: gp.linear(x, w[0], out_dtype=3),
+                 lambda: gp.gated_backward(z, x, *w, (z, "z"))):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    # what the library refuses: rows that overlap, unknown tiles
+    wide = torch.zeros(2, 64, dtype=BF16, device="cuda")[:1].expand(20, 64)
+    for call in (lambda: gp.linear(wide, w[0].new_zeros(8, 64)), lambda: gp.linear(x, w[0], tile=48),
+                 lambda: gp.linear(x, w[0], tile=16, k_splits=8), lambda: gp.linear_backward(z, x, w[0], tile=32)):
+        with pytest.raises((gp.GemmError, ValueError)):
+            call()
+    assert torch.equal(gp.linear(x, w[0]), gp.linear(x, w[0]))      # (still in order)
+    status_ok()
+
+
+def test_gradients_against_differences():
+    """dx, dW and db against the quotient of differences of the forward calls, in directions of their own."""
+    rng = np.random.default_rng(8)
+    M, N, K = 40, 72, 56
+
+    def normal(*s):
+        return torch.from_numpy(rng.standard_normal(s)).cuda()
+
+    for act in ref.ACTS[2:]:
+        x, w, u, b = normal(M, K) / 4, normal(N, K) / 4, normal(N, K) / 4, normal(N)
+        dy = normal(M, N)
+        low = [t.to(F16) for t in (x, w, u, b, dy)]
+        z = low[0].double() @ low[1].double().t() + low[3].double()
+        dx, dw, db = gp.linear_backward(low[4], low[0], low[1], activation=act, kept=(z.to(F16),), bias_grad=True)
+
+        def loss(x, w, b):
+            z = ref.f64(x) @ ref.f64(w).T + ref.f64(b)
+            return float((ref.value(z, act) * ref.f64(low[4])).sum())
+
+        base = [low[0].double(), low[1].double(), low[3].double()]
+        for i, g in enumerate((dx, dw, db)):
+            d = torch.from_numpy(rng.standard_normal(tuple(base[i].shape))).cuda()
+            step = 1e-5
+            plus, minus = [list(base), list(base)]
+            plus[i], minus[i] = base[i] + step * d, base[i] - step * d
+            want = (loss(*plus) - loss(*minus)) / (2 * step)
+            got = float((g.double() * d).sum())
+            # each factor was rounded to 11 bits three times at most (z, dz, the gradient): that many units of the sum of
+            # magnitudes of what was added up
+            scale = float((g.double() * d).abs().sum()) + abs(want)
+            assert abs(got - want) <= 3 * 2.0 ** -11 * 4 * scale, (act, i, got, want)
