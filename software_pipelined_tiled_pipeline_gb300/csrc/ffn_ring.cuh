@@ -96,7 +96,6 @@ struct RingParams {
   int32_t whole;             // tiles that are not cut in halves: the first ones
   int32_t items;             // these, and the halves
   uint32_t idesc, idesc_half;
-  int32_t a_planes, b_planes;   // an MN-major operand's 128 rows come as one box of two planes of 64
   KernelCtl ctl;
 };
 
@@ -128,6 +127,15 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       "[%2];" ::"r"(dst),
       "l"(map), "r"(bar_cluster_addr), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// How 128 rows of an MN-major operand come: as one box of two planes of 64 (0) where
+// its last whole plane reaches that far, or it ends with one; else in boxes of 64,
+// of which the second is left out where no row of it exists (its slot then holds
+// what it held: those rows' sums are not written).
+__device__ __forceinline__ int mn_boxes(int row, int rows) {
+  if (rows % 64 == 0 || row + 128 <= (rows & ~63)) return 0;
+  return row + 64 >= rows ? 1 : 2;
 }
 
 // Instruction descriptor bits 15 and 16: operand A, B is MN-major.
@@ -527,7 +535,8 @@ __device__ __forceinline__ void finish_gated(const RingParams& g, float (&acc)[2
 // ---------------------------------------------------------------------------
 // Maps: a of the first and second source or product, b likewise, or of the two weights of a gated product.
 struct RingMaps {
-  CUtensorMap a[2], b[2], b_half[2];   // (b in boxes of 64 of its rows, for half tiles)
+  CUtensorMap a[2], b[2];
+  CUtensorMap a64[2], b64[2];          // in boxes of 64 of their rows: an MN-major operand's end, half tiles
 };
 
 template <int BN, bool PAIR, RingOut OUT, bool GATED, bool A_MN, bool B_MN>
@@ -597,6 +606,19 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
         const bool half = PAIR && t.half >= 0;
         const int b_row = !half ? (GATED ? t.cb * TILE_COLS : t.cb * BN + static_cast<int>(rank) * Sh::B_ROWS)
                                 : t.cb * TILE_COLS + t.half * (TILE_COLS / 2) + (GATED ? 0 : static_cast<int>(rank) * 64);
+        // boxes of either operand, and the bytes of a slot over all CTAs
+        const int a_boxes = A_MN ? mn_boxes(a_row, g.rows) : 0, b_boxes = B_MN && !half ? mn_boxes(b_row, g.cols) : 0;
+        uint32_t bytes = Sh::CTAS * (half ? Sh::STAGE - 8192 : Sh::STAGE);
+        if (A_MN) {
+#pragma unroll
+          for (int r = 0; r < Sh::CTAS; ++r)
+            if (mn_boxes(t.rb * Sh::TILE_ROWS + r * Sh::A_ROWS, g.rows) == 1) bytes -= 8192;
+        }
+        if (B_MN && !half) {
+#pragma unroll
+          for (int r = 0; r < Sh::CTAS; ++r)
+            if (mn_boxes(t.cb * BN + r * Sh::B_ROWS, g.cols) == 1) bytes -= 8192;
+        }
         for (; kb < kt; kb += kRingProducers) {
           const int s = prod.slot;
           if (!mbar_wait(&bar->empty[s], prod.phase ^ 1u, g.ctl, cta, kSiteProducerEmpty) || cta->abort) { ok = false; break; }
@@ -615,29 +637,29 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
           };
           // Two boxes of 8 KB where one of 16 KB would do cost time in the TMA unit: 4096 x 8192 x 4096 142 us with two
           // boxes per slot, 161 with four.
-          auto load_mn = [&](uint32_t at, const CUtensorMap* m, bool planes, int row, int k) {
-            if (!planes) {
+          auto load_mn = [&](uint32_t at, const CUtensorMap* planes, const CUtensorMap* m, int boxes, int row) {
+            if (boxes) {
               load(at, m, row, k);
-              load(at + 8192, m, row + 64, k);
+              if (boxes == 2) load(at + 8192, m, row + 64, k);
             } else if (PAIR) {
-              tma_load_3d_pair(at, m, full, 0, k, row >> 6);
+              tma_load_3d_pair(at, planes, full, 0, k, row >> 6);
             } else {
-              tma_load_3d(at, m, &bar->full[s], 0, k, row >> 6);
+              tma_load_3d(at, planes, &bar->full[s], 0, k, row >> 6);
             }
           };
           if (item == lose_item && kb == kt - 1) {
             prod.lost = prod.issued;
           } else {
             // (the even CTA's barrier counts the bytes of both CTAs' loads)
-            if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], Sh::CTAS * (half ? Sh::STAGE - 8192 : Sh::STAGE));
+            if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], bytes);
             if (A_MN)
-              load_mn(a_at, ma, g.a_planes, a_row, k);
+              load_mn(a_at, ma, &maps.a64[t.problem | second], a_boxes, a_row);
             else
               load(a_at, ma, k, a_row);
             if (half) {
-              load(b_at, &maps.b_half[which_b], B_MN ? b_row : k, B_MN ? k : b_row);
+              load(b_at, &maps.b64[which_b], B_MN ? b_row : k, B_MN ? k : b_row);
             } else if (B_MN) {
-              load_mn(b_at, mb, g.b_planes, b_row, k);
+              load_mn(b_at, mb, &maps.b64[which_b], b_boxes, b_row);
             } else if (GATED && !PAIR) {
               load(b_at, mb, k, b_row);
               load(b_at + 8192, &maps.b[1], k, b_row);
@@ -856,17 +878,16 @@ inline CUtensorMapDataType ffn_map_type(const FfnOut& o) {
   return o.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
-// Map of an operand of `rows` x `summed`, whose boxes hold box_rows of its rows; stored summed axis first where `mn`: 64 of
-// its rows, or two planes of 64.
+// Map of an operand of `rows` x `summed`, whose boxes hold box_rows of its rows; stored summed axis first where `mn`, in
+// boxes of two planes of 64 of its rows, as far as they go whole (no plane: the map is not used).
 inline cudaError_t ffn_map(CUtensorMap* m, const FfnProduct& p, const void* base, int64_t ld, int64_t rows, bool mn,
                            int box_rows) {
   const uint64_t row_bytes = static_cast<uint64_t>(ld) * 2;
-  if (mn && rows % 64 == 0)   // (otherwise the last plane would end outside of its rows)
-    return make_tmap_3d(m, base, ffn_map_type(p.out), 64, p.summed, row_bytes, rows / 64, 128, 64, kFfnBK, 2,
-                        CU_TENSOR_MAP_SWIZZLE_128B);
-  return mn ? make_tmap_2d(m, base, ffn_map_type(p.out), rows, p.summed, row_bytes, 64, kFfnBK, CU_TENSOR_MAP_SWIZZLE_128B)
-            : make_tmap_2d(m, base, ffn_map_type(p.out), p.summed, rows, row_bytes, kFfnBK, box_rows,
-                           CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!mn)
+    return make_tmap_2d(m, base, ffn_map_type(p.out), p.summed, rows, row_bytes, kFfnBK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rows < 64) return cudaSuccess;
+  return make_tmap_3d(m, base, ffn_map_type(p.out), 64, p.summed, row_bytes, rows / 64, 128, 64, kFfnBK, 2,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // The same in boxes of 64 of its rows.
@@ -901,8 +922,11 @@ cudaError_t launch_ring(FfnProduct& p, const void** kernel) {
     if ((e = ffn_map(&maps.b[0], p, p.b[0], p.ldb[0], p.cols, B_MN, b_box)) != cudaSuccess) return e;
     if ((sum || both) && (e = ffn_map(&maps.a[1], p, p.a[1], p.lda[1], p.rows, A_MN, 128)) != cudaSuccess) return e;
     if ((sum || GATED) && (e = ffn_map(&maps.b[1], p, p.b[1], p.ldb[1], p.cols, B_MN, b_box)) != cudaSuccess) return e;
-    for (int i = 0; PAIR && p.plan.half_tiles && i < (sum || GATED ? 2 : 1); ++i)
-      if ((e = ffn_map64(&maps.b_half[i], p, p.b[i], p.ldb[i], p.cols, B_MN)) != cudaSuccess) return e;
+    for (int i = 0; A_MN && p.rows % 64 != 0 && i < (both ? 2 : 1); ++i)
+      if ((e = ffn_map64(&maps.a64[i], p, p.a[i], p.lda[i], p.rows, A_MN)) != cudaSuccess) return e;
+    const bool b64 = (PAIR && p.plan.half_tiles) || (B_MN && p.cols % 64 != 0);
+    for (int i = 0; b64 && i < (sum || GATED ? 2 : 1); ++i)
+      if ((e = ffn_map64(&maps.b64[i], p, p.b[i], p.ldb[i], p.cols, B_MN)) != cudaSuccess) return e;
   }
   RingParams g = {};
   g.o = p.out;
@@ -918,8 +942,6 @@ cudaError_t launch_ring(FfnProduct& p, const void** kernel) {
   g.idesc_half = umma_idesc_f16(p.out.bf16 != 0, Sh::TILE_ROWS, BN / 2) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
   g.whole = static_cast<int32_t>(p.plan.tiles) - p.plan.half_tiles;
   g.items = g.whole + 2 * p.plan.half_tiles;
-  g.a_planes = A_MN && p.rows % 64 == 0;
-  g.b_planes = B_MN && p.cols % 64 == 0;
   g.ctl = p.ctl;
   if (Sh::SPLIT_REGS) {
     static std::atomic<int> regs{-1};

@@ -60,12 +60,12 @@ struct FewParams {
   int32_t k_log;             // log2 of the CTAs that share a tile's K blocks
   int32_t row_blocks, per_problem;
   uint32_t idesc;
-  int32_t p_planes, q_planes;  // an MN-major operand's 128 rows come as one box of two planes of 64
   KernelCtl ctl;
 };
 
 struct FewMaps {
   CUtensorMap q[2], p[2];
+  CUtensorMap q64[2], p64[2];   // in boxes of 64 of their rows: an MN-major operand's end
 };
 
 __device__ __forceinline__ void tmem_ld_few(uint32_t taddr, uint32_t (&r)[8]) {
@@ -255,6 +255,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (warp != 1 && lane == 0) {
       // ---------------- producers ----------------
       const bool lose = g.ctl.inject_lost_load && tile == static_cast<int>(gridDim.x >> g.k_log) - 1;
+      const int p_boxes = P_MN ? mn_boxes(pb * 128, g.cols) : 0, q_boxes = Q_MN && BN == 128 ? mn_boxes(qb * BN, g.rows) : 0;
+      const uint32_t bytes = Sh::STAGE - (p_boxes == 1 ? 8192 : 0) - (q_boxes == 1 ? 8192 : 0);
       for (int kb = k0 + prod.which; kb < k1; kb += kRingProducers) {
         const int s = prod.slot;
         if (!mbar_wait(&bar->empty[s], prod.phase ^ 1u, g.ctl, cta, kSiteProducerEmpty) || cta->abort) break;
@@ -265,24 +267,24 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           const int second = kb >= g.kt ? 1 : 0, k = (kb - second * g.kt) * kFfnBK;
           const CUtensorMap* mp = &maps.p[second];
           const CUtensorMap* mq = &maps.q[problem | second];
-          mbar_arrive_expect_tx(&bar->full[s], Sh::STAGE);
+          mbar_arrive_expect_tx(&bar->full[s], bytes);
           if (!P_MN) {
             tma_load_2d(at, mp, &bar->full[s], k, pb * 128);
             if (GATED) tma_load_2d(at + Sh::P_BYTES, &maps.p[1], &bar->full[s], k, pb * 128);
-          } else if (g.p_planes) {
+          } else if (p_boxes == 0) {
             tma_load_3d(at, mp, &bar->full[s], 0, k, pb * 2);
           } else {
-            tma_load_2d(at, mp, &bar->full[s], pb * 128, k);
-            tma_load_2d(at + 8192, mp, &bar->full[s], pb * 128 + 64, k);
+            tma_load_2d(at, &maps.p64[second], &bar->full[s], pb * 128, k);
+            if (p_boxes == 2) tma_load_2d(at + 8192, &maps.p64[second], &bar->full[s], pb * 128 + 64, k);
           }
           const uint32_t q_at = at + Sh::PARTS * Sh::P_BYTES;
           if (!Q_MN) {
             tma_load_2d(q_at, mq, &bar->full[s], k, qb * BN);
-          } else if (BN == 128 && g.q_planes) {
+          } else if (BN == 128 && q_boxes == 0) {
             tma_load_3d(q_at, mq, &bar->full[s], 0, k, qb * 2);
           } else {
-            tma_load_2d(q_at, mq, &bar->full[s], qb * BN, k);
-            if (BN == 128) tma_load_2d(q_at + 8192, mq, &bar->full[s], qb * BN + 64, k);
+            tma_load_2d(q_at, &maps.q64[problem | second], &bar->full[s], qb * BN, k);
+            if (BN == 128 && q_boxes == 2) tma_load_2d(q_at + 8192, &maps.q64[problem | second], &bar->full[s], qb * BN + 64, k);
           }
         }
         prod.advance(Sh::STAGES);
@@ -446,16 +448,16 @@ cudaError_t launch_as(FfnProduct& p, const void** kernel) {
   FewMaps maps = {};
   cudaError_t e;
   if (p.summed > 0) {
-    // (64 rows are one plane of the MN-major form, 128 as the ring has them)
-    auto q_map = [&](int i) {
-      return Q_MN && BN == 64 ? make_tmap_2d(&maps.q[i], p.a[i], ffn_map_type(p.out), p.rows, p.summed, static_cast<uint64_t>(p.lda[i]) * 2,
-                                 64, kFfnBK, CU_TENSOR_MAP_SWIZZLE_128B)
-                  : ffn_map(&maps.q[i], p, p.a[i], p.lda[i], p.rows, Q_MN, BN);
-    };
-    if ((e = q_map(0)) != cudaSuccess) return e;
-    if ((e = ffn_map(&maps.p[0], p, p.b[0], p.ldb[0], p.cols, P_MN, 128)) != cudaSuccess) return e;
-    if ((sum || both) && (e = q_map(1)) != cudaSuccess) return e;
-    if ((sum || GATED) && (e = ffn_map(&maps.p[1], p, p.b[1], p.ldb[1], p.cols, P_MN, 128)) != cudaSuccess) return e;
+    for (int i = 0; i < (sum || both ? 2 : 1); ++i) {
+      e = Q_MN && BN == 64 ? cudaSuccess : ffn_map(&maps.q[i], p, p.a[i], p.lda[i], p.rows, Q_MN, BN);
+      if (e == cudaSuccess && Q_MN) e = ffn_map64(&maps.q64[i], p, p.a[i], p.lda[i], p.rows, true);
+      if (e != cudaSuccess) return e;
+    }
+    for (int i = 0; i < (sum || GATED ? 2 : 1); ++i) {
+      e = ffn_map(&maps.p[i], p, p.b[i], p.ldb[i], p.cols, P_MN, 128);
+      if (e == cudaSuccess && P_MN && p.cols % 64 != 0) e = ffn_map64(&maps.p64[i], p, p.b[i], p.ldb[i], p.cols, true);
+      if (e != cudaSuccess) return e;
+    }
   }
   FewParams g = {};
   g.o = p.out;
@@ -469,8 +471,6 @@ cudaError_t launch_as(FfnProduct& p, const void** kernel) {
   g.row_blocks = (g.rows + BN - 1) / BN;
   g.per_problem = g.row_blocks * ((g.cols + 127) / 128);
   g.idesc = umma_idesc_f16(p.out.bf16 != 0, 128, BN) | (P_MN ? kIdescAMn : 0u) | (Q_MN ? kIdescBMn : 0u);
-  g.p_planes = P_MN && p.cols % 64 == 0;
-  g.q_planes = Q_MN && BN == 128 && p.rows % 64 == 0;
   g.ctl = p.ctl;
   if ((e = ensure_smem_attr(*kernel, Sh::SMEM)) != cudaSuccess) return e;
   RingConfig c(p.plan.grid, kFewThreads, p.plan.k_splits, Sh::SMEM, p.stream);
