@@ -1,16 +1,17 @@
 // ffn_math.cuh -- activations of the feed-forward operators and their derivatives, in FP32.
 //
 // sigmoid(z) = 1 / (1 + e) with e = exp(-z), and 1 - sigmoid(z) = e * sigmoid(z)
-// without cancellation.  __expf(t) is off by about |t| 2^-24 relative: as much
-// as half a spacing of its FP32 argument is worth.
+// without cancellation.  exp(t) as 2^(t / ln 2) by ex2.approx is off by two
+// spacings and by |t| 2^-24 relative, as much as half a spacing of its FP32
+// argument is worth; rcp.approx by one.  Both flush what is below 2^-126.
 //
 // gelu needs Phi(z) = erfc(-z / sqrt(2)) / 2, which for z < 0 falls as exp(-z^2 /
 // 2) does, so that 1 + erf would lose it.  With t = 1 / (1 + q |z|) the quotient
 // erfc(|z| / sqrt(2)) / (2 exp(-z^2 / 2)) is t times a polynomial of degree 8 in
 // t, fitted here for the least relative error over |z| <= 13.4 (Lawson's
-// reweighted least squares): 1.7e-8, a third of FP32's half spacing.  With erfcf, 4096 x 8192 outputs of K = 2048 took
-// 135 us against 84 without an activation; two values at a time, packed, share
-// most instructions.
+// reweighted least squares): 1.7e-8, a third of FP32's half spacing.  With erfcf,
+// 4096 x 8192 outputs of K = 2048 took 135 us against 84 without an activation; two
+// values at a time, packed, share most instructions.
 #pragma once
 #include "ffn_internal.h"
 
@@ -20,13 +21,24 @@ constexpr float kRsqrt2Pi = 0.39894228040143268f;        // 1 / sqrt(2 pi)
 constexpr float kTanhScale = 1.59576912160573071f;       // 2 sqrt(2 / pi)
 constexpr float kTanhCube = 0.044715f;
 
+__device__ __forceinline__ float fast_exp(float t) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 struct Sigmoid {
   float s, rest;   // sigmoid and 1 - sigmoid
 };
 __device__ __forceinline__ Sigmoid sigmoid_of(float z) {
   const float t = z < -88.f ? 88.f : -z;     // (e stays finite and s is 0 there; a NaN stays)
-  const float e = __expf(t);
-  const float s = __fdividef(1.f, 1.f + e);
+  const float e = fast_exp(t);
+  const float s = fast_rcp(1.f + e);
   return Sigmoid{s, e * s};
 }
 
@@ -61,12 +73,12 @@ __device__ __forceinline__ Tail tail_of(float z0, float z1) {
   u.x = u.x > 20.f ? 20.f : u.x;
   u.y = u.y > 20.f ? 20.f : u.y;
   const float2 d = of_two(fma_two(two(0.26162952f, 0.26162952f), two(u.x, u.y), two(1.f, 1.f)));
-  const uint64_t t = two(__fdividef(1.f, d.x), __fdividef(1.f, d.y));
+  const uint64_t t = two(fast_rcp(d.x), fast_rcp(d.y));
   uint64_t p = two(0.030961534f, 0.030961534f);
   constexpr float kC[8] = {-0.15163641f, 0.24342063f, -0.14265560f, 0.15540075f, 0.053260274f, 0.10312700f, 0.10371493f, 0.10440688f};
 #pragma unroll
   for (int i = 0; i < 8; ++i) p = fma_two(p, t, two(kC[i], kC[i]));
-  const float2 e = make_float2(__expf(-0.5f * u.x * u.x), __expf(-0.5f * u.y * u.y));
+  const float2 e = make_float2(fast_exp(-0.5f * u.x * u.x), fast_exp(-0.5f * u.y * u.y));
   return Tail{u, of_two(mul_two(two(e.x, e.y), mul_two(t, p))), e};
 }
 
