@@ -26,6 +26,7 @@
  * rounding; where an output is FP32, or 8-bit codes with FP32 scales, that sum
  * is restarted every 768 of the summed axis and the parts are added in FP32.
  * Everything up to an output's one rounding is FP32.
+ * Outputs do not overlap operands, except where it says so.
  *
  * Activations (act'(0) of relu is 0):
  *     relu = max(z, 0)     gelu = z Phi(z)     silu = z sigmoid(z)     sigmoid = 1 / (1 + exp(-z))
@@ -160,7 +161,7 @@ int gemm_weight_grad(const gp_weight_grad* args, void* stream, const gp_ffn_opti
  * without one, as on 152 SMs with gp_plan.grid left 0).  op: 0 gemm_linear, 1 gemm_gated, 2 gemm_input_grad,
  * 3 gemm_weight_grad; M, N, K and count as in that call; kept: 1 where values are kept in 8 bits, or FP32 is written.
  * gp_plan.bm x bn is the tile (where layout is 1, bm counts columns of the output and bn rows); k_splits CTAs, one cluster,
- * share each tile's K loop.
+ * share each tile's K loop; the last half_tiles tiles (after dp_tiles whole ones) run as two halves of their columns each.
  */
 int gemm_ffn_plan(int op, int64_t M, int64_t N, int64_t K, int count, int kept, int sms, const gp_ffn_options* opts,
                   gp_plan* out);
