@@ -145,7 +145,7 @@ typedef struct gp_weight_grad {
     const void* x;               /* M x K */
     const void* addend[2];       /* N x K of out_type, added in FP32 before the rounding, NULL: none (both or neither
                                     of two).  May be dw_i itself, not overlap it otherwise */
-    void* dw[2];                 /* N x K of out_type */
+    void* dw[2];                 /* N x K of out_type; not the same one twice (GP_ERR_ARG) */
     int64_t M, N, K;
     int64_t ld_dz[2], ldx, ld_add[2], ld_dw[2];
     int32_t type, out_type;
@@ -194,7 +194,7 @@ typedef struct gp_gated_backward {
     const void* dh;              /* M x N */
     const void *z_gate, *z_up;   /* g and u of `type`, or NULL both */
     gp_fp8_matrix q_gate, q_up;  /* or both in 8 bits (group 1) */
-    void *dgate, *dup;           /* M x N of `type` (one of them may be dh itself) */
+    void *dgate, *dup;           /* M x N of `type` (one of them may be dh itself; not the same one twice: GP_ERR_ARG) */
     void* h;                     /* M x N of `type`; NULL: not written */
     int64_t M, N;
     int64_t ld_dh, ld_zg, ld_zu, ld_dgate, ld_dup, ldh;

@@ -181,7 +181,7 @@ int gemm_gated(const gp_gated* a, void* stream, const gp_ffn_options* opts) {
     rc = first_error({check_operand(a->x, a->ldx, a->K), check_operand(a->gate, a->ld_gate, a->K),
                       check_operand(a->up, a->ld_up, a->K)});
   const bool real = a->z_gate || a->z_up, codes = a->q_gate.data || a->q_up.data;
-  if (rc == GP_OK && ((real && (!a->z_gate || !a->z_up)) || (codes && (!a->q_gate.data || !a->q_up.data)) || (real && codes)))
+  if (rc == GP_OK && ((real && (!a->z_gate || !a->z_up || a->z_gate == a->z_up)) || (codes && (!a->q_gate.data || !a->q_up.data)) || (real && codes)))
     rc = GP_ERR_ARG;
   if (rc == GP_OK)
     rc = first_error({check_real(a->h, a->ldh, a->N, a->type, false), check_real(a->z_gate, a->ld_zg, a->N, a->type, true),
@@ -263,7 +263,7 @@ int gemm_weight_grad(const gp_weight_grad* a, void* stream, const gp_ffn_options
     rc = first_error({a->M > 0 ? check_operand(a->dz[i], a->ld_dz[i], a->N) : GP_OK,
                       check_real(a->dw[i], a->ld_dw[i], a->K, a->out_type, false),
                       check_real(a->addend[i], a->ld_add[i], a->K, a->out_type, true)});
-  if (rc == GP_OK && a->count == 2 && !a->addend[0] != !a->addend[1]) rc = GP_ERR_ARG;
+  if (rc == GP_OK && a->count == 2 && (!a->addend[0] != !a->addend[1] || a->dw[0] == a->dw[1])) rc = GP_ERR_ARG;
   if (rc != GP_OK) return call_finish(rc);
   FfnProduct p = {};
   p.op = kFfnWeightGrad;
@@ -369,7 +369,8 @@ int ffn_gated_backward(const gp_gated_backward* a, void* stream) {
                     check_real(a->z_up, a->ld_zu, a->N, a->type, true), check_codes(a->q_gate, a->N, true),
                     check_codes(a->q_up, a->N, true), check_real(a->dgate, a->ld_dgate, a->N, a->type, false),
                     check_real(a->dup, a->ld_dup, a->N, a->type, false), check_real(a->h, a->ldh, a->N, a->type, true),
-                    codes && a->q_gate.format != a->q_up.format ? GP_ERR_ARG : GP_OK});
+                    codes && a->q_gate.format != a->q_up.format ? GP_ERR_ARG : GP_OK,
+                    a->dgate == a->dup ? GP_ERR_ARG : GP_OK});
   if (rc != GP_OK) return call_finish(rc);
   CallInfo info;
   cudaError_t e = call_begin(0, &info);

@@ -62,7 +62,7 @@ def input_grad(gp, opts=None, **over):
 
 
 def weight_grad(gp, opts=None, **over):
-    return gp.lib().gemm_weight_grad(fill(b.GpWeightGrad, **dict(dict(dz=(PTR, PTR), x=PTR, dw=(PTR, PTR), M=64, N=200, K=256,
+    return gp.lib().gemm_weight_grad(fill(b.GpWeightGrad, **dict(dict(dz=(PTR, PTR), x=PTR, dw=(PTR, 2 * PTR), M=64, N=200, K=256,
                                                                       ld_dz=(200, 200), ldx=256, ld_add=(256, 256), ld_dw=(256, 256),
                                                                       type=1, out_type=2, count=2), **over)), None, opts)
 
@@ -74,7 +74,7 @@ def act_backward(gp, **over):
 
 
 def gated_backward(gp, **over):
-    return gp.lib().ffn_gated_backward(fill(b.GpGatedBackward, **dict(dict(dh=PTR, z_gate=PTR, z_up=PTR, dgate=PTR, dup=PTR, h=PTR,
+    return gp.lib().ffn_gated_backward(fill(b.GpGatedBackward, **dict(dict(dh=PTR, z_gate=PTR, z_up=PTR, dgate=PTR, dup=2 * PTR, h=PTR,
                                                                            M=64, N=200, ld_dh=200, ld_zg=200, ld_zu=200,
                                                                            ld_dgate=200, ld_dup=200, ldh=200, type=1, activation=4),
                                                                       **over)), None)
@@ -114,6 +114,7 @@ BIG = (1 << 31) - 200
     (gated_backward, dict(z_up=None), "ARG"), (gated_backward, dict(q_gate=codes(), q_up=codes()), "ARG"),
     (gated_backward, dict(z_gate=None, z_up=None), "ARG"), (gated_backward, dict(dgate=None), "ARG"),
     (gated_backward, dict(z_gate=None, z_up=None, q_gate=codes(), q_up=codes(fmt=1)), "ARG"), (gated_backward, dict(ldh=1), "ARG"),
+    (weight_grad, dict(dw=(PTR, PTR)), "ARG"), (gated_backward, dict(dup=PTR), "ARG"), (gated, dict(z_gate=PTR, z_up=PTR), "ARG"),
     (gated_backward, dict(dup=PTR + 1), "UNSUPPORTED"), (gated_backward, dict(M=-1), "ARG"),
 ])
 def test_argument_errors_need_no_device(gp, call, args, code):

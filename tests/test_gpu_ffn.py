@@ -571,6 +571,74 @@ def test_input_gradient_without_x():
     assert gp.linear_backward(z, None, w[0], input_grad=False, weight_grad=False) == (None, None, None)
 
 
+def test_where_weight_gradients_go():
+    """out and addend in every combination, in 16 bits and FP32, rows apart or not."""
+    rng = np.random.default_rng(12)
+    M, N, K = 90, 130, 70
+    dy, x, w = (ref.matrix(rng, r, c, BF16, whole=2) for r, c in ((M, N), (M, K), (N, K)))
+    z = torch.ones(M, N, dtype=BF16, device="cuda")
+    plain = (dy.double().t() @ x.double())
+    for dtype in (BF16, F32):
+        for pad in (0, 1, 10):
+            wide = [torch.full((N, K + pad), 5.0, dtype=dtype, device="cuda") for _ in range(4)]
+            a, b, c, d = (t[:, :K] for t in wide)
+            got = gp.linear_backward(dy, x, w, input_grad=False, out=a)[1]
+            assert got is a and torch.equal(a, plain.to(dtype))
+            got = gp.linear_backward(dy, x, w, input_grad=False, out=a, addend=b)[1]
+            assert got is a and torch.equal(a, (plain + 5).to(dtype))
+            got = gp.linear_backward(dy, x, w, input_grad=False, addend=b)[1]
+            assert got.dtype is dtype and torch.equal(got, (plain + 5).to(dtype)) and bool((b == 5).all())
+            _, g, u = gp.gated_backward(dy, x, w, w, (z, z), activation="relu", input_grad=False, out=(c, d), addend=(b, b))
+            assert g is c and u is d and torch.equal(g, (plain + 5).to(dtype)) and torch.equal(u, g)
+            assert all(bool((t[:, K:] == 5).all()) for t in wide)
+    with pytest.raises(gp.GemmError):
+        gp.gated_backward(dy, x, w, w, (z, z), input_grad=False, out=(c, c))
+
+
+def test_kept_codes_of_any_strides():
+    x, w, _, _, _ = block_operands(70, 300, 136, 9)
+    _, kept = gp.gated(x, *w, keep="fp8")
+    dh = torch.ones(70, 300, dtype=BF16, device="cuda")
+    want = gp.gated_backward(dh, x, *w, kept)
+    data = [torch.zeros(70, 336, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)[:, :300] for _ in range(2)]
+    for a, b in zip(data, kept[::2]):
+        a.copy_(b)
+    for scales in (lambda s: s.contiguous(), lambda s: s.repeat_interleave(3, 1)[:, ::3]):
+        got = gp.gated_backward(dh, x, *w, (data[0], scales(kept[1]), data[1], scales(kept[3])))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """Outputs and inputs of more than 2^31 values: rows from all over against the formulas."""
+    M, N, K = 70000, 33000, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, w = (torch.randint(-2, 3, s, generator=g, device="cuda").to(BF16) for s in ((M, K), (N, K)))
+    rows = torch.tensor([0, 1, 32767, 65077, 65078, M - 2, M - 1], device="cuda")
+    y, (data, scales) = gp.linear(x, w, keep="fp8")
+    status_ok()
+    z = x[rows].double() @ w.double().t()
+    assert torch.equal(y[rows], z.to(BF16))
+    code, s = fp8_ref.quantize(z.cpu().numpy(), "rows", "e4m3")
+    assert fp8_ref.same_codes(fp8_ref.codes(data.view(torch.uint8)[rows].view(torch.float8_e4m3fn)), code, "e4m3")
+    assert np.array_equal(scales[rows].cpu().numpy(), s)
+    dx, _, db = gp.linear_backward(y, None, w, weight_grad=False, bias_grad=True)
+    status_ok()
+    assert torch.equal(dx[rows], (y[rows].double() @ w.double()).to(BF16))
+    want = torch.zeros(N, dtype=torch.float64, device="cuda")
+    for i in range(0, M, 10000):
+        want += y[i:i + 10000].double().sum(0)
+    # whole numbers of 256 at most in a sum of 2^24 at most: exact in FP32
+    assert float(y.abs().max()) <= 256 and torch.equal(db.double(), want)
+    got = gp.gated_backward(y, None, w, w, (data, scales, data, scales), activation="relu", product=True, input_grad=False,
+                            weight_grad=False)[3]
+    status_ok()
+    held = torch.from_numpy(fp8_ref.values(code, s, "e4m3").astype(np.float32)).cuda()   # (a code times its scale in FP32)
+    assert torch.equal(got[rows], (held.clamp(min=0) * held).to(BF16))
+    del y, data, scales, got
+    torch.cuda.empty_cache()
+
+
 def test_refusals():
     x, w, wd, b, r = block_operands(20, 64, 40, 6)
     z = torch.zeros(20, 64, dtype=BF16, device="cuda")
