@@ -96,6 +96,27 @@ Matrix shaped(const at::Tensor& t, int64_t rows, int64_t cols, at::ScalarType ty
   return m;
 }
 
+// Whether two matrices share a byte.  Rows of the same stride may lie side by side, as halves of one matrix do; where the
+// strides differ, ranges that meet count.
+bool meet(const Matrix& a, const at::Tensor& ta, const Matrix& b, const at::Tensor& tb) {
+  if (a.rows == 0 || a.cols == 0 || b.rows == 0 || b.cols == 0) return false;
+  const int64_t wa = a.cols * ta.element_size(), wb = b.cols * tb.element_size();
+  const int64_t sa = a.ld * ta.element_size(), sb = b.ld * tb.element_size();
+  const int64_t at = reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p);   // where b begins, from a
+  if (at >= (a.rows - 1) * sa + wa || -at >= (b.rows - 1) * sb + wb) return false;
+  if (a.rows > 1 && b.rows > 1 && sa != sb) return true;
+  const int64_t s = a.rows > 1 ? sa : (b.rows > 1 ? sb : 0);
+  if (s <= 0) return true;
+  const int64_t in = (at % s + s) % s;
+  return in < wa || in + wb > s;
+}
+// An output that a kernel writes while it reads another matrix: apart from it, or that matrix itself where it may be.
+void apart(const at::Tensor& out, const at::Tensor& other, const char* name, bool may_be_it = false) {
+  const Matrix a = matrix(out, "out"), b = matrix(other, name);
+  if (may_be_it && a.p == b.p && (a.ld == b.ld || a.rows <= 1)) return;
+  if (meet(a, out, b, other)) throw Refused{std::string("out overlaps ") + name};
+}
+
 int type16(const at::Tensor& t, const char* name) {
   const int r = real_of(t.scalar_type());
   if (r != GP_REAL_F16 && r != GP_REAL_BF16)
@@ -283,6 +304,12 @@ PyObject* linear(PyObject* const* a) {
     const Matrix r = shaped(tensor(a[4], "residual"), M, N, y.scalar_type(), x, "residual");
     g.residual = r.p;
     g.ld_res = r.ld;
+    if (a[6] != Py_None) apart(y, tensor(a[4], "residual"), "residual", true);
+  }
+  if (a[6] != Py_None) {
+    apart(y, x, "x");
+    apart(y, tensor(a[1], "weight"), "weight");
+    if (a[2] != Py_None) apart(y, tensor(a[2], "bias").unsqueeze(0), "bias");
   }
   const long keep = PyLong_AsLong(a[5]);
   at::Tensor z;
@@ -329,6 +356,9 @@ PyObject* gated(PyObject* const* a) {
   } else {
     h = tensor(a[5], "out");
     g.ldh = shaped(h, M, N, x.scalar_type(), x, "out").ld;
+    apart(h, x, "x");
+    apart(h, tensor(a[1], "w_gate"), "w_gate");
+    apart(h, tensor(a[2], "w_up"), "w_up");
   }
   g.h = h.data_ptr();
   const long keep = PyLong_AsLong(a[4]);
@@ -380,9 +410,10 @@ PyObject* item(PyObject* o, int i, int count, const char* name) {
   return PySequence_Fast_GET_ITEM(o, i);
 }
 
-// The gradients of the weights of products that share x.
+// The gradients of the weights of products that share x.  x_given, dz_given (NULL: of the call's own): the tensors behind them.
 void weight_gradients(int count, const Matrix* dz, const Operand& x, int64_t N, int real, PyObject* dtype, PyObject* addend,
-                      PyObject* out, const at::Tensor& like, const Call& call, const gp_ffn_options* opts, at::Tensor* dw) {
+                      PyObject* out, const at::Tensor& like, const at::Tensor& x_given, const at::Tensor* dz_given,
+                      const Call& call, const gp_ffn_options* opts, at::Tensor* dw) {
   gp_weight_grad g = {};
   const int64_t K = x.cols;
   at::ScalarType type = out_type(dtype, like.scalar_type(), "out_dtype");
@@ -407,6 +438,17 @@ void weight_gradients(int count, const Matrix* dz, const Operand& x, int64_t N, 
       const Matrix m = shaped(tensor(add, "addend"), N, K, type, like, "addend");
       g.addend[i] = m.p;
       g.ld_add[i] = m.ld;
+    }
+  }
+  if (out != Py_None) {
+    for (int i = 0; i < count; ++i) {
+      apart(dw[i], x_given, "x");
+      if (dz_given) apart(dw[i], *dz_given, "dy");
+      for (int j = 0; j < count; ++j) {
+        PyObject* add = item(addend, j, count, "addend");
+        if (add != Py_None) apart(dw[i], tensor(add, "addend"), "addend", i == j);
+        if (j > i) apart(dw[i], dw[j], "the other out");
+      }
     }
   }
   g.x = x.p;
@@ -485,7 +527,8 @@ PyObject* linear_backward(PyObject* const* a) {
       md16 = operand(dy, "dy", nullptr, call);
     }
     if (want_x) dx = input_gradient(1, &md16, &mw, M, N, vw.cols, real, dy, call, opts);
-    if (want_w) weight_gradients(1, &md16, mx, N, real, a[8], a[9], a[10], dy, call, opts, &dw);
+    if (want_w)
+      weight_gradients(1, &md16, mx, N, real, a[8], a[9], a[10], dy, tensor(a[1], "x"), own ? nullptr : &dy, call, opts, &dw);
   }
   return tuple({dx, dw, dbias});
 }
@@ -549,7 +592,7 @@ PyObject* gated_backward(PyObject* const* a) {
   g.activation = static_cast<int32_t>(PyLong_AsLong(a[5]));
   check(lib.gated_backward(&g, call.stream), "ffn_gated_backward");
   if (want_x) dx = input_gradient(2, dz, mw, M, N, vg.cols, real, dh, call, opts);
-  if (want_w) weight_gradients(2, dz, mx, N, real, a[9], a[10], a[11], dh, call, opts, dw);
+  if (want_w) weight_gradients(2, dz, mx, N, real, a[9], a[10], a[11], dh, tensor(a[1], "x"), nullptr, call, opts, dw);
   return product ? tuple({dx, dw[0], dw[1], h}) : tuple({dx, dw[0], dw[1]});
 }
 

@@ -72,11 +72,11 @@ def linear(x, weight, bias=None, *, activation=None, residual=None, keep=None, o
 
     ``activation``: None, "relu", "gelu", "gelu_tanh", "silu" or "sigmoid".
     ``bias``: N values of x's type or float32.  ``residual``: M x N of the
-    output's type; it may be ``out`` itself.  ``out``: where to write;
-    ``out_dtype``: x's type or float32.  ``keep``: "real" or "fp8" also returns
-    the values before the activation, as ``kept`` of ``linear_backward``: (z,)
-    in x's type, or (codes, scales).  ``tile``, ``k_splits``, ``timeout_ns``,
-    ``inject_lost_load``: see gp_ffn_options.
+    output's type; it may be ``out`` itself.  ``out``: where to write, apart
+    from what is read; ``out_dtype``: x's type or float32.  ``keep``: "real" or
+    "fp8" also returns the values before the activation, as ``kept`` of
+    ``linear_backward``: (z,) in x's type, or (codes, scales).  ``tile``,
+    ``k_splits``, ``timeout_ns``, ``inject_lost_load``: see gp_ffn_options.
 
     Returns y, or (y, kept) with ``keep``.
     """
@@ -113,10 +113,10 @@ def linear_backward(dy, x, weight, *, activation=None, kept=None, bias_grad=Fals
     ``kept``: what ``linear`` returned with ``keep``, where there is an
     activation.  dz = dy * act'(z) is rounded to x's type for the two products.
     dx has x's type, dweight x's type or ``out_dtype`` (float32), and is written
-    to ``out`` if given; ``addend`` (of dweight's type, may be ``out`` itself) is
-    added to it in FP32.  dbias (float32) is summed from dz before its rounding.
-    What is not asked for (``input_grad``, ``weight_grad``, ``bias_grad``) is None;
-    without ``weight_grad`` x may be None too.
+    to ``out`` if given (apart from x and dy); ``addend`` (of dweight's type, may
+    be ``out`` itself) is added to it in FP32.  dbias (float32) is summed from dz
+    before its rounding.  What is not asked for (``input_grad``, ``weight_grad``,
+    ``bias_grad``) is None; without ``weight_grad`` x may be None too.
     """
     if stream is not None:
         with _On(_device_of(dy, "dy"), stream):

@@ -591,8 +591,44 @@ def test_where_weight_gradients_go():
             _, g, u = gp.gated_backward(dy, x, w, w, (z, z), activation="relu", input_grad=False, out=(c, d), addend=(b, b))
             assert g is c and u is d and torch.equal(g, (plain + 5).to(dtype)) and torch.equal(u, g)
             assert all(bool((t[:, K:] == 5).all()) for t in wide)
-    with pytest.raises(gp.GemmError):
+    with pytest.raises(ValueError):
         gp.gated_backward(dy, x, w, w, (z, z), input_grad=False, out=(c, c))
+
+
+def test_outputs_apart_from_what_is_read():
+    """An output that overlaps an operand is refused; one beside it in the same rows, or the addend itself, is not."""
+    rng = np.random.default_rng(13)
+    M, N, K = 70, 64, 64
+    x, w, u, dy, b = (ref.matrix(rng, r, c, BF16, whole=2) for r, c in ((M, K), (N, K), (N, K), (M, N), (1, N)))
+    z = torch.ones(M, N, dtype=BF16, device="cuda")
+    square = ref.matrix(rng, K, K, BF16, whole=2)
+    tall = torch.zeros(M + N + 1, N, dtype=BF16, device="cuda")
+    for call in (lambda: gp.linear(x, w, out=x), lambda: gp.linear(square, w, out=w), lambda: gp.gated(x, w, u, out=x),
+                 lambda: gp.gated(square, w, u, out=u), lambda: gp.gated(square, w, u, out=w),
+                 lambda: gp.linear(x, w, out=tall[1:M + 1], residual=tall[:M]),
+                 lambda: gp.linear(x, w, tall[5], out=tall[:M]),
+                 lambda: gp.linear(x, w, out=tall.flatten()[3:3 + M * N].view(M, N), residual=tall[:M]),
+                 lambda: gp.linear_backward(dy, x, w, out=x[:N]), lambda: gp.linear_backward(dy, x, w, out=dy[1:N + 1]),
+                 lambda: gp.linear_backward(dy, x, w, out=tall[:N], addend=tall[1:N + 1]),
+                 lambda: gp.gated_backward(dy, x, w, u, (z, z), out=(tall[:N], x[:N])),
+                 lambda: gp.gated_backward(dy, x, w, u, (z, z), out=(tall[:N], tall[1:N + 1])),
+                 lambda: gp.gated_backward(dy, x, w, u, (z, z), out=(tall[:N], w), addend=(w, tall[:N]))):
+        with pytest.raises(ValueError, match="overlaps"):
+            call()
+    wide = torch.zeros(M, K + N + 8, dtype=BF16, device="cuda")
+    wide[:, :K].copy_(x)
+    want = (x.double() @ w.double().t()).to(BF16)
+    assert torch.equal(gp.linear(wide[:, :K], w, out=wide[:, K:K + N]), want) and torch.equal(wide[:, :K], x)
+    dw = torch.zeros(N, 2 * K, dtype=F32, device="cuda")
+    halves = (dw[:, :K], dw[:, K:])
+    gp.gated_backward(dy, x, w, u, (z, z), activation="relu", input_grad=False, out=halves, addend=halves)
+    plain = (dy.double().t() @ x.double()).float()
+    assert torch.equal(dw, torch.cat((plain, plain), 1))
+    # the weight itself as dW and addend: it is read for dx before
+    want = ((dy.double() @ w.double()).to(BF16), (w.double() + plain.double()).to(BF16))
+    got = gp.linear_backward(dy, x, w, out=w, addend=w)
+    assert got[1] is w and torch.equal(got[0], want[0]) and torch.equal(w, want[1])
+    status_ok()
 
 
 def test_kept_codes_of_any_strides():
