@@ -315,6 +315,48 @@ __device__ __forceinline__ void add_bias(float* v, const FfnOut& o, int lane, in
   for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, b, i);
 }
 
+// Four lanes' rows of 32 FP32 columns change hands in sectors of eight: where lane b of the four held sector k of row b in
+// v[8k ..], it then has sector b of row k, so that four lanes reach a whole 128-byte line together.  Its own inverse.
+__device__ __forceinline__ void exchange_sectors(float (&v)[32], int lane) {
+#pragma unroll
+  for (int step = 1; step <= 2; ++step) {
+    const bool upper = lane & step;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & step) continue;
+      const int lo = 8 * k, hi = 8 * (k | step);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float got = __shfl_xor_sync(0xffffffffu, upper ? v[lo + i] : v[hi + i], step);
+        if (upper) v[lo + i] = got; else v[hi + i] = got;
+      }
+    }
+  }
+}
+
+// 32 columns from `first` on of a warp's rows, of which this lane holds `row`, added to FP32's addend (if there is one that
+// the sums did not begin with) and written in whole lines.  All 32 columns exist, rows begin on 32-byte boundaries.
+__device__ __forceinline__ void write_lines(const FfnOut& o, int p, float (&v)[32], int lane, int64_t row, int64_t rows,
+                                            int64_t first, bool with_addend) {
+  exchange_sectors(v, lane);
+  const int64_t row0 = row - (lane & 3), col = first + 8 * (lane & 3);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (row0 + k < rows) {
+      if (with_addend && o.add[p]) {
+        Sector<float> was;
+        ld_global_v8(static_cast<const float*>(o.add[p]) + (row0 + k) * o.ld_add[p] + col, was.w);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[8 * k + c] += __uint_as_float(was.w[c]);
+      }
+      uint32_t w[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) w[c] = __float_as_uint(v[8 * k + c]);
+      st_global_v8(static_cast<float*>(o.out[p]) + (row0 + k) * o.ld_out[p] + col, w);
+    }
+  }
+}
+
 // out = act(v) + addend, and v itself where it is kept: a lane's 32 columns.
 template <typename T, typename O>
 __device__ __forceinline__ void emit_row(const FfnOut& o, int p, float (&v)[32], int64_t row, int64_t first, int n,
@@ -346,13 +388,32 @@ __device__ __forceinline__ void emit_row(const FfnOut& o, int p, float (&v)[32],
 }
 
 // An FP32 addend's 64 columns, where the sums begin.
-__device__ __forceinline__ void load_addend(float (&acc)[2][32], const FfnOut& o, int p, int64_t row, int64_t col0, int64_t cols) {
-  const float* const add = static_cast<const float*>(o.add[p]) + row * o.ld_add[p] + col0;
+__device__ __forceinline__ void load_addend(float (&acc)[2][32], const FfnOut& o, int p, int lane, int64_t row, int64_t rows,
+                                            int64_t col0, int64_t cols) {
+  const float* const add = static_cast<const float*>(o.add[p]);
+  if (o.vec == 2 && col0 + 64 <= cols) {
+    const int64_t row0 = row - (lane & 3);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (row0 + k < rows) {
+          Sector<float> s;
+          ld_global_v8(add + (row0 + k) * o.ld_add[p] + col0 + 32 * j + 8 * (lane & 3), s.w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[j][8 * k + i] = __uint_as_float(s.w[i]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) exchange_sectors(acc[j], lane);
+    return;
+  }
+  if (row >= rows) return;
   const int n = cols - col0 < 64 ? static_cast<int>(cols - col0) : 64;   // (may be < 0)
 #pragma unroll
   for (int i = 0; i < 64; i += 8) {
     Sector<float> s;
-    load_sector(s, add + i, n - i, o.vec);
+    load_sector(s, add + row * o.ld_add[p] + col0 + i, n - i, o.vec);
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[i >> 5][(i & 31) + k] = sector_value(s, k);
   }
@@ -469,12 +530,14 @@ __device__ __forceinline__ void emit_codes(const FfnCodes& q, const float* v, fl
 }
 
 // out = act(s + bias) + addend of a lane's 64 columns; `part`: which 64 of the tile's columns.  write false: nothing is
-// written (the row does not exist, or its sums did not come); `added`: the sums began with the addend.
+// written (the row does not exist, or its sums did not come); `whole`: this but for the row; `added`: the sums began with
+// the addend.
 template <typename T, typename O>
 __device__ __forceinline__ void finish_linear(const RingParams& g, int p, float (&acc)[2][32], uint32_t slot, int lane,
-                                              int quarter, int part, int64_t row, int64_t col0, bool write, bool added) {
+                                              int quarter, int part, int64_t row, int64_t col0, bool whole, bool added) {
   const FfnOut& o = g.o;
   const int64_t cols = g.cols;
+  const bool write = whole && row < g.rows;
   if (o.bias) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) add_bias<T>(acc[j], o, lane, col0 + 32 * j, cols);
@@ -493,6 +556,20 @@ __device__ __forceinline__ void finish_linear(const RingParams& g, int p, float 
       if ((part & 1) == 0) q.scales[row * q.stride_row + (col0 >> 7) * q.stride_col] = s.scale;
 #pragma unroll
       for (int j = 0; j < 2; ++j) emit_codes(q, acc[j], s.inv, row, col0 + 32 * j, columns_left(col0 + 32 * j, cols));
+    }
+  }
+  if constexpr (sizeof(O) == 4) {
+    if (o.vec == 2 && col0 + 64 <= cols) {
+      // (warps whose sums did not come, or that have no columns of a half tile, have `whole` false in all lanes)
+      if (!whole) return;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (o.keep[0] && write)
+          store_row(static_cast<T*>(o.keep[0]) + row * o.ld_keep[0] + col0 + 32 * j, acc[j], 32, o.vec);
+        activate_all(acc[j], o.act);
+        write_lines(o, p, acc[j], lane, row, g.rows, col0 + 32 * j, !added);
+      }
+      return;
     }
   }
 #pragma unroll
@@ -780,7 +857,7 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
         for (int i = 0; i < 64; ++i) acc[i >> 5][i & 31] = 0.f;
         if constexpr (!GATED) {
           // an FP32 addend with nothing between it and the sums is what they are added to: it comes while the products run
-          if (add_first && row < g.rows && !idle) load_addend(acc, g.o, problem, row, col0, g.cols);
+          if (add_first && !idle) load_addend(acc, g.o, problem, lane, row, g.rows, col0, g.cols);
         }
 #pragma unroll 1
         for (int kc = 0; kc < kt; kc += g.restart) {
@@ -801,7 +878,7 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
           hand_back();
           if (++a == 2) { a = 0; aph ^= 1u; }
         }
-        const bool write = ok && row < g.rows && !idle;
+        const bool whole = ok && !idle, write = whole && row < g.rows;
         const uint32_t slot = smem_u32(maxima) + e * kMaxSlot;
         if constexpr (GATED) {
           if (g.o.bf16)
@@ -811,14 +888,14 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
         } else {
           if (g.o.bf16) {
             if (g.o.out_f32)
-              finish_linear<__nv_bfloat16, float>(g, problem, acc, slot, lane, quarter, part, row, col0, write, add_first);
+              finish_linear<__nv_bfloat16, float>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, add_first);
             else
-              finish_linear<__nv_bfloat16, __nv_bfloat16>(g, problem, acc, slot, lane, quarter, part, row, col0, write, false);
+              finish_linear<__nv_bfloat16, __nv_bfloat16>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, false);
           } else {
             if (g.o.out_f32)
-              finish_linear<__half, float>(g, problem, acc, slot, lane, quarter, part, row, col0, write, add_first);
+              finish_linear<__half, float>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, add_first);
             else
-              finish_linear<__half, __half>(g, problem, acc, slot, lane, quarter, part, row, col0, write, false);
+              finish_linear<__half, __half>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, false);
           }
         }
       }
