@@ -56,8 +56,17 @@ static_assert(sizeof(RingBarriers) <= kRingBarrierBytes, "barrier region too sma
 // 256 x 256 tile of BF16 took 8000 cycles to leave, beside 16,400 of products at K
 // = 2048).  kStream: straight from TMEM, in a loop.  kHold: a warp takes 64 sums
 // per lane to registers, hands the buffer back and works on them: it can add up
-// several hand-overs, and sees half of a group of 128 columns.
-enum RingOut { kStream = 0, kHold = 1 };
+// several hand-overs, and sees half of a group of 128 columns.  kCodes: the same
+// where 8-bit codes are kept, a kernel of its own as FP32 outputs would pay for its
+// registers (4096^3 with both gradients 168 -> 172 us).
+// L2 takes a request per row and access, beside those of the operands' loads.
+// Where more bytes leave than in 16 bits, lanes therefore exchange pieces first and
+// write longer runs of each row: FP32 128 bytes by four lanes (4096 x 4096 over
+// 4096 added to an addend 106 -> 92 us), what stands beside codes 64 bytes and the
+// codes 32 by two (4096 x 8192 x 2056 122 -> 112 us).  It does not pay where 16
+// bits leave alone (8192 x 8192 x 4096 271 us either way) nor in a gated product,
+// where it costs registers (288 -> 289 us, 323 -> 331 kept up).
+enum RingOut { kStream = 0, kHold = 1, kCodes = 2 };
 
 template <int BN, bool PAIR, RingOut OUT>
 struct RingShape {
@@ -68,12 +77,12 @@ struct RingShape {
   static constexpr int TILE_ROWS = A_ROWS * CTAS;
   static constexpr int A_BYTES = A_ROWS * kFfnBK * 2;
   static constexpr int STAGE = (A_ROWS + B_ROWS) * kFfnBK * 2;
-  static constexpr int EPI_WARPS = OUT == kHold ? BN / 16 : 8;
+  static constexpr int EPI_WARPS = OUT != kStream ? BN / 16 : 8;
   static constexpr int EPI_COLS = 4 * BN / EPI_WARPS;    // TMEM columns of each, over 32 rows
   static_assert(OUT == kStream || EPI_COLS == 64, "held sums");
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
-  static constexpr int SHARED_MAX = OUT == kHold ? EPI_WARPS * 32 * 8 : 0;   // maxima that warps show each other
+  static constexpr int SHARED_MAX = OUT != kStream ? EPI_WARPS * 32 * 8 : 0;   // maxima that warps show each other
   static constexpr int FIXED = SHARED_MAX + kRingBarrierBytes + kSmemAlignSlack;
   static constexpr int FIT = (kSmemPerCtaMax - FIXED) / STAGE;
   static constexpr int STAGES = FIT < kRingMax ? FIT : kRingMax;
@@ -315,20 +324,22 @@ __device__ __forceinline__ void add_bias(float* v, const FfnOut& o, int lane, in
   for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, b, i);
 }
 
-// Four lanes' rows of 32 FP32 columns change hands in sectors of eight: where lane b of the four held sector k of row b in
-// v[8k ..], it then has sector b of row k, so that four lanes reach a whole 128-byte line together.  Its own inverse.
-__device__ __forceinline__ void exchange_sectors(float (&v)[32], int lane) {
+// LANES neighbouring lanes hold a row each, in LANES pieces of R words.  Pieces change hands: lane b, which held piece k of
+// its row in w[R k ..], then has piece b of row k there, so that the lanes reach a longer run of each row together.  Its own
+// inverse.
+template <int LANES, int R, typename W>
+__device__ __forceinline__ void exchange(W* w, int lane) {
 #pragma unroll
-  for (int step = 1; step <= 2; ++step) {
+  for (int step = 1; step < LANES; step *= 2) {
     const bool upper = lane & step;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < LANES; ++k) {
       if (k & step) continue;
-      const int lo = 8 * k, hi = 8 * (k | step);
+      const int lo = R * k, hi = R * (k | step);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float got = __shfl_xor_sync(0xffffffffu, upper ? v[lo + i] : v[hi + i], step);
-        if (upper) v[lo + i] = got; else v[hi + i] = got;
+      for (int i = 0; i < R; ++i) {
+        const W got = __shfl_xor_sync(0xffffffffu, upper ? w[lo + i] : w[hi + i], step);
+        if (upper) w[lo + i] = got; else w[hi + i] = got;
       }
     }
   }
@@ -338,7 +349,7 @@ __device__ __forceinline__ void exchange_sectors(float (&v)[32], int lane) {
 // the sums did not begin with) and written in whole lines.  All 32 columns exist, rows begin on 32-byte boundaries.
 __device__ __forceinline__ void write_lines(const FfnOut& o, int p, float (&v)[32], int lane, int64_t row, int64_t rows,
                                             int64_t first, bool with_addend) {
-  exchange_sectors(v, lane);
+  exchange<4, 8>(v, lane);
   const int64_t row0 = row - (lane & 3), col = first + 8 * (lane & 3);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -353,6 +364,28 @@ __device__ __forceinline__ void write_lines(const FfnOut& o, int p, float (&v)[3
 #pragma unroll
       for (int c = 0; c < 8; ++c) w[c] = __float_as_uint(v[8 * k + c]);
       st_global_v8(static_cast<float*>(o.out[p]) + (row0 + k) * o.ld_out[p] + col, w);
+    }
+  }
+}
+
+// The same in 16 bits and without an addend, 64 bytes of a row by two lanes.
+template <typename T>
+__device__ __forceinline__ void write_half_lines(const FfnOut& o, int p, const float (&v)[32], int lane, int64_t row,
+                                                 int64_t rows, int64_t first) {
+  T t[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) from_f32(v[i], t[i]);
+  uint32_t w[16];
+  memcpy(w, t, 64);
+  exchange<2, 8>(w, lane);
+  const int64_t row0 = row - (lane & 1), col = first + 16 * (lane & 1);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (row0 + k < rows) {
+      uint32_t s[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = w[8 * k + i];
+      st_global_v8(static_cast<T*>(o.out[p]) + (row0 + k) * o.ld_out[p] + col, s);
     }
   }
 }
@@ -405,7 +438,7 @@ __device__ __forceinline__ void load_addend(float (&acc)[2][32], const FfnOut& o
         }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) exchange_sectors(acc[j], lane);
+    for (int j = 0; j < 2; ++j) exchange<4, 8>(acc[j], lane);
     return;
   }
   if (row >= rows) return;
@@ -528,11 +561,23 @@ __device__ __forceinline__ void emit_codes(const FfnCodes& q, const float* v, fl
     store_codes16(p + 16 * i, w, n - 16 * i);
   }
 }
+// The same of a warp's rows, of which this lane holds `row`, where all 32 columns exist: a sector of a row by two lanes.
+__device__ __forceinline__ void emit_code_lines(const FfnCodes& q, const float* v, float inv, int lane, int64_t row, int64_t rows,
+                                                int64_t first) {
+  uint32_t w[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = fp8x4<false>(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
+  exchange<2, 4>(w, lane);
+  const int64_t row0 = row - (lane & 1);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (row0 + k < rows) store_codes16(q.data + (row0 + k) * q.ld + first + 16 * (lane & 1), w + 4 * k, 16);
+}
 
 // out = act(s + bias) + addend of a lane's 64 columns; `part`: which 64 of the tile's columns.  write false: nothing is
 // written (the row does not exist, or its sums did not come); `whole`: this but for the row; `added`: the sums began with
 // the addend.
-template <typename T, typename O>
+template <typename T, typename O, bool CODES>
 __device__ __forceinline__ void finish_linear(const RingParams& g, int p, float (&acc)[2][32], uint32_t slot, int lane,
                                               int quarter, int part, int64_t row, int64_t col0, bool whole, bool added) {
   const FfnOut& o = g.o;
@@ -542,7 +587,7 @@ __device__ __forceinline__ void finish_linear(const RingParams& g, int p, float 
 #pragma unroll
     for (int j = 0; j < 2; ++j) add_bias<T>(acc[j], o, lane, col0 + 32 * j, cols);
   }
-  if (o.codes[0].data) {
+  if constexpr (CODES) {
     if (col0 + 64 > cols) {   // (an infinity times a column that is not there is NaN)
 #pragma unroll
       for (int i = 0; i < 64; ++i)
@@ -552,7 +597,11 @@ __device__ __forceinline__ void finish_linear(const RingParams& g, int p, float 
     share_max(most, slot, lane, part & 1, 2, 2 + quarter * 2 + (part >> 1));
     const GroupScale s = group_scale(__float_as_uint(most[0]), 448.f);
     const FfnCodes& q = o.codes[0];
-    if (write && col0 < cols) {
+    if (whole && col0 + 64 <= cols) {
+      if (write && (part & 1) == 0) q.scales[row * q.stride_row + (col0 >> 7) * q.stride_col] = s.scale;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) emit_code_lines(q, acc[j], s.inv, lane, row, g.rows, col0 + 32 * j);
+    } else if (write && col0 < cols) {
       if ((part & 1) == 0) q.scales[row * q.stride_row + (col0 >> 7) * q.stride_col] = s.scale;
 #pragma unroll
       for (int j = 0; j < 2; ++j) emit_codes(q, acc[j], s.inv, row, col0 + 32 * j, columns_left(col0 + 32 * j, cols));
@@ -564,10 +613,21 @@ __device__ __forceinline__ void finish_linear(const RingParams& g, int p, float 
       if (!whole) return;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (o.keep[0] && write)
+        if (!CODES && o.keep[0] && write)
           store_row(static_cast<T*>(o.keep[0]) + row * o.ld_keep[0] + col0 + 32 * j, acc[j], 32, o.vec);
         activate_all(acc[j], o.act);
         write_lines(o, p, acc[j], lane, row, g.rows, col0 + 32 * j, !added);
+      }
+      return;
+    }
+  }
+  if constexpr (sizeof(O) == 2) {
+    if (o.vec == 2 && col0 + 64 <= cols && !o.add[p]) {   // (held for their codes: nothing else is kept)
+      if (!whole) return;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        activate_all(acc[j], o.act);
+        write_half_lines<O>(o, p, acc[j], lane, row, g.rows, col0 + 32 * j);
       }
       return;
     }
@@ -809,8 +869,7 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
     int a = 0;
     uint32_t aph = 0;
     bool ok = true;   // after a wait that gave up: nothing is written any more
-    const bool add_first = OUT == kHold && !GATED && g.o.out_f32 && g.o.add[0] && g.o.act == GP_ACT_NONE && !g.o.keep[0] &&
-                           !g.o.codes[0].data;
+    const bool add_first = OUT == kHold && !GATED && g.o.out_f32 && g.o.add[0] && g.o.act == GP_ACT_NONE && !g.o.keep[0];
     for (int item = worker; item < items; item += workers) {
       const RingItem t = ring_item(item, g, row_blocks, col_blocks);
       const int problem = t.problem;
@@ -886,16 +945,17 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
           else
             finish_gated<__half>(g, acc, slot, lane, quarter, part, row, col0, write);
         } else {
+          const bool f32 = OUT == kHold || g.o.out_f32;   // (16-bit outputs are held for their codes only)
           if (g.o.bf16) {
-            if (g.o.out_f32)
-              finish_linear<__nv_bfloat16, float>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, add_first);
+            if (f32)
+              finish_linear<__nv_bfloat16, float, OUT == kCodes>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, add_first);
             else
-              finish_linear<__nv_bfloat16, __nv_bfloat16>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, false);
+              finish_linear<__nv_bfloat16, __nv_bfloat16, OUT == kCodes>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, false);
           } else {
-            if (g.o.out_f32)
-              finish_linear<__half, float>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, add_first);
+            if (f32)
+              finish_linear<__half, float, OUT == kCodes>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, add_first);
             else
-              finish_linear<__half, __half>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, false);
+              finish_linear<__half, __half, OUT == kCodes>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, false);
           }
         }
       }
@@ -1034,15 +1094,22 @@ template <bool GATED, bool A_MN, bool B_MN>
 cudaError_t launch_tile(FfnProduct& p, const void** kernel) {
   const bool wide = p.out.out_f32 || p.out.codes[0].data;
   if constexpr (GATED) {   // (8 bits on pairs alone)
-    if (wide) return launch_ring<256, true, kHold, true, A_MN, B_MN>(p, kernel);
+    if (wide) return launch_ring<256, true, kCodes, true, A_MN, B_MN>(p, kernel);
     return p.plan.cta_pair ? launch_ring<256, true, kStream, true, A_MN, B_MN>(p, kernel)
                            : launch_ring<128, false, kStream, true, A_MN, B_MN>(p, kernel);
-  } else if (p.plan.cta_pair)
-    return wide ? launch_ring<256, true, kHold, false, A_MN, B_MN>(p, kernel)
-                : launch_ring<256, true, kStream, false, A_MN, B_MN>(p, kernel);
-  else
-    return wide ? launch_ring<128, false, kHold, false, A_MN, B_MN>(p, kernel)
+  } else {
+    const bool pair = p.plan.cta_pair;
+    if constexpr (!A_MN && !B_MN) {   // (values are kept by the forward product)
+      if (p.out.codes[0].data)
+        return pair ? launch_ring<256, true, kCodes, false, A_MN, B_MN>(p, kernel)
+                    : launch_ring<128, false, kCodes, false, A_MN, B_MN>(p, kernel);
+    }
+    if (wide)
+      return pair ? launch_ring<256, true, kHold, false, A_MN, B_MN>(p, kernel)
+                  : launch_ring<128, false, kHold, false, A_MN, B_MN>(p, kernel);
+    return pair ? launch_ring<256, true, kStream, false, A_MN, B_MN>(p, kernel)
                 : launch_ring<128, false, kStream, false, A_MN, B_MN>(p, kernel);
+  }
 }
 
 }  // namespace gp

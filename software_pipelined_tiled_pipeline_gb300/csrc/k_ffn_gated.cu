@@ -15,8 +15,8 @@ cudaError_t pair_capacity(int* pairs) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 0 && dev < 64 && (*pairs = cached[dev].load()) > 0) return cudaSuccess;
-  using Sh = RingShape<256, true, kHold>;
-  const void* k = reinterpret_cast<const void*>(ffn_ring_kernel<256, true, kHold, true, false, false>);
+  using Sh = RingShape<256, true, kCodes>;
+  const void* k = reinterpret_cast<const void*>(ffn_ring_kernel<256, true, kCodes, true, false, false>);
   if ((e = ensure_smem_attr(k, Sh::SMEM)) != cudaSuccess) return e;
   RingConfig c(2, Sh::THREADS, 2, Sh::SMEM, nullptr);
   if ((e = cudaOccupancyMaxActiveClusters(pairs, k, &c.cfg)) != cudaSuccess) return e;
