@@ -23,8 +23,10 @@
  * and are faster with rows on 16-byte boundaries.
  *
  * Products are summed in FP32 by the tensor cores, which cut instead of
- * rounding; where an output is FP32, or 8-bit codes with FP32 scales, that sum
- * is restarted every 768 of the summed axis and the parts are added in FP32.
+ * rounding.  That sum is restarted, and the parts are added in FP32, every 768 of
+ * the summed axis where an output is FP32, or 8-bit codes with FP32 scales; else
+ * every 4096 (FP16) or 32768 (BF16), so that what is cut stays below the
+ * output's own rounding.
  * Everything up to an output's one rounding is FP32.
  * Outputs do not overlap operands, except where it says so.
  *

@@ -33,7 +33,7 @@ CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUD
 # Kernels whose warps trade registers count on an exact number per thread at launch, and are refused at run time with
 # any other: {source: (kernel, registers)}.  ptxas says what it gave them.
 LAUNCH_REGISTERS = {"k_fp8_gemm.cu": (r"fp8_ring_kernelILi(128|256)E", 168),
-                    **{"k_ffn_%s.cu" % f: (r"ffn_ring_kernelILi256ELb1ELNS_7RingOutE[12]", 96)
+                    **{"k_ffn_%s.cu" % f: (r"ffn_ring_kernelILi256ELb1ELNS_7RingOutE[123]", 96)
                        for f in ("gated", "input_grad", "linear", "weight_grad")},
                     "k_umma.cu": (r"umma_i8_overlap_kernel", 128)}
 

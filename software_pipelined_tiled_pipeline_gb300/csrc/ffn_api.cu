@@ -78,12 +78,12 @@ int current_sms() {
 // Plan and launch a checked product.
 int run_product(FfnProduct& p, const gp_ffn_options* opts) {
   const bool codes = p.out.codes[0].data != nullptr, wide = p.out.out_f32 || codes;
-  int rc = ffn_plan_impl(p.op, p.rows, p.cols, p.summed, p.count, wide, codes, 0, opts, &p.plan);   // what needs no device
+  int rc = ffn_plan_impl(p.op, p.rows, p.cols, p.summed, p.count, wide, codes, p.out.bf16, 0, opts, &p.plan);   // what needs no device
   if (rc != GP_OK) return call_finish(rc);
   CallInfo info;
   cudaError_t e = call_begin(opts ? opts->timeout_ns : 0, &info);
   if (e != cudaSuccess) return call_finish(GP_ERR_CUDA, e, GP_SITE_DEVICE);
-  rc = ffn_plan_impl(p.op, p.rows, p.cols, p.summed, p.count, wide, codes, info.sm_count, opts, &p.plan);
+  rc = ffn_plan_impl(p.op, p.rows, p.cols, p.summed, p.count, wide, codes, p.out.bf16, info.sm_count, opts, &p.plan);
   if (rc != GP_OK) return call_finish(rc);
   e = ffn_fit_pairs(&p.plan, codes && p.op == kFfnGated);
   if (e != cudaSuccess) return call_finish(GP_ERR_CUDA, e, GP_SITE_CAPACITY);
@@ -119,8 +119,8 @@ int gemm_ffn_plan(int op, int64_t M, int64_t N, int64_t K, int count, int kept, 
   const int64_t rows = op == kFfnWeightGrad ? N : M, cols = op == kFfnLinear || op == kFfnGated ? N : K;
   const int64_t summed = op == kFfnInputGrad ? N : (op == kFfnWeightGrad ? M : K);
   if (rows == 0 || cols == 0) return GP_ERR_ARG;
-  return ffn_plan_impl(op, rows, cols, summed, count, kept != 0, kept != 0 && op <= kFfnGated, sms > 0 ? sms : current_sms(),
-                       opts, out);
+  return ffn_plan_impl(op, rows, cols, summed, count, kept != 0, kept != 0 && op <= kFfnGated, true,
+                       sms > 0 ? sms : current_sms(), opts, out);
 }
 
 int gemm_linear(const gp_linear* a, void* stream, const gp_ffn_options* opts) {

@@ -9,6 +9,12 @@ enum FfnOp { kFfnLinear = 0, kFfnGated = 1, kFfnInputGrad = 2, kFfnWeightGrad = 
 
 constexpr int kFfnBK = 64;             // summed axis per ring slot: 128 bytes of 16-bit values
 constexpr int kFfnRestart = 12;        // K blocks between restarts of the accumulator where more than 16 bits leave
+// The same where 16 bits leave: 4096 products in FP16, 32768 in BF16.  The tensor cores cut a sum by 2^-23 of its products'
+// magnitudes at most per product (16 at once: 1.0e-7 on average with operands of one sign, 6.4e-9 a product), so this loses
+// half a spacing of the output at most, and 2.6e-5 and 1.7e-4 were measured, a twentieth of that.  Without restarts FP16
+// lost 8.4e-4 after 131072 products, always towards zero: more than its rounding (4.9e-4).  Held sums cost the ring a
+// little: FP16 4096 x 4096 x 8192 163 -> 169 us.
+constexpr int kFfnRestartF16 = 64, kFfnRestartBF16 = 512;
 constexpr int64_t kFfnMaxTiles = int64_t(1) << 30;   // tile numbers plus a grid stay below 2^31
 
 // 8-bit codes with a scale for each row's 128 values, as the kernels see them.
@@ -48,7 +54,9 @@ struct FfnProduct {
   KernelCtl ctl;
 };
 
-int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count, bool wide_sums, bool codes, int sms,
+// K blocks that one accumulator takes.
+inline int ffn_restart(bool wide, bool bf16) { return wide ? kFfnRestart : (bf16 ? kFfnRestartBF16 : kFfnRestartF16); }
+int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count, bool wide_sums, bool codes, bool bf16, int sms,
                   const gp_ffn_options* opts, gp_plan* p);
 // Pairs must sit on one TPC each: where fewer fit at once than the plan counted on, launch those.
 cudaError_t ffn_fit_pairs(gp_plan* plan, bool whole_groups);

@@ -21,10 +21,10 @@
 // pairs, and take 3.5 instead of 4.
 //
 // The tensor cores cut their FP32 sums instead of rounding them, always towards
-// zero (measured on normal operands: 1.0e-6 relative after 1024 of K, 9e-6 after
-// 8192).  For 16-bit outputs that is far below their rounding (2^-9 on average
-// for BF16).  Where FP32 leaves, or the scales of 8-bit codes, the accumulator is
-// handed over every kFfnRestart slots (768 of K) and added to sums in registers.
+// zero (measured here on operands of one sign: 6e-6 relative after 1024 of K, 5.2e-5
+// after 8192, 4.2e-4 after 65536).  Where FP32 leaves, or the scales of 8-bit codes,
+// the accumulator is handed over every 768 of K and added to sums in registers; where
+// 16 bits leave, before the loss could reach their rounding (ffn_restart).
 #pragma once
 #include <atomic>
 #include <cstring>
@@ -58,7 +58,8 @@ static_assert(sizeof(RingBarriers) <= kRingBarrierBytes, "barrier region too sma
 // per lane to registers, hands the buffer back and works on them: it can add up
 // several hand-overs, and sees half of a group of 128 columns.  kCodes: the same
 // where 8-bit codes are kept, a kernel of its own as FP32 outputs would pay for its
-// registers (4096^3 with both gradients 168 -> 172 us).
+// registers (4096^3 with both gradients 168 -> 172 us).  kLong: the same where 16 bits
+// leave and the summed axis is longer than one accumulator takes.
 // L2 takes a request per row and access, beside those of the operands' loads.
 // Where more bytes leave than in 16 bits, lanes therefore exchange pieces first and
 // write longer runs of each row: FP32 128 bytes by four lanes (4096 x 4096 over
@@ -66,7 +67,7 @@ static_assert(sizeof(RingBarriers) <= kRingBarrierBytes, "barrier region too sma
 // codes 32 by two (4096 x 8192 x 2056 122 -> 112 us).  It does not pay where 16
 // bits leave alone (8192 x 8192 x 4096 271 us either way) nor in a gated product,
 // where it costs registers (288 -> 289 us, 323 -> 331 kept up).
-enum RingOut { kStream = 0, kHold = 1, kCodes = 2 };
+enum RingOut { kStream = 0, kHold = 1, kCodes = 2, kLong = 3 };
 
 template <int BN, bool PAIR, RingOut OUT>
 struct RingShape {
@@ -621,8 +622,8 @@ __device__ __forceinline__ void finish_linear(const RingParams& g, int p, float 
       return;
     }
   }
-  if constexpr (sizeof(O) == 2) {
-    if (o.vec == 2 && col0 + 64 <= cols && !o.add[p]) {   // (held for their codes: nothing else is kept)
+  if constexpr (sizeof(O) == 2 && CODES) {
+    if (o.vec == 2 && col0 + 64 <= cols && !o.add[p]) {   // (beside codes nothing else is kept)
       if (!whole) return;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -641,29 +642,31 @@ __device__ __forceinline__ void finish_linear(const RingParams& g, int p, float 
 
 // h = act(g) * u of a lane's 32 columns: acc[0] are g's sums, acc[1] u's.  `part`: which 32 of the tile's columns, four of
 // which are a group of 128.
-template <typename T>
+template <typename T, bool CODES>
 __device__ __forceinline__ void finish_gated(const RingParams& g, float (&acc)[2][32], uint32_t slot, int lane, int quarter,
                                              int part, int64_t row, int64_t col0, bool write) {
   const FfnOut& o = g.o;
   const int64_t cols = g.cols;
-  if (col0 + 32 > cols) {   // (an infinity times a column that is not there is NaN)
+  if constexpr (CODES) {
+    if (col0 + 32 > cols) {   // (an infinity times a column that is not there is NaN)
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (col0 + i >= cols) acc[0][i] = acc[1][i] = 0.f;
-  }
-  float most[2] = {max_abs_of(acc[0]), max_abs_of(acc[1])};
-  share_max(most, slot, lane, part, 4, 2 + quarter);
-  if (write && col0 < cols) {
-    const int n = columns_left(col0, cols);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const GroupScale s = group_scale(__float_as_uint(most[j]), 448.f);
-      const FfnCodes& q = o.codes[j];
-      if (part == 0) q.scales[row * q.stride_row + (col0 >> 7) * q.stride_col] = s.scale;
-      emit_codes(q, acc[j], s.inv, row, col0, n);
+      for (int i = 0; i < 32; ++i)
+        if (col0 + i >= cols) acc[0][i] = acc[1][i] = 0.f;
     }
-    emit_gated<T>(o, acc[0], acc[1], row, col0, n);
+    float most[2] = {max_abs_of(acc[0]), max_abs_of(acc[1])};
+    share_max(most, slot, lane, part, 4, 2 + quarter);
+    if (write && col0 < cols) {
+      const int n = columns_left(col0, cols);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const GroupScale s = group_scale(__float_as_uint(most[j]), 448.f);
+        const FfnCodes& q = o.codes[j];
+        if (part == 0) q.scales[row * q.stride_row + (col0 >> 7) * q.stride_col] = s.scale;
+        emit_codes(q, acc[j], s.inv, row, col0, n);
+      }
+    }
   }
+  if (write && col0 < cols) emit_gated<T>(o, acc[0], acc[1], row, col0, columns_left(col0, cols));
   __syncwarp();
 }
 
@@ -941,11 +944,11 @@ __global__ void __launch_bounds__(RingShape<BN, PAIR, OUT>::THREADS, 1)
         const uint32_t slot = smem_u32(maxima) + e * kMaxSlot;
         if constexpr (GATED) {
           if (g.o.bf16)
-            finish_gated<__nv_bfloat16>(g, acc, slot, lane, quarter, part, row, col0, write);
+            finish_gated<__nv_bfloat16, OUT == kCodes>(g, acc, slot, lane, quarter, part, row, col0, write);
           else
-            finish_gated<__half>(g, acc, slot, lane, quarter, part, row, col0, write);
+            finish_gated<__half, OUT == kCodes>(g, acc, slot, lane, quarter, part, row, col0, write);
         } else {
-          const bool f32 = OUT == kHold || g.o.out_f32;   // (16-bit outputs are held for their codes only)
+          const bool f32 = OUT == kHold || (OUT == kCodes && g.o.out_f32);
           if (g.o.bf16) {
             if (f32)
               finish_linear<__nv_bfloat16, float, OUT == kCodes>(g, problem, acc, slot, lane, quarter, part, row, col0, whole, add_first);
@@ -1072,8 +1075,7 @@ cudaError_t launch_ring(FfnProduct& p, const void** kernel) {
   g.kt = static_cast<int32_t>((p.summed + kFfnBK - 1) / kFfnBK);
   g.sources = sum ? 2 : 1;
   g.problems = both ? 2 : 1;
-  const bool wide = p.out.out_f32 || p.out.codes[0].data;
-  g.restart = wide ? kFfnRestart : (g.kt > 0 ? g.kt * g.sources : 1);
+  g.restart = ffn_restart(p.out.out_f32 || p.out.codes[0].data, p.out.bf16 != 0);
   g.raster = p.plan.raster_gm;
   g.idesc = umma_idesc_f16(p.out.bf16 != 0, Sh::TILE_ROWS, BN) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
   g.idesc_half = umma_idesc_f16(p.out.bf16 != 0, Sh::TILE_ROWS, BN / 2) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
@@ -1089,12 +1091,16 @@ cudaError_t launch_ring(FfnProduct& p, const void** kernel) {
   return cudaLaunchKernelEx(&c.cfg, k, maps, g);
 }
 
-// The tile of the plan; sums are held where FP32 or 8-bit codes leave.
+// The tile of the plan; sums are held where FP32 or 8-bit codes leave, or one accumulator does not take them all.
 template <bool GATED, bool A_MN, bool B_MN>
 cudaError_t launch_tile(FfnProduct& p, const void** kernel) {
   const bool wide = p.out.out_f32 || p.out.codes[0].data;
+  const bool lasting = !wide && p.plan.k_tiles > ffn_restart(false, p.out.bf16 != 0);
   if constexpr (GATED) {   // (8 bits on pairs alone)
     if (wide) return launch_ring<256, true, kCodes, true, A_MN, B_MN>(p, kernel);
+    if (lasting)
+      return p.plan.cta_pair ? launch_ring<256, true, kLong, true, A_MN, B_MN>(p, kernel)
+                             : launch_ring<128, false, kLong, true, A_MN, B_MN>(p, kernel);
     return p.plan.cta_pair ? launch_ring<256, true, kStream, true, A_MN, B_MN>(p, kernel)
                            : launch_ring<128, false, kStream, true, A_MN, B_MN>(p, kernel);
   } else {
@@ -1107,6 +1113,9 @@ cudaError_t launch_tile(FfnProduct& p, const void** kernel) {
     if (wide)
       return pair ? launch_ring<256, true, kHold, false, A_MN, B_MN>(p, kernel)
                   : launch_ring<128, false, kHold, false, A_MN, B_MN>(p, kernel);
+    if (lasting)
+      return pair ? launch_ring<256, true, kLong, false, A_MN, B_MN>(p, kernel)
+                  : launch_ring<128, false, kLong, false, A_MN, B_MN>(p, kernel);
     return pair ? launch_ring<256, true, kStream, false, A_MN, B_MN>(p, kernel)
                 : launch_ring<128, false, kStream, false, A_MN, B_MN>(p, kernel);
   }

@@ -466,7 +466,7 @@ cudaError_t launch_as(FfnProduct& p, const void** kernel) {
   g.kt = static_cast<int32_t>((p.summed + kFfnBK - 1) / kFfnBK);
   g.sources = sum ? 2 : 1;
   g.problems = both ? 2 : 1;
-  g.restart = p.out.out_f32 ? kFfnRestart : (g.kt > 0 ? g.kt * g.sources : 1);
+  g.restart = ffn_restart(p.out.out_f32 != 0, p.out.bf16 != 0);
   g.k_log = p.plan.k_splits == 8 ? 3 : (p.plan.k_splits == 4 ? 2 : (p.plan.k_splits == 2 ? 1 : 0));
   g.row_blocks = (g.rows + BN - 1) / BN;
   g.per_problem = g.row_blocks * ((g.cols + 127) / 128);

@@ -48,7 +48,7 @@ void ffn_cut_tail(gp_plan* p, bool whole_groups) {
 
 }  // namespace
 
-int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count, bool wide_sums, bool codes, int sms,
+int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count, bool wide_sums, bool codes, bool bf16, int sms,
                   const gp_ffn_options* opts, gp_plan* p) {
   std::memset(p, 0, sizeof(*p));
   const int want = opts ? opts->tile : 0;
@@ -145,7 +145,7 @@ int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count,
     p->cta_pair = tile == 256;
     p->bm = tile;
     p->bn = gated ? tile / 2 : tile;
-    const bool hold = wide_sums;
+    const bool hold = wide_sums || kt > ffn_restart(false, bf16);
     if (tile == 256)
       hold ? ring_shape_of<256, true, kHold>(p) : ring_shape_of<256, true, kStream>(p);
     else

@@ -755,3 +755,96 @@ def test_gradients_against_differences():
             # magnitudes of what was added up
             scale = float((g.double() * d).abs().sum()) + abs(want)
             assert abs(got - want) <= 3 * 2.0 ** -11 * 4 * scale, (act, i, got, want)
+
+
+# ---------------------------------------------------------------------------
+# sums longer than one accumulator takes (4096 products in FP16, 32768 in BF16, 768 where FP32 leaves)
+# ---------------------------------------------------------------------------
+LONGEST = {F16: 4096, BF16: 32768}
+
+
+def one_sign(g, rows, cols, dtype):
+    return (torch.rand(rows, cols, generator=g, device="cuda") * 0.5 + 0.5).mul_(2.0 ** -5).to(dtype)
+
+
+@pytest.mark.parametrize("dtype,K", [(F16, 1 << 20), (BF16, 1 << 22)])
+def test_long_sums_of_one_sign(dtype, K):
+    """What the tensor cores cut of a sum does not grow with its length: at most 2^-23 of the sum per product of one
+    accumulator (half a spacing of the output for as many as it takes), 2^-24 for each of the parts, and the rounding.  A
+    product of two sums (1 + a)(1 + b) is off by 2 share + share^2.  What lies past the type's range is infinite."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    share = LONGEST[dtype] * 2.0 ** -23 + (K // LONGEST[dtype] + 1) * 2.0 ** -24
+
+    def close(got, want, sums=1):
+        off = (1 + share) ** sums - 1
+        past = want >= ref.LARGEST[dtype] * (1 + off)
+        assert bool(torch.isinf(got[past]).all())
+        far = float(((got.double() - want).abs() / want)[~past].max()) if not bool(past.all()) else 0.0
+        assert far <= off + ref.UNIT[dtype] * (1 + off), far
+
+    x, w = one_sign(g, 8, K, dtype), one_sign(g, 24, K, dtype)
+    want = x.double() @ w.double().t()
+    for tile, splits in ((0, 0), (16, 1), (32, 2), (64, 1), (129, 1), (128, 0), (256, 0)):
+        y, (z,) = gp.linear(x, w, keep="real", tile=tile, k_splits=splits)
+        close(y, want)
+        close(z, want)
+        if tile != 129:
+            h, (gate, up) = gp.gated(x, w, w * 0.5, activation=None, keep="real", tile=tile, k_splits=splits)
+            close(h, want * want * 0.5, 2)
+            close(gate, want)
+            close(up, want * 0.5)
+            close(gp.gated(x, w, w * 2.0 ** -6, activation=None, tile=tile, k_splits=splits), want * want * 2.0 ** -6, 2)
+    del x, w
+    dy, x = one_sign(g, K, 8, dtype), one_sign(g, K, 24, dtype)      # K tokens
+    want = dy.double().t() @ x.double()
+    z = torch.ones_like(dy)
+    for tile, splits in ((0, 0), (64, 1), (129, 1), (128, 0), (256, 0)):
+        close(gp.linear_backward(dy, x, x[:8], input_grad=False, tile=tile, k_splits=splits)[1], want)
+        _, dg, du = gp.gated_backward(dy, x, x[:8], x[:8], (z, z), activation="relu", input_grad=False, tile=tile, k_splits=splits)
+        close(dg, want)
+        close(du, want)
+    half = K // 2
+    dy, w = one_sign(g, 8, half, dtype), one_sign(g, half, 24, dtype)
+    want = dy.double() @ w.double()
+    z = torch.ones_like(dy)
+    for tile, splits in ((0, 0), (16, 1), (64, 2), (129, 1), (128, 0), (256, 0)):
+        close(gp.linear_backward(dy, None, w, weight_grad=False, tile=tile, k_splits=splits)[0], want)
+        got = gp.gated_backward(dy, None, w, w, (z, z), activation="relu", weight_grad=False, tile=tile, k_splits=splits)[0]
+        close(got, 2 * want)                                         # two products, one sum
+    status_ok()
+
+
+@pytest.mark.parametrize("tile", [0, 64, 129, 128, 256])
+@pytest.mark.parametrize("K", [4096, 4097, 4160, 8200, 12300])
+def test_long_sums_of_whole_numbers_are_exact(tile, K):
+    """Around the lengths that one accumulator takes, ragged outputs: every part is added once."""
+    M, N = 200, 328
+    check_linear(M, N, K, F16, whole=1, bias=F16, residual=True, tile=tile)
+    check_linear(M, N + 1, K, F16, whole=1, keep="real", tile=tile, ld=N + 8)
+    if tile != 129:
+        check_gated(M, N, K, F16, act=None, keep="real", tile=tile)
+        check_gated(M, N + 3, K, F16, tile=tile)
+    rng = np.random.default_rng(K)
+    dy, x, w = (ref.matrix(rng, r, c, F16, whole=1) for r, c in ((K, M), (K, N), (M, N)))
+    add = ref.matrix(rng, M, N, F16, whole=2)
+    _, dw, _ = gp.linear_backward(dy, x, w, input_grad=False, addend=add, tile=tile)
+    assert torch.equal(dw, (dy.double().t() @ x.double() + add.double()).to(F16))
+    relu = torch.ones_like(dy)
+    _, dg, du = gp.gated_backward(dy, x, w, w, (relu, relu + 1), activation="relu", input_grad=False, tile=tile)
+    assert torch.equal(du, (dy.double().t() @ x.double()).to(F16))
+    assert torch.equal(dg, (2 * (dy.double().t() @ x.double())).to(F16))
+    dy, w = ref.matrix(rng, M, K, F16, whole=1), ref.matrix(rng, K, N, F16, whole=1)
+    assert torch.equal(gp.linear_backward(dy, None, w, weight_grad=False, tile=tile)[0], (dy.double() @ w.double()).to(F16))
+    half = K // 2
+    dy, w, u = ref.matrix(rng, M, half, F16, whole=1), ref.matrix(rng, half, N, F16, whole=1), ref.matrix(rng, half, N, F16, whole=1)
+    relu = torch.ones_like(dy)
+    got = gp.gated_backward(dy, None, w, u, (relu, relu), activation="relu", weight_grad=False, tile=tile)[0]
+    assert torch.equal(got, (dy.double() @ (w.double() + u.double())).to(F16))
+    status_ok()
+
+
+def test_long_sums_cut_in_halves():
+    """More tiles than pairs of CTAs, the last of them as halves of their columns, over more than one accumulator's sum."""
+    for M, N in ((2560, 2304), (2300, 2500)):
+        assert check_linear(M, N, 4200, F16, whole=1, residual=True, tile=256)["half_tiles"] > 0
+        assert check_gated(M, N // 2, 4200, F16, keep="real", tile=256)["half_tiles"] > 0
