@@ -32,14 +32,25 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return r;
 }
 
+// z up to `most` either way, a NaN as it is.
+__device__ __forceinline__ float at_most(float z, float most) {
+  float r;
+  asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, %2;\n\tmax.NaN.f32 %0, t, %3;\n\t}" : "=f"(r) : "f"(z), "f"(most), "f"(-most));
+  return r;
+}
+
 struct Sigmoid {
   float s, rest;   // sigmoid and 1 - sigmoid
 };
-__device__ __forceinline__ Sigmoid sigmoid_of(float z) {
-  const float t = z < -88.f ? 88.f : -z;     // (e stays finite and s is 0 there; a NaN stays)
-  const float e = fast_exp(t);
+__device__ __forceinline__ Sigmoid sigmoid_above(float z) {   // (z above -88.7, where e is finite)
+  const float e = fast_exp(-z);
   const float s = fast_rcp(1.f + e);
   return Sigmoid{s, e * s};
+}
+__device__ __forceinline__ Sigmoid sigmoid_of(float z) {
+  float t;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(t) : "f"(z), "f"(-88.f));   // (s is 0 there; a NaN stays)
+  return sigmoid_above(t);
 }
 
 // Two FP32 values in one 64-bit register: a packed FMA is one instruction, and rounds each half as a single one does.
@@ -103,16 +114,20 @@ struct ActSlope {
 __device__ __forceinline__ ActSlope gelu_slope(float z, float u, float h, float e) {
   return ActSlope{fmaxf(z, 0.f) - u * h, fmaf(copysignf(u, z) * kRsqrt2Pi, e, z > 0.f ? 1.f - h : h)};
 }
+// In silu and gelu_tanh z is a factor of what vanishes for large |z|: it goes up to where that is 0 only, as its square, or an
+// infinity, would make that NaN (values kept in FP16 are infinite where the sum was past 65504, the output beside them not).
 __device__ __forceinline__ ActSlope activate_slope(float z, int act) {
   switch (act) {
     case GP_ACT_RELU: return ActSlope{z > 0.f ? z : (z != z ? z : 0.f), z > 0.f ? 1.f : (z != z ? z : 0.f)};
     case GP_ACT_GELU_TANH: {
-      const Sigmoid g = sigmoid_of(kTanhScale * fmaf(kTanhCube * z * z, z, z));
-      return ActSlope{z * g.s, fmaf(z * g.s * g.rest, kTanhScale * fmaf(3.f * kTanhCube * z, z, 1.f), g.s)};
+      const float c = at_most(z, 20.f);
+      const Sigmoid g = sigmoid_of(kTanhScale * fmaf(kTanhCube * c * c, c, c));
+      return ActSlope{fmaxf(z, c) * g.s, fmaf(c * g.s * g.rest, kTanhScale * fmaf(3.f * kTanhCube * c, c, 1.f), g.s)};
     }
     case GP_ACT_SILU: {
-      const Sigmoid g = sigmoid_of(z);
-      return ActSlope{z * g.s, fmaf(z * g.s, g.rest, g.s)};
+      const float c = at_most(z, 88.f);
+      const Sigmoid g = sigmoid_above(c);
+      return ActSlope{fmaxf(z, c) * g.s, fmaf(c * g.s, g.rest, g.s)};
     }
     case GP_ACT_SIGMOID: {
       const Sigmoid g = sigmoid_of(z);

@@ -848,3 +848,26 @@ def test_long_sums_cut_in_halves():
     for M, N in ((2560, 2304), (2300, 2500)):
         assert check_linear(M, N, 4200, F16, whole=1, residual=True, tile=256)["half_tiles"] > 0
         assert check_gated(M, N // 2, 4200, F16, keep="real", tile=256)["half_tiles"] > 0
+
+
+@pytest.mark.parametrize("act", ref.ACTS[1:])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_slopes_far_from_zero(act, dtype):
+    """Large kept values, and FP16's that were past its range: an activation's slope there is its limit, 1 or 0, and the
+    activation z or 0 (sigmoid: 1 or 0).  A NaN stays one.  Exact, as both are."""
+    values = [3e4, 6e4, float("inf")] if dtype is F16 else [1e5, 7e18, 1e20, 3e38, float("inf")]
+    z = torch.tensor([v for x in values for v in (x, -x)] + [float("nan")], dtype=dtype, device="cuda")
+    n, up = z.numel(), z > 0
+    for N in (n, 136):                           # (rows whose four values a lane takes one by one or together)
+        wide = torch.ones(3, N, dtype=dtype, device="cuda")
+        wide[:, :n] = z
+        dy = torch.full((3, N), 0.5, dtype=dtype, device="cuda")
+        w = torch.eye(N, dtype=dtype, device="cuda")
+        db = gp.linear_backward(dy, None, w, activation=act, kept=(wide,), bias_grad=True, input_grad=False, weight_grad=False)[2]
+        slope = torch.zeros(n, device="cuda") if act == "sigmoid" else up.float()
+        assert torch.equal(db[:n - 1], 1.5 * slope[:-1]) and bool(torch.isnan(db[n - 1])), db
+        h = gp.gated_backward(dy, None, w, w, (wide, torch.full_like(wide, 0.25)), activation=act, product=True, input_grad=False,
+                              weight_grad=False)[3]
+        value = torch.where(up, torch.ones_like(z) if act == "sigmoid" else z, torch.zeros_like(z))
+        assert torch.equal(h[:, :n - 1], (value * 0.25)[:-1].expand(3, n - 1)) and bool(torch.isnan(h[:, n - 1]).all())
+        status_ok()
