@@ -74,6 +74,9 @@ typedef struct gp_ffn_options {
     int32_t inject_lost_load;    /* test hook: the TMA producer skips the last tile load of the problem, so a consumer
                                     wait runs out and the call reports GP_ERR_TIMEOUT (no GPU fault); not with tile 256
                                     (GP_ERR_UNSUPPORTED), and the planner does not choose that then */
+    int32_t continues;           /* 1: gemm_stats() speaks of this call and the one before it by this thread (on the same
+                                    device and stream) together: a wait that gave up in either is GP_ERR_TIMEOUT, the
+                                    rest of the record is this call's.  Several calls may go on so */
 } gp_ffn_options;
 
 /*

@@ -116,7 +116,7 @@ class GpFp8Options(ctypes.Structure):
 class GpFfnOptions(ctypes.Structure):
     _fields_ = [
         ("timeout_ns", ctypes.c_uint64), ("tile", ctypes.c_int32), ("k_splits", ctypes.c_int32),
-        ("inject_lost_load", ctypes.c_int32),
+        ("inject_lost_load", ctypes.c_int32), ("continues", ctypes.c_int32),
     ]
 
 

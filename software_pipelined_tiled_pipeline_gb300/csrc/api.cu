@@ -715,11 +715,13 @@ void record(int status, int cuda_err, int site = 0) {
 // ---------------------------------------------------------------------------
 // per-call state of the FP8 entry points (fp8_api.cu)
 // ---------------------------------------------------------------------------
-void call_reset(cudaStream_t stream) {
+void call_reset(cudaStream_t stream, bool continues) {
   std::memset(&t_last.stats, 0, sizeof(t_last.stats));
-  t_last.status_slot = nullptr;
-  t_last.call_id = 0;
-  t_last.device = -1;
+  if (!continues) {
+    t_last.status_slot = nullptr;
+    t_last.call_id = 0;
+    t_last.device = -1;
+  }
   t_fail_site = 0;
   t_last.stats.last_ms = -1.f;
   t_last.kernel = nullptr;
@@ -735,6 +737,10 @@ cudaError_t call_begin(uint64_t timeout_ns, CallInfo* info) {
   int sms = 0;
   if (e == cudaSuccess) e = device_info(dev, &sms, &call_id, &status);
   if (e != cudaSuccess) return e;
+  if (t_last.status_slot && t_last.device == dev) {   // the call before's (call_reset): the first wait that gave up in either stays there
+    status = t_last.status_slot;
+    call_id = t_last.call_id;
+  }
   t_last.device = dev;
   t_last.status_slot = status;
   t_last.call_id = call_id;

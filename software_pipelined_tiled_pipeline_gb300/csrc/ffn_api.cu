@@ -125,7 +125,7 @@ int gemm_ffn_plan(int op, int64_t M, int64_t N, int64_t K, int count, int kept, 
 
 int gemm_linear(const gp_linear* a, void* stream, const gp_ffn_options* opts) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  call_reset(st);
+  call_reset(st, opts && opts->continues);
   if (!a) return call_finish(GP_ERR_ARG);
   int rc = check_sizes(a->M, a->N, a->K);
   if (rc == GP_OK && (!type_ok(a->type) || !out_ok(a->type, a->out_type) || !act_ok(a->activation))) rc = GP_ERR_ARG;
@@ -171,7 +171,7 @@ int gemm_linear(const gp_linear* a, void* stream, const gp_ffn_options* opts) {
 
 int gemm_gated(const gp_gated* a, void* stream, const gp_ffn_options* opts) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  call_reset(st);
+  call_reset(st, opts && opts->continues);
   if (!a) return call_finish(GP_ERR_ARG);
   int rc = check_sizes(a->M, a->N, a->K);
   if (rc == GP_OK && (!type_ok(a->type) || !act_ok(a->activation))) rc = GP_ERR_ARG;
@@ -218,7 +218,7 @@ int gemm_gated(const gp_gated* a, void* stream, const gp_ffn_options* opts) {
 
 int gemm_input_grad(const gp_input_grad* a, void* stream, const gp_ffn_options* opts) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  call_reset(st);
+  call_reset(st, opts && opts->continues);
   if (!a) return call_finish(GP_ERR_ARG);
   int rc = check_sizes(a->M, a->N, a->K);
   if (rc == GP_OK && (!type_ok(a->type) || !out_ok(a->type, a->out_type) || a->count < 1 || a->count > 2)) rc = GP_ERR_ARG;
@@ -252,7 +252,7 @@ int gemm_input_grad(const gp_input_grad* a, void* stream, const gp_ffn_options* 
 
 int gemm_weight_grad(const gp_weight_grad* a, void* stream, const gp_ffn_options* opts) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  call_reset(st);
+  call_reset(st, opts && opts->continues);
   if (!a) return call_finish(GP_ERR_ARG);
   int rc = check_sizes(a->M, a->N, a->K);
   if (rc == GP_OK && (!type_ok(a->type) || !out_ok(a->type, a->out_type) || a->count < 1 || a->count > 2)) rc = GP_ERR_ARG;

@@ -102,7 +102,7 @@ struct CallInfo {
   KernelCtl ctl;
 };
 // Start this thread's last-call record.
-void call_reset(cudaStream_t stream);
+void call_reset(cudaStream_t stream, bool continues = false);   // continues: with the status slot of the call before
 // Device, SM count and status slot of a call that is about to launch.
 cudaError_t call_begin(uint64_t timeout_ns, CallInfo* info);
 // What the record shows of the launch.

@@ -237,6 +237,18 @@ const gp_ffn_options* options(PyObject* o) {   // None, or the packed struct
   return o == Py_None ? nullptr : reinterpret_cast<const gp_ffn_options*>(PyBytes_AS_STRING(o));
 }
 
+// The options of one of the products that a call makes: `which` in the test hook's bits; one that `continues` shares the
+// record of the product before, so that a wait that gave up in either is the call's status.
+struct ProductOptions {
+  gp_ffn_options own = {};
+  const gp_ffn_options* p;
+  ProductOptions(const gp_ffn_options* given, int which, bool continues) : p(given || continues ? &own : nullptr) {
+    if (given) own = *given;
+    own.inject_lost_load = own.inject_lost_load & which ? 1 : 0;
+    own.continues = continues;
+  }
+};
+
 PyObject* wrap(const at::Tensor& t) {
   if (!t.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(t);
@@ -526,9 +538,10 @@ PyObject* linear_backward(PyObject* const* a) {
     } else {
       md16 = operand(dy, "dy", nullptr, call);
     }
-    if (want_x) dx = input_gradient(1, &md16, &mw, M, N, vw.cols, real, dy, call, opts);
+    if (want_x) dx = input_gradient(1, &md16, &mw, M, N, vw.cols, real, dy, call, ProductOptions(opts, 1, false).p);
     if (want_w)
-      weight_gradients(1, &md16, mx, N, real, a[8], a[9], a[10], dy, tensor(a[1], "x"), own ? nullptr : &dy, call, opts, &dw);
+      weight_gradients(1, &md16, mx, N, real, a[8], a[9], a[10], dy, tensor(a[1], "x"), own ? nullptr : &dy, call,
+                       ProductOptions(opts, 2, want_x).p, &dw);
   }
   return tuple({dx, dw, dbias});
 }
@@ -591,8 +604,10 @@ PyObject* gated_backward(PyObject* const* a) {
   g.type = real;
   g.activation = static_cast<int32_t>(PyLong_AsLong(a[5]));
   check(lib.gated_backward(&g, call.stream), "ffn_gated_backward");
-  if (want_x) dx = input_gradient(2, dz, mw, M, N, vg.cols, real, dh, call, opts);
-  if (want_w) weight_gradients(2, dz, mx, N, real, a[9], a[10], a[11], dh, tensor(a[1], "x"), nullptr, call, opts, dw);
+  if (want_x) dx = input_gradient(2, dz, mw, M, N, vg.cols, real, dh, call, ProductOptions(opts, 1, false).p);
+  if (want_w)
+    weight_gradients(2, dz, mx, N, real, a[9], a[10], a[11], dh, tensor(a[1], "x"), nullptr, call,
+                     ProductOptions(opts, 2, want_x).p, dw);
   return product ? tuple({dx, dw[0], dw[1], h}) : tuple({dx, dw[0], dw[1]});
 }
 

@@ -107,7 +107,7 @@ def gated(x, w_gate, w_up, *, activation="silu", keep=None, out=None, stream=Non
 
 
 def linear_backward(dy, x, weight, *, activation=None, kept=None, bias_grad=False, input_grad=True, weight_grad=True,
-                    out_dtype=None, addend=None, out=None, stream=None, tile=0, k_splits=0, timeout_ns=0):
+                    out_dtype=None, addend=None, out=None, stream=None, tile=0, k_splits=0, timeout_ns=0, inject_lost_load=0):
     """Gradients of y = act(x W^T + bias) + residual: (dx, dweight, dbias); the residual's is dy itself.
 
     ``kept``: what ``linear`` returned with ``keep``, where there is an
@@ -117,33 +117,37 @@ def linear_backward(dy, x, weight, *, activation=None, kept=None, bias_grad=Fals
     be ``out`` itself) is added to it in FP32.  dbias (float32) is summed from dz
     before its rounding.  What is not asked for (``input_grad``, ``weight_grad``,
     ``bias_grad``) is None; without ``weight_grad`` x may be None too.
+    ``gemm_stats(sync=True)`` speaks of both products: a wait that gave up in
+    either is its status.  ``inject_lost_load``: 1 in dx's product, 2 in
+    dweight's, 3 in both.
     """
     if stream is not None:
         with _On(_device_of(dy, "dy"), stream):
             return linear_backward(dy, x, weight, activation=activation, kept=kept, bias_grad=bias_grad,
                                    input_grad=input_grad, weight_grad=weight_grad, out_dtype=out_dtype, addend=addend, out=out,
-                                   tile=tile, k_splits=k_splits, timeout_ns=timeout_ns)
-    opts = _pack(timeout_ns, tile, k_splits, 0) if tile or k_splits or timeout_ns else None
+                                   tile=tile, k_splits=k_splits, timeout_ns=timeout_ns, inject_lost_load=inject_lost_load)
+    opts = _pack(timeout_ns, tile, k_splits, inject_lost_load) if tile or k_splits or timeout_ns or inject_lost_load else None
     return _calls.linear_backward(dy, x, weight, _activation(activation), kept, bool(bias_grad), bool(input_grad),
                                   bool(weight_grad), out_dtype, addend, out, opts)
 
 
 def gated_backward(dh, x, w_gate, w_up, kept, *, activation="silu", product=False, input_grad=True, weight_grad=True,
-                   out_dtype=None, addend=None, out=None, stream=None, tile=0, k_splits=0, timeout_ns=0):
+                   out_dtype=None, addend=None, out=None, stream=None, tile=0, k_splits=0, timeout_ns=0, inject_lost_load=0):
     """Gradients of h = act(x Wg^T) * (x Wu^T): (dx, dw_gate, dw_up), and h once more with ``product``.
 
     ``kept``: what ``gated`` returned with ``keep``.  The gradients of both
     products are rounded to x's type for the products behind them.  ``out_dtype``,
     ``addend``, ``out`` as in ``linear_backward``, the last two a pair each.
     h, for the gradient of the weight that reads it, need not have been kept.
-    Without ``weight_grad`` x may be None.
+    Without ``weight_grad`` x may be None.  ``inject_lost_load`` and what
+    ``gemm_stats`` says as in ``linear_backward``.
     """
     if stream is not None:
         with _On(_device_of(dh, "dh"), stream):
             return gated_backward(dh, x, w_gate, w_up, kept, activation=activation, product=product, input_grad=input_grad,
                                   weight_grad=weight_grad, out_dtype=out_dtype, addend=addend, out=out, tile=tile,
-                                  k_splits=k_splits, timeout_ns=timeout_ns)
-    opts = _pack(timeout_ns, tile, k_splits, 0) if tile or k_splits or timeout_ns else None
+                                  k_splits=k_splits, timeout_ns=timeout_ns, inject_lost_load=inject_lost_load)
+    opts = _pack(timeout_ns, tile, k_splits, inject_lost_load) if tile or k_splits or timeout_ns or inject_lost_load else None
     return _calls.gated_backward(dh, x, w_gate, w_up, kept, _activation(activation), bool(product), bool(input_grad),
                                  bool(weight_grad), out_dtype, addend, out, opts)
 

@@ -871,3 +871,37 @@ def test_slopes_far_from_zero(act, dtype):
         value = torch.where(up, torch.ones_like(z) if act == "sigmoid" else z, torch.zeros_like(z))
         assert torch.equal(h[:, :n - 1], (value * 0.25)[:-1].expand(3, n - 1)) and bool(torch.isnan(h[:, n - 1]).all())
         status_ok()
+
+
+@pytest.mark.parametrize("tile", [64, 128])
+@pytest.mark.parametrize("lost", [1, 2, 3])
+def test_a_lost_load_in_either_product_of_a_backward_call_is_reported(lost, tile):
+    """The status of a call that makes two products is that of both, the first one's too."""
+    x, w, _, _, _ = block_operands(300, 384, 1500, 4)
+    dy = ref.matrix(np.random.default_rng(5), 300, 384, BF16)
+    z = torch.ones_like(dy)
+    calls = (lambda **kw: gp.linear_backward(dy, x, w[0], activation="relu", kept=(z,), tile=tile, **kw),
+             lambda **kw: gp.gated_backward(dy, x, *w, (z, z), tile=tile, **kw))
+    for call in calls:
+        want = call()
+        status_ok()
+        got = call(timeout_ns=5_000_000, inject_lost_load=lost)
+        st = gp.gemm_stats(sync=True)
+        assert st["status"] == gp.GP_ERR_TIMEOUT and st["device_status"] != 0
+        assert gp.gemm_stats(sync=True)["status"] == gp.GP_ERR_TIMEOUT       # (asked again)
+        if lost == 1:
+            assert all(torch.equal(a, b) for a, b in zip(got[1:], want[1:]) if a is not None)
+        if lost == 2:
+            assert torch.equal(got[0], want[0])
+        again = call()                                                        # a record of its own
+        status_ok()
+        assert all(torch.equal(a, b) for a, b in zip(again, want) if a is not None)
+    # one product alone
+    gp.linear_backward(dy, None, w[0], weight_grad=False, tile=tile, timeout_ns=5_000_000, inject_lost_load=1)
+    assert gp.gemm_stats(sync=True)["status"] == gp.GP_ERR_TIMEOUT
+    gp.linear_backward(dy, x, w[0], input_grad=False, tile=tile)
+    status_ok()
+    gp.linear_backward(dy, x, w[0], input_grad=False, tile=tile, timeout_ns=5_000_000, inject_lost_load=2)
+    assert gp.gemm_stats(sync=True)["status"] == gp.GP_ERR_TIMEOUT
+    gp.linear_backward(dy, x, w[0], tile=tile, inject_lost_load=0)
+    status_ok()
