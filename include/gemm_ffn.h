@@ -164,7 +164,8 @@ int gemm_weight_grad(const gp_weight_grad* args, void* stream, const gp_ffn_opti
 /*
  * gemm_ffn_plan -- the kernel and tile that a call would choose on a device with `sms` SMs (0: the current device;
  * without one, as on 152 SMs with gp_plan.grid left 0).  op: 0 gemm_linear, 1 gemm_gated, 2 gemm_input_grad,
- * 3 gemm_weight_grad; M, N, K and count as in that call; kept: 1 where values are kept in 8 bits, or FP32 is written.
+ * 3 gemm_weight_grad; M, N, K and count as in that call; kept: the sum of 1 where values are kept in 8 bits (gradients:
+ * FP32 is written), 2 where FP32 is written, 4 where the type is GP_REAL_F16 (gemm_gated: not 2; others: GP_ERR_ARG).
  * gp_plan.bm x bn is the tile (where layout is 1, bm counts columns of the output and bn rows); k_splits CTAs, one cluster,
  * share each tile's K loop; the last half_tiles tiles (after dp_tiles whole ones) run as two halves of their columns each.
  */

@@ -113,13 +113,15 @@ extern "C" {
 
 int gemm_ffn_plan(int op, int64_t M, int64_t N, int64_t K, int count, int kept, int sms, const gp_ffn_options* opts,
                   gp_plan* out) {
-  if (!out || sms < 0 || op < kFfnLinear || op > kFfnWeightGrad || count < 1 || count > 2) return GP_ERR_ARG;
+  if (!out || sms < 0 || op < kFfnLinear || op > kFfnWeightGrad || count < 1 || count > 2 || kept < 0 || kept > 7 ||
+      (op == kFfnGated && (kept & 2)))
+    return GP_ERR_ARG;
   const int rc = check_sizes(M, N, K);
   if (rc != GP_OK) return rc;
   const int64_t rows = op == kFfnWeightGrad ? N : M, cols = op == kFfnLinear || op == kFfnGated ? N : K;
   const int64_t summed = op == kFfnInputGrad ? N : (op == kFfnWeightGrad ? M : K);
   if (rows == 0 || cols == 0) return GP_ERR_ARG;
-  return ffn_plan_impl(op, rows, cols, summed, count, kept != 0, kept != 0 && op <= kFfnGated, true,
+  return ffn_plan_impl(op, rows, cols, summed, count, (kept & 3) != 0, (kept & 1) != 0 && op <= kFfnGated, (kept & 4) == 0,
                        sms > 0 ? sms : current_sms(), opts, out);
 }
 

@@ -155,9 +155,15 @@ def gated_backward(dh, x, w_gate, w_up, kept, *, activation="silu", product=Fals
 OPERATORS = {"linear": 0, "gated": 1, "input_grad": 2, "weight_grad": 3}
 
 
-def ffn_plan(op, M, N, K, *, count=1, kept=False, sms=0, tile=0, k_splits=0) -> dict:
-    """The kernel and tile that a product of ``linear``, ``gated`` or a backward pass would take (see gemm_ffn_plan)."""
+def ffn_plan(op, M, N, K, *, count=1, kept=False, dtype=torch.bfloat16, out_dtype=None, sms=0, tile=0, k_splits=0) -> dict:
+    """The kernel and tile that a product of ``linear``, ``gated`` or a backward pass would take (see gemm_ffn_plan).
+
+    ``kept``: True where values are kept in 8 bits.  ``dtype``, ``out_dtype``: of the operands, and of what is written.
+    """
     p = GpPlan()
     opts = GpFfnOptions(0, int(tile), int(k_splits), 0)
-    _check(lib().gemm_ffn_plan(_binding._enum(op, OPERATORS, "op"), M, N, K, count, int(kept), sms, opts, p), "gemm_ffn_plan")
+    if dtype not in (torch.float16, torch.bfloat16) or out_dtype not in (None, dtype, torch.float32):
+        raise ValueError("no product of %s into %s" % (dtype, out_dtype))
+    flags = int(kept) + 2 * (out_dtype is torch.float32) + 4 * (dtype is torch.float16)
+    _check(lib().gemm_ffn_plan(_binding._enum(op, OPERATORS, "op"), M, N, K, count, flags, sms, opts, p), "gemm_ffn_plan")
     return p.as_dict()

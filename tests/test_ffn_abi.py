@@ -245,3 +245,30 @@ def test_the_plain_slopes_are_the_values_differences(act):
     d = (ffn_ref.value(z + h, act) - ffn_ref.value(z - h, act)) / (2 * h)
     # the third derivative (below 4) times h^2 / 6, and the values' rounding (2^-53 of 9) over h
     assert np.allclose(d, ffn_ref.slope(z, act), rtol=0, atol=4 * h * h / 6 + 9 * 2.0 ** -53 / h)
+
+
+def test_plan_tells_codes_from_wide_outputs(gp):
+    """FP32 outputs go to the cluster kernels too, values kept in 8 bits do not; long sums into 16 bits are held, by type."""
+    f32, f16, bf16 = torch.float32, torch.float16, torch.bfloat16
+    for M in (1, 40, 100):
+        kernels = [gp.ffn_plan("linear", M, 4096, 4096, sms=152, out_dtype=t)["kernel"] for t in (None, f32)]
+        assert kernels == ["ffn_few", "ffn_few"]
+        assert gp.ffn_plan("linear", M, 4096, 4096, sms=152, kept=True)["kernel"] == "ffn_ring"
+        assert gp.ffn_plan("linear", M, 4096, 4096, sms=152, kept=True, out_dtype=f32)["kernel"] == "ffn_ring"
+    assert gp.ffn_plan("linear", 1, 4096, 4096, sms=152, out_dtype=f32, tile=16)["bn"] == 16
+    with pytest.raises(gp.GemmError):
+        gp.ffn_plan("linear", 1, 4096, 4096, sms=152, kept=True, tile=16)
+    for dtype, longest in ((f16, 4096), (bf16, 32768)):
+        for tile in (128, 256):
+            threads = [gp.ffn_plan("linear", 4096, 4096, K, sms=152, dtype=dtype, tile=tile)["threads"] for K in (longest, longest + 1)]
+            held = gp.ffn_plan("linear", 4096, 4096, 64, sms=152, out_dtype=f32, dtype=dtype, tile=tile)["threads"]
+            assert threads[1] == held and (tile == 128 or threads[0] < held)
+    # both products of a pair's input gradient are one sum
+    one, two = (gp.ffn_plan("input_grad", 4096, 4096, 4096, sms=152, dtype=f16, count=c, tile=256)["threads"] for c in (1, 2))
+    assert one == 384 and two == 640
+    p = b.GpPlan()
+    for op, kept in ((0, -1), (0, 8), (1, 2), (1, 3)):
+        assert gp.lib().gemm_ffn_plan(op, 8, 8, 8, 1, kept, 0, None, p) == gp.GP_ERR_ARG
+    for bad in (dict(dtype=f32), dict(out_dtype=f16), dict(dtype=f16, out_dtype=bf16)):
+        with pytest.raises(ValueError):
+            gp.ffn_plan("linear", 8, 8, 8, **bad)

@@ -905,3 +905,31 @@ def test_a_lost_load_in_either_product_of_a_backward_call_is_reported(lost, tile
     assert gp.gemm_stats(sync=True)["status"] == gp.GP_ERR_TIMEOUT
     gp.linear_backward(dy, x, w[0], tile=tile, inject_lost_load=0)
     status_ok()
+
+
+def test_the_plan_is_what_runs():
+    """gemm_ffn_plan and the record of the call agree, for 16-bit, FP32 and coded outputs of every product."""
+    def same(planned):
+        ran = status_ok()
+        assert {k: v for k, v in planned.items() if ran[k] != v} == {}, ran
+
+    rng = np.random.default_rng(1)
+    for M, N, K in ((1, 4096, 4096), (40, 1000, 520), (130, 264, 4100), (700, 1100, 264), (300, 300, 9000)):
+        for dtype in (F16, BF16):
+            x, w, u, dy = (ref.matrix(rng, r, c, dtype) for r, c in ((M, K), (N, K), (N, K), (M, N)))
+            z = torch.ones_like(dy)
+            for out in (None, F32):
+                for keep in (None, "real", "fp8"):
+                    gp.linear(x, w, keep=keep, out_dtype=out)
+                    same(gp.ffn_plan("linear", M, N, K, dtype=dtype, out_dtype=out, kept=keep == "fp8"))
+                gp.linear_backward(dy, x, w, input_grad=False, out_dtype=out)
+                same(gp.ffn_plan("weight_grad", M, N, K, dtype=dtype, out_dtype=out))
+                gp.gated_backward(dy, x, w, u, (z, z), input_grad=False, out_dtype=out)
+                same(gp.ffn_plan("weight_grad", M, N, K, dtype=dtype, out_dtype=out, count=2))
+            for keep in (None, "real", "fp8"):
+                gp.gated(x, w, u, keep=keep)
+                same(gp.ffn_plan("gated", M, N, K, dtype=dtype, kept=keep == "fp8"))
+            gp.linear_backward(dy, x, w, weight_grad=False)
+            same(gp.ffn_plan("input_grad", M, N, K, dtype=dtype))
+            gp.gated_backward(dy, x, w, u, (z, z), weight_grad=False)
+            same(gp.ffn_plan("input_grad", M, N, K, dtype=dtype, count=2))
