@@ -70,7 +70,8 @@ typedef struct gp_ffn_options {
                                     are kept in 8 bits.  0 = the planner's choice.  Other values, and tiles that the
                                     call does not have: GP_ERR_UNSUPPORTED */
     int32_t k_splits;            /* tiles of a cluster: the CTAs that share a tile's K loop, 1, 2, 4 or 8 (at most 4
-                                    with 16); 0 = the planner's choice.  Others: GP_ERR_UNSUPPORTED */
+                                    with 16); 0 = the planner's choice.  Others: GP_ERR_UNSUPPORTED.  The tiles of 128
+                                    x 128 and 256 x 256 do not look at it, whether forced or the planner's choice */
     int32_t inject_lost_load;    /* test hook: the TMA producer skips the last tile load of the problem, so a consumer
                                     wait runs out and the call reports GP_ERR_TIMEOUT (no GPU fault); not with tile 256
                                     (GP_ERR_UNSUPPORTED), and the planner does not choose that then */

@@ -95,6 +95,7 @@ int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count,
       constexpr int kRows[4] = {16, 32, 64, 128}, kBlock[2][4] = {{130, 110, 150, 220}, {217, 230, 265, 0}};
       for (int i = op == kFfnWeightGrad ? 2 : 0; i < (gated ? 3 : 4); ++i) {
         const int bn = kRows[i], c = few_ctas(bn);
+        if (c > ffn_few_most_ctas(bn)) continue;
         const double rounds = static_cast<double>(blocks(few_tiles(bn) * c, have));
         const double again = (blocks(rows, bn) - 1) * (bn < 64 ? 1500 : 0);   // the other operand once more from L2
         const double once = 4500 + bn * 15 + (gated ? 2000 : 0) + (c > 1 ? 700 : 0) + again;

@@ -272,3 +272,13 @@ def test_plan_tells_codes_from_wide_outputs(gp):
     for bad in (dict(dtype=f32), dict(out_dtype=f16), dict(dtype=f16, out_dtype=bf16)):
         with pytest.raises(ValueError):
             gp.ffn_plan("linear", 8, 8, 8, **bad)
+
+
+@pytest.mark.parametrize("op", ["linear", "gated", "input_grad", "weight_grad"])
+def test_the_planner_chooses_a_tile_that_takes_the_forced_split(gp, op):
+    for M in (1, 5, 16, 17, 64):
+        for splits in (1, 2, 4, 8):
+            p = gp.ffn_plan(op, M, 4096, 4096, sms=152, k_splits=splits)
+            assert p["k_splits"] == (splits if p["layout"] else 1)
+            assert op == "weight_grad" or p["layout"] == 1        # (few rows go to clusters)
+            assert p["bn"] != 16 or splits <= 4

@@ -933,3 +933,10 @@ def test_the_plan_is_what_runs():
             same(gp.ffn_plan("input_grad", M, N, K, dtype=dtype))
             gp.gated_backward(dy, x, w, u, (z, z), weight_grad=False)
             same(gp.ffn_plan("input_grad", M, N, K, dtype=dtype, count=2))
+
+
+@pytest.mark.parametrize("M", [1, 16])
+def test_few_rows_by_eight_ctas(M):
+    assert check_linear(M, 300, 4096, BF16, "silu", bias=BF16, k_splits=8)["k_splits"] == 8
+    assert check_gated(M, 300, 4096, BF16, k_splits=8)["k_splits"] == 8
+    check_linear_backward(M, 4096, 300, BF16, k_splits=8)
