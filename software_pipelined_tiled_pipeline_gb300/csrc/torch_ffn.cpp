@@ -137,26 +137,31 @@ struct Call {
   }
 };
 
-// An operand of a product: rows on 16-byte boundaries, in a copy where they are not.
+// An operand of a product: rows on 16-byte boundaries, or `loose` until lay_out() has copied it.  Calls look at all of
+// their arguments first, and lay out, allocate and launch then.
 struct Operand : Matrix {
+  bool loose = false;
   at::Tensor copy;
 };
-Operand operand(const at::Tensor& t, const char* name, const at::Tensor* like, const Call& call) {
+Operand operand(const at::Tensor& t, const char* name, const at::Tensor* like) {
   Operand m;
   static_cast<Matrix&>(m) = matrix(t, name);
   if (like && (t.scalar_type() != like->scalar_type() || t.get_device() != like->get_device()))
     throw Refused{std::string(name) + " is " + type_of(t) + " on " + t.device().str() + ": want " + type_of(*like) + " on " +
                   like->device().str()};
   if (m.rows <= 1) m.ld = up(m.cols, 8);   // the stride of a single row is never used
-  if ((reinterpret_cast<uintptr_t>(m.p) | static_cast<uintptr_t>(m.ld * 2)) % 16 != 0) {
-    if (m.ld < m.cols && m.rows > 1) throw Refused{std::string("the rows of ") + name + " overlap"};
-    const int64_t ld = up(m.cols, 8);
-    m.copy = at::empty_strided({m.rows, m.cols}, {ld, 1}, t.options());
-    check(lib.pack(m.p, m.ld < m.cols ? m.cols : m.ld, m.copy.data_ptr(), ld, m.rows, m.cols, call.stream), "ffn_pack_rows");
-    m.p = m.copy.data_ptr();
-    m.ld = ld;
-  }
+  m.loose = (reinterpret_cast<uintptr_t>(m.p) | static_cast<uintptr_t>(m.ld * 2)) % 16 != 0;
+  if (m.loose && m.ld < m.cols && m.rows > 1) throw Refused{std::string("the rows of ") + name + " overlap"};
   return m;
+}
+void lay_out(Operand& m, const at::Tensor& like, const Call& call) {
+  if (!m.loose) return;
+  const int64_t ld = up(m.cols, 8);
+  m.copy = at::empty_strided({m.rows, m.cols}, {ld, 1}, like.options());
+  check(lib.pack(m.p, m.ld < m.cols ? m.cols : m.ld, m.copy.data_ptr(), ld, m.rows, m.cols, call.stream), "ffn_pack_rows");
+  m.p = m.copy.data_ptr();
+  m.ld = ld;
+  m.loose = false;
 }
 
 // An output whose rows begin on 16-byte boundaries.
@@ -278,17 +283,13 @@ PyObject* linear(PyObject* const* a) {
   const int real = type16(x, "x");
   const Call call(x);
   gp_linear g = {};
-  const Operand mx = operand(x, "x", nullptr, call), mw = operand(tensor(a[1], "weight"), "weight", &x, call);
+  Operand mx = operand(x, "x", nullptr), mw = operand(tensor(a[1], "weight"), "weight", &x);
   if (mw.cols != mx.cols)
     throw Refused{"x has " + std::to_string(mx.cols) + " columns and weight " + std::to_string(mw.cols)};
   const int64_t M = mx.rows, N = mw.rows;
-  g.x = mx.p;
-  g.weight = mw.p;
   g.M = M;
   g.N = N;
   g.K = mx.cols;
-  g.ldx = mx.ld;
-  g.ldw = mw.ld;
   g.type = g.bias_type = real;
   g.activation = static_cast<int32_t>(PyLong_AsLong(a[3]));
   if (a[2] != Py_None) {
@@ -301,19 +302,19 @@ PyObject* linear(PyObject* const* a) {
     g.bias_type = real_of(b.scalar_type());
   }
   at::Tensor y;
+  at::ScalarType type;
   if (a[6] == Py_None) {
-    y = rows_of(M, N, out_type(a[7], x.scalar_type(), "out_dtype"), x);
-    g.ldy = y.stride(0);
+    type = out_type(a[7], x.scalar_type(), "out_dtype");
   } else {
     y = tensor(a[6], "out");
     if (a[7] != Py_None && (!THPDtype_Check(a[7]) || reinterpret_cast<THPDtype*>(a[7])->scalar_type != y.scalar_type()))
       throw Refused{"out is " + type_of(y) + ": out_dtype asks for another type"};
-    g.ldy = shaped(y, M, N, y.scalar_type() == at::kFloat ? at::kFloat : x.scalar_type(), x, "out").ld;
+    type = y.scalar_type() == at::kFloat ? at::kFloat : x.scalar_type();
+    g.ldy = shaped(y, M, N, type, x, "out").ld;
   }
-  g.y = y.data_ptr();
-  g.out_type = real_of(y.scalar_type());
+  g.out_type = real_of(type);
   if (a[4] != Py_None) {
-    const Matrix r = shaped(tensor(a[4], "residual"), M, N, y.scalar_type(), x, "residual");
+    const Matrix r = shaped(tensor(a[4], "residual"), M, N, type, x, "residual");
     g.residual = r.p;
     g.ld_res = r.ld;
     if (a[6] != Py_None) apart(y, tensor(a[4], "residual"), "residual", true);
@@ -323,6 +324,17 @@ PyObject* linear(PyObject* const* a) {
     apart(y, tensor(a[1], "weight"), "weight");
     if (a[2] != Py_None) apart(y, tensor(a[2], "bias").unsqueeze(0), "bias");
   }
+  lay_out(mx, x, call);
+  lay_out(mw, x, call);
+  g.x = mx.p;
+  g.weight = mw.p;
+  g.ldx = mx.ld;
+  g.ldw = mw.ld;
+  if (a[6] == Py_None) {
+    y = rows_of(M, N, type, x);
+    g.ldy = y.stride(0);
+  }
+  g.y = y.data_ptr();
   const long keep = PyLong_AsLong(a[5]);
   at::Tensor z;
   Codes codes;
@@ -345,32 +357,34 @@ PyObject* gated(PyObject* const* a) {
   gp_gated g = {};
   g.type = type16(x, "x");
   const Call call(x);
-  const Operand mx = operand(x, "x", nullptr, call), mg = operand(tensor(a[1], "w_gate"), "w_gate", &x, call),
-                mu = operand(tensor(a[2], "w_up"), "w_up", &x, call);
+  Operand mx = operand(x, "x", nullptr), mg = operand(tensor(a[1], "w_gate"), "w_gate", &x),
+          mu = operand(tensor(a[2], "w_up"), "w_up", &x);
   const int64_t M = mx.rows, N = mg.rows;
   if (mg.cols != mx.cols || mu.cols != mx.cols || mu.rows != N)
     throw Refused{"x has " + std::to_string(mx.cols) + " columns: the weights are " + shape_of(tensor(a[1], "w_gate")) + " and " +
                   shape_of(tensor(a[2], "w_up"))};
-  g.x = mx.p;
-  g.gate = mg.p;
-  g.up = mu.p;
   g.M = M;
   g.N = N;
   g.K = mx.cols;
-  g.ldx = mx.ld;
-  g.ld_gate = mg.ld;
-  g.ld_up = mu.ld;
   g.activation = static_cast<int32_t>(PyLong_AsLong(a[3]));
   at::Tensor h;
-  if (a[5] == Py_None) {
-    h = rows_of(M, N, x.scalar_type(), x);
-    g.ldh = h.stride(0);
-  } else {
+  if (a[5] != Py_None) {
     h = tensor(a[5], "out");
     g.ldh = shaped(h, M, N, x.scalar_type(), x, "out").ld;
     apart(h, x, "x");
     apart(h, tensor(a[1], "w_gate"), "w_gate");
     apart(h, tensor(a[2], "w_up"), "w_up");
+  }
+  for (Operand* m : {&mx, &mg, &mu}) lay_out(*m, x, call);
+  g.x = mx.p;
+  g.gate = mg.p;
+  g.up = mu.p;
+  g.ldx = mx.ld;
+  g.ld_gate = mg.ld;
+  g.ld_up = mu.ld;
+  if (a[5] == Py_None) {
+    h = rows_of(M, N, x.scalar_type(), x);
+    g.ldh = h.stride(0);
   }
   g.h = h.data_ptr();
   const long keep = PyLong_AsLong(a[4]);
@@ -422,13 +436,20 @@ PyObject* item(PyObject* o, int i, int count, const char* name) {
   return PySequence_Fast_GET_ITEM(o, i);
 }
 
-// The gradients of the weights of products that share x.  x_given, dz_given (NULL: of the call's own): the tensors behind them.
-void weight_gradients(int count, const Matrix* dz, const Operand& x, int64_t N, int real, PyObject* dtype, PyObject* addend,
-                      PyObject* out, const at::Tensor& like, const at::Tensor& x_given, const at::Tensor* dz_given,
-                      const Call& call, const gp_ffn_options* opts, at::Tensor* dw) {
+// Where the gradients of the weights of products that share x go, and what is added to them.
+struct WeightGradients {
   gp_weight_grad g = {};
-  const int64_t K = x.cols;
-  at::ScalarType type = out_type(dtype, like.scalar_type(), "out_dtype");
+  at::ScalarType type;
+  at::Tensor dw[2];      // those that are given
+};
+// x_given, dz_given (NULL: of the call's own): the operands as tensors.
+WeightGradients look_at_weight_gradients(int count, int64_t N, int64_t K, PyObject* dtype, PyObject* addend, PyObject* out,
+                                         const at::Tensor& like, const at::Tensor& x_given, const at::Tensor* dz_given) {
+  WeightGradients r;
+  gp_weight_grad& g = r.g;
+  at::Tensor* const dw = r.dw;
+  at::ScalarType& type = r.type;
+  type = out_type(dtype, like.scalar_type(), "out_dtype");
   if (dtype == Py_None) {   // what is given says
     PyObject* first = out != Py_None ? item(out, 0, count, "out") : item(addend, 0, count, "addend");
     if (first != Py_None && tensor(first, "out").scalar_type() == at::kFloat) type = at::kFloat;
@@ -436,16 +457,10 @@ void weight_gradients(int count, const Matrix* dz, const Operand& x, int64_t N, 
   for (int i = 0; i < count; ++i) {
     PyObject* o = item(out, i, count, "out");
     PyObject* add = item(addend, i, count, "addend");
-    g.dz[i] = dz[i].p;
-    g.ld_dz[i] = dz[i].ld;
-    if (o == Py_None) {
-      dw[i] = rows_of(N, K, type, like);
-      g.ld_dw[i] = dw[i].stride(0);
-    } else {
+    if (o != Py_None) {
       dw[i] = tensor(o, "out");
       g.ld_dw[i] = shaped(dw[i], N, K, type, like, "out").ld;
     }
-    g.dw[i] = dw[i].data_ptr();
     if (add != Py_None) {
       const Matrix m = shaped(tensor(add, "addend"), N, K, type, like, "addend");
       g.addend[i] = m.p;
@@ -454,14 +469,30 @@ void weight_gradients(int count, const Matrix* dz, const Operand& x, int64_t N, 
   }
   if (out != Py_None) {
     for (int i = 0; i < count; ++i) {
+      if (!dw[i].defined()) continue;
       apart(dw[i], x_given, "x");
       if (dz_given) apart(dw[i], *dz_given, "dy");
       for (int j = 0; j < count; ++j) {
         PyObject* add = item(addend, j, count, "addend");
         if (add != Py_None) apart(dw[i], tensor(add, "addend"), "addend", i == j);
-        if (j > i) apart(dw[i], dw[j], "the other out");
+        if (j > i && dw[j].defined()) apart(dw[i], dw[j], "the other out");
       }
     }
+  }
+  return r;
+}
+void weight_gradients(int count, const Matrix* dz, const Operand& x, int64_t N, int real, WeightGradients& r,
+                      const at::Tensor& like, const Call& call, const gp_ffn_options* opts) {
+  gp_weight_grad& g = r.g;
+  const int64_t K = x.cols;
+  for (int i = 0; i < count; ++i) {
+    g.dz[i] = dz[i].p;
+    g.ld_dz[i] = dz[i].ld;
+    if (!r.dw[i].defined()) {
+      r.dw[i] = rows_of(N, K, r.type, like);
+      g.ld_dw[i] = r.dw[i].stride(0);
+    }
+    g.dw[i] = r.dw[i].data_ptr();
   }
   g.x = x.p;
   g.ldx = x.ld;
@@ -469,7 +500,7 @@ void weight_gradients(int count, const Matrix* dz, const Operand& x, int64_t N, 
   g.N = N;
   g.K = K;
   g.type = real;
-  g.out_type = real_of(type);
+  g.out_type = real_of(r.type);
   g.count = count;
   check(lib.weight_grad(&g, call.stream, opts), "gemm_weight_grad");
 }
@@ -487,7 +518,6 @@ PyObject* linear_backward(PyObject* const* a) {
   if (!want_w && (a[9] != Py_None || a[10] != Py_None)) throw Refused{"addend and out are for dweight"};
   const Matrix md = matrix(dy, "dy");
   const int64_t M = md.rows, N = md.cols;
-  // everything is looked over before the first launch
   const at::Tensor& w = tensor(a[2], "weight");
   const Matrix vw = matrix(w, "weight");
   if (vw.rows != N) throw Refused{"dy is " + shape_of(dy) + ": the weight is " + shape_of(w)};
@@ -497,14 +527,19 @@ PyObject* linear_backward(PyObject* const* a) {
     const Matrix vx = matrix(x, "x");
     if (vx.rows != M || vw.cols != vx.cols)
       throw Refused{"dy is " + shape_of(dy) + " and x " + shape_of(x) + ": the weight is " + shape_of(w)};
-    if (want_w) mx = operand(x, "x", &dy, call);
+    if (want_w) mx = operand(x, "x", &dy);
   }
   Kept kept;
   if (act != GP_ACT_NONE) read_kept(a[4], 1, M, N, dy, &kept);
-  if (want_x) mw = operand(w, "weight", &dy, call);
-  at::Tensor dz, dbias, work, dx, dw;
+  if (want_x) mw = operand(w, "weight", &dy);
+  at::Tensor dz, dbias, work, dx;
   Operand md16;
   const bool own = act != GP_ACT_NONE && (want_x || want_w);    // dz in memory of its own
+  if (!own && (want_x || want_w)) md16 = operand(dy, "dy", nullptr);
+  WeightGradients dw;
+  if (want_w)
+    dw = look_at_weight_gradients(1, N, vw.cols, a[8], a[9], a[10], dy, tensor(a[1], "x"), own ? nullptr : &dy);
+  for (Operand* m : {&mx, &mw, &md16}) lay_out(*m, dy, call);
   if (act != GP_ACT_NONE || bias) {
     gp_act_backward g = {};
     g.dy = md.p;
@@ -533,17 +568,11 @@ PyObject* linear_backward(PyObject* const* a) {
     check(lib.act_backward(&g, call.stream), "ffn_act_backward");
   }
   if (want_x || want_w) {
-    if (own) {
-      static_cast<Matrix&>(md16) = Matrix{M, N, dz.stride(0), dz.data_ptr()};
-    } else {
-      md16 = operand(dy, "dy", nullptr, call);
-    }
+    if (own) static_cast<Matrix&>(md16) = Matrix{M, N, dz.stride(0), dz.data_ptr()};
     if (want_x) dx = input_gradient(1, &md16, &mw, M, N, vw.cols, real, dy, call, ProductOptions(opts, 1, false).p);
-    if (want_w)
-      weight_gradients(1, &md16, mx, N, real, a[8], a[9], a[10], dy, tensor(a[1], "x"), own ? nullptr : &dy, call,
-                       ProductOptions(opts, 2, want_x).p, &dw);
+    if (want_w) weight_gradients(1, &md16, mx, N, real, dw, dy, call, ProductOptions(opts, 2, want_x).p);
   }
-  return tuple({dx, dw, dbias});
+  return tuple({dx, dw.dw[0], dbias});
 }
 
 // gated_backward(dh, x, w_gate, w_up, kept, activation, product, input_grad, weight_grad, out_dtype, addend, out, options)
@@ -569,17 +598,20 @@ PyObject* gated_backward(PyObject* const* a) {
     const Matrix vx = matrix(x, "x");
     if (vx.rows != M || vx.cols != vg.cols)
       throw Refused{"dh is " + shape_of(dh) + " and x " + shape_of(x) + ": the weights are " + shape_of(wg) + " and " + shape_of(wu)};
-    if (want_w) mx = operand(x, "x", &dh, call);
+    if (want_w) mx = operand(x, "x", &dh);
   }
   Kept kept[2];
   read_kept(a[4], 2, M, N, dh, kept);
   if (want_x) {
-    mw[0] = operand(wg, "w_gate", &dh, call);
-    mw[1] = operand(wu, "w_up", &dh, call);
+    mw[0] = operand(wg, "w_gate", &dh);
+    mw[1] = operand(wu, "w_up", &dh);
   }
+  WeightGradients dw;
+  if (want_w) dw = look_at_weight_gradients(2, N, vg.cols, a[9], a[10], a[11], dh, tensor(a[1], "x"), nullptr);
+  for (Operand* m : {&mx, &mw[0], &mw[1]}) lay_out(*m, dh, call);
   // the products' gradients, one after the other
   const int64_t ld = up(N, 8);
-  at::Tensor both = at::empty_strided({2 * M, N}, {ld, 1}, dh.options()), h, dx, dw[2];
+  at::Tensor both = at::empty_strided({2 * M, N}, {ld, 1}, dh.options()), h, dx;
   const Matrix dz[2] = {Matrix{M, N, ld, both.data_ptr()},
                         Matrix{M, N, ld, static_cast<char*>(both.data_ptr()) + 2 * M * ld}};
   gp_gated_backward g = {};
@@ -605,10 +637,8 @@ PyObject* gated_backward(PyObject* const* a) {
   g.activation = static_cast<int32_t>(PyLong_AsLong(a[5]));
   check(lib.gated_backward(&g, call.stream), "ffn_gated_backward");
   if (want_x) dx = input_gradient(2, dz, mw, M, N, vg.cols, real, dh, call, ProductOptions(opts, 1, false).p);
-  if (want_w)
-    weight_gradients(2, dz, mx, N, real, a[9], a[10], a[11], dh, tensor(a[1], "x"), nullptr, call,
-                     ProductOptions(opts, 2, want_x).p, dw);
-  return product ? tuple({dx, dw[0], dw[1], h}) : tuple({dx, dw[0], dw[1]});
+  if (want_w) weight_gradients(2, dz, mx, N, real, dw, dh, call, ProductOptions(opts, 2, want_x).p);
+  return product ? tuple({dx, dw.dw[0], dw.dw[1], h}) : tuple({dx, dw.dw[0], dw.dw[1]});
 }
 
 // ---------------------------------------------------------------------------

@@ -940,3 +940,32 @@ def test_few_rows_by_eight_ctas(M):
     assert check_linear(M, 300, 4096, BF16, "silu", bias=BF16, k_splits=8)["k_splits"] == 8
     assert check_gated(M, 300, 4096, BF16, k_splits=8)["k_splits"] == 8
     check_linear_backward(M, 4096, 300, BF16, k_splits=8)
+
+
+def test_a_refused_argument_launches_nothing():
+    """Every argument is looked at before rows are laid out or a product runs: the record is still the call's before."""
+    rng = np.random.default_rng(14)
+    M, N, K = 40, 72, 61
+    x, w, u, dy = (ref.matrix(rng, r, c, BF16) for r, c in ((M, K), (N, K), (N, K), (M, N)))     # rows off 16-byte boundaries
+    z = torch.ones_like(dy)
+    a, b = ref.matrix(rng, 8, 64, BF16), ref.matrix(rng, 16, 64, BF16)
+    gp.linear(a, b)
+    before = status_ok()
+    wrong = torch.zeros(N, K + 1, dtype=BF16, device="cuda")
+    wide = torch.zeros(N, K, dtype=F32, device="cuda")
+    for call in (lambda: gp.linear(x, w[:, :K - 1]), lambda: gp.linear(x, w, z[0, :5]), lambda: gp.linear(x, w, out=wrong),
+                 lambda: gp.linear(x, w, residual=wrong), lambda: gp.linear(x, w, out_dtype=F16), lambda: gp.linear(x, w.half()),
+                 lambda: gp.gated(x, w, u[:5]), lambda: gp.gated(x, w, u.half()), lambda: gp.gated(x, w, u, out=wrong),
+                 lambda: gp.linear_backward(dy, x, w, out=wrong), lambda: gp.linear_backward(dy, x, w, out=x[:N]),
+                 lambda: gp.linear_backward(dy, x, w, addend=wrong), lambda: gp.linear_backward(dy, x, w, out_dtype=F16),
+                 lambda: gp.linear_backward(dy, x, w.half()), lambda: gp.linear_backward(dy, x, w, out=wide, addend=w),
+                 lambda: gp.linear_backward(dy, x, w, activation="gelu", kept=(w,)),
+                 lambda: gp.linear_backward(dy, x, w, activation="gelu", kept=(z,), bias_grad=True, out=wrong),
+                 lambda: gp.gated_backward(dy, x, w, u, (z, w)), lambda: gp.gated_backward(dy, x, w, u, (z, z), out=(wide, wide)),
+                 lambda: gp.gated_backward(dy, x, w, u, (z, z), out=(wrong, w)),
+                 lambda: gp.gated_backward(dy, x, w, u.half(), (z, z)), lambda: gp.gated_backward(dy, x, w, u, (z, z), out_dtype=F16)):
+        with pytest.raises(ValueError):
+            call()
+        assert status_ok() == before
+    got = gp.linear_backward(dy, x, w, activation="relu", kept=(z,), out=wide)[1]        # and an FP32 output of such rows
+    assert got is wide and torch.equal(wide, gp.linear_backward(dy, x, w, activation="relu", kept=(z,), out_dtype=F32)[1])
