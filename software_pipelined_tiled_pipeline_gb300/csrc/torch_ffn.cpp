@@ -86,9 +86,16 @@ Matrix matrix(const at::Tensor& t, const char* name) {
   return Matrix{rows, cols, rows > 1 || ld > cols ? ld : cols, t.data_ptr()};
 }
 
+// One that is read or written: its rows lie apart.
+Matrix rows_apart(const at::Tensor& t, const char* name) {
+  const Matrix m = matrix(t, name);
+  if (m.rows > 1 && m.ld < m.cols) throw Refused{std::string("the rows of ") + name + " overlap"};
+  return m;
+}
+
 // A matrix of given sizes, type and device.
 Matrix shaped(const at::Tensor& t, int64_t rows, int64_t cols, at::ScalarType type, const at::Tensor& like, const char* name) {
-  const Matrix m = matrix(t, name);
+  const Matrix m = rows_apart(t, name);
   if (m.rows != rows || m.cols != cols || t.scalar_type() != type || t.get_device() != like.get_device())
     throw Refused{std::string(name) + " must be " + std::to_string(rows) + " x " + std::to_string(cols) + " of " +
                   c10::toString(type) + " on " + like.device().str() + ": got " + shape_of(t) + " of " + type_of(t) + " on " +
@@ -145,20 +152,19 @@ struct Operand : Matrix {
 };
 Operand operand(const at::Tensor& t, const char* name, const at::Tensor* like) {
   Operand m;
-  static_cast<Matrix&>(m) = matrix(t, name);
+  static_cast<Matrix&>(m) = rows_apart(t, name);
   if (like && (t.scalar_type() != like->scalar_type() || t.get_device() != like->get_device()))
     throw Refused{std::string(name) + " is " + type_of(t) + " on " + t.device().str() + ": want " + type_of(*like) + " on " +
                   like->device().str()};
   if (m.rows <= 1) m.ld = up(m.cols, 8);   // the stride of a single row is never used
   m.loose = (reinterpret_cast<uintptr_t>(m.p) | static_cast<uintptr_t>(m.ld * 2)) % 16 != 0;
-  if (m.loose && m.ld < m.cols && m.rows > 1) throw Refused{std::string("the rows of ") + name + " overlap"};
   return m;
 }
 void lay_out(Operand& m, const at::Tensor& like, const Call& call) {
   if (!m.loose) return;
   const int64_t ld = up(m.cols, 8);
   m.copy = at::empty_strided({m.rows, m.cols}, {ld, 1}, like.options());
-  check(lib.pack(m.p, m.ld < m.cols ? m.cols : m.ld, m.copy.data_ptr(), ld, m.rows, m.cols, call.stream), "ffn_pack_rows");
+  check(lib.pack(m.p, m.ld, m.copy.data_ptr(), ld, m.rows, m.cols, call.stream), "ffn_pack_rows");
   m.p = m.copy.data_ptr();
   m.ld = ld;
   m.loose = false;
@@ -189,7 +195,7 @@ struct Kept {
 };
 gp_fp8_matrix kept_codes(const at::Tensor& data, const at::Tensor& scales, int64_t rows, int64_t cols, const at::Tensor& like,
                          const char* name) {
-  Matrix m = matrix(data, name);
+  const Matrix m = rows_apart(data, name);
   const at::ScalarType t = data.scalar_type();
   if ((t != at::kFloat8_e4m3fn && t != at::kFloat8_e5m2) || m.rows != rows || m.cols != cols ||
       data.get_device() != like.get_device())
@@ -200,7 +206,10 @@ gp_fp8_matrix kept_codes(const at::Tensor& data, const at::Tensor& scales, int64
       scales.get_device() != like.get_device())
     throw Refused{std::string("the scales of ") + name + " must be float32 (" + std::to_string(rows) + ", " +
                   std::to_string((cols + 127) / 128) + ") on its device"};
-  return gp_fp8_matrix{m.p, scales.data_ptr<float>(), rows <= 1 ? up(cols, 16) : m.ld, scales.stride(0), scales.stride(1),
+  const int64_t ld = rows <= 1 ? up(cols, 16) : m.ld;
+  if (rows > 0 && cols > 0 && (reinterpret_cast<uintptr_t>(m.p) | static_cast<uintptr_t>(ld)) % 16 != 0)
+    throw Refused{std::string("the rows of ") + name + " in 8 bits must begin on 16-byte boundaries, as quantize_fp8 lays them out"};
+  return gp_fp8_matrix{m.p, scales.data_ptr<float>(), ld, scales.stride(0), scales.stride(1),
                        t == at::kFloat8_e5m2 ? GP_E5M2 : GP_E4M3, 1};
 }
 void read_kept(PyObject* o, int weights, int64_t rows, int64_t cols, const at::Tensor& like, Kept* kept) {
@@ -516,7 +525,7 @@ PyObject* linear_backward(PyObject* const* a) {
   const gp_ffn_options* opts = options(a[11]);
   if (act == GP_ACT_NONE && a[4] != Py_None) throw Refused{"without an activation nothing is kept"};
   if (!want_w && (a[9] != Py_None || a[10] != Py_None)) throw Refused{"addend and out are for dweight"};
-  const Matrix md = matrix(dy, "dy");
+  const Matrix md = rows_apart(dy, "dy");
   const int64_t M = md.rows, N = md.cols;
   const at::Tensor& w = tensor(a[2], "weight");
   const Matrix vw = matrix(w, "weight");
@@ -586,7 +595,7 @@ PyObject* gated_backward(PyObject* const* a) {
   if (!want_w && (a[10] != Py_None || a[11] != Py_None)) throw Refused{"addend and out are for the weights' gradients"};
   if ((a[10] != Py_None) && (item(a[10], 0, 2, "addend") == Py_None) != (item(a[10], 1, 2, "addend") == Py_None))
     throw Refused{"addend takes 2 matrices"};
-  const Matrix md = matrix(dh, "dh");
+  const Matrix md = rows_apart(dh, "dh");
   const int64_t M = md.rows, N = md.cols;
   const at::Tensor &wg = tensor(a[2], "w_gate"), &wu = tensor(a[3], "w_up");
   const Matrix vg = matrix(wg, "w_gate"), vu = matrix(wu, "w_up");

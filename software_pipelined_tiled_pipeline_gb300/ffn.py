@@ -28,7 +28,14 @@ from ._binding import ACTIVATIONS, GemmError, GpFfnOptions, GpPlan, lib
 from .fp8 import _check, _On
 
 _KEEP = {None: 0, "real": 1, "fp8": 2}
-_pack = struct.Struct("Qiii4x").pack        # gp_ffn_options
+_packed = struct.Struct("Qiii4x").pack        # gp_ffn_options
+
+
+def _pack(timeout_ns, tile, k_splits, inject_lost_load):
+    try:
+        return _packed(timeout_ns, tile, k_splits, inject_lost_load)
+    except struct.error as e:
+        raise ValueError("timeout_ns, tile, k_splits and inject_lost_load: %s" % e) from None
 
 
 def _load():

@@ -969,3 +969,39 @@ def test_a_refused_argument_launches_nothing():
         assert status_ok() == before
     got = gp.linear_backward(dy, x, w, activation="relu", kept=(z,), out=wide)[1]        # and an FP32 output of such rows
     assert got is wide and torch.equal(wide, gp.linear_backward(dy, x, w, activation="relu", kept=(z,), out_dtype=F32)[1])
+
+
+def test_refused_arguments_raise_value_errors():
+    """What the calls look at themselves is a ValueError: codes off 16-byte boundaries, rows that overlap, options out of range."""
+    x, w, wd, b, r = block_operands(20, 64, 40, 6)
+    z = torch.ones(20, 64, dtype=BF16, device="cuda")
+    data, scales = gp.quantize_fp8(z)
+    off = torch.zeros(20, 65, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    late = torch.zeros(20 * 64 + 8, dtype=torch.uint8, device="cuda")[8:].view(20, 64).view(torch.float8_e4m3fn)
+    lines = {n: torch.zeros(1, n, dtype=BF16, device="cuda").expand(20, n) for n in (40, 64)}
+    one = torch.zeros(1, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).expand(20, 64)
+    for call in (lambda q: gp.linear_backward(z, x, w[0], activation="gelu", kept=(q, scales)),
+                 lambda q: gp.gated_backward(z, x, *w, (q, scales, data, scales)),
+                 lambda q: gp.gated_backward(z, x, *w, (data, scales, q, scales))):
+        for q in (off[:, :64], late, one):
+            with pytest.raises(ValueError, match="rows of the"):
+                call(q)
+    for call in (lambda: gp.linear(lines[40], w[0]), lambda: gp.gated(lines[40], *w), lambda: gp.linear(x, w[0], residual=lines[64]),
+                 lambda: gp.linear(x, w[0], out=lines[64]), lambda: gp.gated(x, *w, out=lines[64]),
+                 lambda: gp.linear_backward(lines[64], x, w[0]), lambda: gp.linear_backward(lines[64], x, w[0], bias_grad=True),
+                 lambda: gp.linear_backward(z, x, w[0], activation="gelu", kept=(lines[64],)),
+                 lambda: gp.linear_backward(z, x, w[0], out=torch.zeros(1, 40, dtype=BF16, device="cuda").expand(64, 40)),
+                 lambda: gp.gated_backward(lines[64], x, *w, (z, z)), lambda: gp.gated_backward(z, x, *w, (z, lines[64]))):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    for options in (dict(timeout_ns=-1), dict(tile=1 << 40), dict(tile=64.0), dict(k_splits="2"), dict(timeout_ns=1 << 64)):
+        for call in (lambda: gp.linear(x, w[0], **options), lambda: gp.gated(x, *w, **options),
+                     lambda: gp.linear_backward(z, x, w[0], **options), lambda: gp.gated_backward(z, x, *w, (z, z), **options)):
+            with pytest.raises(ValueError):
+                call()
+    # what is not read may be anything of its shape
+    flat = torch.zeros(1, 40, dtype=BF16, device="cuda").expand(64, 40)
+    assert torch.equal(gp.linear_backward(z, x, flat, input_grad=False)[1], gp.linear_backward(z, x, w[0], input_grad=False)[1])
+    # a single row's stride says nothing
+    gp.linear_backward(z[:1], x[:1], w[0], activation="gelu", kept=(data[:1], scales[:1]))
+    status_ok()
