@@ -124,6 +124,12 @@ void apart(const at::Tensor& out, const at::Tensor& other, const char* name, boo
   if (meet(a, out, b, other)) throw Refused{std::string("out overlaps ") + name};
 }
 
+// A tensor of the caller's that a kernel writes counts as changed, as after torch's own operations in place: autograd then
+// refuses to use what it kept of the values before.
+void changed(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 int type16(const at::Tensor& t, const char* name) {
   const int r = real_of(t.scalar_type());
   if (r != GP_REAL_F16 && r != GP_REAL_BF16)
@@ -355,6 +361,7 @@ PyObject* linear(PyObject* const* a) {
     codes = new_codes(M, N, x, &g.q);
   }
   check(lib.linear(&g, call.stream, options(a[8])), "gemm_linear");
+  if (a[6] != Py_None) changed(y);
   if (keep == kKeepNone) return wrap(y);
   return with_kept(y, keep == kKeepReal ? tuple({z}) : tuple({codes.data, codes.scales}));
 }
@@ -410,6 +417,7 @@ PyObject* gated(PyObject* const* a) {
     cu = new_codes(M, N, x, &g.q_up);
   }
   check(lib.gated(&g, call.stream, options(a[6])), "gemm_gated");
+  if (a[5] != Py_None) changed(h);
   if (keep == kKeepNone) return wrap(h);
   return with_kept(h, keep == kKeepReal ? tuple({zg, zu}) : tuple({cg.data, cg.scales, cu.data, cu.scales}));
 }
@@ -494,10 +502,11 @@ void weight_gradients(int count, const Matrix* dz, const Operand& x, int64_t N, 
                       const at::Tensor& like, const Call& call, const gp_ffn_options* opts) {
   gp_weight_grad& g = r.g;
   const int64_t K = x.cols;
+  bool given[2] = {r.dw[0].defined(), r.dw[1].defined()};
   for (int i = 0; i < count; ++i) {
     g.dz[i] = dz[i].p;
     g.ld_dz[i] = dz[i].ld;
-    if (!r.dw[i].defined()) {
+    if (!given[i]) {
       r.dw[i] = rows_of(N, K, r.type, like);
       g.ld_dw[i] = r.dw[i].stride(0);
     }
@@ -512,6 +521,8 @@ void weight_gradients(int count, const Matrix* dz, const Operand& x, int64_t N, 
   g.out_type = real_of(r.type);
   g.count = count;
   check(lib.weight_grad(&g, call.stream, opts), "gemm_weight_grad");
+  for (int i = 0; i < count; ++i)
+    if (given[i]) changed(r.dw[i]);
 }
 
 // linear_backward(dy, x, weight, activation, kept, bias_grad, input_grad, weight_grad, out_dtype, addend, out, options)

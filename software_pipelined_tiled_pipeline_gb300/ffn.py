@@ -10,6 +10,11 @@ kept in the inputs' type or in 8 bits (E4M3 codes with a scale for each row's
 128 values, as ``quantize_fp8`` makes them), and ``linear_backward`` and
 ``gated_backward`` that read either.
 
+The calls are below autograd, as those of ``fp8``: results carry no graph, also
+where operands require gradients, and a ``torch.autograd.Function`` around a
+forward and its backward call is the program's to write.  What is written to
+``out`` counts as a change of that tensor in place.
+
 Matrices are float16 or bfloat16 with contiguous rows; an output may be float32
 where it says so.  The tensor cores want rows that begin on 16-byte boundaries:
 new outputs are laid out that way (their rows may be a few elements apart), and

@@ -1005,3 +1005,33 @@ def test_refused_arguments_raise_value_errors():
     # a single row's stride says nothing
     gp.linear_backward(z[:1], x[:1], w[0], activation="gelu", kept=(data[:1], scales[:1]))
     status_ok()
+
+
+def test_outputs_given_count_as_changed():
+    """Writing to `out` moves its version, so that autograd refuses values that it kept of it; results carry no graph."""
+    x, w, wd, b, r = block_operands(20, 64, 40, 6)
+    z = torch.ones(20, 64, dtype=BF16, device="cuda")
+    outs = [torch.zeros(20, 64, dtype=BF16, device="cuda"), torch.zeros(20, 64, dtype=BF16, device="cuda")]
+    outs += [torch.zeros(64, 40, dtype=F32, device="cuda") for _ in range(3)]
+    calls = (lambda: gp.linear(x, w[0], out=outs[0]), lambda: gp.gated(x, *w, out=outs[1]),
+             lambda: gp.linear_backward(z, x, w[0], out=outs[2]), lambda: gp.gated_backward(z, x, *w, (z, z), out=outs[3:]))
+    written = ([0], [1], [2], [3, 4])
+    for call, which in zip(calls, written):
+        before = [t._version for t in outs]
+        read = [t._version for t in (x, w[0], w[1], z)]
+        call()
+        assert [t._version - v for t, v in zip(outs, before)] == [int(i in which) for i in range(5)]
+        assert [t._version for t in (x, w[0], w[1], z)] == read
+    leaf = torch.ones(20, 64, device="cuda", requires_grad=True)
+    buf = torch.zeros(20, 64, dtype=BF16, device="cuda")
+    y = (leaf * buf).sum()                       # autograd keeps buf
+    gp.linear(x, w[0], out=buf)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    leaf = w[0].clone().requires_grad_()
+    assert not gp.linear(x, leaf).requires_grad
+    with torch.inference_mode():
+        frozen = torch.zeros(20, 64, dtype=BF16, device="cuda")
+        assert gp.linear(x, w[0], out=frozen) is frozen
+    assert gp.linear(x, w[0], out=frozen) is frozen and torch.equal(frozen, gp.linear(x, w[0]))
+    status_ok()
