@@ -6,9 +6,12 @@ Each CUDA translation unit is compiled to an object in parallel under
 statically; the driver is reached through the runtime's entry-point query, so
 no libcuda is needed at link time).  Beside it ``_torch_ffn.so``, the CPython
 extension that takes torch tensors to the feed-forward calls, is compiled with
-g++ against the installed torch.  Host code is portable C++17: the same sources
+g++ against the installed torch (without a torch it is left out), once for each
+version of torch and Python.  Host code is portable C++17: the same sources
 build on x86_64 and on aarch64.
 """
+import importlib.metadata
+import importlib.util
 import os
 import re
 import subprocess
@@ -24,6 +27,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgemmpipe.so")
 TORCH_SOURCE = "torch_ffn.cpp"
 TORCH_LIB = os.path.join(PKG, "_torch_ffn.so")
+TORCH_STAMP = os.path.join(BUILD, "torch_ffn.for")      # what it was compiled against
 
 SOURCES = ["api.cu", "ffn_api.cu", "fp8_api.cu", "k_ffma.cu", "k_ffn_act.cu", "k_ffn_few.cu", "k_ffn_gated.cu",
            "k_ffn_input_grad.cu", "k_ffn_linear.cu", "k_ffn_weight_grad.cu", "k_fp8_gemm.cu", "k_fp8_norm.cu", "k_fp8_quant.cu", "k_imma.cu", "k_umma.cu", "probe.cu"]
@@ -77,6 +81,31 @@ def _stale(target, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch():
+    """The torch and the Python that an extension is for, or None where there is no torch."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        import torch
+
+        version = torch.__version__
+    return "torch %s, %s" % (version, sysconfig.get_config_var("SOABI"))
+
+
+def _extension_stale(deps) -> bool:
+    now = _torch()
+    if now is None:
+        return False
+    try:
+        with open(TORCH_STAMP) as f:
+            made_for = f.read()
+    except OSError:
+        made_for = None
+    return made_for != now or _stale(TORCH_LIB, deps)
+
+
 def _build_torch_extension():
     """The CPython extension on torch tensors: host code only, against the torch that is installed."""
     import torch
@@ -94,14 +123,27 @@ def _build_torch_extension():
     if r.returncode != 0:
         raise RuntimeError("g++ failed on %s:\n%s%s" % (TORCH_SOURCE, r.stdout, r.stderr))
     os.replace(tmp, TORCH_LIB)
+    with open(TORCH_STAMP, "w") as f:
+        f.write(_torch())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile and link the library if any source is newer than it; return its path."""
+    """Compile and link what is older than its sources, the library and the extension; return the library's path."""
     deps = _deps()
-    if not force and not _stale(LIB, deps) and not _stale(TORCH_LIB, deps):
+    library, extension = force or _stale(LIB, deps), force and _torch() is not None or _extension_stale(deps)
+    if not library and not extension:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        beside = ex.submit(_build_torch_extension) if extension else None
+        if library:
+            _build_library(verbose, ptxas_verbose)
+        if beside:
+            beside.result()      # (raises once the library is there, which does not need it)
+    return LIB
+
+
+def _build_library(verbose, ptxas_verbose):
     cc = nvcc()
 
     def compile_one(src):
@@ -111,10 +153,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, cmd, r
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        extension = ex.submit(_build_torch_extension)
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        extension.result()
     objs = []
     for src, obj, cmd, r in results:
         if verbose or ptxas_verbose:
@@ -131,7 +171,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
