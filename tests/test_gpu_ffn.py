@@ -1035,3 +1035,59 @@ def test_outputs_given_count_as_changed():
         assert gp.linear(x, w[0], out=frozen) is frozen
     assert gp.linear(x, w[0], out=frozen) is frozen and torch.equal(frozen, gp.linear(x, w[0]))
     status_ok()
+
+
+# ---------------------------------------------------------------------------
+# 128 rows by a cluster (tile 129), which the planner takes for some sizes between
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("splits", [0, 1, 2, 4, 8])
+@pytest.mark.parametrize("M,N,K", [(1, 200, 700), (100, 1000, 333), (129, 264, 520), (200, 128, 1300), (513, 700, 1300)])
+def test_linear_128_rows_by_a_cluster(M, N, K, splits):
+    assert check_linear(M, N, K, BF16, "silu", bias=BF16, residual=True, tile=129, k_splits=splits)["bn"] == 128
+    check_linear(M, N, K, F16, None, keep="real", out_dtype=F32, tile=129, k_splits=splits)
+    check_linear(M, N, K, F16, whole=2, residual=True, out_dtype=F32, tile=129, k_splits=splits)
+
+
+# rows of the weight's gradient: ends of 1 to 63, 64, and 65 to 127 past the last 128, and fewer than 64 in all
+ENDS = [1, 40, 63, 64, 65, 100, 127, 128, 129, 191, 192, 193, 255, 300, 512]
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2, 4, 8])
+@pytest.mark.parametrize("N", ENDS)
+def test_backward_128_rows_by_a_cluster(N, splits):
+    for M, K in ((20, 128), (300, 65), (600, 333)):
+        check_linear_backward(M, N, K, BF16, tile=129, k_splits=splits, out_dtype=F32, add=True)
+        check_linear_backward(M, N, K, F16, "silu", "fp8", tile=129, k_splits=splits)
+        check_gated_backward(M, N, K, BF16, tile=129, k_splits=splits)
+
+
+@pytest.mark.parametrize("tile", [64, 129])
+@pytest.mark.parametrize("splits", [0, 1, 2, 4, 8])
+@pytest.mark.parametrize("N", ENDS)
+def test_backward_by_a_cluster_whole_numbers_are_exact(N, splits, tile):
+    """One product and two in a launch, ends of either operand, sums in one part and in many."""
+    rng = np.random.default_rng(N)
+    for M, K in ((20, 128), (130, 65), (1000, 190), (2000, 8)):
+        dy, x, w, u = (ref.matrix(rng, r, c, BF16, whole=2) for r, c in ((M, N), (M, K), (N, K), (N, K)))
+        a, b, c, d = (t.double() for t in (dy, x, w, u))
+        add = ref.matrix(rng, N, K, F32, whole=3)
+        dx, dw, _ = gp.linear_backward(dy, x, w, out_dtype=F32, addend=add, tile=tile, k_splits=splits)
+        plan = status_ok()
+        assert plan["layout"] == 1 and plan["bn"] == min(tile, 128)
+        assert torch.equal(dw.double(), a.t() @ b + add.double()) and torch.equal(dx, (a @ c).to(BF16))
+        z = torch.ones_like(dy)
+        dx, dg, du = gp.gated_backward(dy, x, w, u, (z, z + 1), activation="relu", out_dtype=F32, tile=tile, k_splits=splits)
+        assert torch.equal(dg.double(), 2 * (a.t() @ b)) and torch.equal(du.double(), a.t() @ b)
+        assert torch.equal(dx, (a @ (2 * c + d)).to(BF16))
+        dx, dg, du = gp.gated_backward(dy, x, w, u, (z, z + 1), activation="relu", tile=tile, k_splits=splits)
+        assert torch.equal(dg, (2 * (a.t() @ b)).to(BF16)) and torch.equal(du, (a.t() @ b).to(BF16))
+    status_ok()
+
+
+def test_sizes_where_the_planner_takes_128_rows_by_a_cluster():
+    for op, M, N, K, count in (("weight_grad", 6458, 902, 692, 1), ("input_grad", 199, 4631, 3884, 1), ("input_grad", 512, 2048, 1024, 2)):
+        p = gp.ffn_plan(op, M, N, K, count=count)
+        assert p["layout"] == 1 and p["bn"] == 128, (op, M, N, K, p)
+    check_linear_backward(6458, 902, 692, BF16)
+    check_linear_backward(199, 4631, 3884, F16, weight_grad=False)
+    check_gated_backward(512, 2048, 1024, BF16)
