@@ -1,8 +1,9 @@
 // k_ffn_few.cu -- the products of small problems: for few tokens, and where the
 // ring's tiles would leave SMs idle.  The operand whose rows are the output's
 // columns (a weight, or x in a weight's gradient) fills the tensor cores' M side,
-// 128 rows per CTA, the other one their N side (16, 32 or 64 rows), and a cluster
-// of 1 to 8 CTAs shares a tile's K blocks.
+// 128 rows per CTA, the other one their N side (16, 32, 64 or 128 rows; gated up to
+// 64, a weight's gradient from 64), and a cluster of 1 to 8 CTAs shares a tile's K
+// blocks.
 //
 //   s[c][r] = sum over k of p[c][k] * q[r][k];  then as in ffn_ring.cuh
 //

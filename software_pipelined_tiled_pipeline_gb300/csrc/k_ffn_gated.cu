@@ -81,7 +81,9 @@ int ffn_plan_impl(int op, int64_t rows, int64_t cols, int64_t summed, int count,
     // 4096: 128 x 128 20.6, 128 rows 22.1, 256 x 256 29; gated 333 x 1000 x 776: 128 x 128 8.7, 256 x 256 10.0, 64 rows by
     // two CTAs 10.0; weight gradient of 8192 x 512 x 512: 64 rows by four CTAs 10.5, by one 21.1, 128 x 128 26.4.
     const double read = 2.0 * (static_cast<double>(rows) * summed + (gated ? 2.0 : 1.0) * cols * summed) * (kt > 0 ? count : 0) / 6500;
-    // Rows of a box off 128-byte boundaries take longer to load.
+    // Boxes whose rows begin off 128-byte boundaries take longer to load.  The planner does not see pointers and row
+    // strides: it takes rows to be packed, so that K says where they begin.  Rows of 2056 values laid out 2112 apart are
+    // counted as slow without reason, rows of 2048 laid out 2056 apart as fast; the gradients' are counted as fast.
     const double slow = (op == kFfnLinear || gated) && summed % 64 ? 1.6 : 1.0;
     double best = 0;
     auto take = [&](int t, double once, double k_blocks) {

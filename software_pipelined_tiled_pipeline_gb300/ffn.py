@@ -87,7 +87,10 @@ def linear(x, weight, bias=None, *, activation=None, residual=None, keep=None, o
     output's type; it may be ``out`` itself.  ``out``: where to write, apart
     from what is read; ``out_dtype``: x's type or float32.  ``keep``: "real" or
     "fp8" also returns the values before the activation, as ``kept`` of
-    ``linear_backward``: (z,) in x's type, or (codes, scales).  ``tile``,
+    ``linear_backward``: (z,) in x's type, or (codes, scales).  (Without an
+    activation the backward pass needs, and takes, none of them.)  Activations
+    are off by up to 1e-6 relative where they are not small, and up to 1e-5 in
+    the tails that fall towards 0, which shows in float32 outputs alone.  ``tile``,
     ``k_splits``, ``timeout_ns``, ``inject_lost_load``: see gp_ffn_options.
 
     Returns y, or (y, kept) with ``keep``.
